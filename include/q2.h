@@ -1,7 +1,8 @@
 /*
  * q2.h - C ABI of libq2: the Q2_0 ternary dequantize-and-multiply linear, its
- * rank-r side branch and the 4-bit nibble variant, as hand-written HIP kernels
- * for AMD CDNA4 (gfx950, MI355X).
+ * rank-r side branch and the 4-bit nibble variant, with an epilogue (bias,
+ * activation, gate, residual) and grouped by expert, and the experts' router
+ * and combination, as hand-written HIP kernels for AMD CDNA4 (gfx950, MI355X).
  *
  * Format (We're Teaching Your Browser to Paint, aitherium.com, section "The
  * lucky break that wasn't luck"): a weight row of K inputs is cut into blocks
@@ -28,7 +29,7 @@
  *    16-byte aligned; every other array must be aligned to its element size;
  *    the low-rank workspace to 256 bytes.
  *  - bf16 activations and f16 scales / factors are passed as their uint16
- *    bit patterns.  Outputs are float32.
+ *    bit patterns.  Outputs are float32 unless an entry point says otherwise.
  *  - Every compute entry point is asynchronous on `stream` (0 = the null
  *    stream) and returns only argument, device or launch errors.  Arguments
  *    are checked before any HIP call, so argument errors are reported even on
@@ -278,6 +279,171 @@ int q2_linear_a8(const uint16_t* x_bf16, const uint8_t* packed, const uint16_t* 
 int q4_linear(const uint16_t* x_bf16, const uint8_t* packed4, const uint16_t* scale_f16,
               const uint16_t* zero_f16, float* y, int64_t M, int64_t N, int64_t K,
               hipStream_t stream);
+
+/* Activations of q2_epilogue. */
+typedef enum {
+  Q2_ACT_NONE = 0,      /* v                                                        */
+  Q2_ACT_RELU = 1,      /* max(v, 0)                                                */
+  Q2_ACT_GELU = 2,      /* v (1 + erf(v / sqrt 2)) / 2                              */
+  Q2_ACT_GELU_TANH = 3, /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2        */
+  Q2_ACT_SILU = 4       /* v / (1 + exp(-v))                                        */
+} q2_activation;
+
+/* Flags of q2_epilogue. */
+#define Q2_EPI_GATED 0x1u         /* out = act(v[0 : N/2]) * v[N/2 : N]: y has N/2 columns     */
+#define Q2_EPI_OUT_BF16 0x2u      /* y is bf16 (rounded once, nearest even), else f32          */
+#define Q2_EPI_RESIDUAL_BF16 0x4u /* residual is bf16, else f32                                */
+
+/*
+ * q2_epilogue - what a fused linear does with its product z = x W^T before it
+ * writes, in fp32 per element, n_out = N, or N / 2 with Q2_EPI_GATED:
+ *   v = z + bias;  a = act(v), or act(v[n]) * v[N/2 + n] when gated;
+ *   y = residual + gate[n] * a
+ * The gated form takes the weight of a two-branch layer as one matrix: the
+ * N / 2 rows that pass through the activation first, the N / 2 rows that
+ * multiply it after them.
+ *   bias      f32 [N] ([E, N] for the grouped linears), or NULL
+ *   gate      f32 [n_out], or NULL (1): the modulation of a transformer block
+ *   residual  [M, n_out] f32 or bf16, or NULL (0).  It may be y itself (same
+ *             address and type): every element is read before it is written, by
+ *             the thread that writes it.
+ */
+typedef struct {
+  uint32_t activation; /* q2_activation */
+  uint32_t flags;      /* Q2_EPI_* */
+  const float* bias;
+  const float* gate;
+  const void* residual;
+} q2_epilogue;
+
+/*
+ * q2_linear_fused - the Q2_0 linear, optionally with its rank-r branch, with
+ * an epilogue: y = epilogue(x W^T + (x A^T) B^T).
+ *   x_bf16, packed, scales_f16, A_f16, B_f16, r, M, N, K   as q2_linear_lowrank
+ *              (r == 0: A and B are ignored).  x must be finite.
+ *   epi        host pointer, read before the call returns; NULL is the plain
+ *              product in f32
+ *   y          f32 or bf16 [M, n_out], overwritten; apart from the residual it
+ *              must not overlap an input
+ *   workspace  device scratch of >= q2_linear_fused_workspace_bytes(M, N, K, r)
+ *              bytes, 256-byte aligned (may be NULL when that is 0), owned by
+ *              the caller; overwritten
+ * K == 0 is the empty sum: the epilogue of z = 0.  Products and sums as in
+ * q2_linear: exact products, fp32 sums in a fixed order, so a call is run-to-run
+ * bitwise deterministic.  Errors: those of q2_linear_lowrank; an odd N with
+ * Q2_EPI_GATED is Q2_ERR_SHAPE, an unknown activation or flag Q2_ERR_ARG.
+ * Asynchronous; calls that share a workspace must be ordered on one stream.
+ */
+int q2_linear_fused(const uint16_t* x_bf16, const uint8_t* packed, const uint16_t* scales_f16,
+                    const uint16_t* A_f16, const uint16_t* B_f16, int64_t r, const q2_epilogue* epi,
+                    void* y, int64_t M, int64_t N, int64_t K,
+                    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* q2_linear_fused_workspace_bytes - device bytes q2_linear_fused needs; 0 for
+ * sizes that it refuses or that need none. */
+size_t q2_linear_fused_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r);
+
+/*
+ * q4_linear_fused - q4_linear with an epilogue.  packed4, scale_f16, zero_f16
+ * as q4_linear; epi, y and the errors as q2_linear_fused.  Asynchronous.
+ */
+int q4_linear_fused(const uint16_t* x_bf16, const uint8_t* packed4, const uint16_t* scale_f16,
+                    const uint16_t* zero_f16, const q2_epilogue* epi, void* y,
+                    int64_t M, int64_t N, int64_t K, hipStream_t stream);
+
+/*
+ * q2_linear_grouped - Q2_0 linears of E experts over rows sorted by expert:
+ * for offsets[e] <= i < offsets[e + 1], y[i] = epilogue_e(x[src(i)] W_e^T) with
+ * src(i) = row_index[i], or i without an index.
+ *   x_bf16     u16 [x_rows, K]; x_rows == R without an index         (in)
+ *   row_index  i32 [R] device, or NULL: the row of x that row i reads.  An
+ *              index outside [0, x_rows) reads a row of zeros.
+ *   offsets    i32 [E + 1] device, not decreasing, within [0, R].  Rows before
+ *              offsets[0] and from offsets[E] on are left as they were.  Values
+ *              that break this are clamped: the rows then computed are
+ *              unspecified, but nothing outside the arrays is touched.
+ *   packed     u8  [E, N, K/4]; scales_f16 u16 [E, N, K/128]: the experts'
+ *              Q2_0 weights one after the other                      (in)
+ *   epi        as q2_linear_fused, with bias [E, N]; gate and residual must be
+ *              NULL (Q2_ERR_ARG): the experts' rows are joined by q2_combine
+ *   y          f32 or bf16 [R, n_out]
+ *   workspace  device scratch of >= q2_linear_grouped_workspace_bytes(R, E, N, K)
+ *              bytes, 256-byte aligned (may be NULL when that is 0)
+ * E <= 65536, R and x_rows < 2^31.  The counts stay on the device: the launch
+ * covers any distribution of the R rows over the experts.  Errors as
+ * q2_linear_fused.  Asynchronous; calls that share a workspace must be ordered
+ * on one stream.
+ */
+int q2_linear_grouped(const uint16_t* x_bf16, int64_t x_rows, const int32_t* row_index, const int32_t* offsets,
+                      const uint8_t* packed, const uint16_t* scales_f16, const q2_epilogue* epi, void* y,
+                      int64_t R, int64_t E, int64_t N, int64_t K,
+                      void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* q2_linear_grouped_workspace_bytes - device bytes q2_linear_grouped needs; 0
+ * for sizes that it refuses or that need none. */
+size_t q2_linear_grouped_workspace_bytes(int64_t R, int64_t E, int64_t N, int64_t K);
+
+/*
+ * q4_linear_grouped - q2_linear_grouped for the 4-bit format: packed4 u8
+ * [E, N, K/2], scale_f16 and zero_f16 u16 [E, N, K/128].  Asynchronous.
+ */
+int q4_linear_grouped(const uint16_t* x_bf16, int64_t x_rows, const int32_t* row_index, const int32_t* offsets,
+                      const uint8_t* packed4, const uint16_t* scale_f16, const uint16_t* zero_f16,
+                      const q2_epilogue* epi, void* y, int64_t R, int64_t E, int64_t N, int64_t K,
+                      hipStream_t stream);
+
+/* Flags of q2_route. */
+#define Q2_ROUTE_LOGITS_BF16 0x1u /* logits are bf16, else f32                                  */
+#define Q2_ROUTE_RENORM 0x2u      /* the weights of a token sum to 1 over its chosen experts    */
+
+/*
+ * q2_route - top-k routing of T tokens over E experts, with the row plan that
+ * the grouped linears and q2_combine take.
+ *   logits     f32 or bf16 [T, E]                                    (in)
+ *   expert     i32 [T, k]: the experts with the k largest logits, largest
+ *              first, equal logits by lower expert first; -1 past the last one.
+ *              A logit of -inf or NaN is a masked expert and never chosen.  (out)
+ *   weight     f32 [T, k]: exp(logit) over its sum over all unmasked experts,
+ *              or over the chosen ones with Q2_ROUTE_RENORM; 0 where expert is
+ *              -1.  Logits of +inf share the whole weight equally.       (out)
+ *   offsets    i32 [E + 1]: expert e has rows offsets[e] .. offsets[e + 1] - 1  (out)
+ *   row_token  i32 [T * k]: the token of each row, increasing within an expert;
+ *              -1 from row offsets[E] on                              (out)
+ *   slot       i32 [T, k]: the row of each choice, -1 where expert is -1   (out)
+ *   workspace  device scratch of >= q2_route_workspace_bytes(T, E, k) bytes,
+ *              256-byte aligned (may be NULL when that is 0)
+ * 1 <= k <= min(E, 64), E <= 1024 (Q2_ERR_SHAPE otherwise), T * k < 2^31.  Sums
+ * in fp32 in a fixed order: run-to-run bitwise deterministic.  Asynchronous;
+ * calls that share a workspace must be ordered on one stream.
+ */
+int q2_route(const void* logits, int64_t T, int64_t E, int64_t k, uint32_t flags, int32_t* expert, float* weight,
+             int32_t* offsets, int32_t* row_token, int32_t* slot, void* workspace, size_t workspace_bytes,
+             hipStream_t stream);
+
+/* q2_route_workspace_bytes - device bytes q2_route needs; 0 for sizes that it
+ * refuses or that need none. */
+size_t q2_route_workspace_bytes(int64_t T, int64_t E, int64_t k);
+
+/* Flags of q2_combine. */
+#define Q2_COMBINE_Z_BF16 0x1u        /* z is bf16, else f32        */
+#define Q2_COMBINE_OUT_BF16 0x2u      /* y is bf16, else f32        */
+#define Q2_COMBINE_RESIDUAL_BF16 0x4u /* residual is bf16, else f32 */
+
+/*
+ * q2_combine - the experts' rows back on their tokens:
+ * y[t] = residual[t] + sum_j weight[t, j] * z[slot[t, j]], summed in fp32 in
+ * the order of j, rounded once.
+ *   z         f32 or bf16 [R, N]                                      (in)
+ *   slot      i32 [T, k]; a slot outside [0, R) adds nothing               (in)
+ *   weight    f32 [T, k]                                               (in)
+ *   residual  f32 or bf16 [T, N], or NULL (0); may be y itself (same
+ *             address and type)                                         (in)
+ *   y         f32 or bf16 [T, N]; must not overlap z                     (out)
+ * Pointers aligned to their element.  k <= 64 (Q2_ERR_SHAPE otherwise), k == 0
+ * copies the residual; R < 2^31.  Asynchronous.
+ */
+int q2_combine(const void* z, int64_t R, const int32_t* slot, const float* weight, const void* residual, void* y,
+               int64_t T, int64_t k, int64_t N, uint32_t flags, hipStream_t stream);
 
 /*
  * q2_dequant - test export: w[n, k] = (q - 1) * d as float32 [N, K], exact;

@@ -9,13 +9,14 @@ call, never falls back to anything else.
 
 Tensor conventions: activations torch.bfloat16 [M, K]; Q2_0 codes torch.uint8
 [N, K/4]; scales, low-rank factors and 4-bit scales / zeros torch.float16;
-outputs torch.float32.  All tensors must be contiguous and on the current
-device.
+outputs torch.float32, or torch.bfloat16 where a function takes out_dtype.  All
+tensors must be contiguous and on the current device.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -31,7 +32,23 @@ Q2_ACCUMULATE = 0x1      # q2_linear_ex flag: y += result
 EXPORTS = ("q2_pack", "q2_import_gemlite", "q2_linear", "q2_lowrank_workspace_bytes", "q2_linear_lowrank", "q2_linear_lowrank_noalloc",
            "q2_linear_ex", "q2_slice",
            "q2_a8_workspace_bytes", "q2_linear_a8",
+           "q2_linear_fused", "q2_linear_fused_workspace_bytes", "q4_linear_fused",
+           "q2_linear_grouped", "q2_linear_grouped_workspace_bytes", "q4_linear_grouped",
+           "q2_route", "q2_route_workspace_bytes", "q2_combine",
            "q4_linear", "q2_dequant", "q2_set_dispatch", "q2_strerror", "q2_last_error")
+
+# q2_epilogue: activations by name, and flags
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+Q2_EPI_GATED, Q2_EPI_OUT_BF16, Q2_EPI_RESIDUAL_BF16 = 0x1, 0x2, 0x4
+Q2_ROUTE_LOGITS_BF16, Q2_ROUTE_RENORM = 0x1, 0x2
+Q2_COMBINE_Z_BF16, Q2_COMBINE_OUT_BF16, Q2_COMBINE_RESIDUAL_BF16 = 0x1, 0x2, 0x4
+
+
+class Epilogue(ctypes.Structure):
+    """The C ABI's q2_epilogue."""
+    _fields_ = [("activation", ctypes.c_uint32), ("flags", ctypes.c_uint32), ("bias", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("residual", ctypes.c_void_p)]
+
 
 _lib = None
 
@@ -64,6 +81,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "q2_slice": ([p, p, i64, i64, i64, i64, i64, i64, p, p, p], ctypes.c_int),
         "q2_a8_workspace_bytes": ([i64, i64], sz),
         "q2_linear_a8": ([p, p, p, p, i64, i64, i64, p, sz, p], ctypes.c_int),
+        "q2_linear_fused": ([p, p, p, p, p, i64, p, p, i64, i64, i64, p, sz, p], ctypes.c_int),
+        "q2_linear_fused_workspace_bytes": ([i64, i64, i64, i64], sz),
+        "q4_linear_fused": ([p, p, p, p, p, p, i64, i64, i64, p], ctypes.c_int),
+        "q2_linear_grouped": ([p, i64, p, p, p, p, p, p, i64, i64, i64, i64, p, sz, p], ctypes.c_int),
+        "q2_linear_grouped_workspace_bytes": ([i64, i64, i64, i64], sz),
+        "q4_linear_grouped": ([p, i64, p, p, p, p, p, p, p, i64, i64, i64, i64, p], ctypes.c_int),
+        "q2_route": ([p, i64, i64, i64, ctypes.c_uint32, p, p, p, p, p, p, sz, p], ctypes.c_int),
+        "q2_route_workspace_bytes": ([i64, i64, i64], sz),
+        "q2_combine": ([p, i64, p, p, p, p, i64, i64, i64, ctypes.c_uint32, p], ctypes.c_int),
         "q4_linear": ([p, p, p, p, p, i64, i64, i64, p], ctypes.c_int),
         "q2_dequant": ([p, p, p, i64, i64, p], ctypes.c_int),
         "q2_set_dispatch": ([ctypes.c_char_p, ctypes.c_char_p, ctypes.c_int], ctypes.c_int),
@@ -293,6 +319,221 @@ def q4_linear(x, packed4, scale, zero, y=None) -> torch.Tensor:
         y = torch.empty((m, n), dtype=torch.float32, device=x.device)
     _want(y, torch.float32, (m, n), "y")
     _check(lib.q4_linear(_ptr(x), _ptr(packed4), _ptr(scale), _ptr(zero), _ptr(y), m, n, k, _stream()))
+    return y
+
+
+def _want_here(t: torch.Tensor, dtype, shape: tuple, name: str) -> None:
+    """_want, on the current device (the device of the stream the call goes to)."""
+    _want(t, dtype, shape, name)
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{torch.cuda.current_device()}")
+
+
+def _epilogue(n, rows, bias_shape, bias, activation, gated, gate, residual, out_dtype, y, device):
+    """(q2_epilogue, y) of a fused or grouped linear over a weight of n rows; y is allocated when None."""
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {activation!r}: one of {', '.join(ACTIVATIONS)}")
+    if gated and n % 2:
+        raise ValueError(f"a gated weight has two equal halves of rows, got {n} rows")
+    if y is not None:
+        out_dtype = y.dtype
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"the output is float32 or bfloat16, not {out_dtype}")
+    shape = (rows, n // 2 if gated else n)
+    flags = Q2_EPI_GATED if gated else 0
+    if out_dtype == torch.bfloat16:
+        flags |= Q2_EPI_OUT_BF16
+    if bias is not None:
+        _want_here(bias, torch.float32, bias_shape, "bias")
+    if gate is not None:
+        _want_here(gate, torch.float32, shape[1:], "gate")
+    if residual is not None:
+        if residual.dtype == torch.bfloat16:
+            flags |= Q2_EPI_RESIDUAL_BF16
+        elif residual.dtype != torch.float32:
+            raise ValueError(f"residual is float32 or bfloat16, not {residual.dtype}")
+        _want_here(residual, residual.dtype, shape, "residual")
+    if y is None:
+        y = torch.empty(shape, dtype=out_dtype, device=device)
+    else:
+        _want_here(y, out_dtype, shape, "y")
+    return Epilogue(ACTIVATIONS[activation], flags, _ptr(bias), _ptr(gate), _ptr(residual)), y
+
+
+def _scratch(need: int, workspace, device):
+    """(workspace, its bytes): the caller's, or a new one of `need` bytes."""
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        _want_here(workspace, workspace.dtype, workspace.shape, "workspace")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def linear_fused_workspace_bytes(m: int, n: int, k: int, r: int = 0) -> int:
+    """Workspace bytes of q2_linear_fused for a weight of n rows."""
+    return int(load().q2_linear_fused_workspace_bytes(m, n, k, r))
+
+
+def q2_linear_fused(x, packed, scales, A=None, B=None, bias=None, activation="none", gated=False, gate=None,
+                    residual=None, out_dtype=torch.float32, y=None, workspace=None) -> torch.Tensor:
+    """y = residual + gate * act(x W^T + (x A^T) B^T + bias) for Q2_0 weights, in float32 and rounded once to
+    out_dtype (or y's type).
+
+    gated: the weight holds the rows of two branches, [2 n, K], and act(first half) * second half has n columns.
+    bias f32 [N]; gate f32 [n_out]; residual f32 or bf16 [M, n_out], which may be y itself; A f16 [r, K] and
+    B f16 [N, r] add the rank-r branch.  activation: none, relu, gelu, gelu_tanh or silu."""
+    lib = load()
+    m, k = x.shape
+    n = packed.shape[0]
+    _want_here(x, torch.bfloat16, (m, k), "x")
+    _want_here(packed, torch.uint8, (n, k // 4), "packed")
+    _want_here(scales, torch.float16, (n, k // 128), "scales")
+    if (A is None) != (B is None):
+        raise ValueError("A and B come together")
+    r = 0 if A is None else A.shape[0]
+    if A is not None:
+        _want_here(A, torch.float16, (r, k), "A")
+        _want_here(B, torch.float16, (n, r), "B")
+    epi, y = _epilogue(n, m, (n,), bias, activation, gated, gate, residual, out_dtype, y, x.device)
+    ws, ws_bytes = _scratch(lib.q2_linear_fused_workspace_bytes(m, n, k, r), workspace, x.device)
+    _check(lib.q2_linear_fused(_ptr(x), _ptr(packed), _ptr(scales), _ptr(A), _ptr(B), r, ctypes.addressof(epi), _ptr(y),
+                               m, n, k, _ptr(ws), ws_bytes, _stream()))
+    return y
+
+
+def q4_linear_fused(x, packed4, scale, zero, bias=None, activation="none", gated=False, gate=None, residual=None,
+                    out_dtype=torch.float32, y=None) -> torch.Tensor:
+    """q2_linear_fused (without the branch) for the 4-bit format of q4_linear."""
+    lib = load()
+    m, k = x.shape
+    n = packed4.shape[0]
+    _want_here(x, torch.bfloat16, (m, k), "x")
+    _want_here(packed4, torch.uint8, (n, k // 2), "packed4")
+    _want_here(scale, torch.float16, (n, k // 128), "scale")
+    _want_here(zero, torch.float16, (n, k // 128), "zero")
+    epi, y = _epilogue(n, m, (n,), bias, activation, gated, gate, residual, out_dtype, y, x.device)
+    _check(lib.q4_linear_fused(_ptr(x), _ptr(packed4), _ptr(scale), _ptr(zero), ctypes.addressof(epi), _ptr(y), m, n, k,
+                               _stream()))
+    return y
+
+
+def _groups(x, offsets, experts, row_index):
+    """(rows, x_rows, K) of a grouped call, its integer arguments checked."""
+    x_rows, k = x.shape
+    _want_here(x, torch.bfloat16, (x_rows, k), "x")
+    _want_here(offsets, torch.int32, (experts + 1,), "offsets")
+    if row_index is None:
+        return x_rows, x_rows, k
+    rows = row_index.numel()
+    _want_here(row_index, torch.int32, (rows,), "row_index")
+    return rows, x_rows, k
+
+
+def linear_grouped_workspace_bytes(rows: int, experts: int, n: int, k: int) -> int:
+    """Workspace bytes of q2_linear_grouped for `experts` weights of n rows."""
+    return int(load().q2_linear_grouped_workspace_bytes(rows, experts, n, k))
+
+
+def q2_linear_grouped(x, offsets, packed, scales, row_index=None, bias=None, activation="none", gated=False,
+                      out_dtype=torch.float32, y=None, workspace=None) -> torch.Tensor:
+    """Q2_0 linears of E experts over rows sorted by expert: row i in offsets[e] .. offsets[e+1] - 1 of y is
+    act(x[row_index[i]] W_e^T + bias_e), or of x[i] without an index.
+
+    packed u8 [E, N, K/4], scales f16 [E, N, K/128], offsets i32 [E+1] and row_index i32 [R] as q2_route gives
+    them, bias f32 [E, N]; gated, activation and out_dtype as q2_linear_fused.  Rows that no expert has are left
+    as they are in y (undefined in a y allocated here)."""
+    lib = load()
+    e, n = packed.shape[:2]
+    rows, x_rows, k = _groups(x, offsets, e, row_index)
+    _want_here(packed, torch.uint8, (e, n, k // 4), "packed")
+    _want_here(scales, torch.float16, (e, n, k // 128), "scales")
+    epi, y = _epilogue(n, rows, (e, n), bias, activation, gated, None, None, out_dtype, y, x.device)
+    ws, ws_bytes = _scratch(lib.q2_linear_grouped_workspace_bytes(rows, e, n, k), workspace, x.device)
+    _check(lib.q2_linear_grouped(_ptr(x), x_rows, _ptr(row_index), _ptr(offsets), _ptr(packed), _ptr(scales),
+                                 ctypes.addressof(epi), _ptr(y), rows, e, n, k, _ptr(ws), ws_bytes, _stream()))
+    return y
+
+
+def q4_linear_grouped(x, offsets, packed4, scale, zero, row_index=None, bias=None, activation="none", gated=False,
+                      out_dtype=torch.float32, y=None) -> torch.Tensor:
+    """q2_linear_grouped for the 4-bit format: packed4 u8 [E, N, K/2], scale and zero f16 [E, N, K/128]."""
+    lib = load()
+    e, n = packed4.shape[:2]
+    rows, x_rows, k = _groups(x, offsets, e, row_index)
+    _want_here(packed4, torch.uint8, (e, n, k // 2), "packed4")
+    _want_here(scale, torch.float16, (e, n, k // 128), "scale")
+    _want_here(zero, torch.float16, (e, n, k // 128), "zero")
+    epi, y = _epilogue(n, rows, (e, n), bias, activation, gated, None, None, out_dtype, y, x.device)
+    _check(lib.q4_linear_grouped(_ptr(x), x_rows, _ptr(row_index), _ptr(offsets), _ptr(packed4), _ptr(scale), _ptr(zero),
+                                 ctypes.addressof(epi), _ptr(y), rows, e, n, k, _stream()))
+    return y
+
+
+class Route(NamedTuple):
+    """q2_route's choice and row plan."""
+    expert: torch.Tensor      # i32 [T, k], -1 past the last unmasked expert
+    weight: torch.Tensor      # f32 [T, k]
+    offsets: torch.Tensor     # i32 [E + 1]: the rows of each expert
+    row_token: torch.Tensor   # i32 [T k]: the token of each row, -1 behind the last row
+    slot: torch.Tensor        # i32 [T, k]: the row of each choice, or -1
+
+
+def q2_route(logits, k: int, renormalize: bool = True, workspace=None) -> Route:
+    """Top-k routing of the tokens of logits [T, E] (f32 or bf16): the k largest per token (equal logits: the lower
+    expert first; -inf and NaN are masked experts), their softmax weights over all unmasked experts or, with
+    renormalize, over the chosen ones, and the rows sorted by expert, then token, as the grouped linears
+    (offsets, row_token) and q2_combine (slot, weight) take them."""
+    lib = load()
+    t, e = logits.shape
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"logits are float32 or bfloat16, not {logits.dtype}")
+    _want_here(logits, logits.dtype, (t, e), "logits")
+    flags = (Q2_ROUTE_LOGITS_BF16 if logits.dtype == torch.bfloat16 else 0) | (Q2_ROUTE_RENORM if renormalize else 0)
+    k = int(k)
+    rows = max(t * k, 0)
+    dev = logits.device
+    route = Route(torch.empty((t, max(k, 0)), dtype=torch.int32, device=dev),
+                  torch.empty((t, max(k, 0)), dtype=torch.float32, device=dev),
+                  torch.empty(e + 1, dtype=torch.int32, device=dev),
+                  torch.empty(rows, dtype=torch.int32, device=dev),
+                  torch.empty((t, max(k, 0)), dtype=torch.int32, device=dev))
+    ws, ws_bytes = _scratch(lib.q2_route_workspace_bytes(t, e, k), workspace, dev)
+    _check(lib.q2_route(_ptr(logits), t, e, k, flags, _ptr(route.expert), _ptr(route.weight), _ptr(route.offsets),
+                        _ptr(route.row_token), _ptr(route.slot), _ptr(ws), ws_bytes, _stream()))
+    return route
+
+
+def q2_combine(z, slot, weight, residual=None, out_dtype=torch.float32, y=None) -> torch.Tensor:
+    """y[t] = residual[t] + sum_j weight[t, j] * z[slot[t, j]]: the experts' rows z [R, N] (f32 or bf16) back on
+    their tokens; slot i32 and weight f32 [T, k] as q2_route gives them, a slot outside [0, R) adds nothing;
+    residual f32 or bf16 [T, N], which may be y itself."""
+    lib = load()
+    r, n = z.shape
+    t, k = slot.shape
+    if z.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"z is float32 or bfloat16, not {z.dtype}")
+    _want_here(z, z.dtype, (r, n), "z")
+    _want_here(slot, torch.int32, (t, k), "slot")
+    _want_here(weight, torch.float32, (t, k), "weight")
+    if y is not None:
+        out_dtype = y.dtype
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"the output is float32 or bfloat16, not {out_dtype}")
+    flags = (Q2_COMBINE_Z_BF16 if z.dtype == torch.bfloat16 else 0) | \
+        (Q2_COMBINE_OUT_BF16 if out_dtype == torch.bfloat16 else 0)
+    if residual is not None:
+        if residual.dtype == torch.bfloat16:
+            flags |= Q2_COMBINE_RESIDUAL_BF16
+        elif residual.dtype != torch.float32:
+            raise ValueError(f"residual is float32 or bfloat16, not {residual.dtype}")
+        _want_here(residual, residual.dtype, (t, n), "residual")
+    if y is None:
+        y = torch.empty((t, n), dtype=out_dtype, device=z.device)
+    else:
+        _want_here(y, out_dtype, (t, n), "y")
+    _check(lib.q2_combine(_ptr(z), r, _ptr(slot), _ptr(weight), _ptr(residual), _ptr(y), t, k, n, flags, _stream()))
     return y
 
 

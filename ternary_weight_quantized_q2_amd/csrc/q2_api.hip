@@ -2,86 +2,19 @@
 // Every argument check runs before the first HIP call, so a host without a GPU
 // still gets argument, shape and alignment errors.
 #include <atomic>
-#include <mutex>
-#include <cstdarg>
-#include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <mutex>
 
 #include "q2.h"
+#include "q2_host.h"
 #include "q2_internal.h"
 
 namespace {
 
-thread_local char g_detail[320];
+using namespace q2host;
 
-int fail(int code, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_detail, sizeof g_detail, fmt, ap);
-  va_end(ap);
-  return code;
-}
-
-int ok() {
-  g_detail[0] = '\0';
-  return Q2_OK;
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// pointer must be non-NULL when the buffer is non-empty, and aligned
-int check_ptr(const void* p, bool nonempty, size_t align, const char* name) {
-  if (nonempty && p == nullptr) return fail(Q2_ERR_ARG, "%s is NULL for a non-empty buffer", name);
-  if (p != nullptr && !aligned(p, align)) return fail(Q2_ERR_ALIGN, "%s is not %zu-byte aligned", name, align);
-  return Q2_OK;
-}
-
-int check_sizes(int64_t M, int64_t N, int64_t K) {
-  if (M < 0 || N < 0 || K < 0) return fail(Q2_ERR_ARG, "negative size (M=%lld N=%lld K=%lld)", (long long)M,
-                                           (long long)N, (long long)K);
-  if (K % 128 != 0) return fail(Q2_ERR_SHAPE, "K=%lld is not a multiple of 128", (long long)K);
-  // keep every element index inside int64 with room to spare
-  const int64_t lim = (int64_t)1 << 46;
-  if (M > lim || N > lim || K > lim || (M > 0 && K > lim / M) || (N > 0 && K > lim / N) ||
-      (M > 0 && N > lim / M))
-    return fail(Q2_ERR_ARG, "sizes too large");
-  return Q2_OK;
-}
-
-// The linear kernels address one tile's activation rows and weight columns
-// with 32-bit offsets; K up to 2^24 keeps them in range for every tile shape.
-int check_linear_k(int64_t K) {
-  if (K > ((int64_t)1 << 24)) return fail(Q2_ERR_SHAPE, "K=%lld exceeds 16777216", (long long)K);
-  return Q2_OK;
-}
-
-std::atomic<int> g_arch_ok[64];
 std::mutex g_check_lock;              // q2_pack and q2_import_gemlite share the device's error flags
-
-int check_device() {
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return fail(Q2_ERR_HIP, "hipGetDevice: %s", hipGetErrorString(e));
-  const int slot = (dev >= 0 && dev < 64) ? dev : -1;
-  if (slot >= 0) {
-    const int st = g_arch_ok[slot].load(std::memory_order_relaxed);
-    if (st == 1) return Q2_OK;
-    if (st == -1) return fail(Q2_ERR_DEVICE, "device %d is not gfx950", dev);
-  }
-  hipDeviceProp_t prop;
-  e = hipGetDeviceProperties(&prop, dev);
-  if (e != hipSuccess) return fail(Q2_ERR_HIP, "hipGetDeviceProperties: %s", hipGetErrorString(e));
-  const bool good = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0;
-  if (slot >= 0) g_arch_ok[slot].store(good ? 1 : -1, std::memory_order_relaxed);
-  if (!good) return fail(Q2_ERR_DEVICE, "device %d is %s, not gfx950", dev, prop.gcnArchName);
-  return Q2_OK;
-}
-
-int hip_status(hipError_t e, const char* what) {
-  if (e != hipSuccess) return fail(Q2_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-  return ok();
-}
 
 // Test and profiling control of the launch choice: the path (0 automatic,
 // 1 GEMV, 2 GEMM), a GEMM configuration (0 automatic, else its number, -1 an
@@ -231,7 +164,7 @@ const char* q2_strerror(int status) {
   }
 }
 
-const char* q2_last_error(void) { return g_detail; }
+const char* q2_last_error(void) { return q2host::g_detail; }
 
 int q2_set_dispatch(const char* path, const char* tile, int ksplit) {
   read_dispatch_env();

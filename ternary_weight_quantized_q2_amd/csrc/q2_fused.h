@@ -1,0 +1,148 @@
+// q2_fused.h - arguments, epilogue and row-group lookup shared by the kernels of
+// the fused and grouped linears.
+#pragma once
+#include "q2.h"
+#include "q2_device.h"
+
+namespace q2dev {
+
+// One fused or grouped linear.  Rows of x and y are numbered over all experts;
+// without experts (offsets == nullptr) there is one group of M rows.
+struct FusedArgs {
+  const uint16_t* x;          // bf16 [x_rows, K]
+  const int32_t* row_index;   // row of x that row i reads, or nullptr (i); outside [0, x_rows): zeros
+  int64_t x_rows;
+  const uint8_t* w;           // codes [E, N, K/4] or [E, N, K/2]
+  const uint16_t* s;          // f16 scales [E, N, K/128]
+  const uint16_t* z;          // f16 zero points, 4-bit only
+  const int32_t* offsets;     // [E + 1] or nullptr
+  int64_t E, M, N, K;         // N counts weight rows
+  const uint16_t* lr_t;       // bf16 limbs [M, 2 r8] of x A^T, r > 0
+  const uint16_t* lr_b;       // f16 [N, r]
+  int r;
+  int act, gated, out_bf16, res_bf16;
+  const float* bias;          // [E, N] or nullptr
+  const float* gate;          // [n_out] or nullptr
+  const void* residual;       // [M, n_out] or nullptr
+  void* y;                    // [M, n_out]
+};
+
+__host__ __device__ __forceinline__ int64_t fused_n_out(const FusedArgs& a) { return a.gated ? a.N / 2 : a.N; }
+
+// ---- epilogue ----------------------------------------------------------------
+// exp and the reciprocal are the hardware's (about one ulp each); both GELU and
+// SiLU are v times a logistic or normal distribution function, so a large |v|
+// gives v or a zero, never inf / inf.
+__device__ __forceinline__ float logistic(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
+
+__device__ __forceinline__ float activate(int act, float v) {
+  switch (act) {
+    case Q2_ACT_RELU: return fmaxf(v, 0.0f);
+    case Q2_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    // (1 + tanh u) / 2 is the logistic function of 2 u
+    case Q2_ACT_GELU_TANH: return v * logistic(1.5957691216057308f * (v + 0.044715f * v * v * v));
+    case Q2_ACT_SILU: return v * logistic(v);
+    default: return v;
+  }
+}
+
+__device__ __forceinline__ float load_elem(const void* p, int64_t i, int bf16) {
+  return bf16 ? bf16_to_f32(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+
+// bf16 bits of v, nearest even, NaN kept (the hardware's conversion).
+__device__ __forceinline__ uint16_t to_bf16(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+
+// One output element from its product v (and, gated, the product u of the
+// second half's row): row m, output column n, of an expert with bias `bias`.
+__device__ __forceinline__ void store_out(const FusedArgs& a, const float* bias, int64_t n_out, int64_t m, int64_t n,
+                                          float v, float u) {
+  if (bias) v += bias[n];
+  v = activate(a.act, v);
+  if (a.gated) v *= bias ? u + bias[n_out + n] : u;
+  if (a.gate) v *= a.gate[n];
+  const int64_t i = m * n_out + n;
+  if (a.residual) v += load_elem(a.residual, i, a.res_bf16);
+  if (a.out_bf16) static_cast<uint16_t*>(a.y)[i] = to_bf16(v);
+  else static_cast<float*>(a.y)[i] = v;
+}
+
+// ---- row groups ----------------------------------------------------------------
+// The group (expert) and rows of row tile `slot`, counting the tiles of `bm`
+// rows of all groups in order.  Every wave of the workgroup calls it together
+// and gets the same answer: the 64 lanes take 64 groups at a time, count their
+// tiles and add them up.  Offsets are clamped to [0, M] and to not decrease
+// within a group, so whatever they hold, the rows lie inside x and y.
+struct RowTile {
+  int64_t m0, mend;           // rows m0 .. min(m0 + bm, mend) - 1
+  int64_t expert;
+  bool valid;
+};
+
+__device__ __forceinline__ int64_t clamp_offset(int32_t v, int64_t lo, int64_t hi) {
+  return v < lo ? lo : v > hi ? hi : v;
+}
+
+__device__ __forceinline__ RowTile find_row_tile(const FusedArgs& a, int64_t slot, int bm) {
+  RowTile t;
+  t.expert = 0;
+  t.m0 = slot * bm;
+  t.mend = a.M;
+  t.valid = t.m0 < a.M;
+  if (a.offsets == nullptr) return t;
+  const int lane = threadIdx.x & 63;
+  int64_t before = 0;                                    // tiles of the groups already passed
+  t.valid = false;
+  for (int64_t e0 = 0; e0 < a.E; e0 += 64) {
+    const int64_t e = e0 + lane;
+    int64_t lo = 0, hi = 0;
+    if (e < a.E) {
+      lo = clamp_offset(a.offsets[e], 0, a.M);
+      hi = clamp_offset(a.offsets[e + 1], lo, a.M);
+    }
+    const int mine = (int)((hi - lo + bm - 1) / bm);
+    int sum = mine;                                      // inclusive sum over the lanes
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(sum, d);
+      if (lane >= d) sum += v;
+    }
+    const int total = __shfl(sum, 63);
+    const uint64_t past = __builtin_amdgcn_ballot_w64(before + sum > slot);
+    if (past != 0) {
+      const int l = __builtin_ctzll(past);
+      const int64_t first = before + __shfl(sum - mine, l);
+      t.m0 = __shfl((int)lo, l) + (slot - first) * bm;
+      t.mend = __shfl((int)hi, l);
+      t.expert = e0 + l;
+      t.valid = true;
+      return t;
+    }
+    before += total;
+  }
+  return t;
+}
+
+// At most this many row tiles of bm rows over all groups: each of the at most
+// min(E, M) groups with rows adds less than one tile to M / bm.
+inline int64_t max_row_tiles(const FusedArgs& a, int bm) {
+  if (a.offsets == nullptr) return (a.M + bm - 1) / bm;
+  const int64_t groups = a.E < a.M ? a.E : a.M;
+  return (a.M + groups * (bm - 1)) / bm;
+}
+
+// ---- host side -------------------------------------------------------------------
+// Workspace beside the limbs of a rank-r branch; 0 where none is needed.
+size_t fused_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t E, int fmt);
+// fmt 0 = Q2_0, 1 = 4-bit.  ws: that many bytes.
+hipError_t launch_fused(const FusedArgs& a, int fmt, void* ws, hipStream_t stream);
+
+hipError_t launch_route(const void* logits, int logits_bf16, int64_t T, int64_t E, int k, int renorm, int32_t* expert,
+                        float* weight, int32_t* offsets, int32_t* row_token, int32_t* slot, void* ws,
+                        hipStream_t stream);
+size_t route_workspace_bytes(int64_t T, int64_t E);
+hipError_t launch_combine(const void* z, int z_bf16, int64_t R, const int32_t* slot, const float* weight,
+                          const void* residual, int res_bf16, void* y, int out_bf16, int64_t T, int k, int64_t N,
+                          hipStream_t stream);
+
+}  // namespace q2dev

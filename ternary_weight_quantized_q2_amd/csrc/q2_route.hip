@@ -1,0 +1,358 @@
+// q2_route.hip - the experts' router (top-k choice, softmax weights, row plan)
+// and the combination of the experts' rows.
+#include "q2_fused.h"
+#include <algorithm>
+
+namespace q2dev {
+
+// ============================================================================
+// Router
+// ============================================================================
+// A workgroup of four waves takes 64 tokens, one wave per token at a time.  A
+// lane holds every 64th logit as a 64-bit key (order-preserving bits of the
+// logit above the complement of the expert number), so one maximum over the
+// lanes finds the largest logit and, among equal ones, the lowest expert; k
+// such maxima are the choice.
+//
+// Row plan: each token chooses an expert at most once, so the 64 tokens'
+// choices are one 64-bit mask per expert, and a choice's place among the
+// workgroup's rows of its expert is the number of mask bits below its token.
+// The rows of earlier workgroups and experts come from the workgroups' counts:
+// up to 64 tokens one launch has everything; beyond, the first launch leaves
+// the counts (one byte per workgroup and expert) in the workspace and the
+// second adds them up.  Integer counts in a fixed order: the plan is exact and
+// the same on every run.
+constexpr int RT_TOK = 64, RT_THREADS = 256, RT_WAVES = RT_THREADS / 64;
+
+constexpr int route_pad(int64_t E) { return (int)((E + 15) & ~(int64_t)15); }   // bytes of counts per workgroup
+
+__device__ __forceinline__ uint32_t order_bits(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f);          // -0 counts as +0
+  return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float from_order_bits(uint32_t o) {
+  return __builtin_bit_cast(float, o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) {
+    const uint64_t o = __shfl_xor((unsigned long long)v, d);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+// exp(v - top) of a logit, 1 for the largest itself (also when that is +inf).
+__device__ __forceinline__ float route_exp(float v, float top) { return v == top ? 1.0f : __expf(v - top); }
+
+// Choice and weights of one token: lane j < k returns choice j (-1 for none).
+template <int NE>
+__device__ __forceinline__ void choose(const void* logits, int bf16, int64_t t, int E, int k, int renorm, int lane,
+                                       int& ex, float& wt) {
+  uint64_t key[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const int e = lane + 64 * i;
+    key[i] = 0;                                          // below every unmasked logit
+    if (e < E) {
+      const float v = load_elem(logits, t * E + e, bf16);
+      if (v > -__builtin_inff()) key[i] = ((uint64_t)order_bits(v) << 32) | (uint32_t)~e;
+    }
+  }
+  ex = -1;
+  float mine = 0.f, top = 0.f, total = 0.f;
+  for (int j = 0; j < k; ++j) {
+    uint64_t m = key[0];
+#pragma unroll
+    for (int i = 1; i < NE; ++i) m = key[i] > m ? key[i] : m;
+    m = wave_max(m);
+    if (m == 0) break;                                   // nothing left but masked experts
+    const float v = from_order_bits((uint32_t)(m >> 32));
+    if (j == 0) {
+      top = v;
+      if (!renorm) {                                     // every unmasked expert, before any key is taken out
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+          if (key[i] != 0) total += route_exp(from_order_bits((uint32_t)(key[i] >> 32)), top);
+        total = wave_sum(total);
+      }
+    }
+    const float p = route_exp(v, top);
+    if (renorm) total += p;                              // largest first
+    if (lane == j) {
+      ex = (int)~(uint32_t)m;
+      mine = p;
+    }
+#pragma unroll
+    for (int i = 0; i < NE; ++i) key[i] = key[i] == m ? 0 : key[i];
+  }
+  wt = ex >= 0 ? mine / total : 0.f;
+}
+
+// Offsets of the experts from their totals in tot[] (replaced), by one wave.
+__device__ __forceinline__ void scan_experts(int* tot, int E, int lane) {
+  int run = 0;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const int e = e0 + lane;
+    const int v = e < E ? tot[e] : 0;
+    int s = v;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(s, d);
+      if (lane >= d) s += o;
+    }
+    if (e < E) tot[e] = run + s - v;
+    run += __shfl(s, 63);
+  }
+  if (lane == 0) tot[E] = run;
+}
+
+template <int NE, bool ONE>
+__global__ __launch_bounds__(RT_THREADS) void route_choose_kernel(const void* logits, int bf16, int64_t T, int E, int k,
+                                                                  int renorm, int32_t* expert, float* weight,
+                                                                  int32_t* offsets, int32_t* row_token, int32_t* slot,
+                                                                  uint8_t* counts, int pad) {
+  __shared__ unsigned long long mask[64 * NE];
+  __shared__ int off[ONE ? 64 * NE + 1 : 1];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int64_t t0 = (int64_t)blockIdx.x * RT_TOK;
+  const int nt = (int)std::min<int64_t>(T - t0, RT_TOK);
+  for (int e = threadIdx.x; e < E; e += RT_THREADS) mask[e] = 0;
+  __syncthreads();
+  for (int i = wv; i < nt; i += RT_WAVES) {
+    int ex;
+    float wt;
+    choose<NE>(logits, bf16, t0 + i, E, k, renorm, lane, ex, wt);
+    if (lane < k) {
+      expert[(t0 + i) * k + lane] = ex;
+      weight[(t0 + i) * k + lane] = wt;
+      if (ex >= 0) atomicOr(&mask[ex], 1ull << i);
+    }
+  }
+  __syncthreads();
+  if constexpr (!ONE) {
+    for (int e = threadIdx.x; e < pad; e += RT_THREADS)
+      counts[(int64_t)blockIdx.x * pad + e] = e < E ? (uint8_t)__popcll(mask[e]) : (uint8_t)0;
+  } else {
+    for (int e = threadIdx.x; e < E; e += RT_THREADS) off[e] = __popcll(mask[e]);
+    __syncthreads();
+    if (wv == 0) scan_experts(off, E, lane);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= E; e += RT_THREADS) offsets[e] = off[e];
+    for (int i = threadIdx.x; i < nt * k; i += RT_THREADS) {
+      const int ex = expert[i];                          // written by this workgroup before the barrier
+      const int tok = i / k;
+      int row = -1;
+      if (ex >= 0) {
+        row = off[ex] + __popcll(mask[ex] & ((1ull << tok) - 1));
+        row_token[row] = tok;
+      }
+      slot[i] = row;
+      if (i >= off[E]) row_token[i] = -1;
+    }
+  }
+}
+
+// Second launch: workgroup b adds up the counts of all workgroups and of those
+// before it, and places its tokens' choices.
+__global__ __launch_bounds__(RT_THREADS) void route_place_kernel(const int32_t* expert, int64_t T, int E, int k,
+                                                                 const uint8_t* counts, int pad, int groups,
+                                                                 int32_t* offsets, int32_t* row_token, int32_t* slot) {
+  __shared__ unsigned long long mask[1024];
+  __shared__ int tot[1025], before[1024];
+  const int64_t t0 = (int64_t)blockIdx.x * RT_TOK;
+  const int nt = (int)std::min<int64_t>(T - t0, RT_TOK);
+  for (int e = threadIdx.x; e < E; e += RT_THREADS) {
+    mask[e] = 0;
+    tot[e] = 0;
+    before[e] = 0;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < nt * k; i += RT_THREADS) {
+    const int ex = expert[t0 * k + i];
+    if (ex >= 0) atomicOr(&mask[ex], 1ull << (i / k));
+  }
+  // 16 experts' counts per load; the threads beyond one row of counts take further rows
+  const int vec = pad / 16, rows = std::max(1, RT_THREADS / vec);
+  for (int idx = threadIdx.x; idx < vec * rows; idx += RT_THREADS) {
+    const int q = idx % vec, r0 = idx / vec;
+    int all[16] = {}, pre[16] = {};
+    for (int b = r0; b < groups; b += rows) {
+      const q2_u32x4 v = *reinterpret_cast<const q2_u32x4*>(counts + (int64_t)b * pad + 16 * q);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int n = (v[i >> 2] >> (8 * (i & 3))) & 255;
+        all[i] += n;
+        pre[i] += b < (int)blockIdx.x ? n : 0;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (16 * q + i < E && all[i]) {
+        atomicAdd(&tot[16 * q + i], all[i]);
+        if (pre[i]) atomicAdd(&before[16 * q + i], pre[i]);
+      }
+  }
+  __syncthreads();
+  if (threadIdx.x < 64) scan_experts(tot, E, threadIdx.x);
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int e = threadIdx.x; e <= E; e += RT_THREADS) offsets[e] = tot[e];
+  for (int i = threadIdx.x; i < nt * k; i += RT_THREADS) {
+    const int64_t at = t0 * k + i;
+    const int ex = expert[at], tok = i / k;
+    int row = -1;
+    if (ex >= 0) {
+      row = tot[ex] + before[ex] + __popcll(mask[ex] & ((1ull << tok) - 1));
+      row_token[row] = (int)(t0 + tok);
+    }
+    slot[at] = row;
+    if (at >= tot[E]) row_token[at] = -1;
+  }
+}
+
+__global__ __launch_bounds__(256) void route_empty_kernel(int32_t* offsets, int E) {
+  for (int e = threadIdx.x; e <= E; e += 256) offsets[e] = 0;
+}
+
+size_t route_workspace_bytes(int64_t T, int64_t E) {
+  const int64_t groups = (T + RT_TOK - 1) / RT_TOK;
+  return groups > 1 ? ((size_t)groups * route_pad(E) + 255) & ~(size_t)255 : 0;
+}
+
+template <int NE>
+static hipError_t run_route(const void* logits, int bf16, int64_t T, int E, int k, int renorm, int32_t* expert,
+                            float* weight, int32_t* offsets, int32_t* row_token, int32_t* slot, uint8_t* counts,
+                            hipStream_t stream) {
+  const int groups = (int)((T + RT_TOK - 1) / RT_TOK), pad = route_pad(E);
+  if (groups == 1) {
+    hipLaunchKernelGGL((route_choose_kernel<NE, true>), dim3(1), dim3(RT_THREADS), 0, stream, logits, bf16, T, E, k,
+                       renorm, expert, weight, offsets, row_token, slot, counts, pad);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((route_choose_kernel<NE, false>), dim3(groups), dim3(RT_THREADS), 0, stream, logits, bf16, T, E,
+                     k, renorm, expert, weight, offsets, row_token, slot, counts, pad);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(route_place_kernel, dim3(groups), dim3(RT_THREADS), 0, stream, expert, T, E, k, counts, pad,
+                     groups, offsets, row_token, slot);
+  return hipGetLastError();
+}
+
+hipError_t launch_route(const void* logits, int logits_bf16, int64_t T, int64_t E, int k, int renorm, int32_t* expert,
+                        float* weight, int32_t* offsets, int32_t* row_token, int32_t* slot, void* ws,
+                        hipStream_t stream) {
+  if (T == 0) {
+    hipLaunchKernelGGL(route_empty_kernel, dim3(1), dim3(256), 0, stream, offsets, (int)E);
+    return hipGetLastError();
+  }
+  uint8_t* counts = static_cast<uint8_t*>(ws);
+  const int n = (int)E;
+#define Q2_ROUTE(NE) \
+  return run_route<NE>(logits, logits_bf16, T, n, k, renorm, expert, weight, offsets, row_token, slot, counts, stream)
+  if (n <= 64) Q2_ROUTE(1);
+  if (n <= 128) Q2_ROUTE(2);
+  if (n <= 256) Q2_ROUTE(4);
+  if (n <= 512) Q2_ROUTE(8);
+  Q2_ROUTE(16);
+#undef Q2_ROUTE
+}
+
+// ============================================================================
+// Combination
+// ============================================================================
+// Eight columns per thread, a token's chunks over consecutive workgroups.
+constexpr int CB_COLS = 8;
+
+template <bool VEC>
+__device__ __forceinline__ void load8(const void* p, int64_t i, int bf16, int n, float (&v)[CB_COLS]) {
+  if constexpr (VEC) {
+    if (bf16) {
+      const q2_u32x4 r = *reinterpret_cast<const q2_u32x4*>(static_cast<const uint16_t*>(p) + i);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        v[2 * d] = __builtin_bit_cast(float, r[d] << 16);
+        v[2 * d + 1] = __builtin_bit_cast(float, r[d] & 0xFFFF0000u);
+      }
+    } else {
+      const q2_f32x4* q = reinterpret_cast<const q2_f32x4*>(static_cast<const float*>(p) + i);
+      const q2_f32x4 lo = q[0], hi = q[1];
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        v[d] = lo[d];
+        v[4 + d] = hi[d];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int d = 0; d < CB_COLS; ++d) v[d] = d < n ? load_elem(p, i + d, bf16) : 0.f;
+  }
+}
+
+template <bool VEC>
+__global__ __launch_bounds__(256) void combine_kernel(const void* z, int z_bf16, int64_t R, const int32_t* slot,
+                                                      const float* weight, const void* residual, int res_bf16, void* y,
+                                                      int out_bf16, int64_t T, int k, int64_t N, int64_t chunks) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t t = id / chunks;
+  if (t >= T) return;
+  const int64_t n0 = (id - t * chunks) * CB_COLS;
+  const int nc = (int)std::min<int64_t>(N - n0, CB_COLS);
+  float acc[CB_COLS] = {};
+  for (int j = 0; j < k; ++j) {
+    const int s = slot[t * k + j];
+    if (s < 0 || s >= R) continue;
+    const float w = weight[t * k + j];
+    float v[CB_COLS];
+    load8<VEC>(z, (int64_t)s * N + n0, z_bf16, nc, v);
+#pragma unroll
+    for (int d = 0; d < CB_COLS; ++d) acc[d] = __builtin_fmaf(w, v[d], acc[d]);
+  }
+  const int64_t at = t * N + n0;
+  if (residual) {
+    float v[CB_COLS];
+    load8<VEC>(residual, at, res_bf16, nc, v);
+#pragma unroll
+    for (int d = 0; d < CB_COLS; ++d) acc[d] += v[d];
+  }
+  if (VEC && out_bf16) {
+    q2_u32x4 r;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) r[d] = (uint32_t)to_bf16(acc[2 * d]) | ((uint32_t)to_bf16(acc[2 * d + 1]) << 16);
+    *reinterpret_cast<q2_u32x4*>(static_cast<uint16_t*>(y) + at) = r;
+  } else if (VEC) {
+    q2_f32x4* q = reinterpret_cast<q2_f32x4*>(static_cast<float*>(y) + at);
+    q[0] = q2_f32x4{acc[0], acc[1], acc[2], acc[3]};
+    q[1] = q2_f32x4{acc[4], acc[5], acc[6], acc[7]};
+  } else {
+    for (int d = 0; d < nc; ++d) {
+      if (out_bf16) static_cast<uint16_t*>(y)[at + d] = to_bf16(acc[d]);
+      else static_cast<float*>(y)[at + d] = acc[d];
+    }
+  }
+}
+
+hipError_t launch_combine(const void* z, int z_bf16, int64_t R, const int32_t* slot, const float* weight,
+                          const void* residual, int res_bf16, void* y, int out_bf16, int64_t T, int k, int64_t N,
+                          hipStream_t stream) {
+  const int64_t chunks = (N + CB_COLS - 1) / CB_COLS;
+  const int64_t blocks = (T * chunks + 255) / 256;
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  auto a16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+  const bool vec = N % CB_COLS == 0 && a16(z) && a16(residual) && a16(y);
+  if (vec)
+    hipLaunchKernelGGL((combine_kernel<true>), dim3((unsigned)blocks), dim3(256), 0, stream, z, z_bf16, R, slot,
+                       weight, residual, res_bf16, y, out_bf16, T, k, N, chunks);
+  else
+    hipLaunchKernelGGL((combine_kernel<false>), dim3((unsigned)blocks), dim3(256), 0, stream, z, z_bf16, R, slot,
+                       weight, residual, res_bf16, y, out_bf16, T, k, N, chunks);
+  return hipGetLastError();
+}
+
+}  // namespace q2dev

@@ -1,0 +1,417 @@
+"""GPU tests of the fused and grouped linears against the float64 oracle.
+
+Tolerance of an output: the product z is held to the linears' bar, |err z| <=
+1e-3 of the RMS of z's row; the epilogue passes that on through the activation
+(its largest slope) and the gate; the output type adds half a step of itself
+(finfo.eps / 2 relative).  The epilogue's own fp32 arithmetic is a few ulps of
+its terms, 2^-20 of them is allowed.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle.fused_oracle as F
+import oracle.q2_oracle as O
+import ternary_weight_quantized_q2_amd as q2
+from ternary_weight_quantized_q2_amd import inputs as I
+from tests.test_parity_gpu import DEV, acts, dev_bits, dev_u8, q2_weights
+
+pytestmark = pytest.mark.gpu
+
+ACTS = list(q2.ACTIVATIONS)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    assert torch.cuda.is_available(), "GPU parity tests need a GPU; they must not be skipped silently"
+    torch.cuda.set_device(0)
+    q2.load()
+    yield
+
+
+def q4_weights(cfg, n, k):
+    p, s, z = I.q4_weights(cfg, n, k)
+    return (dev_u8(p), dev_bits(s, torch.float16), dev_bits(z, torch.float16)), (p, s, z)
+
+
+def weights(fmt, cfg, n, k):
+    """(device arguments, float64 weight) of a seeded weight."""
+    if fmt == "q2":
+        p, s, p_ref, s_ref = q2_weights(cfg, n, k)
+        return (p, s), O.unpack_q2(p_ref, s_ref).astype(np.float64)
+    dev, ref = q4_weights(cfg, n, k)
+    return dev, O.unpack_q4(*ref).astype(np.float64)
+
+
+def fused(fmt):
+    return q2.q2_linear_fused if fmt == "q2" else q2.q4_linear_fused
+
+
+def grouped(fmt):
+    return q2.q2_linear_grouped if fmt == "q2" else q2.q4_linear_grouped
+
+
+def rnd(seed, *shape):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed))
+
+
+def host(t):
+    return None if t is None else t.detach().cpu().double().numpy()
+
+
+def tolerance(z, act, gated, bias, gate, residual, out_dtype):
+    """Per-element bound on |y - oracle| (see the module's comment)."""
+    v = z + (0 if bias is None else bias)
+    dz = 1e-3 * np.sqrt(np.mean(z * z, axis=1, keepdims=True)) + 2.0 ** -20 * np.abs(v)
+    slope = F.SLOPE[act]
+    if gated:
+        n = z.shape[1] // 2
+        a, u = F.activate(act, v[:, :n]), v[:, n:]
+        a_err = slope * dz[:, :n] + 2.0 ** -20 * np.abs(a)
+        err = a_err * np.abs(u) + (np.abs(a) + a_err) * dz[:, n:]
+        y = a * u
+    else:
+        y = F.activate(act, v)
+        err = slope * dz + 2.0 ** -20 * np.abs(v)
+    if gate is not None:
+        y, err = y * gate, err * np.abs(gate)
+    err = err + 2.0 ** -20 * np.abs(y)
+    if residual is not None:
+        y = y + residual
+        err = err + 2.0 ** -20 * np.abs(residual)
+    return y, err + (np.abs(y) + err) * torch.finfo(out_dtype).eps / 2
+
+
+def check(got, z, act="none", gated=False, bias=None, gate=None, residual=None, what=""):
+    ref = F.epilogue(z, act, gated, host(bias), host(gate), host(residual))
+    y, tol = tolerance(z, act, gated, host(bias), host(gate), host(residual), got.dtype)
+    assert np.allclose(y, ref, rtol=1e-12, atol=1e-12)
+    g = host(got)
+    assert np.isfinite(g).all(), what
+    bad = np.abs(g - ref) > tol
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} outside, first at {np.argwhere(bad)[0]}: " \
+                          f"{g[bad][0]} for {ref[bad][0]} +- {tol[bad][0]}"
+
+
+# rows: one token, the GEMV's limit and beyond, tile edges; columns: not a multiple of anything, tile edges
+SIZES = [(1, 64, 128), (1, 1000, 2560), (3, 37, 384), (16, 400, 1280), (17, 130, 640), (33, 1, 128), (64, 256, 512),
+         (100, 513, 1152), (130, 200, 384), (257, 770, 1024), (300, 640, 1536)]
+
+
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
+@pytest.mark.parametrize("m,n,k", SIZES)
+def test_plain_sizes(fmt, m, n, k):
+    dev, w = weights(fmt, 301, n, k)
+    xb, x = acts(301, m, k)
+    z = O.bf16_to_f64(xb) @ w.T
+    y = fused(fmt)(x, *dev)
+    assert y.dtype == torch.float32
+    check(y, z, what=f"{fmt} {m} {n} {k}")
+    yb = fused(fmt)(x, *dev, out_dtype=torch.bfloat16)
+    assert torch.equal(yb, y.to(torch.bfloat16)), "the bf16 output is not the f32 one rounded once"
+
+
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m", [2, 40, 150])
+def test_epilogue(fmt, gated, act, m):
+    n, k = 2 * 90, 640
+    n_out = n // 2 if gated else n
+    dev, w = weights(fmt, 302, n, k)
+    xb, x = acts(302, m, k)
+    z = O.bf16_to_f64(xb) @ w.T
+    bias, gate = rnd(1, n).to(DEV), rnd(2, n_out).to(DEV)
+    res = {torch.float32: rnd(3, m, n_out).to(DEV), torch.bfloat16: rnd(3, m, n_out).to(DEV).bfloat16()}
+    for out in (torch.float32, torch.bfloat16):
+        for kw in (dict(), dict(bias=bias), dict(bias=bias, gate=gate), dict(residual=res[torch.bfloat16]),
+                   dict(bias=bias, gate=gate, residual=res[torch.float32]), dict(gate=gate, residual=res[out])):
+            y = fused(fmt)(x, *dev, activation=act, gated=gated, out_dtype=out, **kw)
+            assert y.shape == (m, n_out) and y.dtype == out
+            check(y, z, act, gated, what=f"{fmt} {act} {gated} {out} {sorted(kw)}", **kw)
+
+
+@pytest.mark.parametrize("m,n,k,r", [(1, 300, 512, 4), (16, 70, 256, 33), (50, 200, 384, 32), (150, 300, 640, 64),
+                                     (260, 520, 512, 100), (20, 64, 128, 1)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_rank_r_branch(m, n, k, r, gated):
+    (p, s), w = weights("q2", 303, n, k)
+    xb, x = acts(303, m, k)
+    a, b = I.lowrank_factors(303, r, k, n, std=0.05)
+    A, B = dev_bits(a, torch.float16), dev_bits(b, torch.float16)
+    xd = O.bf16_to_f64(xb)
+    z = xd @ w.T + (xd @ O.f16_to_f64(a).T) @ O.f16_to_f64(b).T
+    bias = rnd(4, n).to(DEV)
+    for out in (torch.float32, torch.bfloat16):
+        y = q2.q2_linear_fused(x, p, s, A, B, bias=bias, activation="silu", gated=gated, out_dtype=out)
+        check(y, z, "silu", gated, bias=bias, what=f"r={r}")
+
+
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("m", [1, 13, 70, 200])
+def test_residual_in_place(fmt, out, m):
+    n, k = 136, 512
+    dev, w = weights(fmt, 304, n, k)
+    xb, x = acts(304, m, k)
+    r0 = rnd(5, m, n).to(DEV).to(out)
+    y = r0.clone()
+    got = fused(fmt)(x, *dev, activation="relu", residual=y, y=y)
+    assert got is y
+    assert torch.equal(y, fused(fmt)(x, *dev, activation="relu", residual=r0, out_dtype=out))
+    check(y, O.bf16_to_f64(xb) @ w.T, "relu", residual=r0)
+
+
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
+@pytest.mark.parametrize("m", [1, 7, 40, 200])
+def test_unaligned_outputs_and_neighbours(fmt, m):
+    """y and the residual one element past any larger boundary; nothing beside y is written."""
+    n, k = 75, 256
+    dev, w = weights(fmt, 305, n, k)
+    xb, x = acts(305, m, k)
+    z = O.bf16_to_f64(xb) @ w.T
+    for out in (torch.float32, torch.bfloat16):
+        flat = torch.full((m * n + 40,), 7.0, device=DEV, dtype=out)
+        rflat = rnd(6, m * n + 1).to(DEV).to(out)
+        y, res = flat[1:1 + m * n].view(m, n), rflat[1:].view(m, n)
+        fused(fmt)(x, *dev, residual=res, y=y)
+        check(y, z, residual=res)
+        assert (flat[:1] == 7).all() and (flat[1 + m * n:] == 7).all()
+
+
+@pytest.mark.parametrize("m", [1, 20, 200])
+def test_empty_sum_and_empty_sizes(m):
+    n = 48
+    x = torch.empty((m, 0), dtype=torch.bfloat16, device=DEV)
+    p, s = torch.empty((n, 0), dtype=torch.uint8, device=DEV), torch.empty((n, 0), dtype=torch.float16, device=DEV)
+    bias = rnd(7, n).to(DEV)
+    y = q2.q2_linear_fused(x, p, s, bias=bias, activation="relu")
+    assert torch.equal(y, bias.clamp(min=0).expand(m, n))
+    y = q2.q4_linear_fused(x, p, s, s, bias=bias)
+    assert torch.equal(y, bias.expand(m, n))
+    (pw, sw), _ = weights("q2", 306, 8, 128)
+    assert q2.q2_linear_fused(torch.empty((0, 128), dtype=torch.bfloat16, device=DEV), pw, sw).shape == (0, 8)
+    assert q2.q2_linear_fused(torch.empty((m, 128), dtype=torch.bfloat16, device=DEV), pw[:0], sw[:0]).shape == (m, 0)
+
+
+@pytest.mark.parametrize("m", [1, 16, 17, 150, 600])
+def test_zero_weights_add_exactly_nothing(m):
+    n, k = 130, 1280
+    xb, x = acts(307, m, k)
+    codes, scales = np.ones((n, k), np.uint8), I.q2_scales(307, n, k)
+    p, s = q2.q2_pack(dev_u8(codes), torch.from_numpy(scales).to(DEV))
+    assert (q2.q2_linear_fused(x, p, s) == 0).all()
+    p4 = torch.full((n, k // 2), 0x55, dtype=torch.uint8, device=DEV)
+    s4 = torch.from_numpy(scales).half().to(DEV)
+    assert (q2.q4_linear_fused(x, p4, s4, torch.full_like(s4, 5.0)) == 0).all()
+
+
+@pytest.mark.parametrize("regime", I.ACT_REGIMES)
+@pytest.mark.parametrize("m", [3, 80, 300])
+def test_activation_regimes(regime, m):
+    n, k = 100, 512
+    (p, s), w = weights("q2", 308, n, k)
+    xb = I.activations_regime_bf16(308, m, k, regime)
+    check(q2.q2_linear_fused(dev_bits(xb, torch.bfloat16), p, s), O.bf16_to_f64(xb) @ w.T, what=regime)
+
+
+@pytest.mark.parametrize("m", [3, 80, 300])
+def test_extreme_scales_and_wide_rows(m):
+    """Scales from subnormal to near the f16 maximum, and rows whose elements span the bf16 range around 1."""
+    n, k = 96, 640
+    codes = I.q2_codes(309, n, k)
+    rng = np.random.default_rng(309)
+    scales = np.ldexp(1.0 + rng.integers(0, 1024, (n, k // 128)) / 1024.0, rng.integers(-14, 15, (n, 1)))
+    scales[::7] = rng.integers(1, 1024, scales[::7].shape) * 2.0 ** -24            # subnormal rows
+    scales = scales.astype(np.float16).astype(np.float32)
+    p, s = q2.q2_pack(dev_u8(codes), torch.from_numpy(scales).to(DEV))
+    w = O.unpack_q2(*O.pack_q2(codes, scales)).astype(np.float64)
+    xf = rng.standard_normal((m, k)) * np.ldexp(1.0, rng.integers(-30, 1, (m, k)))
+    xb = I.f32_to_bf16_bits(xf.astype(np.float32))
+    z = O.bf16_to_f64(xb) @ w.T
+    got = host(q2.q2_linear_fused(dev_bits(xb, torch.bfloat16), p, s))
+    # columns have scales of their own: each is held to the bar of its own terms
+    bar = 1e-3 * np.sqrt((O.bf16_to_f64(xb) ** 2) @ (w ** 2).T)
+    assert (np.abs(got - z) <= bar).all()
+
+
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
+def test_offsets_beyond_32_bits(fmt):
+    """More than 2^32 output elements' bytes: row and element indices beyond 31 bits."""
+    m, n, k = 70001, 32770, 128
+    dev, w = weights(fmt, 310, n, k)
+    xb, x = acts(310, m, k)
+    y = fused(fmt)(x, *dev, out_dtype=torch.bfloat16)
+    assert m * n > 2 ** 31
+    rows = np.array([0, 1, 31999, 65535, 65537, m - 2, m - 1])
+    z = O.bf16_to_f64(xb[rows]) @ w.T
+    check(y[torch.from_numpy(rows).to(DEV)], z)
+
+
+# ---------------------------------------------------------------------------
+# grouped
+# ---------------------------------------------------------------------------
+
+def group_case(fmt, counts, n, k, x_rows=None, seed=320, lead=0, tail=0):
+    """Device weights, float64 weights, offsets, x (bits and tensor) and a row index of ragged groups."""
+    e = len(counts)
+    dev, w = weights(fmt, seed, e * n, k)
+    dev = tuple(t.view(e, n, -1) for t in dev)
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32) + lead
+    rows = int(offsets[-1]) + tail
+    index = None
+    if x_rows is not None:
+        index = np.random.default_rng(seed).integers(0, x_rows, rows).astype(np.int32)
+    xb, x = acts(seed, rows if x_rows is None else x_rows, k)
+    return dev, w.reshape(e, n, k), offsets, xb, x, index
+
+
+COUNTS = [[5], [0, 3, 0, 0, 1], [17, 0, 40, 1, 33], [1] * 8, [0] * 3 + [130], [300, 2, 0, 64, 129],
+          [2, 0, 1] * 25, [0, 0]]
+
+
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
+@pytest.mark.parametrize("counts", COUNTS, ids=lambda c: f"{len(c)}x{sum(c)}")
+@pytest.mark.parametrize("gather", [False, True])
+def test_grouped(fmt, counts, gather):
+    n, k = 2 * 45, 384
+    lead, tail = (0, 0) if gather else (3, 5)
+    dev, w, offsets, xb, x, index = group_case(fmt, counts, n, k, x_rows=37 if gather else None, lead=lead, tail=tail)
+    z = F.grouped_products(O.bf16_to_f64(xb), w, offsets, index)
+    rows, inside = len(z), slice(int(offsets[0]), int(offsets[-1]))
+    expert = np.repeat(np.arange(len(counts)), counts)
+    off = torch.from_numpy(offsets).to(DEV)
+    idx = None if index is None else torch.from_numpy(index).to(DEV)
+    bias = rnd(8, len(counts), n).to(DEV)
+    for act, gated, out, b in (("none", False, torch.float32, None), ("silu", True, torch.bfloat16, bias),
+                               ("gelu", False, torch.float32, bias), ("relu", True, torch.float32, None)):
+        y = torch.full((rows, n // 2 if gated else n), 7.0, device=DEV, dtype=out)
+        grouped(fmt)(x, off, *dev, row_index=idx, bias=b, activation=act, gated=gated, y=y)
+        rb = None if b is None else b[torch.from_numpy(expert).to(DEV)]
+        if sum(counts):
+            check(y[inside], z[inside], act, gated, bias=rb, what=f"{fmt} {counts} {act}")
+        assert (y[:offsets[0]] == 7).all() and (y[offsets[-1]:] == 7).all(), "a row of no expert was written"
+
+
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
+@pytest.mark.parametrize("rows_per", [2, 60])
+def test_grouped_rows_equal_the_experts_own_linears(fmt, rows_per):
+    """Every expert's rows against the fused linear on its own weight (other launch shapes, so within the bar)."""
+    counts = [rows_per, 0, 2 * rows_per, 1]
+    n, k = 200, 512
+    dev, w, offsets, xb, x, _ = group_case(fmt, counts, n, k)
+    y = grouped(fmt)(x, torch.from_numpy(offsets).to(DEV), *dev, activation="gelu_tanh")
+    for e in range(len(counts)):
+        lo, hi = offsets[e], offsets[e + 1]
+        if hi > lo:
+            z = O.bf16_to_f64(xb[lo:hi]) @ w[e].T
+            check(y[lo:hi], z, "gelu_tanh")
+            check(fused(fmt)(x[lo:hi], *(t[e] for t in dev), activation="gelu_tanh"), z, "gelu_tanh")
+
+
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
+@pytest.mark.parametrize("rows", [4, 200])
+def test_grouped_index_outside_x_reads_zeros(fmt, rows):
+    n, k = 64, 256
+    counts = [rows, rows]
+    dev, w, offsets, xb, x, index = group_case(fmt, counts, n, k, x_rows=9)
+    index[::3] = np.array([-1, 9, 2 ** 31 - 1, -2 ** 31] * rows, np.int32)[:len(index[::3])]
+    z = F.grouped_products(O.bf16_to_f64(xb), w, offsets, index)
+    assert (z[::3] == 0).all()
+    y = grouped(fmt)(x, torch.from_numpy(offsets).to(DEV), *dev, row_index=torch.from_numpy(index).to(DEV))
+    check(y, z)
+    assert (y[::3] == 0).all()
+
+
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
+@pytest.mark.parametrize("bad", [[5, 40, 20, 64], [-7, 20, 90, 64], [0, 2 ** 31 - 1, -2 ** 31, 50], [64, 0, 64, 0]])
+def test_grouped_bad_offsets_stay_inside(fmt, bad):
+    """Offsets that decrease or leave [0, R]: only rows of y are written, the rest of its storage is not."""
+    rows, n, k = 64, 40, 128
+    dev, _, _, _, x, _ = group_case(fmt, [rows, 0, 0], n, k)
+    flat = torch.full((3 * rows * n,), 7.0, device=DEV)
+    y = flat[rows * n:2 * rows * n].view(rows, n)
+    grouped(fmt)(x, torch.tensor(bad, dtype=torch.int32, device=DEV), *dev, y=y)
+    torch.cuda.synchronize()
+    assert (flat[:rows * n] == 7).all() and (flat[2 * rows * n:] == 7).all()
+
+
+# ---------------------------------------------------------------------------
+# streams, graphs, repeatability
+# ---------------------------------------------------------------------------
+
+def stream_cases():
+    """(name, call(x) -> tensor, x) over the variants: few rows, many rows, branch, grouped."""
+    out = []
+    (p, s), _ = weights("q2", 330, 256, 512)
+    dev4, _ = weights("q4", 330, 256, 512)
+    a, b = I.lowrank_factors(330, 8, 512, 256)
+    A, B = dev_bits(a, torch.float16), dev_bits(b, torch.float16)
+    for m in (2, 40, 300):
+        _, x = acts(331, m, 512)
+        out.append((f"q2 {m}", lambda x: q2.q2_linear_fused(x, p, s, A, B, activation="silu", gated=True), x))
+        out.append((f"q4 {m}", lambda x: q2.q4_linear_fused(x, *dev4, activation="gelu"), x))
+    for counts in ([1, 0, 2, 1], [100, 0, 37, 163]):
+        dev, _, offsets, _, x, _ = group_case("q2", counts, 64, 512, seed=332)
+        off = torch.from_numpy(offsets).to(DEV)
+        out.append((f"grouped {sum(counts)}", lambda x, off=off, dev=dev: q2.q2_linear_grouped(x, off, *dev), x))
+    return out
+
+
+def test_repeatable_on_a_busy_side_stream():
+    for name, call, x in stream_cases():
+        want = call(x)
+        side = torch.cuda.Stream()
+        late = torch.zeros_like(x)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            big = torch.randn(4096, 4096, device=DEV)
+            for _ in range(4):
+                big = big @ big.clamp(-1e-3, 1e-3)
+            late.copy_(x)                                   # written late on this stream
+            got = call(late)
+        side.synchronize()
+        assert torch.equal(got, want), name
+
+
+def test_graph_replays_equal_eager_calls():
+    for name, call, x in stream_cases():
+        static = x.clone()
+        call(static)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side):
+            call(static)
+            side.synchronize()
+            with torch.cuda.graph(graph, stream=side):
+                y = call(static)
+        for i in range(3):
+            new = torch.roll(x, i + 1, dims=1).contiguous()
+            want = call(new)                                # eager work between the replays
+            static.copy_(new)
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want), f"{name}: replay {i}"
+
+
+def test_refusals():
+    (p, s), _ = weights("q2", 340, 7, 128)
+    _, x = acts(340, 3, 128)
+    with pytest.raises(ValueError, match="activation"):
+        q2.q2_linear_fused(x, p, s, activation="swish")
+    with pytest.raises(ValueError, match="halves"):
+        q2.q2_linear_fused(x, p, s, gated=True)
+    with pytest.raises(ValueError, match="float32 or bfloat16"):
+        q2.q2_linear_fused(x, p, s, out_dtype=torch.float16)
+    with pytest.raises(ValueError, match="residual"):
+        q2.q2_linear_fused(x, p, s, residual=torch.zeros(3, 8, device=DEV))
+    with pytest.raises(ValueError, match="bias"):
+        q2.q2_linear_fused(x, p, s, bias=torch.zeros(7, device=DEV).double())
+    with pytest.raises(ValueError, match="come together"):
+        q2.q2_linear_fused(x, p, s, A=torch.zeros((4, 128), device=DEV).half())
+    with pytest.raises(ValueError, match="offsets"):
+        q2.q2_linear_grouped(x, torch.zeros(3, device=DEV, dtype=torch.int32), p[None], s[None])
+    with pytest.raises(ValueError, match="device tensor"):
+        q2.q2_linear_fused(x.cpu(), p, s)
