@@ -3,6 +3,7 @@
 #pragma once
 #include "q2.h"
 #include "q2_device.h"
+#include <algorithm>
 
 namespace q2dev {
 
@@ -67,6 +68,75 @@ __device__ __forceinline__ void store_out(const FusedArgs& a, const float* bias,
   else static_cast<float*>(a.y)[i] = v;
 }
 
+// ROWS x (64 or 32 output columns) of finished products in LDS (row stride
+// `stride` floats; with a gated epilogue the second factor of column n at
+// `half` + n) to y, by the 64 lanes of one wave: 16-byte pieces of 8 or 4
+// columns where y, the residual and the column count allow it.
+__device__ __forceinline__ bool vec_rows(const FusedArgs& a, int64_t n_out) {
+  // a grouped bias starts E * N floats in: with n_out % 8 == 0 every expert's is aligned with the first
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.residual) |
+                      reinterpret_cast<uintptr_t>(a.bias) | reinterpret_cast<uintptr_t>(a.gate);
+  return n_out % 8 == 0 && (p & 15) == 0;
+}
+
+__device__ __forceinline__ void add4(float (&v)[4], const float* p) {
+  const q2_f32x4 t = *reinterpret_cast<const q2_f32x4*>(p);
+#pragma unroll
+  for (int d = 0; d < 4; ++d) v[d] += t[d];
+}
+
+__device__ __forceinline__ void store_strip(const FusedArgs& a, const float* bias, int64_t n_out, const float* strip,
+                                            int stride, int half, int cols, int64_t m0, int rows, int64_t n0,
+                                            int lane) {
+  if (vec_rows(a, n_out)) {
+    const int per = cols / 4;                            // pieces of four columns per row
+    for (int idx = lane; idx < rows * per; idx += 64) {
+      const int row = idx / per, col = (idx - row * per) * 4;
+      const int64_t n = n0 + col;
+      if (n >= n_out) continue;
+      const float* s = strip + row * stride + col;
+      float v[4] = {s[0], s[1], s[2], s[3]};
+      if (bias) add4(v, bias + n);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) v[d] = activate(a.act, v[d]);
+      if (a.gated) {
+        float u[4] = {s[half], s[half + 1], s[half + 2], s[half + 3]};
+        if (bias) add4(u, bias + n_out + n);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) v[d] *= u[d];
+      }
+      if (a.gate) {
+        const q2_f32x4 t = *reinterpret_cast<const q2_f32x4*>(a.gate + n);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) v[d] *= t[d];
+      }
+      const int64_t i = (m0 + row) * n_out + n;
+      if (a.residual && a.res_bf16) {
+        const q2_u32x2 t = *reinterpret_cast<const q2_u32x2*>(static_cast<const uint16_t*>(a.residual) + i);
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          v[d] += __builtin_bit_cast(float, (d & 1) ? t[d >> 1] & 0xFFFF0000u : t[d >> 1] << 16);
+      } else if (a.residual) {
+        add4(v, static_cast<const float*>(a.residual) + i);
+      }
+      if (a.out_bf16) {
+        *reinterpret_cast<q2_u32x2*>(static_cast<uint16_t*>(a.y) + i) =
+            q2_u32x2{(uint32_t)to_bf16(v[0]) | ((uint32_t)to_bf16(v[1]) << 16),
+                     (uint32_t)to_bf16(v[2]) | ((uint32_t)to_bf16(v[3]) << 16)};
+      } else {
+        *reinterpret_cast<q2_f32x4*>(static_cast<float*>(a.y) + i) = q2_f32x4{v[0], v[1], v[2], v[3]};
+      }
+    }
+  } else {
+    for (int idx = lane; idx < rows * cols; idx += 64) {
+      const int row = idx / cols, col = idx - row * cols;
+      if (n0 + col >= n_out) continue;
+      const float* s = strip + row * stride + col;
+      store_out(a, bias, n_out, m0 + row, n0 + col, s[0], a.gated ? s[half] : 0.f);
+    }
+  }
+}
+
 // ---- row groups ----------------------------------------------------------------
 // The group (expert) and rows of row tile `slot`, counting the tiles of `bm`
 // rows of all groups in order.  Every wave of the workgroup calls it together
@@ -123,6 +193,45 @@ __device__ __forceinline__ RowTile find_row_tile(const FusedArgs& a, int64_t slo
   return t;
 }
 
+// Row tiles of bm rows over all groups; every wave calls it together.
+__device__ __forceinline__ int64_t count_row_tiles(const FusedArgs& a, int bm) {
+  if (a.offsets == nullptr) return (a.M + bm - 1) / bm;
+  const int lane = threadIdx.x & 63;
+  int mine = 0;                                          // at most R + E tiles: fits 32 bits
+  for (int64_t e = lane; e < a.E; e += 64) {
+    const int64_t lo = clamp_offset(a.offsets[e], 0, a.M), hi = clamp_offset(a.offsets[e + 1], lo, a.M);
+    mine += (int)((hi - lo + bm - 1) / bm);
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) mine += __shfl_xor(mine, d);
+  return __builtin_amdgcn_readfirstlane(mine);
+}
+
+// Tile of this workgroup: row tile `slot`, column tile tn; false when there is
+// none for it (the launch covers the most tiles that the offsets can make).
+// Each XCD gets a contiguous range of tile numbers.  Without groups they run
+// over blocks of group_m row tiles, row-fastest inside (see tile_group_rows);
+// with groups over the column tiles of a row tile, so an XCD meets few experts
+// and reads their weights once.
+__device__ __forceinline__ bool tile_of_block(const FusedArgs& a, int bm, int tiles_n, int group_m, int64_t& slot,
+                                              int& tn) {
+  const int tiles_m = (int)count_row_tiles(a, bm);
+  // bad offsets can count more tiles than the launch covers
+  const int tiles = (int)min((int64_t)tiles_m * tiles_n, (int64_t)gridDim.x);
+  if ((int)blockIdx.x >= tiles) return false;
+  const int tile = xcd_tile((int)blockIdx.x, tiles);
+  if (a.offsets) {
+    slot = tile / tiles_n;
+    tn = tile - (int)slot * tiles_n;
+  } else {
+    const int grp = tile / (group_m * tiles_n), gi = tile - grp * group_m * tiles_n;
+    const int gm = min(group_m, tiles_m - grp * group_m);
+    slot = grp * group_m + gi % gm;
+    tn = gi / gm;
+  }
+  return true;
+}
+
 // At most this many row tiles of bm rows over all groups: each of the at most
 // min(E, M) groups with rows adds less than one tile to M / bm.
 inline int64_t max_row_tiles(const FusedArgs& a, int bm) {
@@ -131,11 +240,31 @@ inline int64_t max_row_tiles(const FusedArgs& a, int bm) {
   return (a.M + groups * (bm - 1)) / bm;
 }
 
+// Row tiles per block of the tile order.  Cutting the tile grid into p row parts
+// times 8 / p column parts, one block per XCD, makes the XCDs together read the
+// weights p times and x 8 / p times; once an XCD runs its block in several
+// rounds (`resident` tiles at a time) its rows of x are read again in each,
+// unless they stay in its 4 MB L2.  p is the power of two with the least sum.
+inline int tile_group_rows(int64_t tiles_m, int64_t tiles_n, double xtile, double wtile, int resident) {
+  const double rounds = std::max(1.0, (double)tiles_m * (double)tiles_n / 8.0 / resident);
+  auto cost = [&](int p) {
+    const double xpart = (double)((tiles_m + p - 1) / p) * xtile;
+    return 8.0 * xpart * (xpart <= 2.5e6 ? 1.0 : rounds) + p * wtile * (double)tiles_n;
+  };
+  int best = 1;
+  for (int p = 2; p <= 8 && p <= tiles_m; p *= 2)
+    if (cost(p) < cost(best)) best = p;
+  return (int)((tiles_m + best - 1) / best);
+}
+
 // ---- host side -------------------------------------------------------------------
 // Workspace beside the limbs of a rank-r branch; 0 where none is needed.
 size_t fused_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t E, int fmt);
 // fmt 0 = Q2_0, 1 = 4-bit.  ws: that many bytes.
 hipError_t launch_fused(const FusedArgs& a, int fmt, void* ws, hipStream_t stream);
+
+size_t f16_workspace_bytes(int64_t M, int64_t K);
+hipError_t launch_fused_f16(const FusedArgs& a, void* ws, hipStream_t stream);
 
 hipError_t launch_route(const void* logits, int logits_bf16, int64_t T, int64_t E, int k, int renorm, int32_t* expert,
                         float* weight, int32_t* offsets, int32_t* row_token, int32_t* slot, void* ws,

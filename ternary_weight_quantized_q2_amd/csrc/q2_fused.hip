@@ -124,9 +124,17 @@ __global__ __launch_bounds__(256) void fused_tile_kernel(FusedArgs a, int tiles_
   }
 }
 
-size_t fused_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int) { return 0; }
+// The f16 kernel for Q2_0 weights over many rows.
+static bool use_f16(int64_t M, int64_t N, int64_t K, int64_t E, int fmt) {
+  return fmt == 0 && M >= 128 * std::max<int64_t>(E, 1) / 2 && K >= 128 && K <= (1 << 22);
+}
 
-hipError_t launch_fused(const FusedArgs& a, int fmt, void*, hipStream_t stream) {
+size_t fused_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t E, int fmt) {
+  return use_f16(M, N, K, E, fmt) ? f16_workspace_bytes(M, K) : 0;
+}
+
+hipError_t launch_fused(const FusedArgs& a, int fmt, void* ws, hipStream_t stream) {
+  if (use_f16(a.M, a.N, a.K, a.offsets ? a.E : 0, fmt)) return launch_fused_f16(a, ws, stream);
   const int64_t cols = a.gated ? F_BN / 2 : F_BN;
   const int64_t tiles_n = (fused_n_out(a) + cols - 1) / cols;
   const int64_t slots = max_row_tiles(a, F_BM);

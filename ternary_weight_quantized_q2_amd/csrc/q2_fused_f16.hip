@@ -1,0 +1,312 @@
+// q2_fused_f16.hip - the fused and grouped Q2_0 linears for many rows.
+//
+// A Q2_0 weight is -d, 0 or d with an f16 scale d, so it is an f16 value as it
+// stands; what keeps the product off the f16 matrix cores is the range of the
+// bf16 activations.  Here each row of x is first multiplied by a power of two
+// that puts its largest element into [2^14, 2^15) and converted to f16.  A bf16
+// value has 8 significant bits, so every element down to 2^-31 of its row's
+// largest is exact; below that it becomes an f16 subnormal, off by at most
+// 2^-25, that is 2^-39 of the row's largest element -- far less than fp32 sums
+// over the row keep.  Then the sum over all of K runs in the matrix cores' fp32
+// accumulators with exact products, without a block's start value, row sums or
+// a rescale per block; the power of two is taken back by an exact ldexp.
+#include "q2_fused.h"
+#include "q2_internal.h"
+#include <algorithm>
+
+namespace q2dev {
+
+typedef _Float16 q2_f16x8 __attribute__((ext_vector_type(8)));
+typedef float q2_f32x16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ q2_f32x16 mfma32(q2_u32x4 a, q2_u32x4 b, q2_f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(q2_f16x8, a), __builtin_bit_cast(q2_f16x8, b), c, 0,
+                                                0, 0);
+}
+__device__ __forceinline__ q2_f32x16 mfma32_bf16(q2_u32x4 a, q2_u32x4 b, q2_f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(q2_bf16x8, a), __builtin_bit_cast(q2_bf16x8, b), c,
+                                                 0, 0, 0);
+}
+
+// ============================================================================
+// x as f16: row i of the output is row src(i) of x times 2^-rexp[i]
+// ============================================================================
+// Each group of 16 elements is stored as a transposed 4 x 4 matrix (position
+// 4 j + b holds element 4 b + j), the order in which a dword of sixteen codes
+// decodes.  One wave per row; the row is read twice, the second time from the
+// caches.
+constexpr int CV_ROWS = 4;
+
+__global__ __launch_bounds__(64 * CV_ROWS) void x_to_f16_kernel(const uint16_t* x, const int32_t* row_index,
+                                                                int64_t x_rows, uint16_t* out, int32_t* rexp, int64_t M,
+                                                                int64_t K) {
+  const int lane = threadIdx.x & 63;
+  const int64_t m = (int64_t)blockIdx.x * CV_ROWS + (threadIdx.x >> 6);
+  if (m >= M) return;
+  const int64_t src = row_index ? (int64_t)row_index[m] : m;
+  const int64_t chunks = K / 16;
+  uint16_t* const dst = out + m * K;
+  if (src < 0 || src >= x_rows) {                        // an index outside x: a row of zeros
+    for (int64_t q = lane; q < 2 * chunks; q += 64)
+      reinterpret_cast<q2_u32x4*>(dst)[q] = q2_u32x4{0u, 0u, 0u, 0u};
+    if (lane == 0) rexp[m] = 0;
+    return;
+  }
+  const q2_u32x4* const xr = reinterpret_cast<const q2_u32x4*>(x + src * K);
+  uint32_t top = 0;                                      // largest finite |x|, as bf16 bits
+  for (int64_t q = lane; q < 2 * chunks; q += 64) {
+    const q2_u32x4 v = xr[q];
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const uint32_t lo = v[d] & 0x7FFFu, hi = (v[d] >> 16) & 0x7FFFu;
+      top = max(top, lo < 0x7F80u ? lo : 0u);
+      top = max(top, hi < 0x7F80u ? hi : 0u);
+    }
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+  // floor(log2 |x|) from the bits; a subnormal bf16 is bits * 2^-133
+  const int e = top >= 0x80u ? (int)(top >> 7) - 127 : top ? 31 - __builtin_clz(top) - 133 : 14;
+  const int shift = 14 - e;
+  if (lane == 0) rexp[m] = -shift;
+  for (int64_t q = lane; q < chunks; q += 64) {
+    const q2_u32x4 v0 = xr[2 * q], v1 = xr[2 * q + 1];
+    uint32_t h[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t dw = i < 8 ? v0[i >> 1] : v1[(i - 8) >> 1];
+      const float f = __builtin_bit_cast(float, (i & 1) ? dw & 0xFFFF0000u : dw << 16);
+      h[i] = __builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_ldexpf(f, shift));
+    }
+    q2_u32x4 o[2];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {                        // positions 2 p, 2 p + 1: j = p / 2, b = 2 (p % 2), b + 1
+      const int j = p >> 1, b = 2 * (p & 1);
+      o[p >> 2][p & 3] = h[4 * b + j] | (h[4 * b + 4 + j] << 16);
+    }
+    reinterpret_cast<q2_u32x4*>(dst)[2 * q] = o[0];
+    reinterpret_cast<q2_u32x4*>(dst)[2 * q + 1] = o[1];
+  }
+}
+
+// ============================================================================
+// The product
+// ============================================================================
+// Decode: with c at the low two bits of a byte, a byte permute looks up the low
+// and the high byte of c's weight in two four-entry tables, four codes at a
+// time, and two more permutes join them to f16 pairs: 3 VALU operations per pair.
+struct WTable {
+  uint32_t lo, hi;
+};
+__device__ __forceinline__ WTable weight_table(uint16_t dbits) {
+  const _Float16 d = __builtin_bit_cast(_Float16, dbits);
+  const uint32_t v = dbits, v2 = __builtin_bit_cast(uint16_t, (_Float16)(d + d));
+  const uint32_t pair = v | (v2 << 16);                  // bytes lo, hi, lo2, hi2
+  WTable t;
+  t.lo = __builtin_amdgcn_perm(pair, pair, 0x02000C00u);                       // lo, 0, lo, lo2
+  t.hi = __builtin_amdgcn_perm(pair, pair, 0x03010C01u) ^ 0x00000080u;         // -hi, 0, hi, hi2
+  return t;
+}
+// K step t (0..7) of a block from the lane's four code dwords.
+template <int T>
+__device__ __forceinline__ q2_u32x4 decode_step(const q2_u32x4& w, const WTable& tab) {
+  constexpr int I = T >> 1, J = 2 * (T & 1);
+  q2_u32x4 r;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const uint32_t sel = (w[I] >> (2 * (J + u))) & 0x03030303u;
+    const uint32_t lo = __builtin_amdgcn_perm(0u, tab.lo, sel), hi = __builtin_amdgcn_perm(0u, tab.hi, sel);
+    r[2 * u] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
+    r[2 * u + 1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
+  }
+  return r;
+}
+
+constexpr int FX_BM = 128, FX_BN = 256;                  // rows, weight columns of a workgroup
+constexpr int FX_STAGE = FX_BM * 256;                    // bytes of one 128-wide block of the rows
+constexpr int FX_STRIP = 64 + 4;                         // floats per row of a wave's output strip
+
+__global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const uint16_t* x16, const int32_t* rexp,
+                                                           int tiles_n, int group_m) {
+  __shared__ __align__(16) uint8_t smem[2 * FX_STAGE];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 31, h = lane >> 5;
+
+  int64_t slot;
+  int tn;
+  if (!tile_of_block(a, FX_BM, tiles_n, group_m, slot, tn)) return;
+  const RowTile rt = find_row_tile(a, slot, FX_BM);
+  const int64_t m0 = rt.m0, n_out = fused_n_out(a), K = a.K;
+  const int KB = (int)(K / BLOCK_K);
+  // Columns of the wave's two 32-column tiles: neighbours, or with a gated
+  // epilogue both factors of the same outputs.
+  const int64_t n0 = (int64_t)tn * (a.gated ? FX_BN / 2 : FX_BN) + wv * (a.gated ? 32 : 64);
+  const uint8_t* wp[2];
+  const uint16_t* sp[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    int64_t n = n0 + c + (a.gated ? 0 : 32 * j);
+    n = n < n_out ? n : n_out - 1;
+    if (a.gated && j) n += n_out;
+    const int64_t row = rt.expert * a.N + n;
+    wp[j] = a.w + row * (K / 4) + 16 * h;
+    sp[j] = a.s + row * KB;
+  }
+
+  // Copies of a block's rows: copy kk of wave wv fills tile rows
+  // 16 kk + 4 wv .. + 3; lane l row 4 wv + l / 16 of them and 16-byte position
+  // l % 16, which holds chunk (l % 16) ^ (row % 16).  A wave's 16-byte reads of
+  // 32 rows then hit every bank equally.  Rows past the last one are padding of
+  // the workspace, never stored.
+  const int crow = 4 * wv + (lane >> 4);
+  const uint32_t xoff = (uint32_t)(crow * K * 2) + (uint32_t)(((lane & 15) ^ crow) << 4);
+  const __amdgpu_buffer_rsrc_t rx = buf_rsrc(x16 + m0 * K, (uint32_t)(FX_BM * K * 2));
+  auto copy_block = [&](int blk, int stage) {
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(smem + stage * FX_STAGE + (16 * kk + 4 * wv) * 256), 16,
+                                               xoff, (uint32_t)(16 * kk) * (uint32_t)(K * 2) + (uint32_t)blk * 256u, 0,
+                                               0);
+  };
+  int aoff[8];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) aoff[t] = c * 256 + (((8 * h + t) ^ (c & 15)) << 4);
+
+  q2_f32x16 acc[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+
+  q2_u32x4 wnext[2];
+  uint32_t snext[2];
+  auto load_weights = [&](int blk) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      wnext[j] = *reinterpret_cast<const q2_u32x4*>(wp[j] + (int64_t)blk * 32);
+      snext[j] = sp[j][blk];
+    }
+  };
+  if (KB > 0) {
+    copy_block(0, 0);
+    load_weights(0);
+  }
+  for (int blk = 0; blk < KB; ++blk) {
+    const int stage = blk & 1;
+    stage_barrier<0>();                                  // this block's rows and codes have landed
+    const q2_u32x4 w[2] = {wnext[0], wnext[1]};
+    const WTable tab[2] = {weight_table((uint16_t)snext[0]), weight_table((uint16_t)snext[1])};
+    const int nblk = blk + 1 < KB ? blk + 1 : blk;       // past the end: the last block again, never read
+    copy_block(nblk, stage ^ 1);
+    load_weights(nblk);
+    const uint8_t* st = smem + stage * FX_STAGE;
+#define Q2_STEP(T)                                                                                     \
+  {                                                                                                    \
+    const q2_u32x4 b0 = decode_step<T>(w[0], tab[0]), b1 = decode_step<T>(w[1], tab[1]);               \
+    _Pragma("unroll") for (int i = 0; i < 4; ++i) {                                                    \
+      const q2_u32x4 av = *reinterpret_cast<const q2_u32x4*>(st + i * 8192 + aoff[T]);                 \
+      acc[i][0] = mfma32(av, b0, acc[i][0]);                                                           \
+      acc[i][1] = mfma32(av, b1, acc[i][1]);                                                           \
+    }                                                                                                  \
+  }
+    Q2_STEP(0) Q2_STEP(1) Q2_STEP(2) Q2_STEP(3) Q2_STEP(4) Q2_STEP(5) Q2_STEP(6) Q2_STEP(7)
+#undef Q2_STEP
+  }
+  __builtin_amdgcn_s_waitcnt(0);                         // no copy may still write this workgroup's LDS
+  __syncthreads();
+
+  // The rows' powers of two: element 4 q + e of a tile is row 8 q + 4 h + e.
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t m = m0 + 32 * i + 8 * q + 4 * h;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int s = rexp[m + e];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j][4 * q + e] = __builtin_amdgcn_ldexpf(acc[i][j][4 * q + e], s);
+      }
+    }
+
+  if (a.r > 0) {
+    // (x A^T) B^T as T_hi B_hi + T_hi B_lo + T_lo B_hi in bf16.
+    const int r8 = (a.r + 7) & ~7;
+    for (int part = 0; part < 3; ++part)
+      for (int k0 = 0; k0 < r8; k0 += 16) {
+        const int q0 = k0 + 8 * h;
+        q2_u32x4 bq[2], aq[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          int64_t n = n0 + c + (a.gated ? 0 : 32 * j);
+          n = n < n_out ? n : n_out - 1;
+          if (a.gated && j) n += n_out;
+          uint32_t e[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            uint16_t hi = 0, lo = 0;
+            if (q0 + k < a.r) f16_split_bf16(a.lr_b[n * a.r + q0 + k], hi, lo);
+            e[k] = part == 1 ? lo : hi;
+          }
+          bq[j] = q2_u32x4{e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16), e[6] | (e[7] << 16)};
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          int64_t m = m0 + 32 * i + c;
+          m = m < a.M ? m : a.M - 1;
+          aq[i] = q0 < r8 ? *reinterpret_cast<const q2_u32x4*>(a.lr_t + m * 2 * r8 + (part == 2 ? r8 : 0) + q0)
+                          : q2_u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[i][j] = mfma32_bf16(aq[i], bq[j], acc[i][j]);
+        }
+      }
+  }
+
+  // Out through a strip of 32 rows x 64 columns per wave.
+  const float* bias = a.bias ? a.bias + rt.expert * a.N : nullptr;
+  float* strip = reinterpret_cast<float*>(smem) + wv * 32 * FX_STRIP;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        strip[(8 * (e >> 2) + 4 * h + (e & 3)) * FX_STRIP + 32 * j + c] = acc[i][j][e];
+    __builtin_amdgcn_wave_barrier();
+    const int rows = (int)std::min<int64_t>(rt.mend - m0 - 32 * i, 32);
+    store_strip(a, bias, n_out, strip, FX_STRIP, 32, a.gated ? 32 : 64, m0 + 32 * i, rows, n0, lane);
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// ============================================================================
+// launch
+// ============================================================================
+static size_t pad256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// Rows of the last tile run up to FX_BM - 1 past the end of the workspace's rows.
+size_t f16_workspace_bytes(int64_t M, int64_t K) {
+  return pad256((size_t)(M + FX_BM) * (size_t)K * 2) + pad256((size_t)(M + FX_BM) * 4);
+}
+
+hipError_t launch_fused_f16(const FusedArgs& a, void* ws, hipStream_t stream) {
+  uint16_t* x16 = static_cast<uint16_t*>(ws);
+  int32_t* rexp = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + pad256((size_t)(a.M + FX_BM) * (size_t)a.K * 2));
+  const int64_t cv = (a.M + CV_ROWS - 1) / CV_ROWS;
+  const int64_t cols = a.gated ? FX_BN / 2 : FX_BN;
+  const int64_t tiles_n = (fused_n_out(a) + cols - 1) / cols, slots = max_row_tiles(a, FX_BM);
+  if (cv > 0x7fffffff || tiles_n > 0x7fffffff || slots > 0x7fffffff / tiles_n) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(x_to_f16_kernel, dim3((unsigned)cv), dim3(64 * CV_ROWS), 0, stream, a.x, a.row_index, a.x_rows,
+                     x16, rexp, a.M, a.K);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int group_m = tile_group_rows(slots, tiles_n, 2.0 * FX_BM * (double)a.K, (double)FX_BN * a.K * 0.265625, 64);
+  hipLaunchKernelGGL(fused_f16_kernel, dim3((unsigned)(slots * tiles_n)), dim3(256), 0, stream, a, x16, rexp,
+                     (int)tiles_n, group_m);
+  return hipGetLastError();
+}
+
+}  // namespace q2dev
