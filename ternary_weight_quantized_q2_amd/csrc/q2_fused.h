@@ -177,13 +177,14 @@ __device__ __forceinline__ RowTile find_row_tile(const FusedArgs& a, int64_t slo
       const int v = __shfl_up(sum, d);
       if (lane >= d) sum += v;
     }
-    const int total = __shfl(sum, 63);
+    const int total = __builtin_amdgcn_readlane(sum, 63);
     const uint64_t past = __builtin_amdgcn_ballot_w64(before + sum > slot);
     if (past != 0) {
       const int l = __builtin_ctzll(past);
-      const int64_t first = before + __shfl(sum - mine, l);
-      t.m0 = __shfl((int)lo, l) + (slot - first) * bm;
-      t.mend = __shfl((int)hi, l);
+      const int64_t first = before + __builtin_amdgcn_readlane(sum - mine, l);
+      // readlane: scalars, so that buffer resources built on them stay in scalar registers
+      t.m0 = __builtin_amdgcn_readlane((int)lo, l) + (slot - first) * bm;
+      t.mend = __builtin_amdgcn_readlane((int)hi, l);
       t.expert = e0 + l;
       t.valid = true;
       return t;

@@ -107,9 +107,9 @@ __device__ __forceinline__ WTable weight_table(uint16_t dbits) {
   t.hi = __builtin_amdgcn_perm(pair, pair, 0x03010C01u) ^ 0x00000080u;         // -hi, 0, hi, hi2
   return t;
 }
-// K step t (0..7) of a block from the lane's four code dwords.
+// K step t (0..3) of a 64-wide half block from the lane's two code dwords.
 template <int T>
-__device__ __forceinline__ q2_u32x4 decode_step(const q2_u32x4& w, const WTable& tab) {
+__device__ __forceinline__ q2_u32x4 decode_step(const q2_u32x2& w, const WTable& tab) {
   constexpr int I = T >> 1, J = 2 * (T & 1);
   q2_u32x4 r;
 #pragma unroll
@@ -123,12 +123,30 @@ __device__ __forceinline__ q2_u32x4 decode_step(const q2_u32x4& w, const WTable&
 }
 
 constexpr int FX_BM = 128, FX_BN = 256;                  // rows, weight columns of a workgroup
-constexpr int FX_STAGE = FX_BM * 256;                    // bytes of one 128-wide block of the rows
+constexpr int FX_HALF = FX_BM * 128;                     // bytes of a 64-wide half block of the rows
+constexpr int FX_RING = 3;                               // half blocks in LDS
+constexpr int FX_OFF_W = FX_RING * FX_HALF;
+constexpr int FX_WBUF = 64 * 64;                         // codes of a wave's 64 columns, two blocks
+constexpr int FX_SMEM = FX_OFF_W + 4 * 2 * FX_WBUF;      // 80 KB: two workgroups per CU
 constexpr int FX_STRIP = 64 + 4;                         // floats per row of a wave's output strip
+static_assert(FX_SMEM <= 80 * 1024 && 4 * 32 * FX_STRIP * 4 <= FX_SMEM, "LDS");
 
+// A workgroup of four waves owns 128 rows x 256 weight columns, each wave all
+// the rows of 64 columns, so a column's weights are decoded once.  Two
+// workgroups share a CU and overlap each other's waits.  Per half block (64 of
+// K, half-stage hs) a wave copies a quarter of the tile's rows and a sixteenth
+// of its own columns' codes to LDS, both two or more half-stages ahead:
+//  - rows: a ring of three half blocks; those of hs + 2 are issued at hs;
+//  - codes: two buffers of two blocks (64 bytes of a row at a time: reading a
+//    block's 32 bytes from 32 rows per instruction cost 16 % of the kernel);
+//    piece q of the buffer that is used from half-stage 4 S + 4 on is issued at
+//    4 S - 1 + q, after that buffer's last codes went to registers at 4 S - 2;
+//  - scales: four blocks at a time in registers.
+// One barrier per half-stage; a wave waits until only the last four row copies
+// are in flight, so everything issued before them has landed.
 __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const uint16_t* x16, const int32_t* rexp,
                                                            int tiles_n, int group_m) {
-  __shared__ __align__(16) uint8_t smem[2 * FX_STAGE];
+  __shared__ __align__(16) uint8_t smem[FX_SMEM];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 31, h = lane >> 5;
@@ -138,40 +156,70 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
   if (!tile_of_block(a, FX_BM, tiles_n, group_m, slot, tn)) return;
   const RowTile rt = find_row_tile(a, slot, FX_BM);
   const int64_t m0 = rt.m0, n_out = fused_n_out(a), K = a.K;
-  const int KB = (int)(K / BLOCK_K);
+  const int KB = (int)(K / BLOCK_K), NH = 2 * KB;
   // Columns of the wave's two 32-column tiles: neighbours, or with a gated
   // epilogue both factors of the same outputs.
   const int64_t n0 = (int64_t)tn * (a.gated ? FX_BN / 2 : FX_BN) + wv * (a.gated ? 32 : 64);
-  const uint8_t* wp[2];
-  const uint16_t* sp[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    int64_t n = n0 + c + (a.gated ? 0 : 32 * j);
+  auto wcol = [&](int col) -> int64_t {                  // weight row of the wave's column 0 .. 63
+    int64_t n = n0 + (a.gated ? (col & 31) : col);
     n = n < n_out ? n : n_out - 1;
-    if (a.gated && j) n += n_out;
-    const int64_t row = rt.expert * a.N + n;
-    wp[j] = a.w + row * (K / 4) + 16 * h;
-    sp[j] = a.s + row * KB;
-  }
+    return a.gated && col >= 32 ? n + n_out : n;
+  };
 
-  // Copies of a block's rows: copy kk of wave wv fills tile rows
-  // 16 kk + 4 wv .. + 3; lane l row 4 wv + l / 16 of them and 16-byte position
-  // l % 16, which holds chunk (l % 16) ^ (row % 16).  A wave's 16-byte reads of
-  // 32 rows then hit every bank equally.  Rows past the last one are padding of
-  // the workspace, never stored.
-  const int crow = 4 * wv + (lane >> 4);
-  const uint32_t xoff = (uint32_t)(crow * K * 2) + (uint32_t)(((lane & 15) ^ crow) << 4);
+  // Rows: copy kk fills tile rows 32 kk + 8 wv .. + 7, lane l row l / 8 of them
+  // and 16-byte position l % 8, which holds chunk (l % 8) ^ (row / 2 % 8): the
+  // sixteen rows that one pass of a 16-byte read touches lie in different
+  // banks.  Rows past the last one are padding of the workspace, never stored.
+  const int crow = 8 * wv + (lane >> 3);
+  const uint32_t xoff = (uint32_t)(crow * K * 2) + (uint32_t)(((lane & 7) ^ ((crow >> 1) & 7)) << 4);
   const __amdgpu_buffer_rsrc_t rx = buf_rsrc(x16 + m0 * K, (uint32_t)(FX_BM * K * 2));
-  auto copy_block = [&](int blk, int stage) {
+  auto copy_rows = [&](int hs, int ring) {
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(smem + stage * FX_STAGE + (16 * kk + 4 * wv) * 256), 16,
-                                               xoff, (uint32_t)(16 * kk) * (uint32_t)(K * 2) + (uint32_t)blk * 256u, 0,
+    for (int kk = 0; kk < 4; ++kk)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(smem + ring * FX_HALF + (32 * kk + 8 * wv) * 128), 16,
+                                               xoff, (uint32_t)(32 * kk) * (uint32_t)(K * 2) + (uint32_t)hs * 128u, 0,
                                                0);
   };
-  int aoff[8];
+  int aoff[4];
 #pragma unroll
-  for (int t = 0; t < 8; ++t) aoff[t] = c * 256 + (((8 * h + t) ^ (c & 15)) << 4);
+  for (int t = 0; t < 4; ++t) aoff[t] = c * 128 + (((4 * h + t) ^ ((c >> 1) & 7)) << 4);
+
+  // Codes: piece q holds columns 16 q .. + 15, lane l column l / 4 of them and
+  // 16-byte position l % 4, which holds unit (l % 4) ^ (column / 4 % 4).
+  const __amdgpu_buffer_rsrc_t rw = buf_rsrc(a.w + rt.expert * a.N * (K / 4), (uint32_t)(a.N * (K / 4)));
+  uint32_t woff[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    woff[q] = (uint32_t)(wcol(16 * q + (lane >> 2)) * (K / 4)) + (uint32_t)(((lane & 3) ^ ((lane >> 4) & 3)) << 4);
+  auto copy_codes = [&](int set, int q) {                // past the end of the weight: zeros, never used
+    const uint32_t wo = q == 0 ? woff[0] : q == 1 ? woff[1] : q == 2 ? woff[2] : woff[3];
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rw, (lds_void*)(smem + FX_OFF_W + ((set & 1) * 4 + wv) * FX_WBUF + q * 1024), 16, wo, (uint32_t)set * 64u, 0,
+        0);
+  };
+  const uint8_t* const wbase = smem + FX_OFF_W + wv * FX_WBUF + c * 64 + 8 * h;
+  auto read_codes = [&](int hs, q2_u32x2 (&w)[2]) {
+    const int off = ((hs >> 2) & 1) * 4 * FX_WBUF + (((hs & 3) ^ ((c >> 2) & 3)) << 4);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) w[j] = *reinterpret_cast<const q2_u32x2*>(wbase + off + j * 32 * 64);
+  };
+
+  // Scales of blocks 4 q .. 4 q + 3, a half-word each.
+  const uint16_t* sp[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) sp[j] = a.s + (rt.expert * a.N + wcol(32 * j + c)) * KB;
+  auto load_scales = [&](int q, uint64_t (&sc)[2]) {
+    const int b0 = 4 * q;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (b0 + 4 <= KB) {
+        __builtin_memcpy(&sc[j], sp[j] + b0, 8);
+      } else {
+        sc[j] = 0;
+        for (int e = 0; b0 + e < KB; ++e) sc[j] |= (uint64_t)sp[j][b0 + e] << (16 * e);
+      }
+    }
+  };
 
   q2_f32x16 acc[4][2];
 #pragma unroll
@@ -181,39 +229,54 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
-  q2_u32x4 wnext[2];
-  uint32_t snext[2];
-  auto load_weights = [&](int blk) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      wnext[j] = *reinterpret_cast<const q2_u32x4*>(wp[j] + (int64_t)blk * 32);
-      snext[j] = sp[j][blk];
-    }
-  };
+  q2_u32x2 w[2] = {};
+  uint64_t sc[2] = {0, 0}, scn[2] = {0, 0};
   if (KB > 0) {
-    copy_block(0, 0);
-    load_weights(0);
+    load_scales(0, sc);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) copy_codes(0, q);
+    copy_codes(1, 0);                                    // half-stage -1's piece
+    copy_rows(0, 0);
+    copy_rows(1, 1);
+    __builtin_amdgcn_s_waitcnt(0);
+    read_codes(0, w);
   }
+  int ring = 0;
   for (int blk = 0; blk < KB; ++blk) {
-    const int stage = blk & 1;
-    stage_barrier<0>();                                  // this block's rows and codes have landed
-    const q2_u32x4 w[2] = {wnext[0], wnext[1]};
-    const WTable tab[2] = {weight_table((uint16_t)snext[0]), weight_table((uint16_t)snext[1])};
-    const int nblk = blk + 1 < KB ? blk + 1 : blk;       // past the end: the last block again, never read
-    copy_block(nblk, stage ^ 1);
-    load_weights(nblk);
-    const uint8_t* st = smem + stage * FX_STAGE;
+    if ((blk & 3) == 0) {
+      if (blk > 0) {
+        sc[0] = scn[0];
+        sc[1] = scn[1];
+      }
+      if (blk + 4 < KB) load_scales(blk / 4 + 1, scn);
+    }
+    const int sh = 16 * (blk & 3);
+    const WTable tab[2] = {weight_table((uint16_t)(sc[0] >> sh)), weight_table((uint16_t)(sc[1] >> sh))};
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int hs = 2 * blk + half;
+      stage_barrier<4>();
+      const int ring2 = ring == 0 ? 2 : ring - 1;        // (hs + 2) % 3
+      copy_codes((hs + 1) / 4 + 1, (hs + 1) & 3);
+      copy_rows(hs + 2 < NH ? hs + 2 : NH - 1, ring2);   // past the end: the last one again, never read
+      const uint8_t* st = smem + ring * FX_HALF;
+      q2_u32x2 wn[2];
+      read_codes(hs + 1, wn);
 #define Q2_STEP(T)                                                                                     \
   {                                                                                                    \
     const q2_u32x4 b0 = decode_step<T>(w[0], tab[0]), b1 = decode_step<T>(w[1], tab[1]);               \
     _Pragma("unroll") for (int i = 0; i < 4; ++i) {                                                    \
-      const q2_u32x4 av = *reinterpret_cast<const q2_u32x4*>(st + i * 8192 + aoff[T]);                 \
+      const q2_u32x4 av = *reinterpret_cast<const q2_u32x4*>(st + i * 4096 + aoff[T]);                 \
       acc[i][0] = mfma32(av, b0, acc[i][0]);                                                           \
       acc[i][1] = mfma32(av, b1, acc[i][1]);                                                           \
     }                                                                                                  \
   }
-    Q2_STEP(0) Q2_STEP(1) Q2_STEP(2) Q2_STEP(3) Q2_STEP(4) Q2_STEP(5) Q2_STEP(6) Q2_STEP(7)
+      Q2_STEP(0) Q2_STEP(1) Q2_STEP(2) Q2_STEP(3)
 #undef Q2_STEP
+      w[0] = wn[0];
+      w[1] = wn[1];
+      ring = ring == 2 ? 0 : ring + 1;
+    }
   }
   __builtin_amdgcn_s_waitcnt(0);                         // no copy may still write this workgroup's LDS
   __syncthreads();
