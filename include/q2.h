@@ -412,8 +412,8 @@ int q4_linear_grouped(const uint16_t* x_bf16, int64_t x_rows, const int32_t* row
  *   slot       i32 [T, k]: the row of each choice, -1 where expert is -1   (out)
  *   workspace  device scratch of >= q2_route_workspace_bytes(T, E, k) bytes,
  *              256-byte aligned (may be NULL when that is 0)
- * 1 <= k <= min(E, 64), E <= 1024 (Q2_ERR_SHAPE otherwise), T * k < 2^31.  Sums
- * in fp32 in a fixed order: run-to-run bitwise deterministic.  Asynchronous;
+ * 1 <= k <= min(E, 64), E <= 1024, T <= 2^26, T * k < 2^31 (Q2_ERR_SHAPE
+ * otherwise).  Sums in fp32 in a fixed order: run-to-run bitwise deterministic.  Asynchronous;
  * calls that share a workspace must be ordered on one stream.
  */
 int q2_route(const void* logits, int64_t T, int64_t E, int64_t k, uint32_t flags, int32_t* expert, float* weight,

@@ -116,7 +116,8 @@ def _ptr(t) -> int | None:
 
 
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    # the current stream's handle, without building torch.cuda.current_stream()'s object (2.8 us of host time)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _want(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str) -> None:
@@ -322,14 +323,21 @@ def q4_linear(x, packed4, scale, zero, y=None) -> torch.Tensor:
     return y
 
 
-def _want_here(t: torch.Tensor, dtype, shape: tuple, name: str) -> None:
-    """_want, on the current device (the device of the stream the call goes to)."""
+def _here() -> int:
+    """The current device, whose current stream the call goes to."""
+    return torch.cuda.current_device()
+
+
+def _have(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str, dev: int) -> None:
+    """_want, on device `dev`.  (These checks are most of a small call's host time: the common case is one test.)"""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return
     _want(t, dtype, shape, name)
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{torch.cuda.current_device()}")
+    if t.is_cuda and t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{dev}")
 
 
-def _epilogue(n, rows, bias_shape, bias, activation, gated, gate, residual, out_dtype, y, device):
+def _epilogue(n, rows, bias_shape, bias, activation, gated, gate, residual, out_dtype, y, x, dev):
     """(q2_epilogue, y) of a fused or grouped linear over a weight of n rows; y is allocated when None."""
     if activation not in ACTIVATIONS:
         raise ValueError(f"unknown activation {activation!r}: one of {', '.join(ACTIVATIONS)}")
@@ -344,30 +352,30 @@ def _epilogue(n, rows, bias_shape, bias, activation, gated, gate, residual, out_
     if out_dtype == torch.bfloat16:
         flags |= Q2_EPI_OUT_BF16
     if bias is not None:
-        _want_here(bias, torch.float32, bias_shape, "bias")
+        _have(bias, torch.float32, bias_shape, "bias", dev)
     if gate is not None:
-        _want_here(gate, torch.float32, shape[1:], "gate")
+        _have(gate, torch.float32, shape[1:], "gate", dev)
     if residual is not None:
         if residual.dtype == torch.bfloat16:
             flags |= Q2_EPI_RESIDUAL_BF16
         elif residual.dtype != torch.float32:
             raise ValueError(f"residual is float32 or bfloat16, not {residual.dtype}")
-        _want_here(residual, residual.dtype, shape, "residual")
+        _have(residual, residual.dtype, shape, "residual", dev)
     if y is None:
-        y = torch.empty(shape, dtype=out_dtype, device=device)
+        y = x.new_empty(shape, dtype=out_dtype)
     else:
-        _want_here(y, out_dtype, shape, "y")
+        _have(y, out_dtype, shape, "y", dev)
     return Epilogue(ACTIVATIONS[activation], flags, _ptr(bias), _ptr(gate), _ptr(residual)), y
 
 
-def _scratch(need: int, workspace, device):
+def _scratch(need: int, workspace, dev: int):
     """(workspace, its bytes): the caller's, or a new one of `need` bytes."""
     if workspace is None:
         if need == 0:
             return None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}")
     else:
-        _want_here(workspace, workspace.dtype, workspace.shape, "workspace")
+        _have(workspace, workspace.dtype, workspace.shape, "workspace", dev)
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -385,19 +393,20 @@ def q2_linear_fused(x, packed, scales, A=None, B=None, bias=None, activation="no
     bias f32 [N]; gate f32 [n_out]; residual f32 or bf16 [M, n_out], which may be y itself; A f16 [r, K] and
     B f16 [N, r] add the rank-r branch.  activation: none, relu, gelu, gelu_tanh or silu."""
     lib = load()
+    dev = _here()
     m, k = x.shape
     n = packed.shape[0]
-    _want_here(x, torch.bfloat16, (m, k), "x")
-    _want_here(packed, torch.uint8, (n, k // 4), "packed")
-    _want_here(scales, torch.float16, (n, k // 128), "scales")
+    _have(x, torch.bfloat16, (m, k), "x", dev)
+    _have(packed, torch.uint8, (n, k // 4), "packed", dev)
+    _have(scales, torch.float16, (n, k // 128), "scales", dev)
     if (A is None) != (B is None):
         raise ValueError("A and B come together")
     r = 0 if A is None else A.shape[0]
     if A is not None:
-        _want_here(A, torch.float16, (r, k), "A")
-        _want_here(B, torch.float16, (n, r), "B")
-    epi, y = _epilogue(n, m, (n,), bias, activation, gated, gate, residual, out_dtype, y, x.device)
-    ws, ws_bytes = _scratch(lib.q2_linear_fused_workspace_bytes(m, n, k, r), workspace, x.device)
+        _have(A, torch.float16, (r, k), "A", dev)
+        _have(B, torch.float16, (n, r), "B", dev)
+    epi, y = _epilogue(n, m, (n,), bias, activation, gated, gate, residual, out_dtype, y, x, dev)
+    ws, ws_bytes = _scratch(lib.q2_linear_fused_workspace_bytes(m, n, k, r), workspace, dev)
     _check(lib.q2_linear_fused(_ptr(x), _ptr(packed), _ptr(scales), _ptr(A), _ptr(B), r, ctypes.addressof(epi), _ptr(y),
                                m, n, k, _ptr(ws), ws_bytes, _stream()))
     return y
@@ -407,27 +416,28 @@ def q4_linear_fused(x, packed4, scale, zero, bias=None, activation="none", gated
                     out_dtype=torch.float32, y=None) -> torch.Tensor:
     """q2_linear_fused (without the branch) for the 4-bit format of q4_linear."""
     lib = load()
+    dev = _here()
     m, k = x.shape
     n = packed4.shape[0]
-    _want_here(x, torch.bfloat16, (m, k), "x")
-    _want_here(packed4, torch.uint8, (n, k // 2), "packed4")
-    _want_here(scale, torch.float16, (n, k // 128), "scale")
-    _want_here(zero, torch.float16, (n, k // 128), "zero")
-    epi, y = _epilogue(n, m, (n,), bias, activation, gated, gate, residual, out_dtype, y, x.device)
+    _have(x, torch.bfloat16, (m, k), "x", dev)
+    _have(packed4, torch.uint8, (n, k // 2), "packed4", dev)
+    _have(scale, torch.float16, (n, k // 128), "scale", dev)
+    _have(zero, torch.float16, (n, k // 128), "zero", dev)
+    epi, y = _epilogue(n, m, (n,), bias, activation, gated, gate, residual, out_dtype, y, x, dev)
     _check(lib.q4_linear_fused(_ptr(x), _ptr(packed4), _ptr(scale), _ptr(zero), ctypes.addressof(epi), _ptr(y), m, n, k,
                                _stream()))
     return y
 
 
-def _groups(x, offsets, experts, row_index):
+def _groups(x, offsets, experts, row_index, dev):
     """(rows, x_rows, K) of a grouped call, its integer arguments checked."""
     x_rows, k = x.shape
-    _want_here(x, torch.bfloat16, (x_rows, k), "x")
-    _want_here(offsets, torch.int32, (experts + 1,), "offsets")
+    _have(x, torch.bfloat16, (x_rows, k), "x", dev)
+    _have(offsets, torch.int32, (experts + 1,), "offsets", dev)
     if row_index is None:
         return x_rows, x_rows, k
     rows = row_index.numel()
-    _want_here(row_index, torch.int32, (rows,), "row_index")
+    _have(row_index, torch.int32, (rows,), "row_index", dev)
     return rows, x_rows, k
 
 
@@ -445,12 +455,13 @@ def q2_linear_grouped(x, offsets, packed, scales, row_index=None, bias=None, act
     them, bias f32 [E, N]; gated, activation and out_dtype as q2_linear_fused.  Rows that no expert has are left
     as they are in y (undefined in a y allocated here)."""
     lib = load()
+    dev = _here()
     e, n = packed.shape[:2]
-    rows, x_rows, k = _groups(x, offsets, e, row_index)
-    _want_here(packed, torch.uint8, (e, n, k // 4), "packed")
-    _want_here(scales, torch.float16, (e, n, k // 128), "scales")
-    epi, y = _epilogue(n, rows, (e, n), bias, activation, gated, None, None, out_dtype, y, x.device)
-    ws, ws_bytes = _scratch(lib.q2_linear_grouped_workspace_bytes(rows, e, n, k), workspace, x.device)
+    rows, x_rows, k = _groups(x, offsets, e, row_index, dev)
+    _have(packed, torch.uint8, (e, n, k // 4), "packed", dev)
+    _have(scales, torch.float16, (e, n, k // 128), "scales", dev)
+    epi, y = _epilogue(n, rows, (e, n), bias, activation, gated, None, None, out_dtype, y, x, dev)
+    ws, ws_bytes = _scratch(lib.q2_linear_grouped_workspace_bytes(rows, e, n, k), workspace, dev)
     _check(lib.q2_linear_grouped(_ptr(x), x_rows, _ptr(row_index), _ptr(offsets), _ptr(packed), _ptr(scales),
                                  ctypes.addressof(epi), _ptr(y), rows, e, n, k, _ptr(ws), ws_bytes, _stream()))
     return y
@@ -460,12 +471,13 @@ def q4_linear_grouped(x, offsets, packed4, scale, zero, row_index=None, bias=Non
                       out_dtype=torch.float32, y=None) -> torch.Tensor:
     """q2_linear_grouped for the 4-bit format: packed4 u8 [E, N, K/2], scale and zero f16 [E, N, K/128]."""
     lib = load()
+    dev = _here()
     e, n = packed4.shape[:2]
-    rows, x_rows, k = _groups(x, offsets, e, row_index)
-    _want_here(packed4, torch.uint8, (e, n, k // 2), "packed4")
-    _want_here(scale, torch.float16, (e, n, k // 128), "scale")
-    _want_here(zero, torch.float16, (e, n, k // 128), "zero")
-    epi, y = _epilogue(n, rows, (e, n), bias, activation, gated, None, None, out_dtype, y, x.device)
+    rows, x_rows, k = _groups(x, offsets, e, row_index, dev)
+    _have(packed4, torch.uint8, (e, n, k // 2), "packed4", dev)
+    _have(scale, torch.float16, (e, n, k // 128), "scale", dev)
+    _have(zero, torch.float16, (e, n, k // 128), "zero", dev)
+    epi, y = _epilogue(n, rows, (e, n), bias, activation, gated, None, None, out_dtype, y, x, dev)
     _check(lib.q4_linear_grouped(_ptr(x), x_rows, _ptr(row_index), _ptr(offsets), _ptr(packed4), _ptr(scale), _ptr(zero),
                                  ctypes.addressof(epi), _ptr(y), rows, e, n, k, _stream()))
     return y
@@ -486,19 +498,17 @@ def q2_route(logits, k: int, renormalize: bool = True, workspace=None) -> Route:
     renormalize, over the chosen ones, and the rows sorted by expert, then token, as the grouped linears
     (offsets, row_token) and q2_combine (slot, weight) take them."""
     lib = load()
+    dev = _here()
     t, e = logits.shape
     if logits.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"logits are float32 or bfloat16, not {logits.dtype}")
-    _want_here(logits, logits.dtype, (t, e), "logits")
+    _have(logits, logits.dtype, (t, e), "logits", dev)
     flags = (Q2_ROUTE_LOGITS_BF16 if logits.dtype == torch.bfloat16 else 0) | (Q2_ROUTE_RENORM if renormalize else 0)
     k = int(k)
-    rows = max(t * k, 0)
-    dev = logits.device
-    route = Route(torch.empty((t, max(k, 0)), dtype=torch.int32, device=dev),
-                  torch.empty((t, max(k, 0)), dtype=torch.float32, device=dev),
-                  torch.empty(e + 1, dtype=torch.int32, device=dev),
-                  torch.empty(rows, dtype=torch.int32, device=dev),
-                  torch.empty((t, max(k, 0)), dtype=torch.int32, device=dev))
+    c = max(k, 0)                                          # a refused k still reaches the library's message
+    new, i32 = logits.new_empty, torch.int32
+    route = Route(new((t, c), dtype=i32), new((t, c), dtype=torch.float32), new(e + 1, dtype=i32),
+                  new(t * c, dtype=i32), new((t, c), dtype=i32))
     ws, ws_bytes = _scratch(lib.q2_route_workspace_bytes(t, e, k), workspace, dev)
     _check(lib.q2_route(_ptr(logits), t, e, k, flags, _ptr(route.expert), _ptr(route.weight), _ptr(route.offsets),
                         _ptr(route.row_token), _ptr(route.slot), _ptr(ws), ws_bytes, _stream()))
@@ -510,13 +520,14 @@ def q2_combine(z, slot, weight, residual=None, out_dtype=torch.float32, y=None) 
     their tokens; slot i32 and weight f32 [T, k] as q2_route gives them, a slot outside [0, R) adds nothing;
     residual f32 or bf16 [T, N], which may be y itself."""
     lib = load()
+    dev = _here()
     r, n = z.shape
     t, k = slot.shape
     if z.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"z is float32 or bfloat16, not {z.dtype}")
-    _want_here(z, z.dtype, (r, n), "z")
-    _want_here(slot, torch.int32, (t, k), "slot")
-    _want_here(weight, torch.float32, (t, k), "weight")
+    _have(z, z.dtype, (r, n), "z", dev)
+    _have(slot, torch.int32, (t, k), "slot", dev)
+    _have(weight, torch.float32, (t, k), "weight", dev)
     if y is not None:
         out_dtype = y.dtype
     if out_dtype not in (torch.float32, torch.bfloat16):
@@ -528,11 +539,11 @@ def q2_combine(z, slot, weight, residual=None, out_dtype=torch.float32, y=None) 
             flags |= Q2_COMBINE_RESIDUAL_BF16
         elif residual.dtype != torch.float32:
             raise ValueError(f"residual is float32 or bfloat16, not {residual.dtype}")
-        _want_here(residual, residual.dtype, (t, n), "residual")
+        _have(residual, residual.dtype, (t, n), "residual", dev)
     if y is None:
-        y = torch.empty((t, n), dtype=out_dtype, device=z.device)
+        y = z.new_empty((t, n), dtype=out_dtype)
     else:
-        _want_here(y, out_dtype, (t, n), "y")
+        _have(y, out_dtype, (t, n), "y", dev)
     _check(lib.q2_combine(_ptr(z), r, _ptr(slot), _ptr(weight), _ptr(residual), _ptr(y), t, k, n, flags, _stream()))
     return y
 

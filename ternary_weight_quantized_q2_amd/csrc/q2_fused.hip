@@ -126,7 +126,7 @@ __global__ __launch_bounds__(256) void fused_tile_kernel(FusedArgs a, int tiles_
 
 // The f16 kernel for Q2_0 weights over many rows.
 static bool use_f16(int64_t M, int64_t N, int64_t K, int64_t E, int fmt) {
-  return fmt == 0 && M >= 128 * std::max<int64_t>(E, 1) / 2 && K >= 128 && K <= (1 << 22) && N <= ((int64_t)1 << 33) / K;
+  return fmt == 0 && M >= 128 * std::max<int64_t>(E, 1) / 2 && K >= 512 && K <= (1 << 22) && N <= ((int64_t)1 << 33) / K;
 }
 
 size_t fused_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t E, int fmt) {

@@ -117,7 +117,7 @@ bool sizes_ok(int64_t M, int64_t N, int64_t K) {
 }
 
 bool route_sizes_ok(int64_t T, int64_t E, int64_t k) {
-  return T >= 0 && E >= 1 && E <= 1024 && k >= 1 && k <= E && k <= 64 && T <= 0x7fffffff / k;
+  return T >= 0 && E >= 1 && E <= 1024 && k >= 1 && k <= E && k <= 64 && T <= 0x7fffffff / k && T <= (1 << 26);
 }
 
 }  // namespace
@@ -176,7 +176,7 @@ int q2_route(const void* logits, int64_t T, int64_t E, int64_t k, uint32_t flags
   const uint32_t known = Q2_ROUTE_LOGITS_BF16 | Q2_ROUTE_RENORM;
   if (flags & ~known) return fail(Q2_ERR_ARG, "unknown route flag bits 0x%x", flags & ~known);
   if (!route_sizes_ok(T, E, k))
-    return fail(Q2_ERR_SHAPE, "T=%lld E=%lld k=%lld: 1 <= k <= min(E, 64), E <= 1024, T * k < 2^31", (long long)T,
+    return fail(Q2_ERR_SHAPE, "T=%lld E=%lld k=%lld: 1 <= k <= min(E, 64), E <= 1024, T <= 2^26, T * k < 2^31", (long long)T,
                 (long long)E, (long long)k);
   int st;
   const bool ne = T > 0;

@@ -204,21 +204,13 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
     for (int j = 0; j < 2; ++j) w[j] = *reinterpret_cast<const q2_u32x2*>(wbase + off + j * 32 * 64);
   };
 
-  // Scales of blocks 4 q .. 4 q + 3, a half-word each.
+  // Scales of four blocks, a half-word each, from block min(4 q, KB - 4) on.
   const uint16_t* sp[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) sp[j] = a.s + (rt.expert * a.N + wcol(32 * j + c)) * KB;
   auto load_scales = [&](int q, uint64_t (&sc)[2]) {
-    const int b0 = 4 * q;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if (b0 + 4 <= KB) {
-        __builtin_memcpy(&sc[j], sp[j] + b0, 8);
-      } else {
-        sc[j] = 0;
-        for (int e = 0; b0 + e < KB; ++e) sc[j] |= (uint64_t)sp[j][b0 + e] << (16 * e);
-      }
-    }
+    for (int j = 0; j < 2; ++j) __builtin_memcpy(&sc[j], sp[j] + min(4 * q, KB - 4), 8);
   };
 
   q2_f32x16 acc[4][2];
@@ -230,27 +222,22 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
   q2_u32x2 w[2] = {};
-  uint64_t sc[2] = {0, 0}, scn[2] = {0, 0};
-  if (KB > 0) {
-    load_scales(0, sc);
+  uint64_t scn[2];
+  load_scales(0, scn);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) copy_codes(0, q);
-    copy_codes(1, 0);                                    // half-stage -1's piece
-    copy_rows(0, 0);
-    copy_rows(1, 1);
-    __builtin_amdgcn_s_waitcnt(0);
-    read_codes(0, w);
-  }
+  for (int q = 0; q < 4; ++q) copy_codes(0, q);
+  copy_codes(1, 0);                                      // half-stage -1's piece
+  copy_rows(0, 0);
+  copy_rows(1, 1);
+  __builtin_amdgcn_s_waitcnt(0);
+  read_codes(0, w);
   int ring = 0;
-  for (int blk = 0; blk < KB; ++blk) {
-    if ((blk & 3) == 0) {
-      if (blk > 0) {
-        sc[0] = scn[0];
-        sc[1] = scn[1];
-      }
-      if (blk + 4 < KB) load_scales(blk / 4 + 1, scn);
-    }
-    const int sh = 16 * (blk & 3);
+  for (int quad = 0; 4 * quad < KB; ++quad) {
+   const uint64_t sc[2] = {scn[0], scn[1]};
+   load_scales(quad + 1, scn);                           // past the end: the last four again, never used
+   const int b0 = min(4 * quad, KB - 4), bend = min(4 * quad + 4, KB);
+   for (int blk = 4 * quad; blk < bend; ++blk) {
+    const int sh = 16 * (blk - b0);
     const WTable tab[2] = {weight_table((uint16_t)(sc[0] >> sh)), weight_table((uint16_t)(sc[1] >> sh))};
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -277,6 +264,7 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
       w[1] = wn[1];
       ring = ring == 2 ? 0 : ring + 1;
     }
+   }
   }
   __builtin_amdgcn_s_waitcnt(0);                         // no copy may still write this workgroup's LDS
   __syncthreads();

@@ -8,23 +8,30 @@ namespace q2dev {
 // ============================================================================
 // Router
 // ============================================================================
-// A workgroup of four waves takes 64 tokens, one wave per token at a time.  A
-// lane holds every 64th logit as a 64-bit key (order-preserving bits of the
-// logit above the complement of the expert number), so one maximum over the
-// lanes finds the largest logit and, among equal ones, the lowest expert; k
-// such maxima are the choice.
+// A workgroup of sixteen waves takes 64 tokens, one wave per token at a time.
+// A lane holds every 64th logit as order-preserving bits, 0 for a masked expert
+// or one already chosen; a maximum over the lanes (six data-parallel-primitive
+// moves, no LDS) and a ballot of the lanes that hold it give the largest logit
+// and, among equal ones, the lowest expert.  k such steps are the choice.
 //
-// Row plan: each token chooses an expert at most once, so the 64 tokens'
-// choices are one 64-bit mask per expert, and a choice's place among the
-// workgroup's rows of its expert is the number of mask bits below its token.
-// The rows of earlier workgroups and experts come from the workgroups' counts:
-// up to 64 tokens one launch has everything; beyond, the first launch leaves
-// the counts (one byte per workgroup and expert) in the workspace and the
-// second adds them up.  Integer counts in a fixed order: the plan is exact and
-// the same on every run.
-constexpr int RT_TOK = 64, RT_THREADS = 256, RT_WAVES = RT_THREADS / 64;
+// Row plan: each token chooses an expert at most once, so 64 tokens' choices
+// are one 64-bit mask per expert, and a choice's place among the rows of its
+// expert is the number of mask bits below its token.  The rows of earlier
+// workgroups and experts come from the workgroups' counts: up to 64 tokens one
+// launch has everything; beyond, the first launch leaves its counts in the
+// workspace and every workgroup of the second adds them up.  That sum is
+// (workgroups)^2, so past 1024 workgroups each takes several chunks of 64
+// tokens instead.  Integer counts: the plan is exact, the same on every run.
+// T = 16384, E = 128, k = 8: see the table of measurements beside launch_route.
+constexpr int RT_TOK = 64, RT_THREADS = 1024, RT_WAVES = RT_THREADS / 64;
+constexpr int RT_GROUPS = 1024;
 
-constexpr int route_pad(int64_t E) { return (int)((E + 15) & ~(int64_t)15); }   // bytes of counts per workgroup
+constexpr int route_pad(int64_t E) { return (int)((E + 1) & ~(int64_t)1); }     // counts per workgroup, u16 pairs
+static int route_chunks(int64_t T) { return (int)((T + RT_TOK * RT_GROUPS - 1) / (RT_TOK * RT_GROUPS)); }
+static int64_t route_groups(int64_t T) {
+  const int64_t per = (int64_t)RT_TOK * route_chunks(T);
+  return (T + per - 1) / per;
+}
 
 __device__ __forceinline__ uint32_t order_bits(float v) {
   const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f);          // -0 counts as +0
@@ -34,18 +41,34 @@ __device__ __forceinline__ float from_order_bits(uint32_t o) {
   return __builtin_bit_cast(float, o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) {
-    const uint64_t o = __shfl_xor((unsigned long long)v, d);
-    v = o > v ? o : v;
-  }
-  return v;
+// v from the lane that CTRL names, 0 where there is none.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp0(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+// Largest v (0 at least) and sum over the 64 lanes: shifts by 1, 2, 4, 8 within
+// rows of 16, then rows 0, 2 onto 1, 3 and the lower half onto the upper.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, dpp0<0x111, 0xF>(v));
+  v = max(v, dpp0<0x112, 0xF>(v));
+  v = max(v, dpp0<0x114, 0xF>(v));
+  v = max(v, dpp0<0x118, 0xF>(v));
+  v = max(v, dpp0<0x142, 0xA>(v));
+  v = max(v, dpp0<0x143, 0xC>(v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __builtin_bit_cast(float, dpp0<CTRL, ROWS>(__builtin_bit_cast(uint32_t, v)));
 }
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+  v = add_dpp<0x111, 0xF>(v);
+  v = add_dpp<0x112, 0xF>(v);
+  v = add_dpp<0x114, 0xF>(v);
+  v = add_dpp<0x118, 0xF>(v);
+  v = add_dpp<0x142, 0xA>(v);
+  v = add_dpp<0x143, 0xC>(v);
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
 // exp(v - top) of a logit, 1 for the largest itself (also when that is +inf).
@@ -55,42 +78,50 @@ __device__ __forceinline__ float route_exp(float v, float top) { return v == top
 template <int NE>
 __device__ __forceinline__ void choose(const void* logits, int bf16, int64_t t, int E, int k, int renorm, int lane,
                                        int& ex, float& wt) {
-  uint64_t key[NE];
+  uint32_t key[NE];
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
     const int e = lane + 64 * i;
     key[i] = 0;                                          // below every unmasked logit
     if (e < E) {
       const float v = load_elem(logits, t * E + e, bf16);
-      if (v > -__builtin_inff()) key[i] = ((uint64_t)order_bits(v) << 32) | (uint32_t)~e;
+      if (v > -__builtin_inff()) key[i] = order_bits(v);
     }
   }
   ex = -1;
   float mine = 0.f, top = 0.f, total = 0.f;
   for (int j = 0; j < k; ++j) {
-    uint64_t m = key[0];
+    uint32_t m = key[0];
 #pragma unroll
-    for (int i = 1; i < NE; ++i) m = key[i] > m ? key[i] : m;
+    for (int i = 1; i < NE; ++i) m = max(m, key[i]);
     m = wave_max(m);
     if (m == 0) break;                                   // nothing left but masked experts
-    const float v = from_order_bits((uint32_t)(m >> 32));
+    const float v = from_order_bits(m);
     if (j == 0) {
       top = v;
       if (!renorm) {                                     // every unmasked expert, before any key is taken out
 #pragma unroll
         for (int i = 0; i < NE; ++i)
-          if (key[i] != 0) total += route_exp(from_order_bits((uint32_t)(key[i] >> 32)), top);
+          if (key[i] != 0) total += route_exp(from_order_bits(key[i]), top);
         total = wave_sum(total);
       }
     }
     const float p = route_exp(v, top);
     if (renorm) total += p;                              // largest first
+    int e = -1;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      const uint64_t b = __builtin_amdgcn_ballot_w64(key[i] == m);
+      if (e < 0 && b != 0) {
+        const int l = __builtin_ctzll(b);
+        e = 64 * i + l;
+        if (lane == l) key[i] = 0;
+      }
+    }
     if (lane == j) {
-      ex = (int)~(uint32_t)m;
+      ex = e;
       mine = p;
     }
-#pragma unroll
-    for (int i = 0; i < NE; ++i) key[i] = key[i] == m ? 0 : key[i];
   }
   wt = ex >= 0 ? mine / total : 0.f;
 }
@@ -115,30 +146,38 @@ __device__ __forceinline__ void scan_experts(int* tot, int E, int lane) {
 
 template <int NE, bool ONE>
 __global__ __launch_bounds__(RT_THREADS) void route_choose_kernel(const void* logits, int bf16, int64_t T, int E, int k,
-                                                                  int renorm, int32_t* expert, float* weight,
-                                                                  int32_t* offsets, int32_t* row_token, int32_t* slot,
-                                                                  uint8_t* counts, int pad) {
+                                                                  int renorm, int chunks, int32_t* expert,
+                                                                  float* weight, int32_t* offsets, int32_t* row_token,
+                                                                  int32_t* slot, uint16_t* counts, int pad) {
   __shared__ unsigned long long mask[64 * NE];
-  __shared__ int off[ONE ? 64 * NE + 1 : 1];
+  __shared__ int off[64 * NE + 1];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int64_t t0 = (int64_t)blockIdx.x * RT_TOK;
-  const int nt = (int)std::min<int64_t>(T - t0, RT_TOK);
-  for (int e = threadIdx.x; e < E; e += RT_THREADS) mask[e] = 0;
-  __syncthreads();
-  for (int i = wv; i < nt; i += RT_WAVES) {
-    int ex;
-    float wt;
-    choose<NE>(logits, bf16, t0 + i, E, k, renorm, lane, ex, wt);
-    if (lane < k) {
-      expert[(t0 + i) * k + lane] = ex;
-      weight[(t0 + i) * k + lane] = wt;
-      if (ex >= 0) atomicOr(&mask[ex], 1ull << i);
+  const int64_t first = (int64_t)blockIdx.x * RT_TOK * chunks;
+  if constexpr (!ONE)
+    for (int e = threadIdx.x; e < E; e += RT_THREADS) off[e] = 0;
+  int nt = 0;
+  for (int ch = 0; ch < chunks; ++ch) {
+    const int64_t t0 = first + (int64_t)ch * RT_TOK;
+    nt = (int)std::min<int64_t>(T - t0, RT_TOK);
+    for (int e = threadIdx.x; e < E; e += RT_THREADS) mask[e] = 0;
+    __syncthreads();
+    for (int i = wv; i < nt; i += RT_WAVES) {
+      int ex;
+      float wt;
+      choose<NE>(logits, bf16, t0 + i, E, k, renorm, lane, ex, wt);
+      if (lane < k) {
+        expert[(t0 + i) * k + lane] = ex;
+        weight[(t0 + i) * k + lane] = wt;
+        if (ex >= 0) atomicOr(&mask[ex], 1ull << i);
+      }
     }
+    __syncthreads();
+    if constexpr (!ONE)
+      for (int e = threadIdx.x; e < E; e += RT_THREADS) off[e] += __popcll(mask[e]);
   }
-  __syncthreads();
   if constexpr (!ONE) {
-    for (int e = threadIdx.x; e < pad; e += RT_THREADS)
-      counts[(int64_t)blockIdx.x * pad + e] = e < E ? (uint8_t)__popcll(mask[e]) : (uint8_t)0;
+    for (int e = threadIdx.x; e < pad; e += RT_THREADS)   // off[e] was added up by this thread
+      counts[(int64_t)blockIdx.x * pad + e] = e < E ? (uint16_t)off[e] : (uint16_t)0;
   } else {
     for (int e = threadIdx.x; e < E; e += RT_THREADS) off[e] = __popcll(mask[e]);
     __syncthreads();
@@ -162,58 +201,65 @@ __global__ __launch_bounds__(RT_THREADS) void route_choose_kernel(const void* lo
 // Second launch: workgroup b adds up the counts of all workgroups and of those
 // before it, and places its tokens' choices.
 __global__ __launch_bounds__(RT_THREADS) void route_place_kernel(const int32_t* expert, int64_t T, int E, int k,
-                                                                 const uint8_t* counts, int pad, int groups,
-                                                                 int32_t* offsets, int32_t* row_token, int32_t* slot) {
+                                                                 int chunks, const uint16_t* counts, int pad,
+                                                                 int groups, int32_t* offsets, int32_t* row_token,
+                                                                 int32_t* slot) {
   __shared__ unsigned long long mask[1024];
   __shared__ int tot[1025], before[1024];
-  const int64_t t0 = (int64_t)blockIdx.x * RT_TOK;
-  const int nt = (int)std::min<int64_t>(T - t0, RT_TOK);
   for (int e = threadIdx.x; e < E; e += RT_THREADS) {
-    mask[e] = 0;
     tot[e] = 0;
     before[e] = 0;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < nt * k; i += RT_THREADS) {
-    const int ex = expert[t0 * k + i];
-    if (ex >= 0) atomicOr(&mask[ex], 1ull << (i / k));
-  }
-  // 16 experts' counts per load; the threads beyond one row of counts take further rows
-  const int vec = pad / 16, rows = std::max(1, RT_THREADS / vec);
-  for (int idx = threadIdx.x; idx < vec * rows; idx += RT_THREADS) {
-    const int q = idx % vec, r0 = idx / vec;
-    int all[16] = {}, pre[16] = {};
+  // two experts' counts per load, the threads beyond one row of counts on further rows
+  const int pairs = pad / 2, rows = RT_THREADS / pairs;
+  if ((int)threadIdx.x < pairs * rows) {
+    const int q = threadIdx.x % pairs, r0 = threadIdx.x / pairs;
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(counts) + q;
+    int all0 = 0, all1 = 0, pre0 = 0, pre1 = 0;
+#pragma unroll 8
     for (int b = r0; b < groups; b += rows) {
-      const q2_u32x4 v = *reinterpret_cast<const q2_u32x4*>(counts + (int64_t)b * pad + 16 * q);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int n = (v[i >> 2] >> (8 * (i & 3))) & 255;
-        all[i] += n;
-        pre[i] += b < (int)blockIdx.x ? n : 0;
-      }
+      const uint32_t v = src[(int64_t)b * pairs];
+      const int lo = v & 0xFFFF, hi = v >> 16;
+      all0 += lo;
+      all1 += hi;
+      pre0 += b < (int)blockIdx.x ? lo : 0;
+      pre1 += b < (int)blockIdx.x ? hi : 0;
     }
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (16 * q + i < E && all[i]) {
-        atomicAdd(&tot[16 * q + i], all[i]);
-        if (pre[i]) atomicAdd(&before[16 * q + i], pre[i]);
-      }
+    if (all0) atomicAdd(&tot[2 * q], all0);              // counts past E are 0
+    if (all1) atomicAdd(&tot[2 * q + 1], all1);
+    if (pre0) atomicAdd(&before[2 * q], pre0);
+    if (pre1) atomicAdd(&before[2 * q + 1], pre1);
   }
   __syncthreads();
   if (threadIdx.x < 64) scan_experts(tot, E, threadIdx.x);
   __syncthreads();
   if (blockIdx.x == 0)
     for (int e = threadIdx.x; e <= E; e += RT_THREADS) offsets[e] = tot[e];
-  for (int i = threadIdx.x; i < nt * k; i += RT_THREADS) {
-    const int64_t at = t0 * k + i;
-    const int ex = expert[at], tok = i / k;
-    int row = -1;
-    if (ex >= 0) {
-      row = tot[ex] + before[ex] + __popcll(mask[ex] & ((1ull << tok) - 1));
-      row_token[row] = (int)(t0 + tok);
+  const int64_t first = (int64_t)blockIdx.x * RT_TOK * chunks;
+  for (int ch = 0; ch < chunks; ++ch) {
+    const int64_t t0 = first + (int64_t)ch * RT_TOK;
+    const int nt = (int)std::max<int64_t>(std::min<int64_t>(T - t0, RT_TOK), 0);
+    for (int e = threadIdx.x; e < E; e += RT_THREADS) mask[e] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < nt * k; i += RT_THREADS) {
+      const int ex = expert[t0 * k + i];
+      if (ex >= 0) atomicOr(&mask[ex], 1ull << (i / k));
     }
-    slot[at] = row;
-    if (at >= tot[E]) row_token[at] = -1;
+    __syncthreads();
+    for (int i = threadIdx.x; i < nt * k; i += RT_THREADS) {
+      const int64_t at = t0 * k + i;
+      const int ex = expert[at], tok = i / k;
+      int row = -1;
+      if (ex >= 0) {
+        row = tot[ex] + before[ex] + __popcll(mask[ex] & ((1ull << tok) - 1));
+        row_token[row] = (int)(t0 + tok);
+      }
+      slot[at] = row;
+      if (at >= tot[E]) row_token[at] = -1;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += RT_THREADS) before[e] += __popcll(mask[e]);
   }
 }
 
@@ -222,26 +268,26 @@ __global__ __launch_bounds__(256) void route_empty_kernel(int32_t* offsets, int 
 }
 
 size_t route_workspace_bytes(int64_t T, int64_t E) {
-  const int64_t groups = (T + RT_TOK - 1) / RT_TOK;
-  return groups > 1 ? ((size_t)groups * route_pad(E) + 255) & ~(size_t)255 : 0;
+  return T > RT_TOK ? ((size_t)route_groups(T) * route_pad(E) * 2 + 255) & ~(size_t)255 : 0;
 }
 
 template <int NE>
 static hipError_t run_route(const void* logits, int bf16, int64_t T, int E, int k, int renorm, int32_t* expert,
-                            float* weight, int32_t* offsets, int32_t* row_token, int32_t* slot, uint8_t* counts,
+                            float* weight, int32_t* offsets, int32_t* row_token, int32_t* slot, uint16_t* counts,
                             hipStream_t stream) {
-  const int groups = (int)((T + RT_TOK - 1) / RT_TOK), pad = route_pad(E);
-  if (groups == 1) {
+  const int pad = route_pad(E);
+  if (T <= RT_TOK) {
     hipLaunchKernelGGL((route_choose_kernel<NE, true>), dim3(1), dim3(RT_THREADS), 0, stream, logits, bf16, T, E, k,
-                       renorm, expert, weight, offsets, row_token, slot, counts, pad);
+                       renorm, 1, expert, weight, offsets, row_token, slot, counts, pad);
     return hipGetLastError();
   }
+  const int chunks = route_chunks(T), groups = (int)route_groups(T);
   hipLaunchKernelGGL((route_choose_kernel<NE, false>), dim3(groups), dim3(RT_THREADS), 0, stream, logits, bf16, T, E,
-                     k, renorm, expert, weight, offsets, row_token, slot, counts, pad);
+                     k, renorm, chunks, expert, weight, offsets, row_token, slot, counts, pad);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(route_place_kernel, dim3(groups), dim3(RT_THREADS), 0, stream, expert, T, E, k, counts, pad,
-                     groups, offsets, row_token, slot);
+  hipLaunchKernelGGL(route_place_kernel, dim3(groups), dim3(RT_THREADS), 0, stream, expert, T, E, k, chunks, counts,
+                     pad, groups, offsets, row_token, slot);
   return hipGetLastError();
 }
 
@@ -252,7 +298,7 @@ hipError_t launch_route(const void* logits, int logits_bf16, int64_t T, int64_t 
     hipLaunchKernelGGL(route_empty_kernel, dim3(1), dim3(256), 0, stream, offsets, (int)E);
     return hipGetLastError();
   }
-  uint8_t* counts = static_cast<uint8_t*>(ws);
+  uint16_t* counts = static_cast<uint16_t*>(ws);
   const int n = (int)E;
 #define Q2_ROUTE(NE) \
   return run_route<NE>(logits, logits_bf16, T, n, k, renorm, expert, weight, offsets, row_token, slot, counts, stream)

@@ -76,6 +76,13 @@ def test_route_ties_masks_and_extremes(t, renorm):
     check_route(torch.zeros((t, e)), k, renorm)            # everybody the same experts
 
 
+def test_route_many_tokens():
+    """More tokens than 1024 workgroups of one chunk hold: several chunks each, the last ones partly empty."""
+    v = torch.randint(0, 50, (70001, 6), generator=torch.Generator().manual_seed(2)).float()
+    v[::5] = -np.inf
+    check_route(v, 2, True)
+
+
 def test_route_of_no_tokens():
     got = q2.q2_route(torch.empty((0, 12), device=DEV), 3)
     assert got.offsets.tolist() == [0] * 13 and got.expert.shape == (0, 3) and got.row_token.numel() == 0
