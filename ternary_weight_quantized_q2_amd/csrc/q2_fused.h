@@ -30,6 +30,25 @@ struct FusedArgs {
 
 __host__ __device__ __forceinline__ int64_t fused_n_out(const FusedArgs& a) { return a.gated ? a.N / 2 : a.N; }
 
+// ---- decode --------------------------------------------------------------------
+// q2_bfrag_nat and q4_bfrag_nat of q2_device.h without inline assembly: the
+// compiler spaces a matrix instruction from the vector instruction that writes
+// its operand, but not from one it does not see as such.  (Written with inline
+// assembly, a fragment whose last dword was followed by one scalar instruction
+// and then its matrix instruction came out wrong on every run.)
+typedef uint16_t q2_u16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t shr16(uint32_t v, uint32_t sh) {
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(q2_u16x2, v) >> __builtin_bit_cast(q2_u16x2, sh));
+}
+template <int H>
+__device__ __forceinline__ q2_u32x4 q2_frag(uint32_t w, const NatConsts& k) {
+  const uint32_t u0 = byte_to_halves<2 * H>(w), u1 = byte_to_halves<2 * H + 1>(w);
+  return q2_u32x4{(shr16(u0, k.sh01) & k.mask) | k.one, (shr16(u0, k.sh23) & k.mask) | k.one,
+                  (shr16(u1, k.sh01) & k.mask) | k.one, (shr16(u1, k.sh23) & k.mask) | k.one};
+}
+__device__ __forceinline__ q2_u32x4 q4_frag(uint32_t w, const NatConsts& k) { return q4_bfrag_nat(w, k); }
+
 // ---- epilogue ----------------------------------------------------------------
 // exp and the reciprocal are the hardware's (about one ulp each); both GELU and
 // SiLU are v times a logistic or normal distribution function, so a large |v|
@@ -138,99 +157,79 @@ __device__ __forceinline__ void store_strip(const FusedArgs& a, const float* bia
 }
 
 // ---- row groups ----------------------------------------------------------------
-// The group (expert) and rows of row tile `slot`, counting the tiles of `bm`
-// rows of all groups in order.  Every wave of the workgroup calls it together
-// and gets the same answer: the 64 lanes take 64 groups at a time, count their
-// tiles and add them up.  Offsets are clamped to [0, M] and to not decrease
-// within a group, so whatever they hold, the rows lie inside x and y.
+// Offsets are clamped to [0, M] and to not decrease within a group, so whatever
+// they hold, the rows lie inside x and y.
 struct RowTile {
   int64_t m0, mend;           // rows m0 .. min(m0 + bm, mend) - 1
   int64_t expert;
-  bool valid;
 };
 
 __device__ __forceinline__ int64_t clamp_offset(int32_t v, int64_t lo, int64_t hi) {
   return v < lo ? lo : v > hi ? hi : v;
 }
 
-__device__ __forceinline__ RowTile find_row_tile(const FusedArgs& a, int64_t slot, int bm) {
-  RowTile t;
-  t.expert = 0;
-  t.m0 = slot * bm;
-  t.mend = a.M;
-  t.valid = t.m0 < a.M;
-  if (a.offsets == nullptr) return t;
+// Tiles of bm rows of group e (offsets clamped) for the lane that asks.
+__device__ __forceinline__ int group_tiles(const FusedArgs& a, int64_t e, int bm, int& lo, int& hi) {
+  lo = hi = 0;
+  if (e < a.E) {
+    lo = (int)clamp_offset(a.offsets[e], 0, a.M);
+    hi = (int)clamp_offset(a.offsets[e + 1], lo, a.M);
+  }
+  return (int)(((int64_t)hi - lo + bm - 1) / bm);
+}
+
+// The tile of this workgroup; false when there is none for it (the launch covers
+// the most tiles that the offsets can make).  Each XCD gets a contiguous range
+// of tile numbers.  Without groups they run over blocks of group_m row tiles,
+// row-fastest inside (see tile_group_rows); with groups over the column tiles
+// of a row tile, so an XCD meets few experts and reads their weights once.
+// Every wave of the workgroup calls it together; the results are scalars
+// (readlane), so that buffer resources built on them stay in scalar registers.
+__device__ __forceinline__ bool find_tile(const FusedArgs& a, int bm, int tiles_n, int group_m, RowTile& rt, int& tn) {
+  rt.expert = 0;
+  rt.mend = a.M;
+  if (a.offsets == nullptr) {
+    const int tiles_m = (int)((a.M + bm - 1) / bm);
+    const int tile = xcd_tile((int)blockIdx.x, tiles_m * tiles_n);
+    const int grp = tile / (group_m * tiles_n), gi = tile - grp * group_m * tiles_n;
+    const int gm = min(group_m, tiles_m - grp * group_m);
+    rt.m0 = (int64_t)(grp * group_m + gi % gm) * bm;
+    tn = gi / gm;
+    return true;
+  }
   const int lane = threadIdx.x & 63;
-  int64_t before = 0;                                    // tiles of the groups already passed
-  t.valid = false;
-  for (int64_t e0 = 0; e0 < a.E; e0 += 64) {
-    const int64_t e = e0 + lane;
-    int64_t lo = 0, hi = 0;
-    if (e < a.E) {
-      lo = clamp_offset(a.offsets[e], 0, a.M);
-      hi = clamp_offset(a.offsets[e + 1], lo, a.M);
-    }
-    const int mine = (int)((hi - lo + bm - 1) / bm);
+  int lo, hi, mine = group_tiles(a, lane, bm, lo, hi), total = mine;
+  for (int64_t e = lane + 64; e - lane < a.E; e += 64) {
+    int l, h;
+    total += group_tiles(a, e, bm, l, h);
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) total += __shfl_xor(total, d);
+  total = __builtin_amdgcn_readfirstlane(total);
+  // bad offsets can count more tiles than the launch covers
+  const int tiles = (int)min((int64_t)total * tiles_n, (int64_t)gridDim.x);
+  if ((int)blockIdx.x >= tiles) return false;
+  const int tile = xcd_tile((int)blockIdx.x, tiles);
+  int slot = tile / tiles_n;
+  tn = tile - slot * tiles_n;
+  for (int64_t e0 = 0;; e0 += 64) {                      // slot < total: ends at its group
+    if (e0 > 0) mine = group_tiles(a, e0 + lane, bm, lo, hi);
     int sum = mine;                                      // inclusive sum over the lanes
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int v = __shfl_up(sum, d);
       if (lane >= d) sum += v;
     }
-    const int total = __builtin_amdgcn_readlane(sum, 63);
-    const uint64_t past = __builtin_amdgcn_ballot_w64(before + sum > slot);
+    const uint64_t past = __builtin_amdgcn_ballot_w64(sum > slot);
     if (past != 0) {
       const int l = __builtin_ctzll(past);
-      const int64_t first = before + __builtin_amdgcn_readlane(sum - mine, l);
-      // readlane: scalars, so that buffer resources built on them stay in scalar registers
-      t.m0 = __builtin_amdgcn_readlane((int)lo, l) + (slot - first) * bm;
-      t.mend = __builtin_amdgcn_readlane((int)hi, l);
-      t.expert = e0 + l;
-      t.valid = true;
-      return t;
+      rt.m0 = __builtin_amdgcn_readlane(lo, l) + (int64_t)(slot - __builtin_amdgcn_readlane(sum - mine, l)) * bm;
+      rt.mend = __builtin_amdgcn_readlane(hi, l);
+      rt.expert = e0 + l;
+      return true;
     }
-    before += total;
+    slot -= __builtin_amdgcn_readlane(sum, 63);
   }
-  return t;
-}
-
-// Row tiles of bm rows over all groups; every wave calls it together.
-__device__ __forceinline__ int64_t count_row_tiles(const FusedArgs& a, int bm) {
-  if (a.offsets == nullptr) return (a.M + bm - 1) / bm;
-  const int lane = threadIdx.x & 63;
-  int mine = 0;                                          // at most R + E tiles: fits 32 bits
-  for (int64_t e = lane; e < a.E; e += 64) {
-    const int64_t lo = clamp_offset(a.offsets[e], 0, a.M), hi = clamp_offset(a.offsets[e + 1], lo, a.M);
-    mine += (int)((hi - lo + bm - 1) / bm);
-  }
-#pragma unroll
-  for (int d = 32; d; d >>= 1) mine += __shfl_xor(mine, d);
-  return __builtin_amdgcn_readfirstlane(mine);
-}
-
-// Tile of this workgroup: row tile `slot`, column tile tn; false when there is
-// none for it (the launch covers the most tiles that the offsets can make).
-// Each XCD gets a contiguous range of tile numbers.  Without groups they run
-// over blocks of group_m row tiles, row-fastest inside (see tile_group_rows);
-// with groups over the column tiles of a row tile, so an XCD meets few experts
-// and reads their weights once.
-__device__ __forceinline__ bool tile_of_block(const FusedArgs& a, int bm, int tiles_n, int group_m, int64_t& slot,
-                                              int& tn) {
-  const int tiles_m = (int)count_row_tiles(a, bm);
-  // bad offsets can count more tiles than the launch covers
-  const int tiles = (int)min((int64_t)tiles_m * tiles_n, (int64_t)gridDim.x);
-  if ((int)blockIdx.x >= tiles) return false;
-  const int tile = xcd_tile((int)blockIdx.x, tiles);
-  if (a.offsets) {
-    slot = tile / tiles_n;
-    tn = tile - (int)slot * tiles_n;
-  } else {
-    const int grp = tile / (group_m * tiles_n), gi = tile - grp * group_m * tiles_n;
-    const int gm = min(group_m, tiles_m - grp * group_m);
-    slot = grp * group_m + gi % gm;
-    tn = gi / gm;
-  }
-  return true;
 }
 
 // At most this many row tiles of bm rows over all groups: each of the at most
@@ -264,6 +263,7 @@ size_t fused_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t E, int fmt
 // fmt 0 = Q2_0, 1 = 4-bit.  ws: that many bytes.
 hipError_t launch_fused(const FusedArgs& a, int fmt, void* ws, hipStream_t stream);
 
+hipError_t launch_fused_few(const FusedArgs& a, int fmt, hipStream_t stream);
 size_t f16_workspace_bytes(int64_t M, int64_t K);
 hipError_t launch_fused_f16(const FusedArgs& a, void* ws, hipStream_t stream);
 

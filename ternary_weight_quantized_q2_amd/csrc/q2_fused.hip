@@ -37,10 +37,9 @@ __global__ __launch_bounds__(256) void fused_tile_kernel(FusedArgs a, int tiles_
   __shared__ float out[F_BM][F_BN + 4];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int c = lane & 15, g = lane >> 4;
-  const int64_t slot = blockIdx.x / tiles_n;
-  const int tn = (int)(blockIdx.x - slot * tiles_n);
-  const RowTile rt = find_row_tile(a, slot, F_BM);
-  if (!rt.valid) return;
+  RowTile rt;
+  int tn;
+  if (!find_tile(a, F_BM, tiles_n, 1, rt, tn)) return;
   const int64_t n_out = fused_n_out(a);
   const int out_cols = a.gated ? F_BN / 2 : F_BN;
   const int64_t n0 = (int64_t)tn * out_cols;
@@ -72,14 +71,14 @@ __global__ __launch_bounds__(256) void fused_tile_kernel(FusedArgs a, int tiles_
     float zc = 0.f;
     uint64_t pz;
     if constexpr (FMT == 0) {
-      bf[0] = q2_bfrag_nat<0>(w[0], kc);
-      bf[1] = q2_bfrag_nat<1>(w[0], kc);
-      bf[2] = q2_bfrag_nat<0>(w[1], kc);
-      bf[3] = q2_bfrag_nat<1>(w[1], kc);
+      bf[0] = q2_frag<0>(w[0], kc);
+      bf[1] = q2_frag<1>(w[0], kc);
+      bf[2] = q2_frag<0>(w[1], kc);
+      bf[3] = q2_frag<1>(w[1], kc);
       pz = q2_part_zero(w);
     } else {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) bf[t] = q4_bfrag_nat(w[t], kc);
+      for (int t = 0; t < 4; ++t) bf[t] = q4_frag(w[t], kc);
       zc = f16_to_f32(zp[b]);
       pz = q4_part_zero(w, zc);
     }
@@ -135,6 +134,7 @@ size_t fused_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t E, int fmt
 
 hipError_t launch_fused(const FusedArgs& a, int fmt, void* ws, hipStream_t stream) {
   if (use_f16(a.M, a.N, a.K, a.offsets ? a.E : 0, fmt)) return launch_fused_f16(a, ws, stream);
+  if (a.M <= 16 || (a.offsets && a.M <= 8 * a.E)) return launch_fused_few(a, fmt, stream);
   const int64_t cols = a.gated ? F_BN / 2 : F_BN;
   const int64_t tiles_n = (fused_n_out(a) + cols - 1) / cols;
   const int64_t slots = max_row_tiles(a, F_BM);

@@ -151,10 +151,9 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 31, h = lane >> 5;
 
-  int64_t slot;
+  RowTile rt;
   int tn;
-  if (!tile_of_block(a, FX_BM, tiles_n, group_m, slot, tn)) return;
-  const RowTile rt = find_row_tile(a, slot, FX_BM);
+  if (!find_tile(a, FX_BM, tiles_n, group_m, rt, tn)) return;
   const int64_t m0 = rt.m0, n_out = fused_n_out(a), K = a.K;
   const int KB = (int)(K / BLOCK_K), NH = 2 * KB;
   // Columns of the wave's two 32-column tiles: neighbours, or with a gated

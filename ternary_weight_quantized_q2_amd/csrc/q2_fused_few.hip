@@ -1,0 +1,244 @@
+// q2_fused_few.hip - the fused and grouped linears for up to 16 rows per tile:
+// single tokens, decode batches, experts with a few rows each.
+//
+// What counts here is the read of the packed weights and the latency of one
+// pass: every wave has all loads of its blocks in flight before it computes on
+// any of them, in pieces of at least 64 bytes of a weight row.
+#include "q2_fused.h"
+#include <algorithm>
+
+namespace q2dev {
+
+// The half-words b, b + 1, ... of a row of n (four of them from element
+// min(b, n - 4) on): one 8-byte load, or, for rows of less than four (SHORT),
+// single ones.  A run-time branch between the two would make every later load
+// wait for this one.
+template <bool SHORT>
+__device__ __forceinline__ uint64_t load4h(const uint16_t* p, int b, int n) {
+  uint64_t v;
+  if constexpr (SHORT) {
+    v = p[0] | (uint32_t)p[min(1, n - 1)] << 16 | (uint64_t)p[min(2, n - 1)] << 32;
+  } else {
+    __builtin_memcpy(&v, p + min(b, n - 4), 8);
+  }
+  return v;
+}
+
+constexpr int FEW_COLS = 32;                             // weight columns of a workgroup, two 16-column tiles
+constexpr int FEW_WAVES = 16;                            // at most
+
+// LDS bytes of one row of x over `blocks` blocks, copied 1 KB at a time: 16 bytes
+// of padding put the 16 rows that a fragment read touches into different banks.
+__host__ __device__ constexpr int few_row_bytes(int blocks) { return (blocks + 3) / 4 * 1024 + 16; }
+
+// A workgroup of kg waves owns up to 16 rows x 32 weight columns (with a gated
+// epilogue the second tile holds the other factors of the first one's
+// outputs).  In each pass wave w takes D consecutive 128-wide blocks.  In the
+// matrix-core layout lane (c, g) = (lane % 16, lane / 16) holds inputs 32 g ..
+// 32 g + 31 of weight column c and of row c.  A 4-bit block's 64 bytes per
+// column are loaded that way; of 2-bit codes a lane loads 16 of the 64 bytes
+// that two blocks have per column, and two lane-row swaps bring both blocks
+// into the layout (8 bytes per lane and block would touch 32-byte pieces).  The
+// rows of x are staged in LDS, only those that exist.
+template <int FMT, int D, bool SHORT>
+__global__ __launch_bounds__(64 * FEW_WAVES) void fused_few_kernel(FusedArgs a, int tiles_n) {
+  constexpr int DW = (FMT == 0) ? 2 : 4;
+  extern __shared__ __align__(16) uint8_t xs[];
+  const int lane = threadIdx.x & 63, kg = blockDim.x >> 6;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  RowTile rt;
+  int tn;
+  if (!find_tile(a, 16, tiles_n, 1, rt, tn)) return;
+  const int64_t n_out = fused_n_out(a), K = a.K;
+  const int out_cols = a.gated ? FEW_COLS / 2 : FEW_COLS;
+  const int64_t n0 = (int64_t)tn * out_cols;
+  const int KB = (int)(K / BLOCK_K);
+  const int rows = (int)std::min<int64_t>(rt.mend - rt.m0, 16);
+  const int64_t row_bytes = (FMT == 0) ? K / 4 : K / 2;
+  const NatConsts kc = (FMT == 0) ? q2_nat_consts() : q4_nat_consts();
+
+  const uint8_t* wp[2];
+  const uint16_t *sp[2], *zp[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    int64_t n = n0 + c + (a.gated ? 0 : 16 * j);
+    n = n < n_out ? n : n_out - 1;
+    if (a.gated && j) n += n_out;
+    const int64_t row = rt.expert * a.N + n;
+    wp[j] = a.w + row * row_bytes;
+    sp[j] = a.s + row * KB;
+    zp[j] = (FMT == 1) ? a.z + row * KB : nullptr;
+  }
+
+  // Lane i: the row of x that tile row i reads, -1 for an index outside x.
+  int xsrc = -1;
+  if (lane < rows) {
+    const int64_t src = a.row_index ? (int64_t)a.row_index[rt.m0 + lane] : rt.m0 + lane;
+    xsrc = src >= 0 && src < a.x_rows ? (int)src : -1;
+  }
+
+  const int span = kg * D;                               // blocks of a pass
+  const int rstride = few_row_bytes(span);
+  const uint8_t* const xrow = xs + min(c, rows - 1) * rstride + 64 * g;   // rows past the last one repeat it
+  const uint32_t sone = (FMT == 0) ? 0xBFA0BFA0u : 0xBF80BF80u;           // bf16 -1.25 / -1 pairs
+  const q2_u32x4 sones = q2_u32x4{sone, sone, sone, sone};
+  q2_f32x4 acc[2] = {q2_f32x4{0.f, 0.f, 0.f, 0.f}, q2_f32x4{0.f, 0.f, 0.f, 0.f}};
+
+  for (int p0 = 0; p0 < KB; p0 += span) {
+    const int bb = p0 + wv * D;                          // this wave's first block
+    uint32_t w[2][D][DW];
+    uint64_t s[2], z[2];
+    if (bb < KB) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if constexpr (FMT == 0) {
+#pragma unroll
+          for (int p = 0; p < D / 2; ++p) {
+            const int b = min(bb + 2 * p + (g >> 1), KB - 1);             // past the end: a valid block, dropped below
+            const q2_u32x4 v = *reinterpret_cast<const q2_u32x4*>(wp[j] + (int64_t)b * 32 + 16 * (g & 1));
+            w[j][2 * p][0] = v[0]; w[j][2 * p][1] = v[1];
+            w[j][2 * p + 1][0] = v[2]; w[j][2 * p + 1][1] = v[3];
+          }
+        } else {
+#pragma unroll
+          for (int d = 0; d < D; ++d) {
+            const int b = min(bb + d, KB - 1);
+            const q2_u32x4 v = *reinterpret_cast<const q2_u32x4*>(wp[j] + (int64_t)b * 64 + 16 * g);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[j][d][q] = v[q];
+          }
+        }
+        s[j] = load4h<SHORT>(sp[j], bb, KB);
+        z[j] = (FMT == 1) ? load4h<SHORT>(zp[j], bb, KB) : 0;
+      }
+    }
+    if (p0 > 0) __syncthreads();                         // the last pass's rows are read
+    const int nb = min(span, KB - p0), pieces = (nb + 3) / 4;
+    for (int i = wv; i < rows * pieces; i += kg) {
+      const int row = i / pieces, q = i - row * pieces;
+      const int src = __builtin_amdgcn_readlane(xsrc, row);
+      uint8_t* const dst = xs + row * rstride + q * 1024;
+      if (src >= 0) {                                    // past the pass: its last chunk again
+        const uint16_t* p = a.x + (int64_t)src * K + (int64_t)p0 * BLOCK_K + 8 * min(64 * q + lane, 16 * nb - 1);
+        __builtin_amdgcn_global_load_lds(p, (lds_void*)dst, 16, 0, 0);
+      } else {
+        *reinterpret_cast<q2_u32x4*>(dst + 16 * lane) = q2_u32x4{0u, 0u, 0u, 0u};
+      }
+    }
+    stage_barrier<0>();                                  // all copies have landed
+    if (bb < KB) {
+      const int sh0 = SHORT ? bb : bb - min(bb, KB - 4);
+      if constexpr (FMT == 0) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int p = 0; p < D / 2; ++p)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              auto r = __builtin_amdgcn_permlane16_swap(w[j][2 * p][q], w[j][2 * p + 1][q], false, false);
+              r = __builtin_amdgcn_permlane32_swap(r[0], r[1], false, false);
+              w[j][2 * p][q] = r[0];
+              w[j][2 * p + 1][q] = r[1];
+            }
+      }
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        if (bb + d < KB) {
+          q2_u32x4 av[4];
+          q2_f32x4 sum = q2_f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            av[t] = *reinterpret_cast<const q2_u32x4*>(xrow + (wv * D + d) * 256 + 16 * t);
+            sum = mfma(av[t], sones, sum);
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            q2_u32x4 bf[4];
+            float zc = 0.f;
+            uint64_t pz;
+            if constexpr (FMT == 0) {
+              bf[0] = q2_frag<0>(w[j][d][0], kc);
+              bf[1] = q2_frag<1>(w[j][d][0], kc);
+              bf[2] = q2_frag<0>(w[j][d][1], kc);
+              bf[3] = q2_frag<1>(w[j][d][1], kc);
+              pz = q2_part_zero(w[j][d]);
+            } else {
+#pragma unroll
+              for (int t = 0; t < 4; ++t) bf[t] = q4_frag(w[j][d][t], kc);
+              zc = f16_to_f32((uint16_t)(z[j] >> (16 * (sh0 + d))));
+              pz = q4_part_zero(w[j][d], zc);
+            }
+            const uint32_t sb = (uint32_t)(s[j] >> (16 * (sh0 + d))) & 0xFFFFu;
+            const float dc = f16_to_f32((uint16_t)zero_where(sb, column_all(pz)));
+            const float k4 = 1.f + zc * 0.0625f;
+            q2_f32x4 tmp = (FMT == 0) ? sum : q2_f32x4{k4 * sum[0], k4 * sum[1], k4 * sum[2], k4 * sum[3]};
+#pragma unroll
+            for (int t = 0; t < 4; ++t) tmp = mfma(av[t], bf[t], tmp);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][e] = __builtin_fmaf(dc, tmp[e], acc[j][e]);
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();                                       // the rows' space takes the partial sums
+  float (*const red)[16][FEW_COLS + 1] = reinterpret_cast<float (*)[16][FEW_COLS + 1]>(xs);
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) red[wv][4 * g + e][16 * j + c] = acc[j][e];
+  __syncthreads();
+
+  const float* bias = a.bias ? a.bias + rt.expert * a.N : nullptr;
+  const float fin = (FMT == 0) ? 4.f : 16.f;
+  const int r8 = (a.r + 7) & ~7;
+  for (int idx = threadIdx.x; idx < rows * out_cols; idx += blockDim.x) {
+    const int row = idx / out_cols, col = idx - row * out_cols;
+    const int64_t m = rt.m0 + row, n = n0 + col;
+    if (n >= n_out) continue;
+    float v = 0.f, u = 0.f;
+    for (int q = 0; q < kg; ++q) v += red[q][row][col];  // wave order
+    if (a.gated)
+      for (int q = 0; q < kg; ++q) u += red[q][row][FEW_COLS / 2 + col];
+    v *= fin;
+    u *= fin;
+    for (int j = 0; j < a.r; ++j) {                      // the rank-r branch, from the limbs of x A^T
+      const float t = bf16_to_f32(a.lr_t[m * 2 * r8 + j]) + bf16_to_f32(a.lr_t[m * 2 * r8 + r8 + j]);
+      v = __builtin_fmaf(t, f16_to_f32(a.lr_b[n * a.r + j]), v);
+      if (a.gated) u = __builtin_fmaf(t, f16_to_f32(a.lr_b[(n + n_out) * a.r + j]), u);
+    }
+    store_out(a, bias, n_out, m, n, v, u);
+  }
+}
+
+template <int FMT, int D, bool SHORT>
+static hipError_t run_few(const FusedArgs& a, int64_t slots, int64_t tiles_n, hipStream_t stream) {
+  const int KB = (int)(a.K / BLOCK_K);
+  // one pass where the waves reach, and at most 64 KB of rows
+  const int rows = (int)std::min<int64_t>(a.M, 16);
+  int kg = std::clamp((KB + D - 1) / D, 1, FEW_WAVES);
+  while (kg > 1 && rows * few_row_bytes(kg * D) > 64 * 1024) --kg;
+  const size_t lds = std::max<size_t>((size_t)rows * few_row_bytes(kg * D), (size_t)kg * 16 * (FEW_COLS + 1) * 4);
+  hipLaunchKernelGGL((fused_few_kernel<FMT, D, SHORT>), dim3((unsigned)(slots * tiles_n)), dim3(64 * kg), lds, stream, a,
+                     (int)tiles_n);
+  return hipGetLastError();
+}
+
+template <int FMT>
+static hipError_t pick_few(const FusedArgs& a, int64_t slots, int64_t tiles_n, hipStream_t stream) {
+  const int64_t KB = a.K / BLOCK_K;
+  if (KB < 4) return run_few<FMT, 2, true>(a, slots, tiles_n, stream);
+  // Four blocks per wave, two while that leaves the chip short of waves.
+  if (slots * tiles_n * KB < 4 * 2048) return run_few<FMT, 2, false>(a, slots, tiles_n, stream);
+  return run_few<FMT, 4, false>(a, slots, tiles_n, stream);
+}
+
+hipError_t launch_fused_few(const FusedArgs& a, int fmt, hipStream_t stream) {
+  const int64_t cols = a.gated ? FEW_COLS / 2 : FEW_COLS;
+  const int64_t tiles_n = (fused_n_out(a) + cols - 1) / cols, slots = max_row_tiles(a, 16);
+  if (tiles_n > 0x7fffffff || slots > 0x7fffffff / tiles_n) return hipErrorInvalidValue;
+  return fmt == 0 ? pick_few<0>(a, slots, tiles_n, stream) : pick_few<1>(a, slots, tiles_n, stream);
+}
+
+}  // namespace q2dev
