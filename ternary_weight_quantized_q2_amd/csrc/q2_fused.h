@@ -189,8 +189,13 @@ __device__ __forceinline__ bool find_tile(const FusedArgs& a, int bm, int tiles_
   rt.expert = 0;
   rt.mend = a.M;
   if (a.offsets == nullptr) {
-    const int tiles_m = (int)((a.M + bm - 1) / bm);
+    const int tiles_m = a.M <= bm ? 1 : (int)((a.M + bm - 1) / bm);
     const int tile = xcd_tile((int)blockIdx.x, tiles_m * tiles_n);
+    if (tiles_m == 1) {
+      rt.m0 = 0;
+      tn = tile;
+      return true;
+    }
     const int grp = tile / (group_m * tiles_n), gi = tile - grp * group_m * tiles_n;
     const int gm = min(group_m, tiles_m - grp * group_m);
     rt.m0 = (int64_t)(grp * group_m + gi % gm) * bm;
