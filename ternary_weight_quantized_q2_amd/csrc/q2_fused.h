@@ -49,6 +49,27 @@ __device__ __forceinline__ q2_u32x4 q2_frag(uint32_t w, const NatConsts& k) {
 }
 __device__ __forceinline__ q2_u32x4 q4_frag(uint32_t w, const NatConsts& k) { return q4_bfrag_nat(w, k); }
 
+// ---- the rank-r branch -----------------------------------------------------------
+// Its matrix-core operands: x A^T as limbs [M, 2 r8] (hi | lo), B split exactly
+// into bf16 hi + lo; parts 0, 1, 2 are T_hi B_hi, T_hi B_lo, T_lo B_hi (the
+// dropped T_lo B_lo is 2^-16 of the branch).  Eight elements from q0 on.
+__device__ __forceinline__ q2_u32x4 branch_afrag(const FusedArgs& a, int64_t m, int q0, int part) {
+  const int r8 = (a.r + 7) & ~7;
+  m = m < a.M ? m : a.M - 1;
+  if (q0 >= r8) return q2_u32x4{0u, 0u, 0u, 0u};
+  return *reinterpret_cast<const q2_u32x4*>(a.lr_t + m * 2 * r8 + (part == 2 ? r8 : 0) + q0);
+}
+__device__ __forceinline__ q2_u32x4 branch_bfrag(const FusedArgs& a, int64_t n, int q0, int part) {
+  uint32_t e[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    uint16_t hi = 0, lo = 0;
+    if (q0 + k < a.r) f16_split_bf16(a.lr_b[n * a.r + q0 + k], hi, lo);
+    e[k] = part == 1 ? lo : hi;
+  }
+  return q2_u32x4{e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16), e[6] | (e[7] << 16)};
+}
+
 // ---- epilogue ----------------------------------------------------------------
 // exp and the reciprocal are the hardware's (about one ulp each); both GELU and
 // SiLU are v times a logistic or normal distribution function, so a large |v|
@@ -268,6 +289,8 @@ size_t fused_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t E, int fmt
 // fmt 0 = Q2_0, 1 = 4-bit.  ws: that many bytes.
 hipError_t launch_fused(const FusedArgs& a, int fmt, void* ws, hipStream_t stream);
 
+bool fused_mid_takes(const FusedArgs& a, int fmt);
+hipError_t launch_fused_mid(const FusedArgs& a, int fmt, hipStream_t stream);
 hipError_t launch_fused_few(const FusedArgs& a, int fmt, hipStream_t stream);
 size_t f16_workspace_bytes(int64_t M, int64_t K);
 hipError_t launch_fused_f16(const FusedArgs& a, void* ws, hipStream_t stream);

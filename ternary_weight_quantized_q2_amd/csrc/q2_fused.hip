@@ -135,6 +135,7 @@ size_t fused_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t E, int fmt
 hipError_t launch_fused(const FusedArgs& a, int fmt, void* ws, hipStream_t stream) {
   if (use_f16(a.M, a.N, a.K, a.offsets ? a.E : 0, fmt)) return launch_fused_f16(a, ws, stream);
   if (a.M <= 16 || (a.offsets && a.M <= 8 * a.E)) return launch_fused_few(a, fmt, stream);
+  if (fused_mid_takes(a, fmt)) return launch_fused_mid(a, fmt, stream);
   const int64_t cols = a.gated ? F_BN / 2 : F_BN;
   const int64_t tiles_n = (fused_n_out(a) + cols - 1) / cols;
   const int64_t slots = max_row_tiles(a, F_BM);

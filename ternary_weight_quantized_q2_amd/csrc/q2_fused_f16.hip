@@ -283,34 +283,17 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
     }
 
   if (a.r > 0) {
-    // (x A^T) B^T as T_hi B_hi + T_hi B_lo + T_lo B_hi in bf16.
     const int r8 = (a.r + 7) & ~7;
     for (int part = 0; part < 3; ++part)
       for (int k0 = 0; k0 < r8; k0 += 16) {
-        const int q0 = k0 + 8 * h;
-        q2_u32x4 bq[2], aq[4];
+        q2_u32x4 bq[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          int64_t n = n0 + c + (a.gated ? 0 : 32 * j);
-          n = n < n_out ? n : n_out - 1;
-          if (a.gated && j) n += n_out;
-          uint32_t e[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            uint16_t hi = 0, lo = 0;
-            if (q0 + k < a.r) f16_split_bf16(a.lr_b[n * a.r + q0 + k], hi, lo);
-            e[k] = part == 1 ? lo : hi;
-          }
-          bq[j] = q2_u32x4{e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16), e[6] | (e[7] << 16)};
-        }
+        for (int j = 0; j < 2; ++j) bq[j] = branch_bfrag(a, wcol(32 * j + c), k0 + 8 * h, part);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          int64_t m = m0 + 32 * i + c;
-          m = m < a.M ? m : a.M - 1;
-          aq[i] = q0 < r8 ? *reinterpret_cast<const q2_u32x4*>(a.lr_t + m * 2 * r8 + (part == 2 ? r8 : 0) + q0)
-                          : q2_u32x4{0u, 0u, 0u, 0u};
+          const q2_u32x4 aq = branch_afrag(a, m0 + 32 * i + c, k0 + 8 * h, part);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) acc[i][j] = mfma32_bf16(aq[i], bq[j], acc[i][j]);
+          for (int j = 0; j < 2; ++j) acc[i][j] = mfma32_bf16(aq, bq[j], acc[i][j]);
         }
       }
   }

@@ -1,0 +1,325 @@
+// q2_fused_mid.hip - the fused and grouped linears between a few rows and the
+// f16 kernel's many, and for every row count above 16 of the 4-bit format,
+// whose weights (q - z) s have no exact f16 value.
+//
+// Weights decode to bf16 1 + c / 4 or 1 + q / 16 (q2_device.h); per 128-wide
+// block the row sums of x take the 1 back and one FMA per output applies the
+// block's scale.
+#include "q2_fused.h"
+#include "q2_internal.h"
+#include <algorithm>
+
+namespace q2dev {
+
+// Position of chunk q of row r: q ^ mid_swz(r).  The 16-byte fragment reads of a
+// pass then touch 16 different bank groups (a bit rotation of r mod 16).
+__device__ __forceinline__ int mid_swz(int r) { return ((r >> 2) & 3) | ((r & 3) << 2); }
+
+// A workgroup of KG groups of NW waves owns 16 MT rows x 64 NW weight columns;
+// wave (kg, wn) computes the 64 columns wn from every KG-th unit of blocks (a
+// unit is what one 16-byte load of a lane holds: two 2-bit blocks, one 4-bit
+// block), so a block is decoded once per workgroup.  Rows go to LDS by direct
+// copies, a set of KG blocks per stage, two stages; codes and scales of the next
+// unit to registers while this one is computed.  One barrier per stage waits
+// for both.  Each wave sums its rows on the matrix cores itself (a quarter of
+// its products; sharing the sums would need a second barrier).
+template <int FMT, int MT, int NW, int KG>
+__global__ __launch_bounds__(64 * NW * KG, 2) void fused_mid_kernel(FusedArgs a, int tiles_n, int group_m) {
+  constexpr int NT = 4;                                  // 16-column tiles of a wave
+  constexpr int W = NW * KG, BM = 16 * MT, BN = 64 * NW;
+  constexpr int U = (FMT == 0) ? 2 : 1;                  // blocks per unit
+  constexpr int STAGE = KG * BM * 256;
+  constexpr int STRIDE = BN + 4;                         // floats per row of the output tile
+  constexpr int RG = BM / 4;                             // copies of four rows per block
+  constexpr int RPW = RG / NW;                           // of a wave: its group's block, a share of the rows
+  constexpr int SMEM = 2 * STAGE > 2 * BM * STRIDE * 4 ? 2 * STAGE : 2 * BM * STRIDE * 4;
+  static_assert(RG % NW == 0 && BM % W == 0, "rows divide over the waves");
+  __shared__ __align__(16) uint8_t smem[SMEM];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wv % NW, kg = wv / NW;
+  const int c = lane & 15, g = lane >> 4;
+  RowTile rt;
+  int tn;
+  if (!find_tile(a, BM, tiles_n, group_m, rt, tn)) return;
+  const int64_t n_out = fused_n_out(a), K = a.K, m0 = rt.m0;
+  const int rows = (int)std::min<int64_t>(rt.mend - m0, BM);
+  const int KB = a.x_rows > 0 ? (int)(K / BLOCK_K) : 0;  // no row to read: every product is an empty sum
+  const int64_t row_bytes = (FMT == 0) ? K / 4 : K / 2;
+  const NatConsts kc = (FMT == 0) ? q2_nat_consts() : q4_nat_consts();
+  const int64_t n0 = (int64_t)tn * (a.gated ? BN / 2 : BN);
+  // Weight row of tile column `col`: with a gated epilogue the tile's second
+  // half holds the other factors of the first half's outputs.
+  auto wrow = [&](int col) -> int64_t {
+    const bool up = a.gated && col >= BN / 2;
+    int64_t n = n0 + (up ? col - BN / 2 : col);
+    n = n < n_out ? n : n_out - 1;
+    return up ? n + n_out : n;
+  };
+  // Offsets from the expert's weight fit 32 bits (checked by the launcher).
+  const uint8_t* const wbase = a.w + rt.expert * a.N * row_bytes;
+  const uint16_t* const sbase = a.s + rt.expert * a.N * (K / BLOCK_K);
+  const uint16_t* const zbase = (FMT == 1) ? a.z + rt.expert * a.N * (K / BLOCK_K) : nullptr;
+  uint32_t woff[NT], soff[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int64_t r = wrow(64 * wn + 16 * j + c);
+    woff[j] = (uint32_t)(r * row_bytes);
+    soff[j] = (uint32_t)(r * (K / BLOCK_K) * 2);
+  }
+
+  // Copy r of this wave: rows 4 (RPW wn + r) .. + 3 of its group's block, lane l
+  // row l / 16 of them and position l % 16.
+  const uint16_t* xp[RPW];
+#pragma unroll
+  for (int r = 0; r < RPW; ++r) {
+    const int row = 4 * (RPW * wn + r) + (lane >> 4);
+    const int64_t m = m0 + (row < rows ? row : rows - 1);
+    int64_t src = a.row_index ? (int64_t)a.row_index[m] : m;
+    if (src < 0 || src >= a.x_rows) src = 0;             // read row 0; the result is cleared at the end
+    xp[r] = a.x + src * K + 8 * ((lane & 15) ^ mid_swz(row & 15));
+  }
+  const int units = (KB + U - 1) / U, NS = (units + KG - 1) / KG * U;     // stages
+  auto block_of = [&](int s) { return (KG * (s / U) + kg) * U + s % U; };
+  auto copy_stage = [&](int s) {
+    const int blk = min(block_of(s), KB - 1);            // past the end: the last block again, never used
+#pragma unroll
+    for (int r = 0; r < RPW; ++r) {
+      // through a local: with an array element in the address the host pass drops the kernel's launch stub
+      const uint16_t* p = xp[r] + (int64_t)blk * BLOCK_K;
+      __builtin_amdgcn_global_load_lds(
+          p, (lds_void*)(smem + (s & 1) * STAGE + kg * BM * 256 + (RPW * wn + r) * 1024), 16, 0, 0);
+    }
+  };
+  q2_u32x4 wnext[NT];
+  uint32_t snext[NT], znext[NT];                         // scales (zero points) of the unit's blocks, halves of a dword
+  auto load_unit = [&](int n) {
+    const int b0 = (KG * n + kg) * U;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      if constexpr (FMT == 0) {
+        const int b = min(b0 + (g >> 1), KB - 1);
+        wnext[j] = *reinterpret_cast<const q2_u32x4*>(wbase + (woff[j] + (uint32_t)(b * 32 + 16 * (g & 1))));
+        const uint8_t* sp = reinterpret_cast<const uint8_t*>(sbase) + (soff[j] + 2u * (uint32_t)min(b0, KB - 2));
+        __builtin_memcpy(&snext[j], sp, 4);              // blocks min(b0, KB - 2) and the next
+      } else {
+        const int b = min(b0, KB - 1);
+        wnext[j] = *reinterpret_cast<const q2_u32x4*>(wbase + (woff[j] + (uint32_t)(b * 64 + 16 * g)));
+        snext[j] = *reinterpret_cast<const uint16_t*>(reinterpret_cast<const uint8_t*>(sbase) + (soff[j] + 2u * b));
+        znext[j] = *reinterpret_cast<const uint16_t*>(reinterpret_cast<const uint8_t*>(zbase) + (soff[j] + 2u * b));
+      }
+    }
+  };
+
+  q2_f32x4 acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = q2_f32x4{0.f, 0.f, 0.f, 0.f};
+  int aoff[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) aoff[t] = c * 256 + (((4 * g + t) ^ mid_swz(c)) << 4);
+  const uint32_t sone = (FMT == 0) ? 0xBFA0BFA0u : 0x3F803F80u;   // bf16 -1.25 / 1 pairs
+  const q2_u32x4 sones = q2_u32x4{sone, sone, sone, sone};
+
+  auto compute = [&](const uint8_t* st, const uint32_t (&w)[NT][(FMT == 0) ? 2 : 4], const uint32_t (&sb)[NT],
+                     const uint32_t (&zb)[NT]) {
+    q2_u32x4 av[MT][4];
+    q2_f32x4 sum[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) av[i][t] = *reinterpret_cast<const q2_u32x4*>(st + i * 4096 + aoff[t]);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) sum[i] = q2_f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int i = 0; i < MT; ++i) sum[i] = mfma(av[i][t], sones, sum[i]);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      q2_u32x4 bf[4];
+      float zc = 0.f;
+      uint64_t pz;
+      if constexpr (FMT == 0) {
+        bf[0] = q2_frag<0>(w[j][0], kc);
+        bf[1] = q2_frag<1>(w[j][0], kc);
+        bf[2] = q2_frag<0>(w[j][1], kc);
+        bf[3] = q2_frag<1>(w[j][1], kc);
+        pz = q2_part_zero(w[j]);
+      } else {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) bf[t] = q4_frag(w[j][t], kc);
+        zc = f16_to_f32((uint16_t)zb[j]);
+        pz = q4_part_zero(w[j], zc);
+      }
+      const float dc = f16_to_f32((uint16_t)zero_where(sb[j], column_all(pz)));
+      const float k4 = -dc * (1.f + zc * 0.0625f);
+      q2_f32x4 tmp[MT];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+          tmp[i] = mfma(av[i][t], bf[t], t > 0 ? tmp[i] : FMT == 0 ? sum[i] : q2_f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc[i][j][e] = __builtin_fmaf(dc, tmp[i][e], acc[i][j][e]);
+          if constexpr (FMT == 1) acc[i][j][e] = __builtin_fmaf(k4, sum[i][e], acc[i][j][e]);
+        }
+    }
+  };
+
+  if (KB > 0) {
+    copy_stage(0);
+    load_unit(0);
+  }
+  for (int n = 0; n * U < NS; ++n) {
+    if constexpr (FMT == 0) {
+      // two stages per unit; the swaps bring 64 bytes per column into the matrix layout of two blocks
+      stage_barrier<0>();
+      uint32_t w0[NT][2], w1[NT][2], s0[NT], s1[NT], zb[NT] = {};
+      const int b0 = (KG * n + kg) * U;
+      const int sh = b0 > KB - 2 ? 16 : 0;               // a last odd block sits in the dword's upper half
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          auto r = __builtin_amdgcn_permlane16_swap(wnext[j][q], wnext[j][2 + q], false, false);
+          r = __builtin_amdgcn_permlane32_swap(r[0], r[1], false, false);
+          w0[j][q] = r[0];
+          w1[j][q] = r[1];
+        }
+        s0[j] = (snext[j] >> sh) & 0xFFFFu;
+        s1[j] = snext[j] >> 16;
+      }
+      copy_stage(2 * n + 1);
+      if (b0 < KB) compute(smem + kg * BM * 256, w0, s0, zb);
+      stage_barrier<0>();
+      if (2 * n + 2 < NS) {
+        copy_stage(2 * n + 2);
+        load_unit(n + 1);
+      }
+      if (b0 + 1 < KB) compute(smem + STAGE + kg * BM * 256, w1, s1, zb);
+    } else {
+      stage_barrier<0>();
+      uint32_t w[NT][4], sb[NT], zb[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[j][q] = wnext[j][q];
+        sb[j] = snext[j];
+        zb[j] = znext[j];
+      }
+      if (n + 1 < NS) {
+        copy_stage(n + 1);
+        load_unit(n + 1);
+      }
+      if (block_of(n) < KB) compute(smem + (n & 1) * STAGE + kg * BM * 256, w, sb, zb);
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+
+  // Partial sums of the groups, halving: the upper half's tiles go through LDS
+  // and are added by the lower half, in a fixed order.
+  float* const part = reinterpret_cast<float*>(smem);
+  constexpr int PART = MT * NT * 4 * 64;
+#pragma unroll
+  for (int half = KG / 2; half >= 1; half /= 2) {
+    if (kg >= half && kg < 2 * half) {
+      float* p = part + ((kg - half) * NW + wn) * PART + lane;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[((i * NT + j) * 4 + e) * 64] = acc[i][j][e];
+    }
+    __syncthreads();
+    if (kg < half) {
+      const float* p = part + (kg * NW + wn) * PART + lane;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] += p[((i * NT + j) * 4 + e) * 64];
+    }
+    __syncthreads();
+  }
+  float* const out = part;
+  if (kg == 0) {
+    const float fin = (FMT == 0) ? 4.f : 16.f;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] *= fin;
+    if (FMT == 0 && a.r > 0) {
+      // (x A^T) B^T as T_hi B_hi + T_hi B_lo + T_lo B_hi in bf16
+      const int r8 = (a.r + 7) & ~7;
+      for (int prt = 0; prt < 3; ++prt)
+        for (int k0 = 0; k0 < r8; k0 += 32) {
+          const int q0 = k0 + 8 * g;
+          q2_u32x4 bq[NT];
+#pragma unroll
+          for (int j = 0; j < NT; ++j) bq[j] = branch_bfrag(a, wrow(64 * wn + 16 * j + c), q0, prt);
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            const q2_u32x4 aq = branch_afrag(a, m0 + 16 * i + c, q0, prt);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[i][j] = mfma(aq, bq[j], acc[i][j]);
+          }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[(16 * i + 4 * g + e) * STRIDE + 64 * wn + 16 * j + c] = acc[i][j][e];
+  }
+  __syncthreads();
+  // Each wave stores a share of the rows.
+  constexpr int SR = BM / W;
+  if (a.row_index) {
+    for (int row = wv * SR; row < min((wv + 1) * SR, rows); ++row) {
+      const int64_t src = a.row_index[m0 + row];
+      if (src < 0 || src >= a.x_rows)                    // a row of zeros of x
+        for (int col = lane; col < BN; col += 64) out[row * STRIDE + col] = 0.f;
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  const float* bias = a.bias ? a.bias + rt.expert * a.N : nullptr;
+  store_strip(a, bias, n_out, out + wv * SR * STRIDE, STRIDE, BN / 2, a.gated ? BN / 2 : BN, m0 + wv * SR,
+              min(rows - wv * SR, SR), n0, lane);
+}
+
+template <int FMT, int MT, int NW, int KG>
+static hipError_t run_mid(const FusedArgs& a, hipStream_t stream) {
+  constexpr int BM = 16 * MT, BN = 64 * NW;
+  const int64_t cols = a.gated ? BN / 2 : BN;
+  const int64_t tiles_n = (fused_n_out(a) + cols - 1) / cols, slots = max_row_tiles(a, BM);
+  if (tiles_n > 0x7fffffff || slots > 0x7fffffff / tiles_n) return hipErrorInvalidValue;
+  const int group_m = tile_group_rows(slots, tiles_n, 2.0 * BM * (double)a.K,
+                                      (double)BN * a.K * (FMT == 0 ? 0.265625 : 0.53125), 64);
+  hipLaunchKernelGGL((fused_mid_kernel<FMT, MT, NW, KG>), dim3((unsigned)(slots * tiles_n)), dim3(64 * NW * KG), 0,
+                     stream, a, (int)tiles_n, group_m);
+  return hipGetLastError();
+}
+
+bool fused_mid_takes(const FusedArgs& a, int fmt) {
+  return a.K >= 4 * BLOCK_K && a.N <= ((int64_t)1 << 32) / (fmt == 0 ? a.K / 4 : a.K / 2);
+}
+
+hipError_t launch_fused_mid(const FusedArgs& a, int fmt, hipStream_t stream) {
+  const int64_t per = a.offsets ? (a.M + a.E - 1) / a.E : a.M;
+  if (per <= 32) return fmt == 0 ? run_mid<0, 2, 2, 4>(a, stream) : run_mid<1, 2, 2, 4>(a, stream);
+  return fmt == 0 ? run_mid<0, 4, 2, 2>(a, stream) : run_mid<1, 4, 2, 2>(a, stream);
+}
+
+}  // namespace q2dev
