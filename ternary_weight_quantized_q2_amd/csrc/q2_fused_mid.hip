@@ -23,16 +23,19 @@ __device__ __forceinline__ int mid_swz(int r) { return ((r >> 2) & 3) | ((r & 3)
 // unit to registers while this one is computed.  One barrier per stage waits
 // for both.  Each wave sums its rows on the matrix cores itself (a quarter of
 // its products; sharing the sums would need a second barrier).
-template <int FMT, int MT, int NW, int KG>
-__global__ __launch_bounds__(64 * NW * KG, 2) void fused_mid_kernel(FusedArgs a, int tiles_n, int group_m) {
-  constexpr int NT = 4;                                  // 16-column tiles of a wave
-  constexpr int W = NW * KG, BM = 16 * MT, BN = 64 * NW;
+template <int FMT, int MT, int NT, int NW, int KG, int OCC>
+__global__ __launch_bounds__(64 * NW * KG, OCC) void fused_mid_kernel(FusedArgs a, int tiles_n, int group_m) {
+  constexpr int W = NW * KG, BM = 16 * MT, BN = 16 * NT * NW;
   constexpr int U = (FMT == 0) ? 2 : 1;                  // blocks per unit
   constexpr int STAGE = KG * BM * 256;
   constexpr int STRIDE = BN + 4;                         // floats per row of the output tile
   constexpr int RG = BM / 4;                             // copies of four rows per block
   constexpr int RPW = RG / NW;                           // of a wave: its group's block, a share of the rows
-  constexpr int SMEM = 2 * STAGE > 2 * BM * STRIDE * 4 ? 2 * STAGE : 2 * BM * STRIDE * 4;
+  constexpr int CHUNK = 16;                              // blocks of scales in LDS at a time
+  constexpr int OFF_S = 2 * STAGE;
+  constexpr int PIECES = (BN * (CHUNK / 4) + 64 * W - 1) / (64 * W);      // 8-byte loads per thread and chunk
+  constexpr int SMEM = OFF_S + 2 * CHUNK * BN * 4;
+  static_assert(BM * STRIDE * 4 <= OFF_S && (KG / 2) * NW * MT * NT * 1024 <= OFF_S, "output tile and partial sums");
   static_assert(RG % NW == 0 && BM % W == 0, "rows divide over the waves");
   __shared__ __align__(16) uint8_t smem[SMEM];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -60,13 +63,40 @@ __global__ __launch_bounds__(64 * NW * KG, 2) void fused_mid_kernel(FusedArgs a,
   const uint8_t* const wbase = a.w + rt.expert * a.N * row_bytes;
   const uint16_t* const sbase = a.s + rt.expert * a.N * (K / BLOCK_K);
   const uint16_t* const zbase = (FMT == 1) ? a.z + rt.expert * a.N * (K / BLOCK_K) : nullptr;
-  uint32_t woff[NT], soff[NT];
+  uint32_t woff[NT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int64_t r = wrow(64 * wn + 16 * j + c);
-    woff[j] = (uint32_t)(r * row_bytes);
-    soff[j] = (uint32_t)(r * (K / BLOCK_K) * 2);
-  }
+  for (int j = 0; j < NT; ++j) woff[j] = (uint32_t)(wrow(16 * (NT * wn + j) + c) * row_bytes);
+  // Scales (low half) and zero points (high half) of CHUNK blocks and the tile's
+  // columns sit in LDS as [block][column], two chunks in turn: a half-word per
+  // lane, column and block straight from global memory cost up to a sixth of the
+  // kernel.  A thread loads 8 bytes, four blocks of one row, PIECES times; blocks
+  // past the end load the last four again.
+  uint32_t* const sz = reinterpret_cast<uint32_t*>(smem + OFF_S);
+  uint64_t sreg[PIECES], zreg[PIECES];
+  auto piece_start = [&](int chunk, int idx) { return min(CHUNK * chunk + 4 * (idx % (CHUNK / 4)), KB - 4); };
+  auto load_scales = [&](int chunk) {
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) {
+      const int idx = min(tid + p * 64 * W, BN * (CHUNK / 4) - 1);
+      const uint32_t off = (uint32_t)(wrow(idx / (CHUNK / 4)) * KB + piece_start(chunk, idx));
+      __builtin_memcpy(&sreg[p], sbase + off, 8);
+      if constexpr (FMT == 1) __builtin_memcpy(&zreg[p], zbase + off, 8);
+    }
+  };
+  auto store_scales = [&](int chunk) {
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) {
+      const int idx = min(tid + p * 64 * W, BN * (CHUNK / 4) - 1);
+      const int slot = piece_start(chunk, idx) - CHUNK * chunk;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t v = (uint32_t)(sreg[p] >> (16 * e)) & 0xFFFFu;
+        const uint32_t u = FMT == 1 ? (uint32_t)(zreg[p] >> (16 * e)) << 16 : 0u;
+        if (slot + e >= 0) sz[((chunk & 1) * CHUNK + slot + e) * BN + idx / (CHUNK / 4)] = v | u;
+      }
+    }
+  };
+  const uint32_t* const szl = sz + 16 * NT * wn + c;     // this lane's column of tile j at + 16 j
 
   // Copy r of this wave: rows 4 (RPW wn + r) .. + 3 of its group's block, lane l
   // row l / 16 of them and position l % 16.
@@ -92,7 +122,6 @@ __global__ __launch_bounds__(64 * NW * KG, 2) void fused_mid_kernel(FusedArgs a,
     }
   };
   q2_u32x4 wnext[NT];
-  uint32_t snext[NT], znext[NT];                         // scales (zero points) of the unit's blocks, halves of a dword
   auto load_unit = [&](int n) {
     const int b0 = (KG * n + kg) * U;
 #pragma unroll
@@ -100,13 +129,9 @@ __global__ __launch_bounds__(64 * NW * KG, 2) void fused_mid_kernel(FusedArgs a,
       if constexpr (FMT == 0) {
         const int b = min(b0 + (g >> 1), KB - 1);
         wnext[j] = *reinterpret_cast<const q2_u32x4*>(wbase + (woff[j] + (uint32_t)(b * 32 + 16 * (g & 1))));
-        const uint8_t* sp = reinterpret_cast<const uint8_t*>(sbase) + (soff[j] + 2u * (uint32_t)min(b0, KB - 2));
-        __builtin_memcpy(&snext[j], sp, 4);              // blocks min(b0, KB - 2) and the next
       } else {
         const int b = min(b0, KB - 1);
         wnext[j] = *reinterpret_cast<const q2_u32x4*>(wbase + (woff[j] + (uint32_t)(b * 64 + 16 * g)));
-        snext[j] = *reinterpret_cast<const uint16_t*>(reinterpret_cast<const uint8_t*>(sbase) + (soff[j] + 2u * b));
-        znext[j] = *reinterpret_cast<const uint16_t*>(reinterpret_cast<const uint8_t*>(zbase) + (soff[j] + 2u * b));
       }
     }
   };
@@ -122,8 +147,8 @@ __global__ __launch_bounds__(64 * NW * KG, 2) void fused_mid_kernel(FusedArgs a,
   const uint32_t sone = (FMT == 0) ? 0xBFA0BFA0u : 0x3F803F80u;   // bf16 -1.25 / 1 pairs
   const q2_u32x4 sones = q2_u32x4{sone, sone, sone, sone};
 
-  auto compute = [&](const uint8_t* st, const uint32_t (&w)[NT][(FMT == 0) ? 2 : 4], const uint32_t (&sb)[NT],
-                     const uint32_t (&zb)[NT]) {
+  auto compute = [&](const uint8_t* st, const uint32_t (&w)[NT][(FMT == 0) ? 2 : 4], int blk) {
+    const uint32_t* const sp = szl + (blk & (2 * CHUNK - 1)) * BN;
     q2_u32x4 av[MT][4];
     q2_f32x4 sum[MT];
 #pragma unroll
@@ -139,6 +164,7 @@ __global__ __launch_bounds__(64 * NW * KG, 2) void fused_mid_kernel(FusedArgs a,
       for (int i = 0; i < MT; ++i) sum[i] = mfma(av[i][t], sones, sum[i]);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
+      const uint32_t sv = sp[16 * j];                    // scale | zero point << 16
       q2_u32x4 bf[4];
       float zc = 0.f;
       uint64_t pz;
@@ -151,10 +177,10 @@ __global__ __launch_bounds__(64 * NW * KG, 2) void fused_mid_kernel(FusedArgs a,
       } else {
 #pragma unroll
         for (int t = 0; t < 4; ++t) bf[t] = q4_frag(w[j][t], kc);
-        zc = f16_to_f32((uint16_t)zb[j]);
+        zc = f16_to_f32((uint16_t)(sv >> 16));
         pz = q4_part_zero(w[j], zc);
       }
-      const float dc = f16_to_f32((uint16_t)zero_where(sb[j], column_all(pz)));
+      const float dc = f16_to_f32((uint16_t)zero_where(sv & 0xFFFFu, column_all(pz)));
       const float k4 = -dc * (1.f + zc * 0.0625f);
       q2_f32x4 tmp[MT];
 #pragma unroll
@@ -172,19 +198,32 @@ __global__ __launch_bounds__(64 * NW * KG, 2) void fused_mid_kernel(FusedArgs a,
     }
   };
 
+  // A chunk's scales are loaded two stages before its first block and written
+  // one stage before, so a stage's barrier lies between the writes and the reads.
+  constexpr int PER = CHUNK / (KG * U) * U;              // stages per chunk
+  static_assert(PER >= 2 && CHUNK % (KG * U) == 0, "scale chunks");
+  auto stage_scales = [&](int s) {                       // after stage s's barrier
+    const int in = s % PER, next = s / PER + 1;
+    if (CHUNK * next < KB) {
+      if (in == PER - 2) load_scales(next);
+      if (in == PER - 1) store_scales(next);
+    }
+  };
   if (KB > 0) {
+    load_scales(0);
     copy_stage(0);
     load_unit(0);
+    store_scales(0);
   }
   for (int n = 0; n * U < NS; ++n) {
     if constexpr (FMT == 0) {
       // two stages per unit; the swaps bring 64 bytes per column into the matrix layout of two blocks
       stage_barrier<0>();
-      uint32_t w0[NT][2], w1[NT][2], s0[NT], s1[NT], zb[NT] = {};
+      stage_scales(2 * n);
+      uint32_t w0[NT][2], w1[NT][2];
       const int b0 = (KG * n + kg) * U;
-      const int sh = b0 > KB - 2 ? 16 : 0;               // a last odd block sits in the dword's upper half
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           auto r = __builtin_amdgcn_permlane16_swap(wnext[j][q], wnext[j][2 + q], false, false);
@@ -192,32 +231,28 @@ __global__ __launch_bounds__(64 * NW * KG, 2) void fused_mid_kernel(FusedArgs a,
           w0[j][q] = r[0];
           w1[j][q] = r[1];
         }
-        s0[j] = (snext[j] >> sh) & 0xFFFFu;
-        s1[j] = snext[j] >> 16;
-      }
       copy_stage(2 * n + 1);
-      if (b0 < KB) compute(smem + kg * BM * 256, w0, s0, zb);
+      if (b0 < KB) compute(smem + kg * BM * 256, w0, b0);
       stage_barrier<0>();
+      stage_scales(2 * n + 1);
       if (2 * n + 2 < NS) {
         copy_stage(2 * n + 2);
         load_unit(n + 1);
       }
-      if (b0 + 1 < KB) compute(smem + STAGE + kg * BM * 256, w1, s1, zb);
+      if (b0 + 1 < KB) compute(smem + STAGE + kg * BM * 256, w1, b0 + 1);
     } else {
       stage_barrier<0>();
-      uint32_t w[NT][4], sb[NT], zb[NT];
+      stage_scales(n);
+      uint32_t w[NT][4];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q) w[j][q] = wnext[j][q];
-        sb[j] = snext[j];
-        zb[j] = znext[j];
-      }
       if (n + 1 < NS) {
         copy_stage(n + 1);
         load_unit(n + 1);
       }
-      if (block_of(n) < KB) compute(smem + (n & 1) * STAGE + kg * BM * 256, w, sb, zb);
+      if (block_of(n) < KB) compute(smem + (n & 1) * STAGE + kg * BM * 256, w, block_of(n));
     }
   }
   __builtin_amdgcn_s_waitcnt(0);
@@ -267,7 +302,7 @@ __global__ __launch_bounds__(64 * NW * KG, 2) void fused_mid_kernel(FusedArgs a,
           const int q0 = k0 + 8 * g;
           q2_u32x4 bq[NT];
 #pragma unroll
-          for (int j = 0; j < NT; ++j) bq[j] = branch_bfrag(a, wrow(64 * wn + 16 * j + c), q0, prt);
+          for (int j = 0; j < NT; ++j) bq[j] = branch_bfrag(a, wrow(16 * (NT * wn + j) + c), q0, prt);
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
             const q2_u32x4 aq = branch_afrag(a, m0 + 16 * i + c, q0, prt);
@@ -281,7 +316,7 @@ __global__ __launch_bounds__(64 * NW * KG, 2) void fused_mid_kernel(FusedArgs a,
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) out[(16 * i + 4 * g + e) * STRIDE + 64 * wn + 16 * j + c] = acc[i][j][e];
+        for (int e = 0; e < 4; ++e) out[(16 * i + 4 * g + e) * STRIDE + 16 * (NT * wn + j) + c] = acc[i][j][e];
   }
   __syncthreads();
   // Each wave stores a share of the rows.
@@ -299,15 +334,15 @@ __global__ __launch_bounds__(64 * NW * KG, 2) void fused_mid_kernel(FusedArgs a,
               min(rows - wv * SR, SR), n0, lane);
 }
 
-template <int FMT, int MT, int NW, int KG>
+template <int FMT, int MT, int NT, int NW, int KG, int OCC>
 static hipError_t run_mid(const FusedArgs& a, hipStream_t stream) {
-  constexpr int BM = 16 * MT, BN = 64 * NW;
+  constexpr int BM = 16 * MT, BN = 16 * NT * NW;
   const int64_t cols = a.gated ? BN / 2 : BN;
   const int64_t tiles_n = (fused_n_out(a) + cols - 1) / cols, slots = max_row_tiles(a, BM);
   if (tiles_n > 0x7fffffff || slots > 0x7fffffff / tiles_n) return hipErrorInvalidValue;
   const int group_m = tile_group_rows(slots, tiles_n, 2.0 * BM * (double)a.K,
                                       (double)BN * a.K * (FMT == 0 ? 0.265625 : 0.53125), 64);
-  hipLaunchKernelGGL((fused_mid_kernel<FMT, MT, NW, KG>), dim3((unsigned)(slots * tiles_n)), dim3(64 * NW * KG), 0,
+  hipLaunchKernelGGL((fused_mid_kernel<FMT, MT, NT, NW, KG, OCC>), dim3((unsigned)(slots * tiles_n)), dim3(64 * NW * KG), 0,
                      stream, a, (int)tiles_n, group_m);
   return hipGetLastError();
 }
@@ -318,8 +353,14 @@ bool fused_mid_takes(const FusedArgs& a, int fmt) {
 
 hipError_t launch_fused_mid(const FusedArgs& a, int fmt, hipStream_t stream) {
   const int64_t per = a.offsets ? (a.M + a.E - 1) / a.E : a.M;
-  if (per <= 32) return fmt == 0 ? run_mid<0, 2, 2, 4>(a, stream) : run_mid<1, 2, 2, 4>(a, stream);
-  return fmt == 0 ? run_mid<0, 4, 2, 2>(a, stream) : run_mid<1, 4, 2, 2>(a, stream);
+  const int64_t tiles = max_row_tiles(a, 32) * ((a.N + 127) / 128);
+  // Few tiles: narrow ones with K over eight groups, so that the chip is covered
+  // (128 rows, K = 9728, N = 2560 4-bit: 30 us against 58 for 32 x 128 tiles).
+  // Otherwise 64 rows per tile once a group fills two of them (384 rows, K = 2560,
+  // 2 x 9728 4-bit: 74 us against 87), 32 below (16 .. 64 rows per expert: 70 against 81).
+  if (tiles <= 128) return fmt == 0 ? run_mid<0, 2, 4, 1, 8, 2>(a, stream) : run_mid<1, 2, 4, 1, 8, 2>(a, stream);
+  if (per >= 128) return fmt == 0 ? run_mid<0, 4, 4, 2, 2, 2>(a, stream) : run_mid<1, 4, 4, 2, 2, 2>(a, stream);
+  return fmt == 0 ? run_mid<0, 2, 4, 2, 2, 2>(a, stream) : run_mid<1, 2, 4, 2, 2, 2>(a, stream);
 }
 
 }  // namespace q2dev
