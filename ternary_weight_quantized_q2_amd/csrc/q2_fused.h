@@ -18,7 +18,8 @@ struct FusedArgs {
   const uint16_t* z;          // f16 zero points, 4-bit only
   const int32_t* offsets;     // [E + 1] or nullptr
   int64_t E, M, N, K;         // N counts weight rows
-  const uint16_t* lr_t;       // bf16 limbs [M, 2 r8] of x A^T, r > 0
+  const uint16_t* lr_a;       // f16 [r, K]; r > 0 only without groups
+  uint16_t* lr_t;             // bf16 limbs [M, 2 r8] of x A^T, written by the launch
   const uint16_t* lr_b;       // f16 [N, r]
   int r;
   int act, gated, out_bf16, res_bf16;
@@ -292,7 +293,8 @@ hipError_t launch_fused(const FusedArgs& a, int fmt, void* ws, hipStream_t strea
 bool fused_mid_takes(const FusedArgs& a, int fmt);
 hipError_t launch_fused_mid(const FusedArgs& a, int fmt, hipStream_t stream);
 hipError_t launch_fused_few(const FusedArgs& a, int fmt, hipStream_t stream);
-size_t f16_workspace_bytes(int64_t M, int64_t K);
+size_t f16_workspace_bytes(int64_t rows, int64_t K);
+bool fused_f16_takes(int64_t rows, int64_t N, int64_t K);
 hipError_t launch_fused_f16(const FusedArgs& a, void* ws, hipStream_t stream);
 
 hipError_t launch_route(const void* logits, int logits_bf16, int64_t T, int64_t E, int k, int renorm, int32_t* expert,

@@ -8,6 +8,7 @@
 #include "q2_fused.h"
 #include "q2_internal.h"
 #include <algorithm>
+#include <cmath>
 
 namespace q2dev {
 
@@ -123,9 +124,18 @@ __global__ __launch_bounds__(256) void fused_tile_kernel(FusedArgs a, int tiles_
   }
 }
 
-// The f16 kernel for Q2_0 weights over many rows.
+// The f16 kernel for Q2_0 weights, from the sizes alone (the workspace goes by
+// them too).  Its 128 x 256 tiles must come near the chip's 512 places (two
+// workgroups per CU), and its column count must pay for converting x: K = 4096,
+// N = 12288: 123 us against the mid kernel's 139 at M = 1024 (384 tiles), 114
+// against 112 at M = 768 (288); 8192 rows over 32 experts, K = 2048, 138 us
+// against 172 at N = 2816 (gated), 102 against 97 at K = 1408, N = 2048.
 static bool use_f16(int64_t M, int64_t N, int64_t K, int64_t E, int fmt) {
-  return fmt == 0 && M >= 128 * std::max<int64_t>(E, 1) / 2 && K >= 512 && K <= (1 << 22) && N <= ((int64_t)1 << 33) / K;
+  if (fmt != 0 || !fused_f16_takes(M, N, K)) return false;
+  // groups add half a tile each
+  const double tiles = (M / 128.0 + (E > 0 ? 0.5 * std::min(E, M) : 0.0)) * std::ceil(N / 256.0);
+  const double fill = E > 0 ? (double)M / ((double)M + 64.0 * (double)E) : 1.0;          // rows that are not padding
+  return tiles >= 320.0 && fill >= 0.7 && N >= 2304;
 }
 
 size_t fused_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t E, int fmt) {
@@ -133,12 +143,18 @@ size_t fused_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t E, int fmt
 }
 
 hipError_t launch_fused(const FusedArgs& a, int fmt, void* ws, hipStream_t stream) {
-  if (use_f16(a.M, a.N, a.K, a.offsets ? a.E : 0, fmt)) return launch_fused_f16(a, ws, stream);
+  const int64_t groups = a.offsets ? a.E : 0;
+  const bool f16 = use_f16(a.M, a.N, a.K, groups, fmt) && a.x_rows > 0 && a.x_rows <= a.M;
+  if (a.r > 0 && !(f16 && a.r <= 64)) {                  // else converted and multiplied in one pass over x
+    const hipError_t e = launch_lowrank_t(a.x, a.lr_a, a.lr_t, a.M, a.K, a.r, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (f16) return launch_fused_f16(a, ws, stream);
   if (a.M <= 16 || (a.offsets && a.M <= 8 * a.E)) return launch_fused_few(a, fmt, stream);
   if (fused_mid_takes(a, fmt)) return launch_fused_mid(a, fmt, stream);
+  // Short K (less than four blocks) or a weight beyond 4 GB: the plain kernel.
   const int64_t cols = a.gated ? F_BN / 2 : F_BN;
-  const int64_t tiles_n = (fused_n_out(a) + cols - 1) / cols;
-  const int64_t slots = max_row_tiles(a, F_BM);
+  const int64_t tiles_n = (fused_n_out(a) + cols - 1) / cols, slots = max_row_tiles(a, F_BM);
   if (tiles_n > 0x7fffffff || slots > 0x7fffffff / tiles_n) return hipErrorInvalidValue;
   const dim3 grid((unsigned)(slots * tiles_n));
   if (fmt == 0) hipLaunchKernelGGL((fused_tile_kernel<0>), grid, dim3(256), 0, stream, a, (int)tiles_n);

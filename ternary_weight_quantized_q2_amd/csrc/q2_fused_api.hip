@@ -69,10 +69,9 @@ int fused_entry(int fmt, const uint16_t* x, const uint8_t* w, const uint16_t* s,
   a.x = x; a.x_rows = M; a.w = w; a.s = s; a.z = z;
   a.E = 1; a.M = M; a.N = N; a.K = K;
   if (r > 0) {
-    uint16_t* t = static_cast<uint16_t*>(workspace);
-    if ((st = hip_status(q2dev::launch_lowrank_t(x, A, t, M, K, (int)r, stream), "low-rank x A^T launch"))) return st;
-    a.lr_t = t;
+    a.lr_a = A;
     a.lr_b = B;
+    a.lr_t = static_cast<uint16_t*>(workspace);
     a.r = (int)r;
   }
   set_epilogue(a, e);

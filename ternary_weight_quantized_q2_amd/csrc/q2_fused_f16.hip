@@ -29,63 +29,208 @@ __device__ __forceinline__ q2_f32x16 mfma32_bf16(q2_u32x4 a, q2_u32x4 b, q2_f32x
 }
 
 // ============================================================================
-// x as f16: row i of the output is row src(i) of x times 2^-rexp[i]
+// x as f16: row i of the output is row i of x times 2^-rexp[i]
 // ============================================================================
 // Each group of 16 elements is stored as a transposed 4 x 4 matrix (position
 // 4 j + b holds element 4 b + j), the order in which a dword of sixteen codes
-// decodes.  One wave per row; the row is read twice, the second time from the
-// caches.
+// decodes.
+
+// The largest finite |x| of 16 elements (two 16-byte pieces), as bf16 bits.
+__device__ __forceinline__ uint32_t top_bits(uint32_t top, const q2_u32x4& v) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const uint32_t lo = v[d] & 0x7FFFu, hi = (v[d] >> 16) & 0x7FFFu;
+    top = max(top, lo < 0x7F80u ? lo : 0u);
+    top = max(top, hi < 0x7F80u ? hi : 0u);
+  }
+  return top;
+}
+// The shift that puts it into [2^14, 2^15): floor(log2 |x|) from the bits (a
+// subnormal bf16 is bits * 2^-133); 0 for a row of zeros.
+__device__ __forceinline__ int top_shift(uint32_t top) {
+  const int e = top >= 0x80u ? (int)(top >> 7) - 127 : top ? 31 - __builtin_clz(top) - 133 : 14;
+  return 14 - e;
+}
+// Sixteen elements as f16 pairs in their own order.
+__device__ __forceinline__ void to_f16(const q2_u32x4& v0, const q2_u32x4& v1, int shift, uint32_t (&h)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t w = i < 4 ? v0[i] : v1[i - 4];
+    const _Float16 lo = (_Float16)__builtin_amdgcn_ldexpf(__builtin_bit_cast(float, w << 16), shift);
+    const _Float16 hi = (_Float16)__builtin_amdgcn_ldexpf(__builtin_bit_cast(float, w & 0xFFFF0000u), shift);
+    h[i] = (uint32_t)__builtin_bit_cast(uint16_t, lo) | ((uint32_t)__builtin_bit_cast(uint16_t, hi) << 16);
+  }
+}
+// The stored order: positions 2 p, 2 p + 1 hold elements 4 b + j and 4 b + 4 + j
+// with j = p / 2, b = 2 (p % 2), i.e. halves j % 2 of dwords 2 b + j / 2 and + 2.
+__device__ __forceinline__ void store_f16(q2_u32x4* dst, const uint32_t (&h)[8]) {
+  q2_u32x4 o[2];
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    const int j = p >> 1, b = 2 * (p & 1), d = 2 * b + (j >> 1);
+    o[p >> 2][p & 3] = __builtin_amdgcn_perm(h[d + 2], h[d], (j & 1) ? 0x07060302u : 0x05040100u);
+  }
+  dst[0] = o[0];
+  dst[1] = o[1];
+}
+
+// Rows without a branch: one wave per row, which stays in registers up to
+// 1024 NCH elements between the search for its largest element and the
+// conversion (NCH = 0: longer rows, read twice).  Row M (of M + 1) is a row of
+// zeros that indexes outside x are pointed to.
 constexpr int CV_ROWS = 4;
 
-__global__ __launch_bounds__(64 * CV_ROWS) void x_to_f16_kernel(const uint16_t* x, const int32_t* row_index,
-                                                                int64_t x_rows, uint16_t* out, int32_t* rexp, int64_t M,
-                                                                int64_t K) {
+template <int NCH>
+__global__ __launch_bounds__(64 * CV_ROWS) void x_to_f16_kernel(const uint16_t* x, uint16_t* out, int32_t* rexp,
+                                                                int64_t M, int64_t K) {
   const int lane = threadIdx.x & 63;
   const int64_t m = (int64_t)blockIdx.x * CV_ROWS + (threadIdx.x >> 6);
-  if (m >= M) return;
-  const int64_t src = row_index ? (int64_t)row_index[m] : m;
+  if (m > M) return;
   const int64_t chunks = K / 16;
-  uint16_t* const dst = out + m * K;
-  if (src < 0 || src >= x_rows) {                        // an index outside x: a row of zeros
-    for (int64_t q = lane; q < 2 * chunks; q += 64)
-      reinterpret_cast<q2_u32x4*>(dst)[q] = q2_u32x4{0u, 0u, 0u, 0u};
+  q2_u32x4* const dst = reinterpret_cast<q2_u32x4*>(out + m * K);
+  if (m == M) {
+    for (int64_t q = lane; q < 2 * chunks; q += 64) dst[q] = q2_u32x4{0u, 0u, 0u, 0u};
     if (lane == 0) rexp[m] = 0;
     return;
   }
-  const q2_u32x4* const xr = reinterpret_cast<const q2_u32x4*>(x + src * K);
-  uint32_t top = 0;                                      // largest finite |x|, as bf16 bits
-  for (int64_t q = lane; q < 2 * chunks; q += 64) {
-    const q2_u32x4 v = xr[q];
+  const q2_u32x4* const xr = reinterpret_cast<const q2_u32x4*>(x + m * K);
+  constexpr int N = NCH > 0 ? NCH : 1;
+  q2_u32x4 v[N][2];
+  uint32_t top = 0;
+  if constexpr (NCH > 0) {
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      const uint32_t lo = v[d] & 0x7FFFu, hi = (v[d] >> 16) & 0x7FFFu;
-      top = max(top, lo < 0x7F80u ? lo : 0u);
-      top = max(top, hi < 0x7F80u ? hi : 0u);
+    for (int i = 0; i < NCH; ++i) {
+      const int64_t q = std::min<int64_t>(lane + 64 * i, chunks - 1);     // past the row: its last elements again
+      v[i][0] = xr[2 * q];
+      v[i][1] = xr[2 * q + 1];
     }
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) top = top_bits(top_bits(top, v[i][0]), v[i][1]);
+  } else {
+    for (int64_t q = lane; q < 2 * chunks; q += 64) top = top_bits(top, xr[q]);
   }
 #pragma unroll
   for (int d = 32; d; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-  // floor(log2 |x|) from the bits; a subnormal bf16 is bits * 2^-133
-  const int e = top >= 0x80u ? (int)(top >> 7) - 127 : top ? 31 - __builtin_clz(top) - 133 : 14;
-  const int shift = 14 - e;
+  const int shift = top_shift(top);
   if (lane == 0) rexp[m] = -shift;
-  for (int64_t q = lane; q < chunks; q += 64) {
-    const q2_u32x4 v0 = xr[2 * q], v1 = xr[2 * q + 1];
-    uint32_t h[16];
+  uint32_t h[8];
+  if constexpr (NCH > 0) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t dw = i < 8 ? v0[i >> 1] : v1[(i - 8) >> 1];
-      const float f = __builtin_bit_cast(float, (i & 1) ? dw & 0xFFFF0000u : dw << 16);
-      h[i] = __builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_ldexpf(f, shift));
+    for (int i = 0; i < NCH; ++i) {
+      const int64_t q = lane + 64 * i;
+      if (q < chunks) {
+        to_f16(v[i][0], v[i][1], shift, h);
+        store_f16(dst + 2 * q, h);
+      }
     }
-    q2_u32x4 o[2];
+  } else {
+    for (int64_t q = lane; q < chunks; q += 64) {
+      to_f16(xr[2 * q], xr[2 * q + 1], shift, h);
+      store_f16(dst + 2 * q, h);
+    }
+  }
+}
+
+// Rows with a rank-r branch, r <= 64: sixteen rows per workgroup of sixteen
+// waves, each wave every sixteenth run of 64 inputs (lane (c, g): row c, inputs
+// 16 g .. + 15 of the run).  x is read once up to K = 12288 (8192 for r > 32), converted, stored
+// and multiplied by A (f16 as it is: exact products) while it is in registers;
+// the waves' sums of x A^T meet in LDS and leave as the branch's bf16 limbs.
+// Reading x once for both took M = 4093, K = 12288, r = 32 from 102 us (43 to
+// convert, 59 for x A^T on its own) to XA_US.
+constexpr int XA_WAVES = 16, XA_MAX_RANK = 64;
+
+__device__ __forceinline__ q2_f32x4 mfma16_f16(q2_u32x4 a, q2_u32x4 b, q2_f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(q2_f16x8, a), __builtin_bit_cast(q2_f16x8, b), c, 0,
+                                                0, 0);
+}
+
+template <int CT>
+__global__ __launch_bounds__(64 * XA_WAVES) void x_to_f16_branch_kernel(const uint16_t* x, const uint16_t* A,
+                                                                        uint16_t* out, int32_t* rexp, uint16_t* limbs,
+                                                                        int64_t M, int64_t K, int r) {
+  constexpr int XA_RUNS = CT <= 2 ? 12 : 8;              // of a wave, in registers
+  __shared__ uint32_t tops[XA_WAVES][16];
+  __shared__ q2_f32x4 red[XA_WAVES][CT][64];
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t m0 = (int64_t)blockIdx.x * 16;
+  const int64_t m = std::min<int64_t>(m0 + c, M - 1);    // rows past the end repeat the last one, not stored
+  const bool live = m0 + c < M;
+  const int runs = (int)(K / 64);
+  const uint16_t* const xr = x + m * K + 16 * g;
+  q2_u32x4 v[XA_RUNS][2];
+  uint32_t top = 0;
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {                        // positions 2 p, 2 p + 1: j = p / 2, b = 2 (p % 2), b + 1
-      const int j = p >> 1, b = 2 * (p & 1);
-      o[p >> 2][p & 3] = h[4 * b + j] | (h[4 * b + 4 + j] << 16);
+  for (int i = 0; i < XA_RUNS; ++i) {
+    const int s = min(wv + XA_WAVES * i, runs - 1);
+    const q2_u32x4* p = reinterpret_cast<const q2_u32x4*>(xr + (int64_t)s * 64);
+    v[i][0] = p[0];
+    v[i][1] = p[1];
+  }
+#pragma unroll
+  for (int i = 0; i < XA_RUNS; ++i) top = top_bits(top_bits(top, v[i][0]), v[i][1]);
+  for (int s = wv + XA_WAVES * XA_RUNS; s < runs; s += XA_WAVES) {
+    const q2_u32x4* p = reinterpret_cast<const q2_u32x4*>(xr + (int64_t)s * 64);
+    top = top_bits(top_bits(top, p[0]), p[1]);
+  }
+  top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+  top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+  if (g == 0) tops[wv][c] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < XA_WAVES; ++w) top = max(top, tops[w][c]);
+  const int shift = top_shift(top);
+  if (wv == 0 && g == 0 && live) rexp[m] = -shift;
+
+  const uint16_t* ar[CT];
+#pragma unroll
+  for (int t = 0; t < CT; ++t) ar[t] = A + (int64_t)min(16 * t + c, r - 1) * K + 16 * g;   // columns past r: not stored
+  q2_f32x4 acc[CT];
+#pragma unroll
+  for (int t = 0; t < CT; ++t) acc[t] = q2_f32x4{0.f, 0.f, 0.f, 0.f};
+  auto step = [&](int s, const q2_u32x4& v0, const q2_u32x4& v1) {
+    uint32_t h[8];
+    to_f16(v0, v1, shift, h);
+    if (live) store_f16(reinterpret_cast<q2_u32x4*>(out + m * K + (int64_t)s * 64 + 16 * g), h);
+#pragma unroll
+    for (int t = 0; t < CT; ++t) {
+      const q2_u32x4* p = reinterpret_cast<const q2_u32x4*>(ar[t] + (int64_t)s * 64);
+      acc[t] = mfma16_f16(q2_u32x4{h[0], h[1], h[2], h[3]}, p[0], acc[t]);
+      acc[t] = mfma16_f16(q2_u32x4{h[4], h[5], h[6], h[7]}, p[1], acc[t]);
     }
-    reinterpret_cast<q2_u32x4*>(dst)[2 * q] = o[0];
-    reinterpret_cast<q2_u32x4*>(dst)[2 * q + 1] = o[1];
+  };
+#pragma unroll
+  for (int i = 0; i < XA_RUNS; ++i) {
+    const int s = wv + XA_WAVES * i;
+    if (s < runs) step(s, v[i][0], v[i][1]);
+  }
+  for (int s = wv + XA_WAVES * XA_RUNS; s < runs; s += XA_WAVES) {
+    const q2_u32x4* p = reinterpret_cast<const q2_u32x4*>(xr + (int64_t)s * 64);
+    step(s, p[0], p[1]);
+  }
+#pragma unroll
+  for (int t = 0; t < CT; ++t) red[wv][t][lane] = acc[t];
+  __syncthreads();
+  const int r8 = (r + 7) & ~7;
+  if (wv < CT) {                                         // one wave per column tile, waves in order
+    q2_f32x4 sum = red[0][wv][lane];
+#pragma unroll
+    for (int w = 1; w < XA_WAVES; ++w) sum += red[w][wv][lane];
+    const int col = 16 * wv + c;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int row = 4 * g + e;
+      uint32_t rt = 0;
+#pragma unroll
+      for (int w = 0; w < XA_WAVES; ++w) rt = max(rt, tops[w][row]);
+      if (m0 + row < M && col < r8) {
+        const float t = col < r ? __builtin_amdgcn_ldexpf(sum[e], -top_shift(rt)) : 0.f;
+        const uint16_t hi = f32_to_bf16_rn(t), lo = f32_to_bf16_rn(t - bf16_to_f32(hi));
+        limbs[(m0 + row) * 2 * r8 + col] = hi;
+        limbs[(m0 + row) * 2 * r8 + r8 + col] = lo;
+      }
+    }
   }
 }
 
@@ -120,6 +265,12 @@ __device__ __forceinline__ q2_u32x4 decode_step(const q2_u32x2& w, const WTable&
     r[2 * u + 1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
   }
   return r;
+}
+
+// Row of x16 that row m reads: x_rows (zeros) for an index outside x.
+__device__ __forceinline__ int64_t source_row(const FusedArgs& a, int64_t m) {
+  const int64_t src = a.row_index[m];
+  return src >= 0 && src < a.x_rows ? src : a.x_rows;
 }
 
 constexpr int FX_BM = 128, FX_BN = 256;                  // rows, weight columns of a workgroup
@@ -169,15 +320,25 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
   // and 16-byte position l % 8, which holds chunk (l % 8) ^ (row / 2 % 8): the
   // sixteen rows that one pass of a 16-byte read touches lie in different
   // banks.  Rows past the last one are padding of the workspace, never stored.
+  // With a row index the four copies' rows lie anywhere in x16.
   const int crow = 8 * wv + (lane >> 3);
-  const uint32_t xoff = (uint32_t)(crow * K * 2) + (uint32_t)(((lane & 7) ^ ((crow >> 1) & 7)) << 4);
-  const __amdgpu_buffer_rsrc_t rx = buf_rsrc(x16 + m0 * K, (uint32_t)(FX_BM * K * 2));
+  const uint32_t chunk = (uint32_t)(((lane & 7) ^ ((crow >> 1) & 7)) << 4);
+  uint32_t xoff[4];
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) {
+    int64_t row = crow + 32 * kk;
+    if (a.row_index) row = source_row(a, std::min<int64_t>(m0 + row, rt.mend - 1));
+    xoff[kk] = (uint32_t)(row * K * 2) + chunk;
+  }
+  const __amdgpu_buffer_rsrc_t rx =
+      a.row_index ? buf_rsrc(x16, (uint32_t)((a.x_rows + 1) * K * 2)) : buf_rsrc(x16 + m0 * K, (uint32_t)(FX_BM * K * 2));
   auto copy_rows = [&](int hs, int ring) {
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(smem + ring * FX_HALF + (32 * kk + 8 * wv) * 128), 16,
-                                               xoff, (uint32_t)(32 * kk) * (uint32_t)(K * 2) + (uint32_t)hs * 128u, 0,
-                                               0);
+    for (int kk = 0; kk < 4; ++kk) {
+      const uint32_t xo = kk == 0 ? xoff[0] : kk == 1 ? xoff[1] : kk == 2 ? xoff[2] : xoff[3];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(smem + ring * FX_HALF + (32 * kk + 8 * wv) * 128), 16, xo,
+                                               (uint32_t)hs * 128u, 0, 0);
+    }
   };
   int aoff[4];
 #pragma unroll
@@ -276,7 +437,7 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
       const int64_t m = m0 + 32 * i + 8 * q + 4 * h;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int s = rexp[m + e];
+        const int s = rexp[a.row_index ? source_row(a, std::min<int64_t>(m + e, rt.mend - 1)) : m + e];
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j][4 * q + e] = __builtin_amdgcn_ldexpf(acc[i][j][4 * q + e], s);
       }
@@ -320,23 +481,46 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
 // ============================================================================
 static size_t pad256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-// Rows of the last tile run up to FX_BM - 1 past the end of the workspace's rows.
-size_t f16_workspace_bytes(int64_t M, int64_t K) {
-  return pad256((size_t)(M + FX_BM) * (size_t)K * 2) + pad256((size_t)(M + FX_BM) * 4);
+// `rows` rows of x and their exponents.  The last tile's rows run up to FX_BM - 1
+// past them, a row index needs one row of zeros behind them.
+size_t f16_workspace_bytes(int64_t rows, int64_t K) {
+  return pad256((size_t)(rows + FX_BM) * (size_t)K * 2) + pad256((size_t)(rows + FX_BM) * 4);
+}
+
+// Rows of x are addressed with 32 bits from a tile's first row, and with a row
+// index from the first row of x; codes from an expert's weight.
+bool fused_f16_takes(int64_t rows, int64_t N, int64_t K) {
+  return K >= 4 * BLOCK_K && K <= (1 << 22) && N <= ((int64_t)1 << 33) / K && rows <= ((int64_t)1 << 30) / K;
 }
 
 hipError_t launch_fused_f16(const FusedArgs& a, void* ws, hipStream_t stream) {
+  const int64_t rows = a.x_rows, K = a.K;
   uint16_t* x16 = static_cast<uint16_t*>(ws);
-  int32_t* rexp = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + pad256((size_t)(a.M + FX_BM) * (size_t)a.K * 2));
-  const int64_t cv = (a.M + CV_ROWS - 1) / CV_ROWS;
+  int32_t* rexp = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + pad256((size_t)(a.M + FX_BM) * (size_t)K * 2));
   const int64_t cols = a.gated ? FX_BN / 2 : FX_BN;
   const int64_t tiles_n = (fused_n_out(a) + cols - 1) / cols, slots = max_row_tiles(a, FX_BM);
-  if (cv > 0x7fffffff || tiles_n > 0x7fffffff || slots > 0x7fffffff / tiles_n) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(x_to_f16_kernel, dim3((unsigned)cv), dim3(64 * CV_ROWS), 0, stream, a.x, a.row_index, a.x_rows,
-                     x16, rexp, a.M, a.K);
+  if (tiles_n > 0x7fffffff || slots > 0x7fffffff / tiles_n) return hipErrorInvalidValue;
+  if (a.r > 0 && a.r <= XA_MAX_RANK) {
+    const dim3 grid((unsigned)((rows + 15) / 16)), block(64 * XA_WAVES);
+#define Q2_XA(CT)                                                                                                  \
+  hipLaunchKernelGGL((x_to_f16_branch_kernel<CT>), grid, block, 0, stream, a.x, a.lr_a, x16, rexp, a.lr_t, rows, K, \
+                     a.r)
+    if (a.r <= 16) Q2_XA(1);
+    else if (a.r <= 32) Q2_XA(2);
+    else Q2_XA(4);
+#undef Q2_XA
+  } else {
+    const dim3 grid((unsigned)(rows / CV_ROWS + 1)), block(64 * CV_ROWS);
+#define Q2_CV(NCH) hipLaunchKernelGGL((x_to_f16_kernel<NCH>), grid, block, 0, stream, a.x, x16, rexp, rows, K)
+    if (K <= 2048) Q2_CV(2);
+    else if (K <= 4096) Q2_CV(4);
+    else if (K <= 12288) Q2_CV(12);
+    else Q2_CV(0);
+#undef Q2_CV
+  }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int group_m = tile_group_rows(slots, tiles_n, 2.0 * FX_BM * (double)a.K, (double)FX_BN * a.K * 0.265625, 64);
+  const int group_m = tile_group_rows(slots, tiles_n, 2.0 * FX_BM * (double)K, (double)FX_BN * K * 0.265625, 64);
   hipLaunchKernelGGL(fused_f16_kernel, dim3((unsigned)(slots * tiles_n)), dim3(256), 0, stream, a, x16, rexp,
                      (int)tiles_n, group_m);
   return hipGetLastError();

@@ -79,7 +79,10 @@ def tolerance(z, act, gated, bias, gate, residual, out_dtype):
     if residual is not None:
         y = y + residual
         err = err + 2.0 ** -20 * np.abs(residual)
-    return y, err + (np.abs(y) + err) * torch.finfo(out_dtype).eps / 2
+    # half a step of the output type: relative to the value, and below the smallest normal number, where the steps
+    # stop shrinking, half of the last step (smallest_normal * eps is the distance of neighbours there)
+    t = torch.finfo(out_dtype)
+    return y, err + (np.abs(y) + err) * t.eps / 2 + t.smallest_normal * t.eps / 2
 
 
 def check(got, z, act="none", gated=False, bias=None, gate=None, residual=None, what=""):
@@ -109,6 +112,94 @@ def test_plain_sizes(fmt, m, n, k):
     check(y, z, what=f"{fmt} {m} {n} {k}")
     yb = fused(fmt)(x, *dev, out_dtype=torch.bfloat16)
     assert torch.equal(yb, y.to(torch.bfloat16)), "the bf16 output is not the f32 one rounded once"
+
+
+# The kernel for many rows needs many tiles: wide weights, sampled columns (both factors' of a gated layer).
+MANY = [(300, 32770, 512, 0, False), (1025, 9000, 1152, 0, True), (2000, 5250, 4224, 0, False), (700, 16400, 640, 5, True),
+        (1500, 7000, 12416, 32, False), (1300, 8200, 2560, 64, True), (900, 12300, 512, 100, False)]
+
+
+def sample(n, gated, seed):
+    """Sorted sample of the output columns, the first and last ones in it, and of the weight rows behind them."""
+    n_out = n // 2 if gated else n
+    rng = np.random.default_rng(seed)
+    cols = np.unique(np.concatenate([np.arange(40), n_out - 1 - np.arange(40), rng.choice(n_out, 60)]))
+    return cols, np.concatenate([cols, cols + n_out]) if gated else cols
+
+
+def spread_rows(seed, x):
+    """bf16 bits whose rows have scales of their own, from 2^-60 to 2^60, one of them zero."""
+    e = np.random.default_rng(seed).integers(-60, 61, (len(x), 1))
+    e[len(x) // 3] = -1000
+    return I.f32_to_bf16_bits(np.ldexp(O.bf16_to_f64(x), e).astype(np.float32))
+
+
+@pytest.mark.parametrize("m,n,k,r,gated", MANY)
+def test_many_rows(m, n, k, r, gated):
+    codes = np.random.default_rng(315).integers(0, 3, (n, k)).astype(np.uint8)
+    scales = I.q2_scales(315, n, k)
+    p, s = q2.q2_pack(dev_u8(codes), torch.from_numpy(scales).to(DEV))
+    cols, rows = sample(n, gated, 315)
+    w = (codes[rows].astype(np.float64) - 1) * np.repeat(scales[rows].astype(np.float64), 128, axis=1)
+    xb = spread_rows(315, I.activations_bf16(315, m, k))
+    x = dev_bits(xb, torch.bfloat16)
+    xd = O.bf16_to_f64(xb)
+    z = xd @ w.T
+    A = B = None
+    if r:
+        a, b = I.lowrank_factors(315, r, k, n, std=0.05)
+        A, B = dev_bits(a, torch.float16), dev_bits(b, torch.float16)
+        z = z + (xd @ O.f16_to_f64(a).T) @ O.f16_to_f64(b[rows]).T
+    act = "relu" if gated else "none"                      # rows far from 1: what scales with them
+    y = q2.q2_linear_fused(x, p, s, A, B, activation=act, gated=gated)
+    sel = torch.from_numpy(cols).to(DEV)
+    check(y[:, sel], z, act, gated, what="f32")
+    assert (y[m // 3] == 0).all()
+    yb = q2.q2_linear_fused(x, p, s, A, B, activation=act, gated=gated, out_dtype=torch.bfloat16)
+    assert torch.equal(yb, y.to(torch.bfloat16))
+    # the epilogue, with ordinary rows
+    xb = I.activations_bf16(316, m, k)
+    x, xd = dev_bits(xb, torch.bfloat16), O.bf16_to_f64(xb)
+    z = xd @ w.T
+    if r:
+        z = z + (xd @ O.f16_to_f64(a).T) @ O.f16_to_f64(b[rows]).T
+    bias, gate = rnd(1, n).to(DEV), rnd(2, len(y[0])).to(DEV)
+    res = rnd(3, *y.shape).to(DEV).bfloat16()
+    y = q2.q2_linear_fused(x, p, s, A, B, bias=bias, gate=gate, residual=res, activation="gelu", gated=gated,
+                           out_dtype=torch.bfloat16)
+    check(y[:, sel], z, "gelu", gated, bias[torch.from_numpy(rows).to(DEV)], gate[sel], res[:, sel])
+
+
+@pytest.mark.parametrize("counts,n,k,gated", [([900], 12000, 512, True), ([300, 0, 1, 799], 10010, 640, False),
+                                              ([257, 640], 13000, 1152, True)])
+@pytest.mark.parametrize("gather", [False, True])
+def test_many_rows_grouped(counts, n, k, gated, gather):
+    e, lead, tail = len(counts), 2, 3
+    rows = sum(counts) + lead + tail
+    codes = np.random.default_rng(317).integers(0, 3, (e * n, k)).astype(np.uint8)
+    scales = I.q2_scales(317, e * n, k)
+    p, s = q2.q2_pack(dev_u8(codes), torch.from_numpy(scales).to(DEV))
+    cols, wr = sample(n, gated, 317)
+    pick = (np.arange(e)[:, None] * n + wr).ravel()
+    w = ((codes[pick].astype(np.float64) - 1) * np.repeat(scales[pick].astype(np.float64), 128, axis=1)).reshape(e, len(wr), k)
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32) + lead
+    x_rows = 401 if gather else rows
+    index = None
+    if gather:
+        index = np.random.default_rng(318).integers(0, x_rows, rows).astype(np.int32)
+        index[5::50] = -1
+        index[6::50] = x_rows
+    xb = spread_rows(318, I.activations_bf16(318, x_rows, k))
+    z = F.grouped_products(O.bf16_to_f64(xb), w, offsets, index)
+    inside = slice(int(offsets[0]), int(offsets[-1]))
+    sel = torch.from_numpy(cols).to(DEV)
+    for out in (torch.float32, torch.bfloat16):
+        y = torch.full((rows, n // 2 if gated else n), 7.0, device=DEV, dtype=out)
+        q2.q2_linear_grouped(dev_bits(xb, torch.bfloat16), torch.from_numpy(offsets).to(DEV), p.view(e, n, -1),
+                             s.view(e, n, -1), row_index=None if index is None else torch.from_numpy(index).to(DEV),
+                             activation="relu", gated=gated, y=y)
+        check(y[inside][:, sel], z[inside], "relu", gated)
+        assert (y[:lead] == 7).all() and (y[offsets[-1]:] == 7).all()
 
 
 @pytest.mark.parametrize("fmt", ["q2", "q4"])
