@@ -111,8 +111,8 @@ __device__ __forceinline__ void store_out(const FusedArgs& a, const float* bias,
 
 // ROWS x (64 or 32 output columns) of finished products in LDS (row stride
 // `stride` floats; with a gated epilogue the second factor of column n at
-// `half` + n) to y, by the 64 lanes of one wave: 16-byte pieces of 8 or 4
-// columns where y, the residual and the column count allow it.
+// `half` + n) to y, by the 64 lanes of one wave: pieces of eight columns
+// where y, the residual and the column count allow it.
 __device__ __forceinline__ bool vec_rows(const FusedArgs& a, int64_t n_out) {
   // a grouped bias starts E * N floats in: with n_out % 8 == 0 every expert's is aligned with the first
   const uintptr_t p = reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.residual) |
@@ -120,52 +120,72 @@ __device__ __forceinline__ bool vec_rows(const FusedArgs& a, int64_t n_out) {
   return n_out % 8 == 0 && (p & 15) == 0;
 }
 
-__device__ __forceinline__ void add4(float (&v)[4], const float* p) {
-  const q2_f32x4 t = *reinterpret_cast<const q2_f32x4*>(p);
+struct Eight {
+  float v[8];
+};
+__device__ __forceinline__ Eight load8f(const float* p) {
+  const q2_f32x4 a = reinterpret_cast<const q2_f32x4*>(p)[0], b = reinterpret_cast<const q2_f32x4*>(p)[1];
+  return Eight{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
+}
+__device__ __forceinline__ Eight load8h(const uint16_t* p) {
+  const q2_u32x4 t = *reinterpret_cast<const q2_u32x4*>(p);
+  Eight r;
 #pragma unroll
-  for (int d = 0; d < 4; ++d) v[d] += t[d];
+  for (int d = 0; d < 8; ++d)
+    r.v[d] = __builtin_bit_cast(float, (d & 1) ? t[d >> 1] & 0xFFFF0000u : t[d >> 1] << 16);
+  return r;
 }
 
 __device__ __forceinline__ void store_strip(const FusedArgs& a, const float* bias, int64_t n_out, const float* strip,
                                             int stride, int half, int cols, int64_t m0, int rows, int64_t n0,
                                             int lane) {
   if (vec_rows(a, n_out)) {
-    const int per = cols / 4;                            // pieces of four columns per row
+    const int per = cols / 8;                            // pieces of eight columns per row
     for (int idx = lane; idx < rows * per; idx += 64) {
-      const int row = idx / per, col = (idx - row * per) * 4;
+      const int row = idx / per, col = (idx - row * per) * 8;
       const int64_t n = n0 + col;
       if (n >= n_out) continue;
       const float* s = strip + row * stride + col;
-      float v[4] = {s[0], s[1], s[2], s[3]};
-      if (bias) add4(v, bias + n);
+      Eight v = load8f(s);
+      if (bias) {
+        const Eight b = load8f(bias + n);
 #pragma unroll
-      for (int d = 0; d < 4; ++d) v[d] = activate(a.act, v[d]);
+        for (int d = 0; d < 8; ++d) v.v[d] += b.v[d];
+      }
+#pragma unroll
+      for (int d = 0; d < 8; ++d) v.v[d] = activate(a.act, v.v[d]);
       if (a.gated) {
-        float u[4] = {s[half], s[half + 1], s[half + 2], s[half + 3]};
-        if (bias) add4(u, bias + n_out + n);
+        Eight u = load8f(s + half);
+        if (bias) {
+          const Eight b = load8f(bias + n_out + n);
 #pragma unroll
-        for (int d = 0; d < 4; ++d) v[d] *= u[d];
+          for (int d = 0; d < 8; ++d) u.v[d] += b.v[d];
+        }
+#pragma unroll
+        for (int d = 0; d < 8; ++d) v.v[d] *= u.v[d];
       }
       if (a.gate) {
-        const q2_f32x4 t = *reinterpret_cast<const q2_f32x4*>(a.gate + n);
+        const Eight g = load8f(a.gate + n);
 #pragma unroll
-        for (int d = 0; d < 4; ++d) v[d] *= t[d];
+        for (int d = 0; d < 8; ++d) v.v[d] *= g.v[d];
       }
       const int64_t i = (m0 + row) * n_out + n;
-      if (a.residual && a.res_bf16) {
-        const q2_u32x2 t = *reinterpret_cast<const q2_u32x2*>(static_cast<const uint16_t*>(a.residual) + i);
+      if (a.residual) {
+        const Eight r = a.res_bf16 ? load8h(static_cast<const uint16_t*>(a.residual) + i)
+                                   : load8f(static_cast<const float*>(a.residual) + i);
 #pragma unroll
-        for (int d = 0; d < 4; ++d)
-          v[d] += __builtin_bit_cast(float, (d & 1) ? t[d >> 1] & 0xFFFF0000u : t[d >> 1] << 16);
-      } else if (a.residual) {
-        add4(v, static_cast<const float*>(a.residual) + i);
+        for (int d = 0; d < 8; ++d) v.v[d] += r.v[d];
       }
       if (a.out_bf16) {
-        *reinterpret_cast<q2_u32x2*>(static_cast<uint16_t*>(a.y) + i) =
-            q2_u32x2{(uint32_t)to_bf16(v[0]) | ((uint32_t)to_bf16(v[1]) << 16),
-                     (uint32_t)to_bf16(v[2]) | ((uint32_t)to_bf16(v[3]) << 16)};
+        q2_u32x4 o;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          o[d] = (uint32_t)to_bf16(v.v[2 * d]) | ((uint32_t)to_bf16(v.v[2 * d + 1]) << 16);
+        *reinterpret_cast<q2_u32x4*>(static_cast<uint16_t*>(a.y) + i) = o;
       } else {
-        *reinterpret_cast<q2_f32x4*>(static_cast<float*>(a.y) + i) = q2_f32x4{v[0], v[1], v[2], v[3]};
+        q2_f32x4* y = reinterpret_cast<q2_f32x4*>(static_cast<float*>(a.y) + i);
+        y[0] = q2_f32x4{v.v[0], v.v[1], v.v[2], v.v[3]};
+        y[1] = q2_f32x4{v.v[4], v.v[5], v.v[6], v.v[7]};
       }
     }
   } else {

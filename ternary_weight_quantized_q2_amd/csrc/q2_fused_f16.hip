@@ -340,6 +340,11 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
                                                (uint32_t)hs * 128u, 0, 0);
     }
   };
+  int row_exp = 0;
+  if (tid < FX_BM) {
+    const int64_t m = std::min<int64_t>(m0 + tid, rt.mend - 1);
+    row_exp = rexp[a.row_index ? source_row(a, m) : m];
+  }
   int aoff[4];
 #pragma unroll
   for (int t = 0; t < 4; ++t) aoff[t] = c * 128 + (((4 * h + t) ^ ((c >> 1) & 7)) << 4);
@@ -430,18 +435,20 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
   __syncthreads();
 
   // The rows' powers of two: element 4 q + e of a tile is row 8 q + 4 h + e.
+  int* const exps = reinterpret_cast<int*>(smem);
+  if (tid < FX_BM) exps[tid] = row_exp;
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int64_t m = m0 + 32 * i + 8 * q + 4 * h;
+    for (int q = 0; q < 4; ++q)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int s = rexp[a.row_index ? source_row(a, std::min<int64_t>(m + e, rt.mend - 1)) : m + e];
+        const int s = exps[32 * i + 8 * q + 4 * h + e];
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j][4 * q + e] = __builtin_amdgcn_ldexpf(acc[i][j][4 * q + e], s);
       }
-    }
+  __syncthreads();                                       // read before the strips overwrite them
 
   if (a.r > 0) {
     const int r8 = (a.r + 7) & ~7;
