@@ -273,30 +273,32 @@ __device__ __forceinline__ int64_t source_row(const FusedArgs& a, int64_t m) {
   return src >= 0 && src < a.x_rows ? src : a.x_rows;
 }
 
-constexpr int FX_BM = 128, FX_BN = 256;                  // rows, weight columns of a workgroup
-constexpr int FX_HALF = FX_BM * 128;                     // bytes of a 64-wide half block of the rows
-constexpr int FX_RING = 3;                               // half blocks in LDS
-constexpr int FX_OFF_W = FX_RING * FX_HALF;
+constexpr int FX_BN = 256;                               // weight columns of a workgroup
+constexpr int FX_MAX_BM = 128;
 constexpr int FX_WBUF = 64 * 64;                         // codes of a wave's 64 columns, two blocks
-constexpr int FX_SMEM = FX_OFF_W + 4 * 2 * FX_WBUF;      // 80 KB: two workgroups per CU
 constexpr int FX_STRIP = 64 + 4;                         // floats per row of a wave's output strip
-static_assert(FX_SMEM <= 80 * 1024 && 4 * 32 * FX_STRIP * 4 <= FX_SMEM, "LDS");
 
-// A workgroup of four waves owns 128 rows x 256 weight columns, each wave all
-// the rows of 64 columns, so a column's weights are decoded once.  Two
+// A workgroup of four waves owns 128 or 96 rows x 256 weight columns, each wave
+// all the rows of 64 columns, so a column's weights are decoded once.  Two
 // workgroups share a CU and overlap each other's waits.  Per half block (64 of
 // K, half-stage hs) a wave copies a quarter of the tile's rows and a sixteenth
-// of its own columns' codes to LDS, both two or more half-stages ahead:
-//  - rows: a ring of three half blocks; those of hs + 2 are issued at hs;
+// of its own columns' codes to LDS:
+//  - rows: two half blocks; those of hs + 1 are issued at hs (a third buffer and
+//    issuing them at hs - 1 made no difference);
 //  - codes: two buffers of two blocks (64 bytes of a row at a time: reading a
 //    block's 32 bytes from 32 rows per instruction cost 16 % of the kernel);
 //    piece q of the buffer that is used from half-stage 4 S + 4 on is issued at
 //    4 S - 1 + q, after that buffer's last codes went to registers at 4 S - 2;
 //  - scales: four blocks at a time in registers.
-// One barrier per half-stage; a wave waits until only the last four row copies
-// are in flight, so everything issued before them has landed.
+// One barrier per half-stage, at which every copy issued before it has landed.
+template <int MT>
 __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const uint16_t* x16, const int32_t* rexp,
                                                            int tiles_n, int group_m) {
+  constexpr int FX_BM = 32 * MT;                         // rows of a workgroup
+  constexpr int FX_HALF = FX_BM * 128;                   // bytes of a 64-wide half block of the rows
+  constexpr int FX_OFF_W = 2 * FX_HALF;
+  constexpr int FX_SMEM = FX_OFF_W + 4 * 2 * FX_WBUF;    // 56 or 64 KB: two workgroups per CU
+  static_assert(FX_SMEM <= 80 * 1024 && 4 * 32 * FX_STRIP * 4 <= FX_SMEM && FX_BM <= FX_MAX_BM, "LDS");
   __shared__ __align__(16) uint8_t smem[FX_SMEM];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -323,20 +325,20 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
   // With a row index the four copies' rows lie anywhere in x16.
   const int crow = 8 * wv + (lane >> 3);
   const uint32_t chunk = (uint32_t)(((lane & 7) ^ ((crow >> 1) & 7)) << 4);
-  uint32_t xoff[4];
+  uint32_t xoff[MT];
 #pragma unroll
-  for (int kk = 0; kk < 4; ++kk) {
+  for (int kk = 0; kk < MT; ++kk) {
     int64_t row = crow + 32 * kk;
     if (a.row_index) row = source_row(a, std::min<int64_t>(m0 + row, rt.mend - 1));
     xoff[kk] = (uint32_t)(row * K * 2) + chunk;
   }
   const __amdgpu_buffer_rsrc_t rx =
       a.row_index ? buf_rsrc(x16, (uint32_t)((a.x_rows + 1) * K * 2)) : buf_rsrc(x16 + m0 * K, (uint32_t)(FX_BM * K * 2));
-  auto copy_rows = [&](int hs, int ring) {
+  auto copy_rows = [&](int hs, int buf) {
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      const uint32_t xo = kk == 0 ? xoff[0] : kk == 1 ? xoff[1] : kk == 2 ? xoff[2] : xoff[3];
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(smem + ring * FX_HALF + (32 * kk + 8 * wv) * 128), 16, xo,
+    for (int kk = 0; kk < MT; ++kk) {
+      const uint32_t xo = xoff[kk];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(smem + buf * FX_HALF + (32 * kk + 8 * wv) * 128), 16, xo,
                                                (uint32_t)hs * 128u, 0, 0);
     }
   };
@@ -378,9 +380,9 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
     for (int j = 0; j < 2; ++j) __builtin_memcpy(&sc[j], sp[j] + min(4 * q, KB - 4), 8);
   };
 
-  q2_f32x16 acc[4][2];
+  q2_f32x16 acc[MT][2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -393,10 +395,8 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
   for (int q = 0; q < 4; ++q) copy_codes(0, q);
   copy_codes(1, 0);                                      // half-stage -1's piece
   copy_rows(0, 0);
-  copy_rows(1, 1);
   __builtin_amdgcn_s_waitcnt(0);
   read_codes(0, w);
-  int ring = 0;
   for (int quad = 0; 4 * quad < KB; ++quad) {
    const uint64_t sc[2] = {scn[0], scn[1]};
    load_scales(quad + 1, scn);                           // past the end: the last four again, never used
@@ -407,17 +407,16 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int hs = 2 * blk + half;
-      stage_barrier<4>();
-      const int ring2 = ring == 0 ? 2 : ring - 1;        // (hs + 2) % 3
+      stage_barrier<0>();
       copy_codes((hs + 1) / 4 + 1, (hs + 1) & 3);
-      copy_rows(hs + 2 < NH ? hs + 2 : NH - 1, ring2);   // past the end: the last one again, never read
-      const uint8_t* st = smem + ring * FX_HALF;
+      copy_rows(hs + 1 < NH ? hs + 1 : NH - 1, half ^ 1);          // past the end: the last one again, never read
+      const uint8_t* st = smem + half * FX_HALF;
       q2_u32x2 wn[2];
       read_codes(hs + 1, wn);
 #define Q2_STEP(T)                                                                                     \
   {                                                                                                    \
     const q2_u32x4 b0 = decode_step<T>(w[0], tab[0]), b1 = decode_step<T>(w[1], tab[1]);               \
-    _Pragma("unroll") for (int i = 0; i < 4; ++i) {                                                    \
+    _Pragma("unroll") for (int i = 0; i < MT; ++i) {                                                   \
       const q2_u32x4 av = *reinterpret_cast<const q2_u32x4*>(st + i * 4096 + aoff[T]);                 \
       acc[i][0] = mfma32(av, b0, acc[i][0]);                                                           \
       acc[i][1] = mfma32(av, b1, acc[i][1]);                                                           \
@@ -427,7 +426,6 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
 #undef Q2_STEP
       w[0] = wn[0];
       w[1] = wn[1];
-      ring = ring == 2 ? 0 : ring + 1;
     }
    }
   }
@@ -439,7 +437,7 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
   if (tid < FX_BM) exps[tid] = row_exp;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -458,7 +456,7 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
 #pragma unroll
         for (int j = 0; j < 2; ++j) bq[j] = branch_bfrag(a, wcol(32 * j + c), k0 + 8 * h, part);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < MT; ++i) {
           const q2_u32x4 aq = branch_afrag(a, m0 + 32 * i + c, k0 + 8 * h, part);
 #pragma unroll
           for (int j = 0; j < 2; ++j) acc[i][j] = mfma32_bf16(aq, bq[j], acc[i][j]);
@@ -470,7 +468,7 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
   const float* bias = a.bias ? a.bias + rt.expert * a.N : nullptr;
   float* strip = reinterpret_cast<float*>(smem) + wv * 32 * FX_STRIP;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < MT; ++i) {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -488,10 +486,10 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
 // ============================================================================
 static size_t pad256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-// `rows` rows of x and their exponents.  The last tile's rows run up to FX_BM - 1
+// `rows` rows of x and their exponents.  The last tile's rows run up to FX_MAX_BM - 1
 // past them, a row index needs one row of zeros behind them.
 size_t f16_workspace_bytes(int64_t rows, int64_t K) {
-  return pad256((size_t)(rows + FX_BM) * (size_t)K * 2) + pad256((size_t)(rows + FX_BM) * 4);
+  return pad256((size_t)(rows + FX_MAX_BM) * (size_t)K * 2) + pad256((size_t)(rows + FX_MAX_BM) * 4);
 }
 
 // Rows of x are addressed with 32 bits from a tile's first row, and with a row
@@ -500,12 +498,29 @@ bool fused_f16_takes(int64_t rows, int64_t N, int64_t K) {
   return K >= 4 * BLOCK_K && K <= (1 << 22) && N <= ((int64_t)1 << 33) / K && rows <= ((int64_t)1 << 30) / K;
 }
 
+// Rows of a workgroup.  The chip holds 512 workgroups, and one that has a CU for
+// itself runs about twice as fast, so a launch takes its full rounds of 512 plus
+// half a round for up to 256 more tiles.  A round of 96-row tiles takes 0.85 of
+// one of 128-row tiles (each decode serves fewer rows).  Measured, 128 / 96 rows:
+// 1536 rows K = 4096 N = 12288 182 / 157 us (576 and 768 tiles), N = 8192 121 /
+// 108; 1024 rows N = 12288 116 / 139; 4093 rows K = 12288 N = 4096 371 / 417.
+// Groups of rows, whose tiles are not known here: 128; both were within 2 %.
+static int rows_per_tile(const FusedArgs& a, int64_t cols) {
+  if (a.offsets) return 128;
+  auto rounds = [&](int64_t bm) {
+    const int64_t tiles = ((a.M + bm - 1) / bm) * ((fused_n_out(a) + cols - 1) / cols), rest = tiles % 512;
+    return (double)(tiles / 512) + (rest == 0 ? 0.0 : rest <= 256 ? 0.5 : 1.0);
+  };
+  return 0.85 * rounds(96) < rounds(128) ? 96 : 128;
+}
+
 hipError_t launch_fused_f16(const FusedArgs& a, void* ws, hipStream_t stream) {
   const int64_t rows = a.x_rows, K = a.K;
   uint16_t* x16 = static_cast<uint16_t*>(ws);
-  int32_t* rexp = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + pad256((size_t)(a.M + FX_BM) * (size_t)K * 2));
+  int32_t* rexp = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + pad256((size_t)(a.M + FX_MAX_BM) * (size_t)K * 2));
   const int64_t cols = a.gated ? FX_BN / 2 : FX_BN;
-  const int64_t tiles_n = (fused_n_out(a) + cols - 1) / cols, slots = max_row_tiles(a, FX_BM);
+  const int bm = rows_per_tile(a, cols);
+  const int64_t tiles_n = (fused_n_out(a) + cols - 1) / cols, slots = max_row_tiles(a, bm);
   if (tiles_n > 0x7fffffff || slots > 0x7fffffff / tiles_n) return hipErrorInvalidValue;
   if (a.r > 0 && a.r <= XA_MAX_RANK) {
     const dim3 grid((unsigned)((rows + 15) / 16)), block(64 * XA_WAVES);
@@ -527,9 +542,13 @@ hipError_t launch_fused_f16(const FusedArgs& a, void* ws, hipStream_t stream) {
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int group_m = tile_group_rows(slots, tiles_n, 2.0 * FX_BM * (double)K, (double)FX_BN * K * 0.265625, 64);
-  hipLaunchKernelGGL(fused_f16_kernel, dim3((unsigned)(slots * tiles_n)), dim3(256), 0, stream, a, x16, rexp,
-                     (int)tiles_n, group_m);
+  const int group_m = tile_group_rows(slots, tiles_n, 2.0 * bm * (double)K, (double)FX_BN * K * 0.265625, 64);
+  const dim3 grid((unsigned)(slots * tiles_n));
+#define Q2_FX(MT) \
+  hipLaunchKernelGGL((fused_f16_kernel<MT>), grid, dim3(256), 0, stream, a, x16, rexp, (int)tiles_n, group_m)
+  if (bm == 96) Q2_FX(3);
+  else Q2_FX(4);
+#undef Q2_FX
   return hipGetLastError();
 }
 

@@ -115,7 +115,8 @@ def test_plain_sizes(fmt, m, n, k):
 
 
 # The kernel for many rows needs many tiles: wide weights, sampled columns (both factors' of a gated layer).
-MANY = [(300, 32770, 512, 0, False), (1025, 9000, 1152, 0, True), (2000, 5250, 4224, 0, False), (700, 16400, 640, 5, True),
+MANY = [(1531, 8120, 640, 40, False), (1531, 8120, 512, 0, True),
+        (300, 32770, 512, 0, False), (1025, 9000, 1152, 0, True), (2000, 5250, 4224, 0, False), (700, 16400, 640, 5, True),
         (1500, 7000, 12416, 32, False), (1300, 8200, 2560, 64, True), (900, 12300, 512, 100, False)]
 
 
