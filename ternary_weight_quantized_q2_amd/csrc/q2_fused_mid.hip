@@ -19,14 +19,19 @@ __device__ __forceinline__ int mid_swz(int r) { return ((r >> 2) & 3) | ((r & 3)
 // wave (kg, wn) computes the 64 columns wn from every KG-th unit of blocks (a
 // unit is what one 16-byte load of a lane holds: two 2-bit blocks, one 4-bit
 // block), so a block is decoded once per workgroup.  Rows go to LDS by direct
-// copies, a set of KG blocks per stage, two stages; codes and scales of the next
-// unit to registers while this one is computed.  One barrier per stage waits
-// for both.  Each wave sums its rows on the matrix cores itself (a quarter of
+// copies, a set of KG blocks per stage, two stages; one barrier per stage waits
+// for them.  Codes of the next unit are loaded to registers of their own while
+// this one is computed (ROLL = false), or, in tiles of 64 rows, which have no
+// room for them, column tile by column tile as this one's are decoded: 64 x 160
+// tiles then fit 256 registers, and 64 x 128 ones gained 3 %, 32-row ones lost 4 %.
+// x and the codes are addressed with a scalar block offset (buffer loads): 8 % less
+// time for 20 rows per expert than 64-bit addresses.  Each wave sums its rows on the matrix cores itself (a quarter of
 // its products; sharing the sums would need a second barrier).
 template <int FMT, int MT, int NT, int NW, int KG, int OCC>
 __global__ __launch_bounds__(64 * NW * KG, OCC) void fused_mid_kernel(FusedArgs a, int tiles_n, int group_m) {
   constexpr int W = NW * KG, BM = 16 * MT, BN = 16 * NT * NW;
   constexpr int U = (FMT == 0) ? 2 : 1;                  // blocks per unit
+  constexpr bool ROLL = MT > 2;
   constexpr int STAGE = KG * BM * 256;
   constexpr int STRIDE = BN + 4;                         // floats per row of the output tile
   constexpr int RG = BM / 4;                             // copies of four rows per block
@@ -65,7 +70,7 @@ __global__ __launch_bounds__(64 * NW * KG, OCC) void fused_mid_kernel(FusedArgs 
   const uint16_t* const zbase = (FMT == 1) ? a.z + rt.expert * a.N * (K / BLOCK_K) : nullptr;
   uint32_t woff[NT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) woff[j] = (uint32_t)(wrow(16 * (NT * wn + j) + c) * row_bytes);
+  for (int j = 0; j < NT; ++j) woff[j] = (uint32_t)(wrow(16 * (NT * wn + j) + c) * row_bytes) + 16u * g;
   // Scales (low half) and zero points (high half) of CHUNK blocks and the tile's
   // columns sit in LDS as [block][column], two chunks in turn: a half-word per
   // lane, column and block straight from global memory cost up to a sixth of the
@@ -100,40 +105,36 @@ __global__ __launch_bounds__(64 * NW * KG, OCC) void fused_mid_kernel(FusedArgs 
 
   // Copy r of this wave: rows 4 (RPW wn + r) .. + 3 of its group's block, lane l
   // row l / 16 of them and position l % 16.
-  const uint16_t* xp[RPW];
+  uint32_t xoff[RPW];
 #pragma unroll
   for (int r = 0; r < RPW; ++r) {
     const int row = 4 * (RPW * wn + r) + (lane >> 4);
     const int64_t m = m0 + (row < rows ? row : rows - 1);
     int64_t src = a.row_index ? (int64_t)a.row_index[m] : m;
     if (src < 0 || src >= a.x_rows) src = 0;             // read row 0; the result is cleared at the end
-    xp[r] = a.x + src * K + 8 * ((lane & 15) ^ mid_swz(row & 15));
+    xoff[r] = (uint32_t)((a.row_index ? src : src - m0) * K * 2) + 16u * ((lane & 15) ^ mid_swz(row & 15));
   }
+  const __amdgpu_buffer_rsrc_t rx = a.row_index ? buf_rsrc(a.x, (uint32_t)(a.x_rows * K * 2))
+                                                : buf_rsrc(a.x + m0 * K, (uint32_t)(rows * K * 2));
+  const __amdgpu_buffer_rsrc_t rw = buf_rsrc(wbase, (uint32_t)(a.N * row_bytes));
   const int units = (KB + U - 1) / U, NS = (units + KG - 1) / KG * U;     // stages
   auto block_of = [&](int s) { return (KG * (s / U) + kg) * U + s % U; };
   auto copy_stage = [&](int s) {
     const int blk = min(block_of(s), KB - 1);            // past the end: the last block again, never used
 #pragma unroll
     for (int r = 0; r < RPW; ++r) {
-      // through a local: with an array element in the address the host pass drops the kernel's launch stub
-      const uint16_t* p = xp[r] + (int64_t)blk * BLOCK_K;
-      __builtin_amdgcn_global_load_lds(
-          p, (lds_void*)(smem + (s & 1) * STAGE + kg * BM * 256 + (RPW * wn + r) * 1024), 16, 0, 0);
+      const uint32_t xo = xoff[r];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rx, (lds_void*)(smem + (s & 1) * STAGE + kg * BM * 256 + (RPW * wn + r) * 1024), 16, xo,
+          (uint32_t)blk * 256u, 0, 0);
     }
   };
-  q2_u32x4 wnext[NT];
-  auto load_unit = [&](int n) {
-    const int b0 = (KG * n + kg) * U;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      if constexpr (FMT == 0) {
-        const int b = min(b0 + (g >> 1), KB - 1);
-        wnext[j] = *reinterpret_cast<const q2_u32x4*>(wbase + (woff[j] + (uint32_t)(b * 32 + 16 * (g & 1))));
-      } else {
-        const int b = min(b0, KB - 1);
-        wnext[j] = *reinterpret_cast<const q2_u32x4*>(wbase + (woff[j] + (uint32_t)(b * 64 + 16 * g)));
-      }
-    }
+  q2_u32x4 w[NT], wnext[ROLL ? 1 : NT];                  // this lane's 16 bytes of a unit's codes
+  auto load_codes = [&](int j, int n) {
+    const uint32_t so = (uint32_t)((KG * n + kg) * U) * (FMT == 0 ? 32u : 64u);
+    const q2_u32x4 v = __builtin_bit_cast(q2_u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, woff[j], so, 0));
+    if constexpr (ROLL) w[j] = v;
+    else wnext[j] = v;
   };
 
   q2_f32x4 acc[MT][NT];
@@ -147,7 +148,7 @@ __global__ __launch_bounds__(64 * NW * KG, OCC) void fused_mid_kernel(FusedArgs 
   const uint32_t sone = (FMT == 0) ? 0xBFA0BFA0u : 0x3F803F80u;   // bf16 -1.25 / 1 pairs
   const q2_u32x4 sones = q2_u32x4{sone, sone, sone, sone};
 
-  auto compute = [&](const uint8_t* st, const uint32_t (&w)[NT][(FMT == 0) ? 2 : 4], int blk) {
+  auto compute = [&](const uint8_t* st, int half, int blk, int next) {
     const uint32_t* const sp = szl + (blk & (2 * CHUNK - 1)) * BN;
     q2_u32x4 av[MT][4];
     q2_f32x4 sum[MT];
@@ -169,17 +170,20 @@ __global__ __launch_bounds__(64 * NW * KG, OCC) void fused_mid_kernel(FusedArgs 
       float zc = 0.f;
       uint64_t pz;
       if constexpr (FMT == 0) {
-        bf[0] = q2_frag<0>(w[j][0], kc);
-        bf[1] = q2_frag<1>(w[j][0], kc);
-        bf[2] = q2_frag<0>(w[j][1], kc);
-        bf[3] = q2_frag<1>(w[j][1], kc);
-        pz = q2_part_zero(w[j]);
+        const uint32_t w2[2] = {w[j][2 * half], w[j][2 * half + 1]};
+        bf[0] = q2_frag<0>(w2[0], kc);
+        bf[1] = q2_frag<1>(w2[0], kc);
+        bf[2] = q2_frag<0>(w2[1], kc);
+        bf[3] = q2_frag<1>(w2[1], kc);
+        pz = q2_part_zero(w2);
       } else {
+        const uint32_t w4[4] = {w[j][0], w[j][1], w[j][2], w[j][3]};
 #pragma unroll
-        for (int t = 0; t < 4; ++t) bf[t] = q4_frag(w[j][t], kc);
+        for (int t = 0; t < 4; ++t) bf[t] = q4_frag(w4[t], kc);
         zc = f16_to_f32((uint16_t)(sv >> 16));
-        pz = q4_part_zero(w[j], zc);
+        pz = q4_part_zero(w4, zc);
       }
+      if (ROLL && next >= 0) load_codes(j, next);
       const float dc = f16_to_f32((uint16_t)zero_where(sv & 0xFFFFu, column_all(pz)));
       const float k4 = -dc * (1.f + zc * 0.0625f);
       q2_f32x4 tmp[MT];
@@ -212,47 +216,47 @@ __global__ __launch_bounds__(64 * NW * KG, OCC) void fused_mid_kernel(FusedArgs 
   if (KB > 0) {
     load_scales(0);
     copy_stage(0);
-    load_unit(0);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) load_codes(j, 0);
     store_scales(0);
   }
   for (int n = 0; n * U < NS; ++n) {
+    const int b0 = (KG * n + kg) * U;
+    stage_barrier<ROLL ? NT : 0>();                      // the unit's codes may still be in flight
+    stage_scales(U * n);
+    if constexpr (!ROLL)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) w[j] = wnext[j];
     if constexpr (FMT == 0) {
+      copy_stage(2 * n + 1);
       // two stages per unit; the swaps bring 64 bytes per column into the matrix layout of two blocks
-      stage_barrier<0>();
-      stage_scales(2 * n);
-      uint32_t w0[NT][2], w1[NT][2];
-      const int b0 = (KG * n + kg) * U;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          auto r = __builtin_amdgcn_permlane16_swap(wnext[j][q], wnext[j][2 + q], false, false);
+          auto r = __builtin_amdgcn_permlane16_swap(w[j][q], w[j][2 + q], false, false);
           r = __builtin_amdgcn_permlane32_swap(r[0], r[1], false, false);
-          w0[j][q] = r[0];
-          w1[j][q] = r[1];
+          w[j][q] = r[0];
+          w[j][2 + q] = r[1];
         }
-      copy_stage(2 * n + 1);
-      if (b0 < KB) compute(smem + kg * BM * 256, w0, b0);
+      if (b0 < KB) compute(smem + kg * BM * 256, 0, b0, -1);
       stage_barrier<0>();
       stage_scales(2 * n + 1);
       if (2 * n + 2 < NS) {
         copy_stage(2 * n + 2);
-        load_unit(n + 1);
+        if constexpr (!ROLL)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) load_codes(j, n + 1);
       }
-      if (b0 + 1 < KB) compute(smem + STAGE + kg * BM * 256, w1, b0 + 1);
+      if (b0 + 1 < KB) compute(smem + STAGE + kg * BM * 256, 1, b0 + 1, n + 1);
     } else {
-      stage_barrier<0>();
-      stage_scales(n);
-      uint32_t w[NT][4];
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) w[j][q] = wnext[j][q];
       if (n + 1 < NS) {
         copy_stage(n + 1);
-        load_unit(n + 1);
+        if constexpr (!ROLL)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) load_codes(j, n + 1);
       }
-      if (block_of(n) < KB) compute(smem + (n & 1) * STAGE + kg * BM * 256, w, block_of(n));
+      if (b0 < KB) compute(smem + (n & 1) * STAGE + kg * BM * 256, 0, b0, n + 1);
     }
   }
   __builtin_amdgcn_s_waitcnt(0);
@@ -341,26 +345,70 @@ static hipError_t run_mid(const FusedArgs& a, hipStream_t stream) {
   const int64_t tiles_n = (fused_n_out(a) + cols - 1) / cols, slots = max_row_tiles(a, BM);
   if (tiles_n > 0x7fffffff || slots > 0x7fffffff / tiles_n) return hipErrorInvalidValue;
   const int group_m = tile_group_rows(slots, tiles_n, 2.0 * BM * (double)a.K,
-                                      (double)BN * a.K * (FMT == 0 ? 0.265625 : 0.53125), 64);
+                                      (double)BN * a.K * (FMT == 0 ? 0.265625 : 0.53125), KG > 2 ? 32 : 64);
   hipLaunchKernelGGL((fused_mid_kernel<FMT, MT, NT, NW, KG, OCC>), dim3((unsigned)(slots * tiles_n)), dim3(64 * NW * KG), 0,
                      stream, a, (int)tiles_n, group_m);
   return hipGetLastError();
 }
 
+// Offsets of 32 bits: from an expert's weight; from a tile's first row of x, with
+// a row index from the first row.
 bool fused_mid_takes(const FusedArgs& a, int fmt) {
-  return a.K >= 4 * BLOCK_K && a.N <= ((int64_t)1 << 32) / (fmt == 0 ? a.K / 4 : a.K / 2);
+  const int64_t most = ((int64_t)1 << 32) - 1;
+  return a.K >= 4 * BLOCK_K && a.K <= ((int64_t)1 << 24) && a.N <= most / (fmt == 0 ? a.K / 4 : a.K / 2) &&
+         (!a.row_index || a.x_rows <= most / (2 * a.K));
+}
+
+// The tile.  K split over four or eight groups of waves makes a workgroup take a
+// CU for itself, so 256 of them are a round; two of K split over two share a CU.
+// Of the sizes below the one with the least rounds times the time of a round is
+// taken (K = 2560, 4-bit, us per round: 32 x 64 over eight groups 12.6; over four
+// 32 x 96 14.5, 64 x 64 17.0, 64 x 96 20.5, 64 x 128 23.4, 64 x 160 26.4; over two
+// 64 x 128 28 up to 256 workgroups and 36 up to 512).  So 128 rows, N = 2 x 9728
+// take 64 x 160 (29 us, 36 with 64 x 128 over two), N = 8192 64 x 64, N = 2560
+// 32 x 64 (12.6, 18 over two), 384 rows N = 2 x 9728 64 x 128 over two (69, 75 with
+// 64 x 160).
+// Groups of rows, whose number of tiles is not known here, take K over two, with
+// 64 rows per tile once the mean group fills two of them (128 rows each, K = 2048,
+// 2 x 1408 4-bit: 114 us against 116), else 32 (64 rows each: 69 against 98 with K
+// over four); a launch that can make few tiles only takes 32 x 64.
+template <int FMT>
+static hipError_t pick_mid(const FusedArgs& a, hipStream_t stream) {
+  if (a.offsets) {
+    if (max_row_tiles(a, 32) * ((a.N + 127) / 128) <= 128) return run_mid<FMT, 2, 4, 1, 8, 2>(a, stream);
+    if (a.M >= 128 * a.E) return run_mid<FMT, 4, 4, 2, 2, 2>(a, stream);
+    return run_mid<FMT, 2, 4, 2, 2, 2>(a, stream);
+  }
+  auto tiles = [&](int64_t bm, int64_t bn) {
+    const int64_t cols = a.gated ? bn / 2 : bn;
+    return ((a.M + bm - 1) / bm) * ((fused_n_out(a) + cols - 1) / cols);
+  };
+  const int64_t pairs = tiles(64, 128), rest = pairs % 512;
+  double least = (double)(pairs / 512) * 36. + (rest == 0 ? 0. : rest <= 256 ? 28. : 36.);
+  int pick = 0;
+  auto offer = [&](int id, int64_t bm, int64_t bn, double round) {
+    const double t = (double)((tiles(bm, bn) + 255) / 256) * round;
+    if (t < least) least = t, pick = id;
+  };
+  offer(1, 32, 64, 12.6);
+  offer(2, 32, 96, 14.5);
+  offer(3, 64, 64, 17.0);
+  offer(4, 64, 96, 20.5);
+  offer(5, 64, 128, 23.4);
+  offer(6, 64, 160, 26.4);
+  switch (pick) {
+    case 1: return run_mid<FMT, 2, 4, 1, 8, 2>(a, stream);
+    case 2: return run_mid<FMT, 2, 3, 2, 4, 2>(a, stream);
+    case 3: return run_mid<FMT, 4, 2, 2, 4, 2>(a, stream);
+    case 4: return run_mid<FMT, 4, 3, 2, 4, 2>(a, stream);
+    case 5: return run_mid<FMT, 4, 4, 2, 4, 2>(a, stream);
+    case 6: return run_mid<FMT, 4, 5, 2, 4, 2>(a, stream);
+    default: return run_mid<FMT, 4, 4, 2, 2, 2>(a, stream);
+  }
 }
 
 hipError_t launch_fused_mid(const FusedArgs& a, int fmt, hipStream_t stream) {
-  const int64_t per = a.offsets ? (a.M + a.E - 1) / a.E : a.M;
-  const int64_t tiles = max_row_tiles(a, 32) * ((a.N + 127) / 128);
-  // Few tiles: narrow ones with K over eight groups, so that the chip is covered
-  // (128 rows, K = 9728, N = 2560 4-bit: 30 us against 58 for 32 x 128 tiles).
-  // Otherwise 64 rows per tile once a group fills two of them (384 rows, K = 2560,
-  // 2 x 9728 4-bit: 74 us against 87), 32 below (16 .. 64 rows per expert: 70 against 81).
-  if (tiles <= 128) return fmt == 0 ? run_mid<0, 2, 4, 1, 8, 2>(a, stream) : run_mid<1, 2, 4, 1, 8, 2>(a, stream);
-  if (per >= 128) return fmt == 0 ? run_mid<0, 4, 4, 2, 2, 2>(a, stream) : run_mid<1, 4, 4, 2, 2, 2>(a, stream);
-  return fmt == 0 ? run_mid<0, 2, 4, 2, 2, 2>(a, stream) : run_mid<1, 2, 4, 2, 2, 2>(a, stream);
+  return fmt == 0 ? pick_mid<0>(a, stream) : pick_mid<1>(a, stream);
 }
 
 }  // namespace q2dev

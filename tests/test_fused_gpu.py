@@ -171,6 +171,28 @@ def test_many_rows(m, n, k, r, gated):
     check(y[:, sel], z, "gelu", gated, bias[torch.from_numpy(rows).to(DEV)], gate[sel], res[:, sel])
 
 
+# The tile of the kernel between few and many rows goes by the number of rows and columns.
+TILES = [(40, 500), (40, 9000), (100, 7000), (100, 10000), (100, 16000), (100, 19000), (100, 21010), (130, 13000)]
+
+
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("k", [640, 2176])
+@pytest.mark.parametrize("m,n", TILES)
+def test_tiles(fmt, gated, k, m, n):
+    dev, w = weights(fmt, 319, n, k)
+    cols, rows = sample(n, gated, 319)
+    xb, x = acts(319, m, k)
+    z = O.bf16_to_f64(xb) @ w[rows].T
+    bias = rnd(1, n).to(DEV)
+    res = rnd(3, m, n // 2 if gated else n).to(DEV)
+    y = fused(fmt)(x, *dev, bias=bias, residual=res, activation="silu", gated=gated)
+    sel = torch.from_numpy(cols).to(DEV)
+    check(y[:, sel], z, "silu", gated, bias[torch.from_numpy(rows).to(DEV)], residual=res[:, sel])
+    yb = fused(fmt)(x, *dev, bias=bias, residual=res, activation="silu", gated=gated, out_dtype=torch.bfloat16)
+    assert torch.equal(yb, y.to(torch.bfloat16))
+
+
 @pytest.mark.parametrize("counts,n,k,gated", [([900], 12000, 512, True), ([300, 0, 1, 799], 10010, 640, False),
                                               ([257, 640], 13000, 1152, True)])
 @pytest.mark.parametrize("gather", [False, True])
