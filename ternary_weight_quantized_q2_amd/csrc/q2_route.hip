@@ -74,20 +74,24 @@ __device__ __forceinline__ float wave_sum(float v) {
 // exp(v - top) of a logit, 1 for the largest itself (also when that is +inf).
 __device__ __forceinline__ float route_exp(float v, float top) { return v == top ? 1.0f : __expf(v - top); }
 
-// Choice and weights of one token: lane j < k returns choice j (-1 for none).
+// A token's logits as order-preserving bits, 0 (below every other) for masked ones.
 template <int NE>
-__device__ __forceinline__ void choose(const void* logits, int bf16, int64_t t, int E, int k, int renorm, int lane,
-                                       int& ex, float& wt) {
-  uint32_t key[NE];
+__device__ __forceinline__ void load_keys(const void* logits, int bf16, int64_t t, int E, int lane,
+                                          uint32_t (&key)[NE]) {
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
     const int e = lane + 64 * i;
-    key[i] = 0;                                          // below every unmasked logit
+    key[i] = 0;
     if (e < E) {
       const float v = load_elem(logits, t * E + e, bf16);
       if (v > -__builtin_inff()) key[i] = order_bits(v);
     }
   }
+}
+
+// Choice and weights of one token: lane j < k returns choice j (-1 for none).
+template <int NE>
+__device__ __forceinline__ void choose(uint32_t (&key)[NE], int k, int renorm, int lane, int& ex, float& wt) {
   ex = -1;
   float mine = 0.f, top = 0.f, total = 0.f;
   for (int j = 0; j < k; ++j) {
@@ -151,6 +155,8 @@ __global__ __launch_bounds__(RT_THREADS) void route_choose_kernel(const void* lo
                                                                   int32_t* slot, uint16_t* counts, int pad) {
   __shared__ unsigned long long mask[64 * NE];
   __shared__ int off[64 * NE + 1];
+  // A wave loads the logits of all its tokens at once where they fit.
+  constexpr int AHEAD = NE <= 4 ? RT_TOK / RT_WAVES : 1;
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int64_t first = (int64_t)blockIdx.x * RT_TOK * chunks;
   if constexpr (!ONE)
@@ -161,14 +167,23 @@ __global__ __launch_bounds__(RT_THREADS) void route_choose_kernel(const void* lo
     nt = (int)std::min<int64_t>(T - t0, RT_TOK);
     for (int e = threadIdx.x; e < E; e += RT_THREADS) mask[e] = 0;
     __syncthreads();
-    for (int i = wv; i < nt; i += RT_WAVES) {
-      int ex;
-      float wt;
-      choose<NE>(logits, bf16, t0 + i, E, k, renorm, lane, ex, wt);
-      if (lane < k) {
-        expert[(t0 + i) * k + lane] = ex;
-        weight[(t0 + i) * k + lane] = wt;
-        if (ex >= 0) atomicOr(&mask[ex], 1ull << i);
+    for (int i0 = wv; i0 < nt; i0 += RT_WAVES * AHEAD) {
+      uint32_t key[AHEAD][NE];
+#pragma unroll
+      for (int p = 0; p < AHEAD; ++p)
+        load_keys<NE>(logits, bf16, t0 + std::min(i0 + RT_WAVES * p, nt - 1), E, lane, key[p]);
+#pragma unroll
+      for (int p = 0; p < AHEAD; ++p) {
+        const int i = i0 + RT_WAVES * p;
+        if (i >= nt) break;
+        int ex;
+        float wt;
+        choose<NE>(key[p], k, renorm, lane, ex, wt);
+        if (lane < k) {
+          expert[(t0 + i) * k + lane] = ex;
+          weight[(t0 + i) * k + lane] = wt;
+          if (ex >= 0) atomicOr(&mask[ex], 1ull << i);
+        }
       }
     }
     __syncthreads();
