@@ -8,11 +8,14 @@ namespace q2dev {
 // ============================================================================
 // Router
 // ============================================================================
-// A workgroup of sixteen waves takes 64 tokens, one wave per token at a time.
-// A lane holds every 64th logit as order-preserving bits, 0 for a masked expert
-// or one already chosen; a maximum over the lanes (six data-parallel-primitive
-// moves, no LDS) and a ballot of the lanes that hold it give the largest logit
-// and, among equal ones, the lowest expert.  k such steps are the choice.
+// A workgroup of sixteen waves takes 64 tokens.  Logits are held as
+// order-preserving bits, 0 for a masked expert or one already chosen, and k steps
+// each take the largest and, among equal ones, the lowest expert.  Up to 16
+// choices among up to 256 experts, sixteen lanes work on a token (choose16): a
+// step takes 65 vector instructions for four tokens at E = 128, where a wave per
+// token (choose: lane l holds every 64th logit, a maximum over the lanes by six
+// data-parallel-primitive moves and a ballot of the lanes that hold it) takes 45
+// for one.  The steps' instructions bound the kernel, not the logits' 4 MB.
 //
 // Row plan: each token chooses an expert at most once, so 64 tokens' choices
 // are one 64-bit mask per expert, and a choice's place among the rows of its
@@ -22,7 +25,8 @@ namespace q2dev {
 // workspace and every workgroup of the second adds them up.  That sum is
 // (workgroups)^2, so past 1024 workgroups each takes several chunks of 64
 // tokens instead.  Integer counts: the plan is exact, the same on every run.
-// T = 16384, E = 128, k = 8: see the table of measurements beside launch_route.
+// T = 16384, E = 128, k = 8, bf16 logits: choice 9.5 us (14.8 with a wave per
+// token), plan 6.2; T = 4096, E = 256 both 19 us (23); one token, E = 64: 3.7.
 constexpr int RT_TOK = 64, RT_THREADS = 1024, RT_WAVES = RT_THREADS / 64;
 constexpr int RT_GROUPS = 1024;
 
@@ -39,6 +43,25 @@ __device__ __forceinline__ uint32_t order_bits(float v) {
 }
 __device__ __forceinline__ float from_order_bits(uint32_t o) {
   return __builtin_bit_cast(float, o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+// Logits of experts e0 + step i of a token as order-preserving bits; 0, below
+// every other, for masked experts and past the last one.
+template <int NE>
+__device__ __forceinline__ void load_keys(const void* logits, int bf16, int64_t t, int E, int e0, int step,
+                                          uint32_t (&key)[NE]) {
+  float v[NE];
+  if (bf16) {
+    const uint16_t* p = static_cast<const uint16_t*>(logits) + t * E;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) v[i] = bf16_to_f32(p[min(e0 + step * i, E - 1)]);
+  } else {
+    const float* p = static_cast<const float*>(logits) + t * E;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) v[i] = p[min(e0 + step * i, E - 1)];
+  }
+#pragma unroll
+  for (int i = 0; i < NE; ++i) key[i] = e0 + step * i < E && v[i] > -__builtin_inff() ? order_bits(v[i]) : 0u;
 }
 
 // v from the lane that CTRL names, 0 where there is none.
@@ -74,24 +97,12 @@ __device__ __forceinline__ float wave_sum(float v) {
 // exp(v - top) of a logit, 1 for the largest itself (also when that is +inf).
 __device__ __forceinline__ float route_exp(float v, float top) { return v == top ? 1.0f : __expf(v - top); }
 
-// A token's logits as order-preserving bits, 0 (below every other) for masked ones.
-template <int NE>
-__device__ __forceinline__ void load_keys(const void* logits, int bf16, int64_t t, int E, int lane,
-                                          uint32_t (&key)[NE]) {
-#pragma unroll
-  for (int i = 0; i < NE; ++i) {
-    const int e = lane + 64 * i;
-    key[i] = 0;
-    if (e < E) {
-      const float v = load_elem(logits, t * E + e, bf16);
-      if (v > -__builtin_inff()) key[i] = order_bits(v);
-    }
-  }
-}
-
 // Choice and weights of one token: lane j < k returns choice j (-1 for none).
 template <int NE>
-__device__ __forceinline__ void choose(uint32_t (&key)[NE], int k, int renorm, int lane, int& ex, float& wt) {
+__device__ __forceinline__ void choose(const void* logits, int bf16, int64_t t, int E, int k, int renorm, int lane,
+                                       int& ex, float& wt) {
+  uint32_t key[NE];
+  load_keys<NE>(logits, bf16, t, E, lane, 64, key);
   ex = -1;
   float mine = 0.f, top = 0.f, total = 0.f;
   for (int j = 0; j < k; ++j) {
@@ -130,6 +141,70 @@ __device__ __forceinline__ void choose(uint32_t (&key)[NE], int k, int renorm, i
   wt = ex >= 0 ? mine / total : 0.f;
 }
 
+// Up to 16 choices among up to 256 experts: sixteen lanes per token, four tokens
+// of a wave together.  Lane l of a token holds experts NK l .. NK l + NK - 1, so
+// the lowest expert among equal logits is in the lowest lane.  Rotations within
+// the sixteen lanes leave the maximum (and the sum, whose four additions are the
+// same pairs in every lane) in all of them.
+template <int N>
+__device__ __forceinline__ uint32_t ror16(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 | N, 0xF, 0xF, true);
+}
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+  v = max(v, ror16<8>(v));
+  v = max(v, ror16<4>(v));
+  v = max(v, ror16<2>(v));
+  return max(v, ror16<1>(v));
+}
+__device__ __forceinline__ float sum16(float v) {
+  auto add = [](float a, uint32_t b) { return a + __builtin_bit_cast(float, b); };
+  v = add(v, ror16<8>(__builtin_bit_cast(uint32_t, v)));
+  v = add(v, ror16<4>(__builtin_bit_cast(uint32_t, v)));
+  v = add(v, ror16<2>(__builtin_bit_cast(uint32_t, v)));
+  return add(v, ror16<1>(__builtin_bit_cast(uint32_t, v)));
+}
+
+// Lane l < k of the token's sixteen returns choice l.
+template <int NK>
+__device__ __forceinline__ void choose16(const void* logits, int bf16, int64_t t, int E, int k, int renorm, int l,
+                                         int& ex, float& wt) {
+  uint32_t key[NK];
+  load_keys<NK>(logits, bf16, t, E, NK * l, 1, key);
+  ex = -1;
+  float mine = 0.f, top = 0.f, total = 0.f;
+  for (int j = 0; j < k; ++j) {
+    uint32_t m = key[0];
+#pragma unroll
+    for (int i = 1; i < NK; ++i) m = max(m, key[i]);
+    m = max16(m);
+    if (__builtin_amdgcn_ballot_w64(m != 0) == 0) break; // nothing left in any of the four tokens
+    const float v = from_order_bits(m);
+    if (j == 0) {
+      top = v;
+      if (!renorm) {
+#pragma unroll
+        for (int i = 0; i < NK; ++i)
+          if (key[i] != 0) total += route_exp(from_order_bits(key[i]), top);
+        total = sum16(total);
+      }
+    }
+    const float p = m != 0 ? route_exp(v, top) : 0.f;
+    if (renorm) total += p;                              // largest first
+    // the complement of the lowest expert that holds m; a token with none left has every key 0
+    uint32_t at = 0;
+#pragma unroll
+    for (int i = NK - 1; i >= 0; --i) at = key[i] == m ? ~(uint32_t)(NK * l + i) : at;
+    const int e = (int)~max16(at), own = e - NK * l;
+#pragma unroll
+    for (int i = 0; i < NK; ++i) key[i] = i == own ? 0u : key[i];
+    if (l == j && m != 0) {
+      ex = e;
+      mine = p;
+    }
+  }
+  wt = ex >= 0 ? mine / total : 0.f;
+}
+
 // Offsets of the experts from their totals in tot[] (replaced), by one wave.
 __device__ __forceinline__ void scan_experts(int* tot, int E, int lane) {
   int run = 0;
@@ -148,15 +223,13 @@ __device__ __forceinline__ void scan_experts(int* tot, int E, int lane) {
   if (lane == 0) tot[E] = run;
 }
 
-template <int NE, bool ONE>
+template <int NE, int LANES, bool ONE>
 __global__ __launch_bounds__(RT_THREADS) void route_choose_kernel(const void* logits, int bf16, int64_t T, int E, int k,
                                                                   int renorm, int chunks, int32_t* expert,
                                                                   float* weight, int32_t* offsets, int32_t* row_token,
                                                                   int32_t* slot, uint16_t* counts, int pad) {
-  __shared__ unsigned long long mask[64 * NE];
-  __shared__ int off[64 * NE + 1];
-  // A wave loads the logits of all its tokens at once where they fit.
-  constexpr int AHEAD = NE <= 4 ? RT_TOK / RT_WAVES : 1;
+  __shared__ unsigned long long mask[LANES * NE];
+  __shared__ int off[LANES * NE + 1];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int64_t first = (int64_t)blockIdx.x * RT_TOK * chunks;
   if constexpr (!ONE)
@@ -167,23 +240,19 @@ __global__ __launch_bounds__(RT_THREADS) void route_choose_kernel(const void* lo
     nt = (int)std::min<int64_t>(T - t0, RT_TOK);
     for (int e = threadIdx.x; e < E; e += RT_THREADS) mask[e] = 0;
     __syncthreads();
-    for (int i0 = wv; i0 < nt; i0 += RT_WAVES * AHEAD) {
-      uint32_t key[AHEAD][NE];
-#pragma unroll
-      for (int p = 0; p < AHEAD; ++p)
-        load_keys<NE>(logits, bf16, t0 + std::min(i0 + RT_WAVES * p, nt - 1), E, lane, key[p]);
-#pragma unroll
-      for (int p = 0; p < AHEAD; ++p) {
-        const int i = i0 + RT_WAVES * p;
-        if (i >= nt) break;
-        int ex;
-        float wt;
-        choose<NE>(key[p], k, renorm, lane, ex, wt);
-        if (lane < k) {
-          expert[(t0 + i) * k + lane] = ex;
-          weight[(t0 + i) * k + lane] = wt;
-          if (ex >= 0) atomicOr(&mask[ex], 1ull << i);
-        }
+    constexpr int AT_ONCE = 64 / LANES;                  // tokens of a wave
+    const int l = lane % LANES;
+    for (int i0 = wv * AT_ONCE; i0 < nt; i0 += RT_WAVES * AT_ONCE) {
+      const int i = i0 + lane / LANES;
+      const int64_t t = t0 + min(i, nt - 1);             // past the last token: the last one again, not stored
+      int ex;
+      float wt;
+      if constexpr (LANES == 16) choose16<NE>(logits, bf16, t, E, k, renorm, l, ex, wt);
+      else choose<NE>(logits, bf16, t, E, k, renorm, l, ex, wt);
+      if (l < k && i < nt) {
+        expert[t * k + l] = ex;
+        weight[t * k + l] = wt;
+        if (ex >= 0) atomicOr(&mask[ex], 1ull << i);
       }
     }
     __syncthreads();
@@ -286,18 +355,18 @@ size_t route_workspace_bytes(int64_t T, int64_t E) {
   return T > RT_TOK ? ((size_t)route_groups(T) * route_pad(E) * 2 + 255) & ~(size_t)255 : 0;
 }
 
-template <int NE>
+template <int NE, int LANES>
 static hipError_t run_route(const void* logits, int bf16, int64_t T, int E, int k, int renorm, int32_t* expert,
                             float* weight, int32_t* offsets, int32_t* row_token, int32_t* slot, uint16_t* counts,
                             hipStream_t stream) {
   const int pad = route_pad(E);
   if (T <= RT_TOK) {
-    hipLaunchKernelGGL((route_choose_kernel<NE, true>), dim3(1), dim3(RT_THREADS), 0, stream, logits, bf16, T, E, k,
+    hipLaunchKernelGGL((route_choose_kernel<NE, LANES, true>), dim3(1), dim3(RT_THREADS), 0, stream, logits, bf16, T, E, k,
                        renorm, 1, expert, weight, offsets, row_token, slot, counts, pad);
     return hipGetLastError();
   }
   const int chunks = route_chunks(T), groups = (int)route_groups(T);
-  hipLaunchKernelGGL((route_choose_kernel<NE, false>), dim3(groups), dim3(RT_THREADS), 0, stream, logits, bf16, T, E,
+  hipLaunchKernelGGL((route_choose_kernel<NE, LANES, false>), dim3(groups), dim3(RT_THREADS), 0, stream, logits, bf16, T, E,
                      k, renorm, chunks, expert, weight, offsets, row_token, slot, counts, pad);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -315,13 +384,17 @@ hipError_t launch_route(const void* logits, int logits_bf16, int64_t T, int64_t 
   }
   uint16_t* counts = static_cast<uint16_t*>(ws);
   const int n = (int)E;
-#define Q2_ROUTE(NE) \
-  return run_route<NE>(logits, logits_bf16, T, n, k, renorm, expert, weight, offsets, row_token, slot, counts, stream)
-  if (n <= 64) Q2_ROUTE(1);
-  if (n <= 128) Q2_ROUTE(2);
-  if (n <= 256) Q2_ROUTE(4);
-  if (n <= 512) Q2_ROUTE(8);
-  Q2_ROUTE(16);
+#define Q2_ROUTE(NE, LANES)                                                                                          \
+  return run_route<NE, LANES>(logits, logits_bf16, T, n, k, renorm, expert, weight, offsets, row_token, slot, counts, \
+                              stream)
+  if (k <= 16 && n <= 64) Q2_ROUTE(4, 16);
+  if (k <= 16 && n <= 128) Q2_ROUTE(8, 16);
+  if (k <= 16 && n <= 256) Q2_ROUTE(16, 16);
+  if (n <= 64) Q2_ROUTE(1, 64);
+  if (n <= 128) Q2_ROUTE(2, 64);
+  if (n <= 256) Q2_ROUTE(4, 64);
+  if (n <= 512) Q2_ROUTE(8, 64);
+  Q2_ROUTE(16, 64);
 #undef Q2_ROUTE
 }
 

@@ -52,6 +52,19 @@ def test_route(t, e, k, dtype, renorm):
     check_route((rnd(t + e, t, e) * 3).to(dtype), k, renorm)
 
 
+@pytest.mark.parametrize("t", [1, 61, 130])
+@pytest.mark.parametrize("e,k", [(64, 8), (61, 17), (100, 16), (128, 17), (130, 8), (256, 30), (300, 5), (1000, 12)])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_ties_at_every_size(t, e, k, renorm):
+    """Few values, many of them masked: equal logits go to the lower expert wherever the experts are held."""
+    v = torch.randint(-2, 3, (t, e), generator=torch.Generator().manual_seed(3)).float()
+    v[torch.rand((t, e), generator=torch.Generator().manual_seed(4)) < 0.6] = -np.inf
+    v[t // 2, 3:] = -np.inf
+    v[t // 3, : e // 2] = np.nan
+    check_route(v, k, renorm)
+    check_route(v.bfloat16(), k, renorm)
+
+
 @pytest.mark.parametrize("t", [40, 300])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_route_ties_masks_and_extremes(t, renorm):
