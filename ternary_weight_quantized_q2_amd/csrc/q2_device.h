@@ -114,14 +114,11 @@ __device__ __forceinline__ q2_f32x4 mfma(q2_u32x4 a, q2_u32x4 b, q2_f32x4 c) {
                                                   __builtin_bit_cast(q2_bf16x8, b), c, 0, 0, 0);
 }
 
-// (a & m) | o in one v_and_or_b32.  gfx950 VOP3 encodings take no literal
-// operands, so the two constants are passed in VGPRs (kept live by the caller);
-// written plainly, the compiler splits the expression into an AND and an OR.
-__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t m, uint32_t o) {
-  uint32_t r;
-  asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(m), "v"(o));
-  return r;
-}
+// (a & m) | o, one v_and_or_b32 as long as m and o are opaque registers (gfx950
+// VOP3 encodings take no literals).  Not an asm block: the result feeds a matrix
+// instruction, which must not follow its writer too closely, and the compiler
+// leaves room only behind instructions that it knows.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t m, uint32_t o) { return (a & m) | o; }
 
 // Decoder constants: mask of the code field in each 16-bit half, and the bf16
 // pattern of 1.0 in both halves.
