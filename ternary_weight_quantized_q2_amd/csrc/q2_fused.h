@@ -259,7 +259,7 @@ __device__ __forceinline__ bool find_tile(const FusedArgs& a, int bm, int tiles_
   const int tile = xcd_tile((int)blockIdx.x, tiles);
   int slot = tile / tiles_n;
   tn = tile - slot * tiles_n;
-  for (int64_t e0 = 0;; e0 += 64) {                      // slot < total: ends at its group
+  for (int64_t e0 = 0; e0 < a.E; e0 += 64) {             // slot < total: found before the last group's end
     if (e0 > 0) mine = group_tiles(a, e0 + lane, bm, lo, hi);
     int sum = mine;                                      // inclusive sum over the lanes
 #pragma unroll
@@ -277,6 +277,7 @@ __device__ __forceinline__ bool find_tile(const FusedArgs& a, int bm, int tiles_
     }
     slot -= __builtin_amdgcn_readlane(sum, 63);
   }
+  return false;                                          // bad offsets whose tiles overflow their sum
 }
 
 // At most this many row tiles of bm rows over all groups: each of the at most

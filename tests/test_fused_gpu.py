@@ -387,8 +387,9 @@ COUNTS = [[5], [0, 3, 0, 0, 1], [17, 0, 40, 1, 33], [1] * 8, [0] * 3 + [130], [3
 @pytest.mark.parametrize("fmt", ["q2", "q4"])
 @pytest.mark.parametrize("counts", COUNTS, ids=lambda c: f"{len(c)}x{sum(c)}")
 @pytest.mark.parametrize("gather", [False, True])
-def test_grouped(fmt, counts, gather):
-    n, k = 2 * 45, 384
+@pytest.mark.parametrize("k", [384, 640])
+def test_grouped(fmt, counts, gather, k):
+    n = 2 * 45
     lead, tail = (0, 0) if gather else (3, 5)
     dev, w, offsets, xb, x, index = group_case(fmt, counts, n, k, x_rows=37 if gather else None, lead=lead, tail=tail)
     z = F.grouped_products(O.bf16_to_f64(xb), w, offsets, index)
@@ -425,8 +426,9 @@ def test_grouped_rows_equal_the_experts_own_linears(fmt, rows_per):
 
 @pytest.mark.parametrize("fmt", ["q2", "q4"])
 @pytest.mark.parametrize("rows", [4, 200])
-def test_grouped_index_outside_x_reads_zeros(fmt, rows):
-    n, k = 64, 256
+@pytest.mark.parametrize("k", [256, 1152])
+def test_grouped_index_outside_x_reads_zeros(fmt, rows, k):
+    n = 64
     counts = [rows, rows]
     dev, w, offsets, xb, x, index = group_case(fmt, counts, n, k, x_rows=9)
     index[::3] = np.array([-1, 9, 2 ** 31 - 1, -2 ** 31] * rows, np.int32)[:len(index[::3])]
@@ -439,15 +441,81 @@ def test_grouped_index_outside_x_reads_zeros(fmt, rows):
 
 @pytest.mark.parametrize("fmt", ["q2", "q4"])
 @pytest.mark.parametrize("bad", [[5, 40, 20, 64], [-7, 20, 90, 64], [0, 2 ** 31 - 1, -2 ** 31, 50], [64, 0, 64, 0]])
-def test_grouped_bad_offsets_stay_inside(fmt, bad):
+@pytest.mark.parametrize("k", [128, 640])
+def test_grouped_bad_offsets_stay_inside(fmt, bad, k):
     """Offsets that decrease or leave [0, R]: only rows of y are written, the rest of its storage is not."""
-    rows, n, k = 64, 40, 128
+    rows, n = 64, 40
     dev, _, _, _, x, _ = group_case(fmt, [rows, 0, 0], n, k)
     flat = torch.full((3 * rows * n,), 7.0, device=DEV)
     y = flat[rows * n:2 * rows * n].view(rows, n)
     grouped(fmt)(x, torch.tensor(bad, dtype=torch.int32, device=DEV), *dev, y=y)
     torch.cuda.synchronize()
     assert (flat[:rows * n] == 7).all() and (flat[2 * rows * n:] == 7).all()
+
+
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
+@pytest.mark.parametrize("counts", [[60, 0, 90, 45, 100], [300, 150, 0, 400]])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("k", [640, 2176])
+def test_grouped_wide(fmt, counts, gather, k):
+    """Enough columns for the wider tiles; rows of no expert hold NaN, which no other row may read."""
+    n, lead, tail = 1320, 3, 5
+    dev, w, offsets, xb, x, index = group_case(fmt, counts, n, k, x_rows=77 if gather else None, lead=lead, tail=tail)
+    if not gather:
+        x[:lead] = np.nan
+        x[-tail:] = np.nan
+    else:
+        index[:lead] = 2 ** 30
+        index[-tail:] = -5
+    z = F.grouped_products(O.bf16_to_f64(xb), w, offsets, index)
+    inside = slice(int(offsets[0]), int(offsets[-1]))
+    expert = torch.from_numpy(np.repeat(np.arange(len(counts)), counts)).to(DEV)
+    bias = rnd(8, len(counts), n).to(DEV)
+    idx = None if index is None else torch.from_numpy(index).to(DEV)
+    for gated, out in ((False, torch.float32), (True, torch.bfloat16), (True, torch.float32)):
+        y = torch.full((len(z), n // 2 if gated else n), 7.0, device=DEV, dtype=out)
+        grouped(fmt)(x, torch.from_numpy(offsets).to(DEV), *dev, row_index=idx, bias=bias, activation="silu",
+                     gated=gated, y=y)
+        check(y[inside], z[inside], "silu", gated, bias=bias[expert])
+        assert (y[:lead] == 7).all() and (y[-tail:] == 7).all()
+
+
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
+@pytest.mark.parametrize("m,n,k", [(3, 200, 512), (40, 300, 640), (100, 16000, 640), (50, 70, 256), (900, 8200, 512)])
+def test_non_finite_rows_stay_alone(fmt, m, n, k):
+    """A row of x that holds an infinity or a NaN has no finite product; every other row is what it is without it."""
+    dev, _ = weights(fmt, 341, n, k)
+    _, x = acts(341, m, k)
+    want = fused(fmt)(x, *dev)
+    bad = x.clone()
+    bad[1, 5], bad[2, k - 1] = np.inf, np.nan
+    got = fused(fmt)(bad, *dev)
+    assert not torch.isfinite(got[1:3]).any()
+    keep = torch.ones(m, dtype=torch.bool, device=DEV)
+    keep[1:3] = False
+    assert torch.equal(got[keep], want[keep]) and torch.isfinite(want).all()
+
+
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
+@pytest.mark.parametrize("rows,k", [(3, 128), (3, 640), (60, 256), (200, 640), (1100, 512)])
+def test_grouped_without_a_row_of_x(fmt, rows, k):
+    """An index into no rows: every product is empty, the epilogue remains."""
+    n = 2400
+    dev, _ = weights(fmt, 342, 2 * n, k)
+    bias = rnd(9, 2, n).to(DEV)
+    y = grouped(fmt)(torch.empty((0, k), device=DEV, dtype=torch.bfloat16),
+                     torch.tensor([0, 1, rows], dtype=torch.int32, device=DEV), *(t.view(2, n, -1) for t in dev),
+                     row_index=torch.zeros(rows, dtype=torch.int32, device=DEV), bias=bias, activation="relu")
+    assert torch.equal(y[:1], bias[:1].clamp(min=0)) and torch.equal(y[1:], bias[1:].clamp(min=0).expand(rows - 1, n))
+
+
+@pytest.mark.parametrize("m", [1, 30])
+def test_branch_of_an_empty_sum(m):
+    n, r = 48, 4
+    e = lambda *shape, dtype=torch.float16: torch.empty(shape, dtype=dtype, device=DEV)      # noqa: E731
+    y = q2.q2_linear_fused(e(m, 0, dtype=torch.bfloat16), e(n, 0, dtype=torch.uint8), e(n, 0), e(r, 0),
+                           torch.ones((n, r), device=DEV).half())
+    assert y.shape == (m, n) and (y == 0).all()
 
 
 # ---------------------------------------------------------------------------
@@ -465,6 +533,10 @@ def stream_cases():
         _, x = acts(331, m, 512)
         out.append((f"q2 {m}", lambda x: q2.q2_linear_fused(x, p, s, A, B, activation="silu", gated=True), x))
         out.append((f"q4 {m}", lambda x: q2.q4_linear_fused(x, *dev4, activation="gelu"), x))
+    (pw, sw), _ = weights("q2", 333, 12300, 512)
+    Bw = dev_bits(I.lowrank_factors(330, 8, 512, 12300)[1], torch.float16)
+    _, x = acts(331, 900, 512)
+    out.append(("q2 900", lambda x: q2.q2_linear_fused(x, pw, sw, A, Bw, activation="silu"), x))
     for counts in ([1, 0, 2, 1], [100, 0, 37, 163]):
         dev, _, offsets, _, x, _ = group_case("q2", counts, 64, 512, seed=332)
         off = torch.from_numpy(offsets).to(DEV)
@@ -508,6 +580,29 @@ def test_graph_replays_equal_eager_calls():
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(y, want), f"{name}: replay {i}"
+
+
+def test_two_graphs_and_an_eager_call_at_once():
+    """Two captured calls replayed on two streams while a third runs eagerly: each has scratch of its own."""
+    for name, call, x in stream_cases():
+        streams, xs, ys, graphs = [torch.cuda.Stream() for _ in range(2)], [], [], []
+        want = [call(torch.roll(x, i, dims=1).contiguous()) for i in range(3)]
+        torch.cuda.synchronize()
+        for i in range(2):
+            xs.append(torch.roll(x, i, dims=1).contiguous())
+            torch.cuda.synchronize()
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.stream(streams[i]), torch.cuda.graph(graphs[i], stream=streams[i]):
+                ys.append(call(xs[i]))
+        third = torch.roll(x, 2, dims=1).contiguous()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for i in range(2):
+                with torch.cuda.stream(streams[i]):
+                    graphs[i].replay()
+            eager = call(third)
+            torch.cuda.synchronize()
+            assert torch.equal(eager, want[2]) and torch.equal(ys[0], want[0]) and torch.equal(ys[1], want[1]), name
 
 
 def test_refusals():
