@@ -450,18 +450,25 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
 
   if (a.r > 0) {
     const int r8 = (a.r + 7) & ~7;
-    for (int part = 0; part < 3; ++part)
-      for (int k0 = 0; k0 < r8; k0 += 16) {
-        q2_u32x4 bq[2];
+    for (int k0 = 0; k0 < r8; k0 += 16) {
+      const int q0 = k0 + 8 * h;
+      BranchB bq[2];
+      q2_u32x4 aq[MT][2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) bq[j] = branch_bfrag(a, wcol(32 * j + c), k0 + 8 * h, part);
+      for (int j = 0; j < 2; ++j) bq[j] = branch_bfrag(a, wcol(32 * j + c), q0);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const q2_u32x4 aq = branch_afrag(a, m0 + 32 * i + c, k0 + 8 * h, part);
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) acc[i][j] = mfma32_bf16(aq, bq[j], acc[i][j]);
+        for (int l = 0; l < 2; ++l) aq[i][l] = branch_afrag(a, m0 + 32 * i + c, q0, l != 0);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          acc[i][j] = mfma32_bf16(aq[i][0], bq[j].hi, acc[i][j]);
+          acc[i][j] = mfma32_bf16(aq[i][0], bq[j].lo, acc[i][j]);
+          acc[i][j] = mfma32_bf16(aq[i][1], bq[j].hi, acc[i][j]);
         }
-      }
+    }
   }
 
   // Out through a strip of 32 rows x 64 columns per wave.

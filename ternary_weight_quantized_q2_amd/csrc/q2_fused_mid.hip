@@ -301,19 +301,24 @@ __global__ __launch_bounds__(64 * NW * KG, OCC) void fused_mid_kernel(FusedArgs 
     if (FMT == 0 && a.r > 0) {
       // (x A^T) B^T as T_hi B_hi + T_hi B_lo + T_lo B_hi in bf16
       const int r8 = (a.r + 7) & ~7;
-      for (int prt = 0; prt < 3; ++prt)
-        for (int k0 = 0; k0 < r8; k0 += 32) {
-          const int q0 = k0 + 8 * g;
-          q2_u32x4 bq[NT];
+      for (int k0 = 0; k0 < r8; k0 += 32) {
+        const int q0 = k0 + 8 * g;
+        q2_u32x4 aq[MT][2];
 #pragma unroll
-          for (int j = 0; j < NT; ++j) bq[j] = branch_bfrag(a, wrow(16 * (NT * wn + j) + c), q0, prt);
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int l = 0; l < 2; ++l) aq[i][l] = branch_afrag(a, m0 + 16 * i + c, q0, l != 0);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const BranchB bq = branch_bfrag(a, wrow(16 * (NT * wn + j) + c), q0);
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
-            const q2_u32x4 aq = branch_afrag(a, m0 + 16 * i + c, q0, prt);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) acc[i][j] = mfma(aq, bq[j], acc[i][j]);
+            acc[i][j] = mfma(aq[i][0], bq.hi, acc[i][j]);
+            acc[i][j] = mfma(aq[i][0], bq.lo, acc[i][j]);
+            acc[i][j] = mfma(aq[i][1], bq.hi, acc[i][j]);
           }
         }
+      }
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i)
