@@ -125,19 +125,21 @@ __global__ __launch_bounds__(256) void fused_tile_kernel(FusedArgs a, int tiles_
 }
 
 // The f16 kernel for Q2_0 weights, from the sizes alone (the workspace goes by
-// them too).  Its 128 x 256 tiles must cover most of the chip's 256 CUs, the
+// them too).  Its 128 x 256 tiles must cover half of the chip's 256 CUs, the
 // columns must be enough to pay for converting x, and groups must fill their
 // tiles.  Measured, this kernel / the one of q2_fused_mid.hip, in us: K = 4096,
-// N = 12288: M = 512 (192 tiles) 75 / 71, M = 640 (240) 79 / 89, M = 1024 (384)
-// 117 / 136; M = 2048, N = 4096 84 / 93; M = 4096, N = 2048 88 / 90; M = 8192,
-// K = 2048, N = 1024 59 / 52.  32 groups, K = 2048, N = 2 x 1408: 4096 rows (two
-// thirds of the tiles' rows) 94 / 92, 6400 rows 104 / 133.
+// N = 12288: M = 320 (120 tiles) 54 / 48, M = 384 (144) 55 / 65, M = 1024 (384)
+// 111 / 132; M = 1536, N = 4096 64 / 71; M = 4096, N = 2048 80 / 91; M = 4096,
+// K = 12288, N = 1536 192 / 190; M = 8192, K = 2048, N = 1024 53 / 50.  32 groups,
+// K = 2048, N = 2 x 1408: 2048 rows (half of the tiles' rows) 62 / 56, 4096 rows
+// (two thirds) 89 / 91, 6400 rows 98 / 123; K = 1408, N = 2048: 4096 rows 55 / 49,
+// 8192 rows 80 / 83.
 static bool use_f16(int64_t M, int64_t N, int64_t K, int64_t E, int fmt) {
   if (fmt != 0 || !fused_f16_takes(M, N, K)) return false;
   // groups add half a tile each
   const double tiles = (M / 128.0 + (E > 0 ? 0.5 * std::min(E, M) : 0.0)) * std::ceil(N / 256.0);
   const double fill = E > 0 ? (double)M / ((double)M + 64.0 * (double)E) : 1.0;          // rows that are not padding
-  return tiles >= 224.0 && fill >= 0.7 && N >= 2304;
+  return tiles >= 140.0 && fill >= 0.7 && N >= 1536;
 }
 
 size_t fused_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t E, int fmt) {
