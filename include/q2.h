@@ -320,7 +320,8 @@ typedef struct {
  * q2_linear_fused - the Q2_0 linear, optionally with its rank-r branch, with
  * an epilogue: y = epilogue(x W^T + (x A^T) B^T).
  *   x_bf16, packed, scales_f16, A_f16, B_f16, r, M, N, K   as q2_linear_lowrank
- *              (r == 0: A and B are ignored).  x must be finite.
+ *              (r == 0: A and B are ignored).  A row of x that holds an infinity
+ *              or a NaN has no finite product; the other rows are not affected.
  *   epi        host pointer, read before the call returns; NULL is the plain
  *              product in f32
  *   y          f32 or bf16 [M, n_out], overwritten; apart from the residual it

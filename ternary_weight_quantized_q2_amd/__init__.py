@@ -505,7 +505,7 @@ def q2_route(logits, k: int, renormalize: bool = True, workspace=None) -> Route:
     _have(logits, logits.dtype, (t, e), "logits", dev)
     flags = (Q2_ROUTE_LOGITS_BF16 if logits.dtype == torch.bfloat16 else 0) | (Q2_ROUTE_RENORM if renormalize else 0)
     k = int(k)
-    c = max(k, 0)                                          # a refused k still reaches the library's message
+    c = k if 0 < k <= e else 0                             # a refused k allocates nothing and reaches the library's message
     new, i32 = logits.new_empty, torch.int32
     route = Route(new((t, c), dtype=i32), new((t, c), dtype=torch.float32), new(e + 1, dtype=i32),
                   new(t * c, dtype=i32), new((t, c), dtype=i32))

@@ -274,6 +274,11 @@ __device__ __forceinline__ int64_t source_row(const FusedArgs& a, int64_t m) {
   return src >= 0 && src < a.x_rows ? src : a.x_rows;
 }
 
+// M = 4093, K = 12288, N = 4096 1.25 PFLOP/s in this kernel, 8192 x 8192 x 8192
+// 1.28 with the conversion, M = 1536, K = 4096, N = 12288 1.10.  The matrix cores are
+// busy 70 % of the time at the 1.7 GHz that the power limit leaves them; 256-row
+// tiles with half of the decode, deeper prefetch and other orders of the same
+// instructions moved a call by at most 4 %.
 constexpr int FX_BN = 256;                               // weight columns of a workgroup
 constexpr int FX_MAX_BM = 128;
 constexpr int FX_WBUF = 64 * 64;                         // codes of a wave's 64 columns, two blocks

@@ -103,7 +103,7 @@ def test_route_of_no_tokens():
 
 def test_route_refusals():
     x = torch.zeros((2, 8), device=DEV)
-    for k in (0, 9, -1):
+    for k in (0, 9, -1, 10 ** 12):
         with pytest.raises(q2.Q2Error):
             q2.q2_route(x, k)
     with pytest.raises(ValueError, match="float32 or bfloat16"):
