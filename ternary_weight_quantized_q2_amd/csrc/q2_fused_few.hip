@@ -28,6 +28,7 @@ __device__ __forceinline__ uint64_t load4h(const uint16_t* p, int b, int n) {
 
 constexpr int FEW_COLS = 32;                             // weight columns of a workgroup, two 16-column tiles
 constexpr int FEW_WAVES = 16;                            // at most
+constexpr int FEW_BLOCKS = 2;                            // of a wave in a pass
 
 // LDS bytes of one row of x over `blocks` blocks, copied 1 KB at a time: 16 bytes
 // of padding put the 16 rows that a fragment read touches into different banks.
@@ -35,16 +36,16 @@ __host__ __device__ constexpr int few_row_bytes(int blocks) { return (blocks + 3
 
 // A workgroup of kg waves owns up to 16 rows x 32 weight columns (with a gated
 // epilogue the second tile holds the other factors of the first one's
-// outputs).  In each pass wave w takes D consecutive 128-wide blocks.  In the
+// outputs).  In each pass wave w takes two consecutive 128-wide blocks.  In the
 // matrix-core layout lane (c, g) = (lane % 16, lane / 16) holds inputs 32 g ..
 // 32 g + 31 of weight column c and of row c.  A 4-bit block's 64 bytes per
 // column are loaded that way; of 2-bit codes a lane loads 16 of the 64 bytes
 // that two blocks have per column, and two lane-row swaps bring both blocks
 // into the layout (8 bytes per lane and block would touch 32-byte pieces).  The
 // rows of x are staged in LDS, only those that exist.
-template <int FMT, int D, bool SHORT>
+template <int FMT, bool SHORT>
 __global__ __launch_bounds__(64 * FEW_WAVES) void fused_few_kernel(FusedArgs a, int bm, int tiles_n) {
-  constexpr int DW = (FMT == 0) ? 2 : 4;
+  constexpr int DW = (FMT == 0) ? 2 : 4, D = FEW_BLOCKS;
   extern __shared__ __align__(16) uint8_t xs[];
   const int lane = threadIdx.x & 63, kg = blockDim.x >> 6;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -224,36 +225,40 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void fused_few_kernel(FusedArgs a, 
   }
 }
 
-template <int FMT, int D, bool SHORT>
+// Waves of a workgroup, two blocks each per pass: four once that gives the chip
+// a thousand waves, eight, sixteen for fewer workgroups.  Short passes keep few
+// rows of x in LDS and few registers, so more workgroups share a CU.  Measured
+// against four blocks per wave and all of K in one pass where the waves reach, us:
+// 23 tokens to 4 of 32 experts, K = 2560, N = 1408 16.0 / 20.7 (4-bit 20.0 /
+// 22.3); 16 rows, K = 4096, N = 12288 13.3 / 16.6; one row, K = 2560, 2 x 9728
+// 10.0 / 9.8 (4-bit 11.9 / 13.1); K = 4096, N = 4096 (128 workgroups, eight waves)
+// 6.2 / 6.4; K = 9728, N = 2560 (80, sixteen) 10.1 / 10.0.
+template <int FMT, bool SHORT>
 static hipError_t run_few(const FusedArgs& a, int bm, int64_t slots, int64_t tiles_n, hipStream_t stream) {
   const int KB = (int)(a.K / BLOCK_K);
-  // one pass where the waves reach, and at most 64 KB of rows
-  const int rows = (int)std::min<int64_t>(a.M, bm);
-  int kg = std::clamp((KB + D - 1) / D, 1, FEW_WAVES);
-  // The 4-bit kernel's 112 registers leave four waves per SIMD: workgroups of five
-  // waves fit less often than of four, which more than pays for a second pass
-  // (K = 2560: 27.6 -> 22.7 us for 92 rows over 32 experts of 1408 columns).
-  if (FMT == 1 && kg > 4 && slots * tiles_n * kg >= 2048) kg &= ~3;
-  while (kg > 1 && rows * few_row_bytes(kg * D) > 64 * 1024) --kg;
-  const size_t lds = std::max<size_t>((size_t)rows * few_row_bytes(kg * D), (size_t)kg * 16 * (FEW_COLS + 1) * 4);
-  hipLaunchKernelGGL((fused_few_kernel<FMT, D, SHORT>), dim3((unsigned)(slots * tiles_n)), dim3(64 * kg), lds, stream, a,
-                     bm, (int)tiles_n);
+  const int rows = (int)std::min<int64_t>(a.M, bm);      // at most 64 KB of them in LDS
+  const int64_t wgs = slots * tiles_n;
+  int kg = wgs >= 256 ? 4 : wgs >= 128 ? 8 : FEW_WAVES;
+  kg = std::clamp((KB + FEW_BLOCKS - 1) / FEW_BLOCKS, 1, kg);
+  while (kg > 1 && rows * few_row_bytes(kg * FEW_BLOCKS) > 64 * 1024) --kg;
+  const size_t lds = std::max<size_t>((size_t)rows * few_row_bytes(kg * FEW_BLOCKS),
+                                      (size_t)kg * 16 * (FEW_COLS + 1) * 4);
+  hipLaunchKernelGGL((fused_few_kernel<FMT, SHORT>), dim3((unsigned)wgs), dim3(64 * kg), lds, stream, a, bm,
+                     (int)tiles_n);
   return hipGetLastError();
 }
 
 template <int FMT>
 static hipError_t pick_few(const FusedArgs& a, int bm, int64_t slots, int64_t tiles_n, hipStream_t stream) {
-  const int64_t KB = a.K / BLOCK_K;
-  if (KB < 4) return run_few<FMT, 2, true>(a, bm, slots, tiles_n, stream);
-  // Four blocks per wave, two while that leaves the chip short of waves.
-  if (slots * tiles_n * KB < 4 * 2048) return run_few<FMT, 2, false>(a, bm, slots, tiles_n, stream);
-  return run_few<FMT, 4, false>(a, bm, slots, tiles_n, stream);
+  return a.K < 4 * BLOCK_K ? run_few<FMT, true>(a, bm, slots, tiles_n, stream)
+                           : run_few<FMT, false>(a, bm, slots, tiles_n, stream);
 }
 
 hipError_t launch_fused_few(const FusedArgs& a, int fmt, hipStream_t stream) {
-  // Rows per tile: the fewer, the less LDS and the more workgroups share a CU; an
-  // expert with more rows reads its weights again, from the caches.
-  const int bm = a.offsets == nullptr || a.M > 4 * a.E ? 16 : a.M > 2 * a.E ? 8 : 4;
+  // Rows per tile: groups of a few rows take eight (half the LDS, fewer idle tiles
+  // in the launch; 92 rows over 32 experts, K = 2560, N = 1408 4-bit: 20.0 us, 22.1
+  // with sixteen); a group with more reads its weights again, from the caches.
+  const int bm = a.offsets != nullptr ? 8 : 16;
   const int64_t cols = a.gated ? FEW_COLS / 2 : FEW_COLS;
   const int64_t tiles_n = (fused_n_out(a) + cols - 1) / cols, slots = max_row_tiles(a, bm);
   if (tiles_n > 0x7fffffff || slots > 0x7fffffff / tiles_n) return hipErrorInvalidValue;
