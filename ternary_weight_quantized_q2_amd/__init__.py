@@ -507,8 +507,9 @@ def q2_route(logits, k: int, renormalize: bool = True, workspace=None) -> Route:
     k = int(k)
     c = k if 0 < k <= e else 0                             # a refused k allocates nothing and reaches the library's message
     new, i32 = logits.new_empty, torch.int32
-    route = Route(new((t, c), dtype=i32), new((t, c), dtype=torch.float32), new(e + 1, dtype=i32),
-                  new(t * c, dtype=i32), new((t, c), dtype=i32))
+    expert = new((t, c), dtype=i32)
+    route = Route(expert, new((t, c), dtype=torch.float32), new(e + 1, dtype=i32), new(t * c, dtype=i32),
+                  torch.empty_like(expert))
     ws, ws_bytes = _scratch(lib.q2_route_workspace_bytes(t, e, k), workspace, dev)
     _check(lib.q2_route(_ptr(logits), t, e, k, flags, _ptr(route.expert), _ptr(route.weight), _ptr(route.offsets),
                         _ptr(route.row_token), _ptr(route.slot), _ptr(ws), ws_bytes, _stream()))

@@ -98,7 +98,8 @@ def check(got, z, act="none", gated=False, bias=None, gate=None, residual=None, 
 
 # rows: one token, the GEMV's limit and beyond, tile edges; columns: not a multiple of anything, tile edges
 SIZES = [(1, 64, 128), (1, 1000, 2560), (3, 37, 384), (16, 400, 1280), (17, 130, 640), (33, 1, 128), (64, 256, 512),
-         (100, 513, 1152), (130, 200, 384), (257, 770, 1024), (300, 640, 1536)]
+         (100, 513, 1152), (130, 200, 384), (257, 770, 1024), (300, 640, 1536), (1, 200, 12416), (16, 96, 12416),
+         (9, 4200, 4224), (2, 9000, 640), (30, 70, 12416)]
 
 
 @pytest.mark.parametrize("fmt", ["q2", "q4"])
