@@ -380,6 +380,7 @@ hipError_t launch_fused(const FusedArgs& a, int fmt, void* ws, hipStream_t strea
 
 bool fused_mid_takes(const FusedArgs& a, int fmt);
 hipError_t launch_fused_mid(const FusedArgs& a, int fmt, hipStream_t stream);
+int64_t few_tiles(const FusedArgs& a);                   // workgroups of launch_fused_few without groups
 hipError_t launch_fused_few(const FusedArgs& a, int fmt, hipStream_t stream);
 size_t f16_workspace_bytes(int64_t rows, int64_t K);
 bool fused_f16_takes(int64_t rows, int64_t N, int64_t K);

@@ -156,10 +156,12 @@ hipError_t launch_fused(const FusedArgs& a, int fmt, void* ws, hipStream_t strea
     if (e != hipSuccess) return e;
   }
   if (f16) return launch_fused_f16(a, ws, stream);
-  // 16 rows, K = 4096, N = 12288: 13.1 us there, 13.6 in the next one; N = 4096 10.0,
-  // 12.1; over 32 experts, K = 2048, 2 x 1408: 128 rows 24.3, 25.9, 256 rows 32.1, 25.8
-  // (4-bit 30.2, 30.0 and 38.0, 30.2).
-  if (a.M <= 16 || (a.offsets && a.M <= 4 * a.E)) return launch_fused_few(a, fmt, stream);
+  // Few rows, or few tiles of them: up to 256 workgroups without groups, up to four
+  // rows per group.  There / in the next one, us: 16 rows, K = 4096, N = 12288 13.1 /
+  // 13.6; N = 4096 (256 workgroups) 32 rows 11.2 / 12.7, 4-bit 13.0 / 15.1; N = 6144
+  // (384) 13.5 / 12.9; 128 rows, K = 2560, N = 1024 8.4 / 11.6; over 32 experts,
+  // K = 2048, 2 x 1408, 128 rows 24.3 / 25.9, 256 rows 32.1 / 25.8.
+  if (a.M <= 16 || (a.offsets ? a.M <= 4 * a.E : few_tiles(a) <= 256)) return launch_fused_few(a, fmt, stream);
   if (fused_mid_takes(a, fmt)) return launch_fused_mid(a, fmt, stream);
   // Short K (less than four blocks) or a weight beyond 4 GB: the plain kernel.
   const int64_t cols = a.gated ? F_BN / 2 : F_BN;

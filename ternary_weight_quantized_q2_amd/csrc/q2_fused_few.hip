@@ -43,7 +43,7 @@ __host__ __device__ constexpr int few_row_bytes(int blocks) { return (blocks + 3
 // that two blocks have per column, and two lane-row swaps bring both blocks
 // into the layout (8 bytes per lane and block would touch 32-byte pieces).  The
 // rows of x are staged in LDS, only those that exist.
-template <int FMT, bool SHORT>
+template <int FMT, bool SHORT, bool BRANCH>
 __global__ __launch_bounds__(64 * FEW_WAVES) void fused_few_kernel(FusedArgs a, int bm, int tiles_n) {
   constexpr int DW = (FMT == 0) ? 2 : 4, D = FEW_BLOCKS;
   extern __shared__ __align__(16) uint8_t xs[];
@@ -63,11 +63,13 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void fused_few_kernel(FusedArgs a, 
 
   const uint8_t* wp[2];
   const uint16_t *sp[2], *zp[2];
+  int64_t wrow[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     int64_t n = n0 + c + (a.gated ? 0 : 16 * j);
     n = n < n_out ? n : n_out - 1;
     if (a.gated && j) n += n_out;
+    wrow[j] = n;
     const int64_t row = rt.expert * a.N + n;
     wp[j] = a.w + row * row_bytes;
     sp[j] = a.s + row * KB;
@@ -127,6 +129,25 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void fused_few_kernel(FusedArgs a, 
         __builtin_amdgcn_global_load_lds(p, (lds_void*)dst, 16, 0, 0);
       } else {
         *reinterpret_cast<q2_u32x4*>(dst + 16 * lane) = q2_u32x4{0u, 0u, 0u, 0u};
+      }
+    }
+    if (BRANCH && p0 == 0) {
+      // The rank-r branch while the weights are on their way: T_hi B_hi + T_hi B_lo +
+      // T_lo B_hi in bf16, 32 of r per wave, in the block sums' units (a fourth).  In
+      // a kernel of its own: its 16 registers cost linears without one up to 17 %.
+      const int r8 = (a.r + 7) & ~7;
+      for (int k0 = 32 * wv; k0 < r8; k0 += 32 * kg) {
+        const int64_t m = rt.m0 + min(c, rows - 1);
+        const q2_u32x4 hi = branch_afrag(a, m, k0 + 8 * g, false), lo = branch_afrag(a, m, k0 + 8 * g, true);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const BranchB bq = branch_bfrag(a, wrow[j], k0 + 8 * g);
+          q2_f32x4 br = mfma(hi, bq.hi, q2_f32x4{0.f, 0.f, 0.f, 0.f});
+          br = mfma(hi, bq.lo, br);
+          br = mfma(lo, bq.hi, br);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[j][e] = __builtin_fmaf(0.25f, br[e], acc[j][e]);
+        }
       }
     }
     stage_barrier<0>();                                  // all copies have landed
@@ -205,7 +226,6 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void fused_few_kernel(FusedArgs a, 
 
   const float* bias = a.bias ? a.bias + rt.expert * a.N : nullptr;
   const float fin = (FMT == 0) ? 4.f : 16.f;
-  const int r8 = (a.r + 7) & ~7;
   for (int idx = threadIdx.x; idx < rows * out_cols; idx += blockDim.x) {
     const int row = idx / out_cols, col = idx - row * out_cols;
     const int64_t m = rt.m0 + row, n = n0 + col;
@@ -216,11 +236,6 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void fused_few_kernel(FusedArgs a, 
       for (int q = 0; q < kg; ++q) u += red[q][row][FEW_COLS / 2 + col];
     v *= fin;
     u *= fin;
-    for (int j = 0; j < a.r; ++j) {                      // the rank-r branch, from the limbs of x A^T
-      const float t = bf16_to_f32(a.lr_t[m * 2 * r8 + j]) + bf16_to_f32(a.lr_t[m * 2 * r8 + r8 + j]);
-      v = __builtin_fmaf(t, f16_to_f32(a.lr_b[n * a.r + j]), v);
-      if (a.gated) u = __builtin_fmaf(t, f16_to_f32(a.lr_b[(n + n_out) * a.r + j]), u);
-    }
     store_out(a, bias, n_out, m, n, v, u);
   }
 }
@@ -233,7 +248,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void fused_few_kernel(FusedArgs a, 
 // 22.3); 16 rows, K = 4096, N = 12288 13.3 / 16.6; one row, K = 2560, 2 x 9728
 // 10.0 / 9.8 (4-bit 11.9 / 13.1); K = 4096, N = 4096 (128 workgroups, eight waves)
 // 6.2 / 6.4; K = 9728, N = 2560 (80, sixteen) 10.1 / 10.0.
-template <int FMT, bool SHORT>
+template <int FMT, bool SHORT, bool BRANCH>
 static hipError_t run_few(const FusedArgs& a, int bm, int64_t slots, int64_t tiles_n, hipStream_t stream) {
   const int KB = (int)(a.K / BLOCK_K);
   const int rows = (int)std::min<int64_t>(a.M, bm);      // at most 64 KB of them in LDS
@@ -243,15 +258,27 @@ static hipError_t run_few(const FusedArgs& a, int bm, int64_t slots, int64_t til
   while (kg > 1 && rows * few_row_bytes(kg * FEW_BLOCKS) > 64 * 1024) --kg;
   const size_t lds = std::max<size_t>((size_t)rows * few_row_bytes(kg * FEW_BLOCKS),
                                       (size_t)kg * 16 * (FEW_COLS + 1) * 4);
-  hipLaunchKernelGGL((fused_few_kernel<FMT, SHORT>), dim3((unsigned)wgs), dim3(64 * kg), lds, stream, a, bm,
+  hipLaunchKernelGGL((fused_few_kernel<FMT, SHORT, BRANCH>), dim3((unsigned)wgs), dim3(64 * kg), lds, stream, a, bm,
                      (int)tiles_n);
   return hipGetLastError();
 }
 
 template <int FMT>
 static hipError_t pick_few(const FusedArgs& a, int bm, int64_t slots, int64_t tiles_n, hipStream_t stream) {
-  return a.K < 4 * BLOCK_K ? run_few<FMT, true>(a, bm, slots, tiles_n, stream)
-                           : run_few<FMT, false>(a, bm, slots, tiles_n, stream);
+  const bool is_short = a.K < 4 * BLOCK_K;
+  if constexpr (FMT == 0)
+    if (a.r > 0)
+      return is_short ? run_few<FMT, true, true>(a, bm, slots, tiles_n, stream)
+                      : run_few<FMT, false, true>(a, bm, slots, tiles_n, stream);
+  return is_short ? run_few<FMT, true, false>(a, bm, slots, tiles_n, stream)
+                  : run_few<FMT, false, false>(a, bm, slots, tiles_n, stream);
+}
+
+static int64_t few_columns(const FusedArgs& a) {         // output columns of a workgroup
+  return a.gated ? FEW_COLS / 2 : FEW_COLS;
+}
+int64_t few_tiles(const FusedArgs& a) {
+  return ((a.M + 15) / 16) * ((fused_n_out(a) + few_columns(a) - 1) / few_columns(a));
 }
 
 hipError_t launch_fused_few(const FusedArgs& a, int fmt, hipStream_t stream) {
@@ -259,7 +286,7 @@ hipError_t launch_fused_few(const FusedArgs& a, int fmt, hipStream_t stream) {
   // in the launch; 92 rows over 32 experts, K = 2560, N = 1408 4-bit: 20.0 us, 22.1
   // with sixteen); a group with more reads its weights again, from the caches.
   const int bm = a.offsets != nullptr ? 8 : 16;
-  const int64_t cols = a.gated ? FEW_COLS / 2 : FEW_COLS;
+  const int64_t cols = few_columns(a);
   const int64_t tiles_n = (fused_n_out(a) + cols - 1) / cols, slots = max_row_tiles(a, bm);
   if (tiles_n > 0x7fffffff || slots > 0x7fffffff / tiles_n) return hipErrorInvalidValue;
   return fmt == 0 ? pick_few<0>(a, bm, slots, tiles_n, stream) : pick_few<1>(a, bm, slots, tiles_n, stream);
