@@ -246,8 +246,30 @@ def test_epilogue(fmt, gated, act, m):
             check(y, z, act, gated, what=f"{fmt} {act} {gated} {out} {sorted(kw)}", **kw)
 
 
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("act", ACTS)
+def test_epilogue_of_wide_weights(fmt, gated, act):
+    m, n, k = 70, 2 * 4200, 640
+    n_out = n // 2 if gated else n
+    dev, w = weights(fmt, 343, n, k)
+    xb, x = acts(343, m, k)
+    z = O.bf16_to_f64(xb) @ w.T
+    bias, gate = rnd(1, n).to(DEV), rnd(2, n_out).to(DEV)
+    res = rnd(3, m, n_out).to(DEV)
+    for out in (torch.float32, torch.bfloat16):
+        for kw in (dict(bias=bias, gate=gate, residual=res), dict(gate=gate, residual=res.bfloat16()), dict(bias=bias)):
+            y = fused(fmt)(x, *dev, activation=act, gated=gated, out_dtype=out, **kw)
+            check(y, z, act, gated, what=f"{fmt} {act} {gated} {out} {sorted(kw)}", **kw)
+        y = kw_res = res.to(out).clone()
+        fused(fmt)(x, *dev, activation=act, gated=gated, residual=y, y=y)
+        assert y is kw_res
+        check(y, z, act, gated, residual=res.to(out), what="in place")
+
+
 @pytest.mark.parametrize("m,n,k,r", [(1, 300, 512, 4), (16, 70, 256, 33), (50, 200, 384, 32), (150, 300, 640, 64),
-                                     (260, 520, 512, 100), (20, 64, 128, 1)])
+                                     (260, 520, 512, 100), (20, 64, 128, 1), (90, 9000, 640, 24), (40, 9000, 512, 7),
+                                     (16, 2000, 1152, 200)])
 @pytest.mark.parametrize("gated", [False, True])
 def test_rank_r_branch(m, n, k, r, gated):
     (p, s), w = weights("q2", 303, n, k)
@@ -279,9 +301,9 @@ def test_residual_in_place(fmt, out, m):
 
 @pytest.mark.parametrize("fmt", ["q2", "q4"])
 @pytest.mark.parametrize("m", [1, 7, 40, 200])
-def test_unaligned_outputs_and_neighbours(fmt, m):
+@pytest.mark.parametrize("n,k", [(75, 256), (75, 640), (8200, 512)])
+def test_unaligned_outputs_and_neighbours(fmt, m, n, k):
     """y and the residual one element past any larger boundary; nothing beside y is written."""
-    n, k = 75, 256
     dev, w = weights(fmt, 305, n, k)
     xb, x = acts(305, m, k)
     z = O.bf16_to_f64(xb) @ w.T
@@ -310,8 +332,8 @@ def test_empty_sum_and_empty_sizes(m):
 
 
 @pytest.mark.parametrize("m", [1, 16, 17, 150, 600])
-def test_zero_weights_add_exactly_nothing(m):
-    n, k = 130, 1280
+@pytest.mark.parametrize("n,k", [(130, 1280), (6000, 640), (130, 256)])
+def test_zero_weights_add_exactly_nothing(m, n, k):
     xb, x = acts(307, m, k)
     codes, scales = np.ones((n, k), np.uint8), I.q2_scales(307, n, k)
     p, s = q2.q2_pack(dev_u8(codes), torch.from_numpy(scales).to(DEV))
@@ -536,6 +558,11 @@ def stream_cases():
         out.append((f"q4 {m}", lambda x: q2.q4_linear_fused(x, *dev4, activation="gelu"), x))
     (pw, sw), _ = weights("q2", 333, 12300, 512)
     Bw = dev_bits(I.lowrank_factors(330, 8, 512, 12300)[1], torch.float16)
+    dev4w, _ = weights("q4", 333, 9000, 512)
+    for m in (100, 300):
+        _, x = acts(331, m, 512)
+        out.append((f"q2 wide {m}", lambda x: q2.q2_linear_fused(x, pw, sw, A, Bw, activation="silu", gated=True), x))
+        out.append((f"q4 wide {m}", lambda x: q2.q4_linear_fused(x, *dev4w, activation="gelu"), x))
     _, x = acts(331, 900, 512)
     out.append(("q2 900", lambda x: q2.q2_linear_fused(x, pw, sw, A, Bw, activation="silu"), x))
     for counts in ([1, 0, 2, 1], [100, 0, 37, 163]):
