@@ -406,32 +406,10 @@ hipError_t launch_route(const void* logits, int logits_bf16, int64_t T, int64_t 
 // copy of 1 GiB: 5.2).
 constexpr int CB_COLS = 8;
 
-template <bool VEC>
-__device__ __forceinline__ void load8(const void* p, int64_t i, int bf16, int n, float (&v)[CB_COLS]) {
-  if constexpr (VEC) {
-    if (bf16) {
-      const q2_u32x4 r = *reinterpret_cast<const q2_u32x4*>(static_cast<const uint16_t*>(p) + i);
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        v[2 * d] = __builtin_bit_cast(float, r[d] << 16);
-        v[2 * d + 1] = __builtin_bit_cast(float, r[d] & 0xFFFF0000u);
-      }
-    } else {
-      const q2_f32x4* q = reinterpret_cast<const q2_f32x4*>(static_cast<const float*>(p) + i);
-      const q2_f32x4 lo = q[0], hi = q[1];
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        v[d] = lo[d];
-        v[4 + d] = hi[d];
-      }
-    }
-  } else {
-#pragma unroll
-    for (int d = 0; d < CB_COLS; ++d) v[d] = d < n ? load_elem(p, i + d, bf16) : 0.f;
-  }
+__device__ __forceinline__ Eight load8(const void* p, int64_t i, int bf16) {
+  return raw_floats(load8raw(p, i, bf16), bf16);
 }
 
-template <bool VEC>
 __global__ __launch_bounds__(256) void combine_kernel(const void* z, int z_bf16, int64_t R, const int32_t* slot,
                                                       const float* weight, const void* residual, int res_bf16, void* y,
                                                       int out_bf16, int64_t T, int k, int64_t N, int64_t chunks) {
@@ -439,55 +417,129 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* z, int z_bf16,
   const int64_t t = id / chunks;
   if (t >= T) return;
   const int64_t n0 = (id - t * chunks) * CB_COLS;
-  const int nc = (int)std::min<int64_t>(N - n0, CB_COLS);
   float acc[CB_COLS] = {};
   for (int j = 0; j < k; ++j) {
     const int s = slot[t * k + j];
     if (s < 0 || s >= R) continue;
     const float w = weight[t * k + j];
-    float v[CB_COLS];
-    load8<VEC>(z, (int64_t)s * N + n0, z_bf16, nc, v);
+    const Eight v = load8(z, (int64_t)s * N + n0, z_bf16);
 #pragma unroll
-    for (int d = 0; d < CB_COLS; ++d) acc[d] = __builtin_fmaf(w, v[d], acc[d]);
+    for (int d = 0; d < CB_COLS; ++d) acc[d] = __builtin_fmaf(w, v.v[d], acc[d]);
   }
   const int64_t at = t * N + n0;
   if (residual) {
-    float v[CB_COLS];
-    load8<VEC>(residual, at, res_bf16, nc, v);
+    const Eight v = load8(residual, at, res_bf16);
 #pragma unroll
-    for (int d = 0; d < CB_COLS; ++d) acc[d] += v[d];
+    for (int d = 0; d < CB_COLS; ++d) acc[d] += v.v[d];
   }
-  if (VEC && out_bf16) {
+  if (out_bf16) {
     q2_u32x4 r;
 #pragma unroll
     for (int d = 0; d < 4; ++d) r[d] = (uint32_t)to_bf16(acc[2 * d]) | ((uint32_t)to_bf16(acc[2 * d + 1]) << 16);
     *reinterpret_cast<q2_u32x4*>(static_cast<uint16_t*>(y) + at) = r;
-  } else if (VEC) {
+  } else {
     q2_f32x4* q = reinterpret_cast<q2_f32x4*>(static_cast<float*>(y) + at);
     q[0] = q2_f32x4{acc[0], acc[1], acc[2], acc[3]};
     q[1] = q2_f32x4{acc[4], acc[5], acc[6], acc[7]};
+  }
+}
+
+// Rows that are not whole 16-byte pieces: a wave per token and 256 W columns, lane
+// l holding W neighbours at W l and every 64 W columns on, so that a load's lanes
+// read neighbours.  Pairs (W = 2) where the rows allow them: 3081 tokens, six bf16
+// rows of 3586 65 us, one by one 89; f32 rows 60 us, 287 MB at 4.8 TB/s.
+constexpr int CR_STEPS = 4, CR_WAVES = 4;
+
+template <int W>
+struct RaggedCols {
+  float v[CR_STEPS * W];
+};
+template <int W>
+__device__ __forceinline__ RaggedCols<W> load_ragged(const void* p, int64_t i, int bf16, int64_t left) {
+  typedef uint16_t half_w __attribute__((ext_vector_type(W)));
+  typedef float float_w __attribute__((ext_vector_type(W)));
+  RaggedCols<W> r = {};
+  if (bf16) {
+    const uint16_t* q = static_cast<const uint16_t*>(p) + i;
+#pragma unroll
+    for (int d = 0; d < CR_STEPS; ++d)
+      if (64 * W * d < left) {
+        const half_w t = *reinterpret_cast<const half_w*>(q + 64 * W * d);
+#pragma unroll
+        for (int e = 0; e < W; ++e) r.v[W * d + e] = bf16_to_f32(t[e]);
+      }
   } else {
-    for (int d = 0; d < nc; ++d) {
-      if (out_bf16) static_cast<uint16_t*>(y)[at + d] = to_bf16(acc[d]);
-      else static_cast<float*>(y)[at + d] = acc[d];
+    const float* q = static_cast<const float*>(p) + i;
+#pragma unroll
+    for (int d = 0; d < CR_STEPS; ++d)
+      if (64 * W * d < left) {
+        const float_w t = *reinterpret_cast<const float_w*>(q + 64 * W * d);
+#pragma unroll
+        for (int e = 0; e < W; ++e) r.v[W * d + e] = t[e];
+      }
+  }
+  return r;
+}
+
+template <int W>
+__global__ __launch_bounds__(64 * CR_WAVES) void combine_ragged_kernel(const void* z, int z_bf16, int64_t R,
+                                                                       const int32_t* slot, const float* weight,
+                                                                       const void* residual, int res_bf16, void* y,
+                                                                       int out_bf16, int64_t T, int k, int64_t N,
+                                                                       int64_t chunks) {
+  typedef uint16_t half_w __attribute__((ext_vector_type(W)));
+  typedef float float_w __attribute__((ext_vector_type(W)));
+  const int64_t id = (int64_t)blockIdx.x * CR_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = id / chunks;
+  if (t >= T) return;
+  const int64_t n = (id - t * chunks) * (64 * W * CR_STEPS) + (threadIdx.x & 63) * W, left = N - n;
+  RaggedCols<W> acc = {};
+  for (int j = 0; j < k; ++j) {
+    const int s = slot[t * k + j];
+    if (s < 0 || s >= R) continue;
+    const float w = weight[t * k + j];
+    const RaggedCols<W> v = load_ragged<W>(z, (int64_t)s * N + n, z_bf16, left);
+#pragma unroll
+    for (int d = 0; d < CR_STEPS * W; ++d) acc.v[d] = __builtin_fmaf(w, v.v[d], acc.v[d]);
+  }
+  const int64_t at = t * N + n;
+  if (residual) {
+    const RaggedCols<W> v = load_ragged<W>(residual, at, res_bf16, left);
+#pragma unroll
+    for (int d = 0; d < CR_STEPS * W; ++d) acc.v[d] += v.v[d];
+  }
+#pragma unroll
+  for (int d = 0; d < CR_STEPS; ++d) {
+    if (64 * W * d >= left) continue;
+    half_w h;
+    float_w f;
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      f[e] = acc.v[W * d + e];
+      h[e] = to_bf16(f[e]);
     }
+    if (out_bf16) *reinterpret_cast<half_w*>(static_cast<uint16_t*>(y) + at + 64 * W * d) = h;
+    else *reinterpret_cast<float_w*>(static_cast<float*>(y) + at + 64 * W * d) = f;
   }
 }
 
 hipError_t launch_combine(const void* z, int z_bf16, int64_t R, const int32_t* slot, const float* weight,
                           const void* residual, int res_bf16, void* y, int out_bf16, int64_t T, int k, int64_t N,
                           hipStream_t stream) {
-  const int64_t chunks = (N + CB_COLS - 1) / CB_COLS;
-  const int64_t blocks = (T * chunks + 255) / 256;
+  auto on = [](const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; };
+  const bool vec = N % CB_COLS == 0 && on(z, 16) && on(residual, 16) && on(y, 16);
+  const bool pairs = N % 2 == 0 && on(z, z_bf16 ? 4 : 8) && on(residual, res_bf16 ? 4 : 8) && on(y, out_bf16 ? 4 : 8);
+  const int64_t wide = 64 * CR_STEPS * (pairs ? 2 : 1);
+  const int64_t chunks = vec ? N / CB_COLS : (N + wide - 1) / wide;
+  const int64_t per = vec ? 256 : CR_WAVES, blocks = (T * chunks + per - 1) / per;
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  auto a16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
-  const bool vec = N % CB_COLS == 0 && a16(z) && a16(residual) && a16(y);
-  if (vec)
-    hipLaunchKernelGGL((combine_kernel<true>), dim3((unsigned)blocks), dim3(256), 0, stream, z, z_bf16, R, slot,
-                       weight, residual, res_bf16, y, out_bf16, T, k, N, chunks);
-  else
-    hipLaunchKernelGGL((combine_kernel<false>), dim3((unsigned)blocks), dim3(256), 0, stream, z, z_bf16, R, slot,
-                       weight, residual, res_bf16, y, out_bf16, T, k, N, chunks);
+#define Q2_COMBINE(KERNEL)                                                                                            \
+  hipLaunchKernelGGL(KERNEL, dim3((unsigned)blocks), dim3(256), 0, stream, z, z_bf16, R, slot, weight, residual,      \
+                     res_bf16, y, out_bf16, T, k, N, chunks)
+  if (vec) Q2_COMBINE(combine_kernel);
+  else if (pairs) Q2_COMBINE((combine_ragged_kernel<2>));
+  else Q2_COMBINE((combine_ragged_kernel<1>));
+#undef Q2_COMBINE
   return hipGetLastError();
 }
 

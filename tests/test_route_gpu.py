@@ -133,7 +133,7 @@ def check_combine(t, k, n, r, zt, rt, out, seed=0, slot=None):
 
 
 @pytest.mark.parametrize("t,k,n,r", [(1, 8, 2048, 8), (5, 1, 1, 3), (3, 2, 8, 4), (7, 4, 37, 20), (130, 3, 264, 300),
-                                     (2, 64, 100, 50), (4, 0, 16, 2)])
+                                     (2, 64, 100, 50), (4, 0, 16, 2), (9, 3, 518, 30), (5, 2, 257, 9), (3, 2, 1030, 7)])
 @pytest.mark.parametrize("zt", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("rt", [None, torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
