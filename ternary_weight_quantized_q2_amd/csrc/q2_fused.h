@@ -256,11 +256,45 @@ __device__ __forceinline__ void store_strip(const FusedArgs& a, const float* bia
       }
     }
   } else {
-    for (int idx = lane; idx < rows * cols; idx += 64) {
-      const int row = idx / cols, col = idx - row * cols;
-      if (n0 + col >= n_out) continue;
-      const float* s = strip + row * stride + col;
-      store_out(a, bias, n_out, m0 + row, n0 + col, s[0], a.gated ? s[half] : 0.f);
+    // A lane keeps its column (and with narrow strips a share of the rows), eight
+    // rows at a time: M = 1536, K = 4096, N = 12289 with a residual 209 us, an
+    // element at a time 373 (N = 12288: 168).
+    constexpr int ROWS = 8;
+    const int share = cols < 64 && 64 % cols == 0 ? 64 / cols : 1;
+    const int lrow = share > 1 ? lane / cols : 0, lcol = lane - lrow * cols * (share > 1);
+    for (int c0 = 0; c0 < cols; c0 += 64) {
+      const int col = c0 + lcol;
+      const int64_t n = n0 + col;
+      const bool live = col < cols && n < n_out;
+      const float b = bias && live ? bias[n] : 0.f, bu = bias && a.gated && live ? bias[n_out + n] : 0.f;
+      const float g = a.gate && live ? a.gate[n] : 1.f;
+      if (!live) continue;
+      for (int r0 = lrow; r0 < rows; r0 += ROWS * share) {
+        float v[ROWS], u[ROWS], res[ROWS];
+#pragma unroll
+        for (int q = 0; q < ROWS; ++q) {
+          const int row = min(r0 + q * share, rows - 1); // past the end: the last row again, not stored
+          res[q] = a.residual ? load_elem(a.residual, (m0 + row) * n_out + n, a.res_bf16) : 0.f;
+          v[q] = strip[row * stride + col];
+          u[q] = a.gated ? strip[row * stride + half + col] : 0.f;
+        }
+        if (bias) {
+#pragma unroll
+          for (int q = 0; q < ROWS; ++q) v[q] += b, u[q] += bu;
+        }
+        activate8(a.act, v);
+#pragma unroll
+        for (int q = 0; q < ROWS; ++q) {
+          if (a.gated) v[q] *= u[q];
+          if (a.gate) v[q] *= g;
+          if (a.residual) v[q] += res[q];
+          const int row = r0 + q * share;
+          const int64_t i = (m0 + row) * n_out + n;
+          if (row >= rows) continue;
+          if (a.out_bf16) static_cast<uint16_t*>(a.y)[i] = to_bf16(v[q]);
+          else static_cast<float*>(a.y)[i] = v[q];
+        }
+      }
     }
   }
 }
