@@ -50,6 +50,20 @@ __device__ __forceinline__ q2_u32x4 q2_frag(uint32_t w, const NatConsts& k) {
 }
 __device__ __forceinline__ q2_u32x4 q4_frag(uint32_t w, const NatConsts& k) { return q4_bfrag_nat(w, k); }
 
+// ---- the codes of a row, 64 bytes at a time --------------------------------------
+// A unit is four 16-byte pieces of a row: `per` blocks, two of 2-bit codes or one
+// of 4-bit codes.  Prefetches run past the last unit and, with an odd number of
+// 2-bit blocks, past the row inside it; what they load there is never used, but the
+// scalar offset of a buffer load is no part of its bounds check, so they stay in the
+// row: piece p of unit u lies at unit_start + 16 p - unit_back.
+__host__ __device__ constexpr int last_unit(int blocks, int per) { return (blocks + per - 1) / per - 1; }
+__host__ __device__ constexpr uint32_t unit_start(int u, int blocks, int per) {
+  return 64u * (uint32_t)(u < last_unit(blocks, per) ? u : last_unit(blocks, per));
+}
+__host__ __device__ constexpr uint32_t unit_back(int u, int blocks, int per, int piece) {
+  return per == 2 && (blocks & 1) && u >= last_unit(blocks, per) && piece >= 2 ? 32u : 0u;
+}
+
 // ---- the rank-r branch -----------------------------------------------------------
 // Its matrix-core operands: x A^T as limbs [M, 2 r8] (hi | lo), B split exactly
 // into bf16 hi + lo, added up as T_hi B_hi + T_hi B_lo + T_lo B_hi (the dropped

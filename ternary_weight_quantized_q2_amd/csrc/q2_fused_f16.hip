@@ -368,11 +368,11 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
 #pragma unroll
   for (int q = 0; q < 4; ++q)
     woff[q] = (uint32_t)(wcol(16 * q + (lane >> 2)) * (K / 4)) + (uint32_t)(((lane & 3) ^ ((lane >> 4) & 3)) << 4);
-  auto copy_codes = [&](int set, int q) {                // past the end of the weight: zeros, never used
+  auto copy_codes = [&](int set, int q) {                // past the last set: that one again, never used
     const uint32_t wo = q == 0 ? woff[0] : q == 1 ? woff[1] : q == 2 ? woff[2] : woff[3];
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        rw, (lds_void*)(smem + FX_OFF_W + ((set & 1) * 4 + wv) * FX_WBUF + q * 1024), 16, wo, (uint32_t)set * 64u, 0,
-        0);
+        rw, (lds_void*)(smem + FX_OFF_W + ((set & 1) * 4 + wv) * FX_WBUF + q * 1024), 16,
+        wo - unit_back(set, KB, 2, (lane & 3) ^ ((lane >> 4) & 3)), unit_start(set, KB, 2), 0, 0);
   };
   const uint8_t* const wbase = smem + FX_OFF_W + wv * FX_WBUF + c * 64 + 8 * h;
   auto read_codes = [&](int hs, q2_u32x2 (&w)[2]) {

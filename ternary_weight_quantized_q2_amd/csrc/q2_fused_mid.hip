@@ -130,9 +130,10 @@ __global__ __launch_bounds__(64 * NW * KG, OCC) void fused_mid_kernel(FusedArgs 
     }
   };
   q2_u32x4 w[NT], wnext[ROLL ? 1 : NT];                  // this lane's 16 bytes of a unit's codes
-  auto load_codes = [&](int j, int n) {
-    const uint32_t so = (uint32_t)((KG * n + kg) * U) * (FMT == 0 ? 32u : 64u);
-    const q2_u32x4 v = __builtin_bit_cast(q2_u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, woff[j], so, 0));
+  auto load_codes = [&](int j, int n) {                  // past the last unit: that one again, never used
+    const int u = KG * n + kg;
+    const q2_u32x4 v = __builtin_bit_cast(
+        q2_u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, woff[j] - unit_back(u, KB, U, g), unit_start(u, KB, U), 0));
     if constexpr (ROLL) w[j] = v;
     else wnext[j] = v;
   };

@@ -115,6 +115,22 @@ def test_plain_sizes(fmt, m, n, k):
     assert torch.equal(yb, y.to(torch.bfloat16)), "the bf16 output is not the f32 one rounded once"
 
 
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
+@pytest.mark.parametrize("m,n,k", [(8192, 1, 512), (4500, 1, 640), (8200, 3, 640), (5000, 9, 1152)])
+def test_narrow_weights_over_many_rows(fmt, m, n, k):
+    """Weights smaller than what the kernel prefetches."""
+    dev, w = weights(fmt, 302, n, k)
+    xb, x = acts(302, m, k)
+    check_terms(fused(fmt)(x, *dev), O.bf16_to_f64(xb), w)
+
+
+def check_terms(got, x, w):
+    """got against x W^T, every element by the RMS sum of its own terms: a row's RMS over one to nine outputs may be
+    far below the sums' rounding, and outputs of one row may differ in size by any factor."""
+    bad = np.abs(host(got) - x @ w.T) > 1e-3 * np.sqrt((x * x) @ (w * w).T)
+    assert not bad.any(), f"{bad.sum()} of {bad.size}, first at {np.argwhere(bad)[0]}"
+
+
 # The kernel for many rows needs many tiles: wide weights, sampled columns (both factors' of a gated layer).
 MANY = [(1531, 8120, 640, 40, False), (1531, 8120, 512, 0, True),
         (300, 32770, 512, 0, False), (1025, 9000, 1152, 0, True), (2000, 5250, 4224, 0, False), (700, 16400, 640, 5, True),
