@@ -15,6 +15,7 @@ tensors must be contiguous and on the current device.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -337,6 +338,12 @@ def _have(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str, dev: int
         raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{dev}")
 
 
+def _maker(like: torch.Tensor, dev: int):
+    """What allocates a call's outputs, on the device: an input without elements may be a host tensor.  (new_empty
+    costs less host time.)"""
+    return like.new_empty if like.is_cuda else functools.partial(torch.empty, device=f"cuda:{dev}")
+
+
 def _epilogue(n, rows, bias_shape, bias, activation, gated, gate, residual, out_dtype, y, x, dev):
     """(q2_epilogue, y) of a fused or grouped linear over a weight of n rows; y is allocated when None."""
     if activation not in ACTIVATIONS:
@@ -362,7 +369,7 @@ def _epilogue(n, rows, bias_shape, bias, activation, gated, gate, residual, out_
             raise ValueError(f"residual is float32 or bfloat16, not {residual.dtype}")
         _have(residual, residual.dtype, shape, "residual", dev)
     if y is None:
-        y = x.new_empty(shape, dtype=out_dtype)
+        y = _maker(x, dev)(shape, dtype=out_dtype)
     else:
         _have(y, out_dtype, shape, "y", dev)
     return Epilogue(ACTIVATIONS[activation], flags, _ptr(bias), _ptr(gate), _ptr(residual)), y
@@ -506,7 +513,7 @@ def q2_route(logits, k: int, renormalize: bool = True, workspace=None) -> Route:
     flags = (Q2_ROUTE_LOGITS_BF16 if logits.dtype == torch.bfloat16 else 0) | (Q2_ROUTE_RENORM if renormalize else 0)
     k = int(k)
     c = k if 0 < k <= e else 0                             # a refused k allocates nothing and reaches the library's message
-    new, i32 = logits.new_empty, torch.int32
+    new, i32 = _maker(logits, dev), torch.int32
     expert = new((t, c), dtype=i32)
     route = Route(expert, new((t, c), dtype=torch.float32), new(e + 1, dtype=i32), new(t * c, dtype=i32),
                   torch.empty_like(expert))
@@ -542,7 +549,7 @@ def q2_combine(z, slot, weight, residual=None, out_dtype=torch.float32, y=None) 
             raise ValueError(f"residual is float32 or bfloat16, not {residual.dtype}")
         _have(residual, residual.dtype, (t, n), "residual", dev)
     if y is None:
-        y = z.new_empty((t, n), dtype=out_dtype)
+        y = _maker(z, dev)((t, n), dtype=out_dtype)
     else:
         _have(y, out_dtype, (t, n), "y", dev)
     _check(lib.q2_combine(_ptr(z), r, _ptr(slot), _ptr(weight), _ptr(residual), _ptr(y), t, k, n, flags, _stream()))

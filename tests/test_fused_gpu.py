@@ -347,6 +347,19 @@ def test_empty_sum_and_empty_sizes(m):
     assert q2.q2_linear_fused(torch.empty((m, 128), dtype=torch.bfloat16, device=DEV), pw[:0], sw[:0]).shape == (m, 0)
 
 
+@pytest.mark.parametrize("m", [1, 20])
+def test_host_inputs_without_elements(m):
+    """Inputs that hold nothing may lie on the host; the outputs do not."""
+    n, bias = 48, rnd(7, 48).to(DEV)
+    x, p, s = torch.empty((m, 0), dtype=torch.bfloat16), torch.empty((n, 0), dtype=torch.uint8), torch.empty((n, 0)).half()
+    for y in (q2.q2_linear_fused(x, p, s, bias=bias), q2.q4_linear_fused(x, p, s, s, bias=bias)):
+        assert y.is_cuda and torch.equal(y, bias.expand(m, n))
+    dev, _ = weights("q2", 306, n, 128)
+    y = q2.q2_linear_grouped(torch.empty((0, 128), dtype=torch.bfloat16), torch.tensor([0, m], dtype=torch.int32, device=DEV),
+                             *(t[None] for t in dev), row_index=torch.zeros(m, dtype=torch.int32, device=DEV), bias=bias[None])
+    assert y.is_cuda and torch.equal(y, bias.expand(m, n))
+
+
 @pytest.mark.parametrize("m", [1, 16, 17, 150, 600])
 @pytest.mark.parametrize("n,k", [(130, 1280), (6000, 640), (130, 256)])
 def test_zero_weights_add_exactly_nothing(m, n, k):

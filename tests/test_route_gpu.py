@@ -101,6 +101,18 @@ def test_route_of_no_tokens():
     assert got.offsets.tolist() == [0] * 13 and got.expert.shape == (0, 3) and got.row_token.numel() == 0
 
 
+def test_host_inputs_without_elements():
+    """Inputs that hold nothing may lie on the host; the outputs do not."""
+    got = q2.q2_route(torch.empty((0, 12)), 3)
+    assert all(t.is_cuda for t in got) and got.offsets.tolist() == [0] * 13
+    res = rnd(1, 3, 8).to(DEV)
+    y = q2.q2_combine(torch.empty((0, 8)), torch.zeros((3, 2), dtype=torch.int32, device=DEV),
+                      torch.ones((3, 2), device=DEV), residual=res)
+    assert y.is_cuda and torch.equal(y, res)
+    assert torch.equal(q2.q2_combine(torch.empty((0, 8)), torch.empty((3, 0), dtype=torch.int32), torch.empty((3, 0)),
+                                     residual=res), res)
+
+
 def test_route_refusals():
     x = torch.zeros((2, 8), device=DEV)
     for k in (0, 9, -1, 10 ** 12):
