@@ -28,10 +28,13 @@ namespace q2dev {
 // T = 16384, E = 128, k = 8, bf16 logits: choice 9.5 us (14.8 with a wave per
 // token), plan 6.2; T = 4096, E = 256 both 19 us (23); one token, E = 64: 3.7.
 constexpr int RT_TOK = 64, RT_THREADS = 1024, RT_WAVES = RT_THREADS / 64;
-constexpr int RT_GROUPS = 1024;
+constexpr int RT_GROUPS = 1024, RT_CHUNKS = 1023;       // workgroups, while a workgroup's chunks are at most so many
+static_assert(RT_TOK * RT_CHUNKS <= 0xFFFF, "a workgroup's count of an expert has 16 bits");
 
 constexpr int route_pad(int64_t E) { return (int)((E + 1) & ~(int64_t)1); }     // counts per workgroup, u16 pairs
-static int route_chunks(int64_t T) { return (int)((T + RT_TOK * RT_GROUPS - 1) / (RT_TOK * RT_GROUPS)); }
+static int route_chunks(int64_t T) {
+  return (int)std::min<int64_t>((T + RT_TOK * RT_GROUPS - 1) / (RT_TOK * RT_GROUPS), RT_CHUNKS);
+}
 static int64_t route_groups(int64_t T) {
   const int64_t per = (int64_t)RT_TOK * route_chunks(T);
   return (T + per - 1) / per;

@@ -166,3 +166,11 @@ def test_combine_by_hand():
     z = np.array([[1.0], [10.0]])
     y = F.combine(z, np.array([[0, 1], [-1, 1], [2, -5]]), np.array([[2.0, 3.0]] * 3), np.array([[0.5]] * 3))
     assert y.tolist() == [[32.5], [30.5], [0.5]]
+
+
+def test_route_workgroups_hold_few_enough_tokens_for_their_counts(lib):
+    """A workgroup counts its tokens per expert in 16 bits: it must not have more than 65535 (k = E chooses every
+    expert for each of them).  1024 experts: 2048 bytes of counts per workgroup."""
+    for t in (65, 70001, 1023 * 65536, 1023 * 65536 + 1, 2 ** 26 - 1, 2 ** 26):
+        groups = lib.q2_route_workspace_bytes(t, 1024, 1) // 2048
+        assert groups * 65535 >= t, t

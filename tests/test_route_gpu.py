@@ -96,6 +96,35 @@ def test_route_many_tokens():
     check_route(v, 2, True)
 
 
+@pytest.mark.parametrize("t", [1023 * 65536 + 1, 2 ** 26])
+@pytest.mark.parametrize("e,k", [(1, 1), (2, 2)])
+def test_route_of_the_most_tokens(t, e, k):
+    """Every token chooses every expert: expert j's rows are all tokens in their order.  (t, e, k) up to the largest t."""
+    logits = torch.zeros((t, e), device=DEV, dtype=torch.bfloat16)
+    got = q2.q2_route(logits, k)
+    assert got.offsets.tolist() == [j * t for j in range(e + 1)]
+    token = torch.arange(t, device=DEV, dtype=torch.int32)
+    for j in range(e):
+        assert torch.equal(got.expert[:, j], torch.full_like(token, j))
+        assert torch.equal(got.slot[:, j], token + j * t) and torch.equal(got.row_token[j * t:(j + 1) * t], token)
+    assert (got.weight == 1 / k).all()
+
+
+def test_route_of_the_most_tokens_to_one_expert():
+    """The last workgroups' tokens all choose one expert of three, most of the others' none."""
+    t = 2 ** 26
+    logits = torch.zeros((t, 3), device=DEV, dtype=torch.bfloat16)
+    logits[:t // 2] = -np.inf
+    logits[t // 2:, 1] = 1
+    logits[5, 2] = 0
+    got = q2.q2_route(logits, 1)
+    rows = t // 2
+    assert got.offsets.tolist() == [0, 0, rows, rows + 1]
+    assert torch.equal(got.slot[t // 2:, 0], torch.arange(rows, device=DEV, dtype=torch.int32))
+    assert torch.equal(got.row_token[:rows], torch.arange(rows, t, device=DEV, dtype=torch.int32))
+    assert got.slot[5].item() == rows and got.row_token[rows].item() == 5 and (got.row_token[rows + 1:] == -1).all()
+
+
 def test_route_of_no_tokens():
     got = q2.q2_route(torch.empty((0, 12), device=DEV), 3)
     assert got.offsets.tolist() == [0] * 13 and got.expert.shape == (0, 3) and got.row_token.numel() == 0
