@@ -3,16 +3,21 @@
 // A Q2_0 weight is -d, 0 or d with an f16 scale d, so it is an f16 value as it
 // stands; what keeps the product off the f16 matrix cores is the range of the
 // bf16 activations.  Here each row of x is first multiplied by a power of two
-// that puts its largest element into [2^14, 2^15) and converted to f16.  A bf16
-// value has 8 significant bits, so every element down to 2^-31 of its row's
-// largest is exact; below that it becomes an f16 subnormal, off by at most
-// 2^-25, that is 2^-39 of the row's largest element -- far less than fp32 sums
-// over the row keep.  Then the sum over all of K runs in the matrix cores' fp32
+// that puts its largest element into [2^15, 2^16) and converted to f16.  A bf16
+// value has 8 significant bits, so every element down to 2^-32 of its row's
+// largest is exact.  Then the sum over all of K runs in the matrix cores' fp32
 // accumulators with exact products, without a block's start value, row sums or
 // a rescale per block; the power of two is taken back by an exact ldexp.
+//
+// A row with smaller elements (a wide row) stays bf16, and a tile that holds one
+// runs on the bf16 matrix cores with each weight as the exact sum of two bf16
+// values, at twice the products.  Rounding those elements instead would cost at
+// most 2^-40 of the row's largest one, but that is the whole result of an output
+// whose weights at the larger elements are zero.
 #include "q2_fused.h"
 #include "q2_internal.h"
 #include <algorithm>
+#include <type_traits>
 
 namespace q2dev {
 
@@ -35,21 +40,42 @@ __device__ __forceinline__ q2_f32x16 mfma32_bf16(q2_u32x4 a, q2_u32x4 b, q2_f32x
 // 4 j + b holds element 4 b + j), the order in which a dword of sixteen codes
 // decodes.
 
-// The largest finite |x| of 16 elements (two 16-byte pieces), as bf16 bits.
-__device__ __forceinline__ uint32_t top_bits(uint32_t top, const q2_u32x4& v) {
+// The largest and the smallest nonzero |x| of the elements so far, as bf16 bits in
+// each half of a word, the smallest less one: zeros count as 0xFFFF.  An infinity or
+// a NaN is the largest; its row has no finite product whatever its exponent is.
+struct Span {
+  q2_u16x2 top = {0, 0}, low = {0xFFFF, 0xFFFF};
+  __device__ __forceinline__ void add(const q2_u32x4& v) {
 #pragma unroll
-  for (int d = 0; d < 4; ++d) {
-    const uint32_t lo = v[d] & 0x7FFFu, hi = (v[d] >> 16) & 0x7FFFu;
-    top = max(top, lo < 0x7F80u ? lo : 0u);
-    top = max(top, hi < 0x7F80u ? hi : 0u);
+    for (int d = 0; d < 4; ++d) {
+      const q2_u16x2 m = __builtin_bit_cast(q2_u16x2, v[d] & 0x7FFF7FFFu);
+      top = __builtin_elementwise_max(top, m);
+      low = __builtin_elementwise_min(low, (q2_u16x2)(m - q2_u16x2{1, 1}));
+    }
   }
-  return top;
+  // Both in one word of which a maximum per half joins two: top, low's complement.
+  __device__ __forceinline__ uint32_t word() const {
+    return (uint32_t)max(top[0], top[1]) << 16 | (0xFFFFu - min(low[0], low[1]));
+  }
+};
+__device__ __forceinline__ uint32_t join_span(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(
+      uint32_t, __builtin_elementwise_max(__builtin_bit_cast(q2_u16x2, a), __builtin_bit_cast(q2_u16x2, b)));
 }
-// The shift that puts it into [2^14, 2^15): floor(log2 |x|) from the bits (a
+// A wide row: its smallest nonzero element lies below 2^-32 times the power of two
+// of its largest.  (Every bf16 is a multiple of 2^-133, which is exact as long as the
+// largest element lies below 2^-93.)
+__device__ __forceinline__ bool is_wide(uint32_t span) {
+  const int limit = (int)(span >> 23) - 32;              // exponent of 2^-32 times the largest
+  return limit > 1 && span >> 16 < 0x7F80u && 0x10000u - (span & 0xFFFFu) < (uint32_t)limit << 7;
+}
+constexpr int ROW_WIDE = 1 << 16;                        // in the place of its exponent
+
+// The shift that puts the largest into [2^15, 2^16): floor(log2 |x|) from the bits (a
 // subnormal bf16 is bits * 2^-133); 0 for a row of zeros.
 __device__ __forceinline__ int top_shift(uint32_t top) {
-  const int e = top >= 0x80u ? (int)(top >> 7) - 127 : top ? 31 - __builtin_clz(top) - 133 : 14;
-  return 14 - e;
+  const int e = top >= 0x80u ? (int)(top >> 7) - 127 : top ? 31 - __builtin_clz(top) - 133 : 15;
+  return 15 - e;
 }
 // Sixteen elements as f16 pairs in their own order.
 __device__ __forceinline__ void to_f16(const q2_u32x4& v0, const q2_u32x4& v1, int shift, uint32_t (&h)[8]) {
@@ -74,6 +100,12 @@ __device__ __forceinline__ void store_f16(q2_u32x4* dst, const uint32_t (&h)[8])
   dst[1] = o[1];
 }
 
+// The elements of a wide row, kept: bf16 bits.
+__device__ __forceinline__ void keep_bf16(const q2_u32x4& v0, const q2_u32x4& v1, uint32_t (&h)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = i < 4 ? v0[i] : v1[i - 4];
+}
+
 // Rows without a branch: one wave per row, which stays in registers up to
 // 1024 NCH elements between the search for its largest element and the
 // conversion (NCH = 0: longer rows, read twice).  Row M (of M + 1) is a row of
@@ -96,7 +128,7 @@ __global__ __launch_bounds__(64 * CV_ROWS) void x_to_f16_kernel(const uint16_t* 
   const q2_u32x4* const xr = reinterpret_cast<const q2_u32x4*>(x + m * K);
   constexpr int N = NCH > 0 ? NCH : 1;
   q2_u32x4 v[N][2];
-  uint32_t top = 0;
+  Span sp;
   if constexpr (NCH > 0) {
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
@@ -105,15 +137,28 @@ __global__ __launch_bounds__(64 * CV_ROWS) void x_to_f16_kernel(const uint16_t* 
       v[i][1] = xr[2 * q + 1];
     }
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) top = top_bits(top_bits(top, v[i][0]), v[i][1]);
+    for (int i = 0; i < NCH; ++i) {
+      sp.add(v[i][0]);
+      sp.add(v[i][1]);
+    }
   } else {
-    for (int64_t q = lane; q < 2 * chunks; q += 64) top = top_bits(top, xr[q]);
+    for (int64_t q = lane; q < 2 * chunks; q += 64) sp.add(xr[q]);
   }
+  uint32_t span = sp.word();
 #pragma unroll
-  for (int d = 32; d; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-  const int shift = top_shift(top);
-  if (lane == 0) rexp[m] = -shift;
+  for (int d = 32; d; d >>= 1) span = join_span(span, (uint32_t)__shfl_xor((int)span, d));
+  const int shift = top_shift(span >> 16);
+  const bool wide = __builtin_amdgcn_readfirstlane(is_wide(span));
+  if (lane == 0) rexp[m] = wide ? ROW_WIDE : -shift;
   uint32_t h[8];
+  if (wide) {                                            // rare: from memory again, in a short loop
+#pragma unroll 1
+    for (int64_t q = lane; q < chunks; q += 64) {
+      keep_bf16(xr[2 * q], xr[2 * q + 1], h);
+      store_f16(dst + 2 * q, h);
+    }
+    return;
+  }
   if constexpr (NCH > 0) {
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
@@ -151,7 +196,7 @@ __global__ __launch_bounds__(64 * XA_WAVES) void x_to_f16_branch_kernel(const ui
                                                                         uint16_t* out, int32_t* rexp, uint16_t* limbs,
                                                                         int64_t M, int64_t K, int r) {
   constexpr int XA_RUNS = CT <= 2 ? 12 : 8;              // of a wave, in registers
-  __shared__ uint32_t tops[XA_WAVES][16];
+  __shared__ uint32_t spans[XA_WAVES][16];
   __shared__ q2_f32x4 red[XA_WAVES][CT][64];
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -161,7 +206,7 @@ __global__ __launch_bounds__(64 * XA_WAVES) void x_to_f16_branch_kernel(const ui
   const int runs = (int)(K / 64);
   const uint16_t* const xr = x + m * K + 16 * g;
   q2_u32x4 v[XA_RUNS][2];
-  uint32_t top = 0;
+  Span sp;
 #pragma unroll
   for (int i = 0; i < XA_RUNS; ++i) {
     const int s = min(wv + XA_WAVES * i, runs - 1);
@@ -170,19 +215,27 @@ __global__ __launch_bounds__(64 * XA_WAVES) void x_to_f16_branch_kernel(const ui
     v[i][1] = p[1];
   }
 #pragma unroll
-  for (int i = 0; i < XA_RUNS; ++i) top = top_bits(top_bits(top, v[i][0]), v[i][1]);
+  for (int i = 0; i < XA_RUNS; ++i) {
+    sp.add(v[i][0]);
+    sp.add(v[i][1]);
+  }
   for (int s = wv + XA_WAVES * XA_RUNS; s < runs; s += XA_WAVES) {
     const q2_u32x4* p = reinterpret_cast<const q2_u32x4*>(xr + (int64_t)s * 64);
-    top = top_bits(top_bits(top, p[0]), p[1]);
+    sp.add(p[0]);
+    sp.add(p[1]);
   }
-  top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-  top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-  if (g == 0) tops[wv][c] = top;
+  uint32_t span = sp.word();
+  span = join_span(span, (uint32_t)__shfl_xor((int)span, 16));
+  span = join_span(span, (uint32_t)__shfl_xor((int)span, 32));
+  if (g == 0) spans[wv][c] = span;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < XA_WAVES; ++w) top = max(top, tops[w][c]);
-  const int shift = top_shift(top);
-  if (wv == 0 && g == 0 && live) rexp[m] = -shift;
+  for (int w = 0; w < XA_WAVES; ++w) span = join_span(span, spans[w][c]);
+  const int shift = top_shift(span >> 16);
+  const bool wide = is_wide(span);
+  const bool any_wide =                                  // among the sixteen rows; readfirstlane: a scalar branch
+      __builtin_amdgcn_readfirstlane((int)(__builtin_amdgcn_ballot_w64(wide) != 0)) != 0;
+  if (wv == 0 && g == 0 && live) rexp[m] = wide ? ROW_WIDE : -shift;
 
   const uint16_t* ar[CT];
 #pragma unroll
@@ -190,25 +243,55 @@ __global__ __launch_bounds__(64 * XA_WAVES) void x_to_f16_branch_kernel(const ui
   q2_f32x4 acc[CT];
 #pragma unroll
   for (int t = 0; t < CT; ++t) acc[t] = q2_f32x4{0.f, 0.f, 0.f, 0.f};
-  auto step = [&](int s, const q2_u32x4& v0, const q2_u32x4& v1) {
-    uint32_t h[8];
+  // With a wide row among them, all sixteen are multiplied as bf16, A as two bf16 values.
+  auto product = [&](auto any, int s, const q2_u32x4& v0, const q2_u32x4& v1) {
+    uint32_t h[8], raw[8];
     to_f16(v0, v1, shift, h);
-    if (live) store_f16(reinterpret_cast<q2_u32x4*>(out + m * K + (int64_t)s * 64 + 16 * g), h);
+    q2_u32x4* const dst = reinterpret_cast<q2_u32x4*>(out + m * K + (int64_t)s * 64 + 16 * g);
+    if constexpr (decltype(any)::value) {
+      keep_bf16(v0, v1, raw);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) raw[i] = wide ? raw[i] : h[i];
+      if (live) store_f16(dst, raw);
+    } else {
+      if (live) store_f16(dst, h);
+    }
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
       const q2_u32x4* p = reinterpret_cast<const q2_u32x4*>(ar[t] + (int64_t)s * 64);
-      acc[t] = mfma16_f16(q2_u32x4{h[0], h[1], h[2], h[3]}, p[0], acc[t]);
-      acc[t] = mfma16_f16(q2_u32x4{h[4], h[5], h[6], h[7]}, p[1], acc[t]);
+      if constexpr (decltype(any)::value) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const q2_u32x4 av = p[i], xv = i ? v1 : v0;
+          q2_u32x4 hi, lo;
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            hi[d] = f16x2_bf16_hi(av[d]);
+            lo[d] = f16x2_bf16_lo(av[d]);
+          }
+          acc[t] = mfma(xv, hi, acc[t]);
+          acc[t] = mfma(xv, lo, acc[t]);
+        }
+      } else {
+        acc[t] = mfma16_f16(q2_u32x4{h[0], h[1], h[2], h[3]}, p[0], acc[t]);
+        acc[t] = mfma16_f16(q2_u32x4{h[4], h[5], h[6], h[7]}, p[1], acc[t]);
+      }
     }
   };
-#pragma unroll
-  for (int i = 0; i < XA_RUNS; ++i) {
-    const int s = wv + XA_WAVES * i;
-    if (s < runs) step(s, v[i][0], v[i][1]);
-  }
-  for (int s = wv + XA_WAVES * XA_RUNS; s < runs; s += XA_WAVES) {
+  auto reread = [&](auto any, int s) {
     const q2_u32x4* p = reinterpret_cast<const q2_u32x4*>(xr + (int64_t)s * 64);
-    step(s, p[0], p[1]);
+    product(any, s, p[0], p[1]);
+  };
+  if (!any_wide) {
+#pragma unroll
+    for (int i = 0; i < XA_RUNS; ++i) {
+      const int s = wv + XA_WAVES * i;
+      if (s < runs) product(std::false_type{}, s, v[i][0], v[i][1]);
+    }
+    for (int s = wv + XA_WAVES * XA_RUNS; s < runs; s += XA_WAVES) reread(std::false_type{}, s);
+  } else {                                               // rare: from memory again, in a short loop
+#pragma unroll 1
+    for (int s = wv; s < runs; s += XA_WAVES) reread(std::true_type{}, s);
   }
 #pragma unroll
   for (int t = 0; t < CT; ++t) red[wv][t][lane] = acc[t];
@@ -222,11 +305,11 @@ __global__ __launch_bounds__(64 * XA_WAVES) void x_to_f16_branch_kernel(const ui
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int row = 4 * g + e;
-      uint32_t rt = 0;
+      uint32_t rs = 0;
 #pragma unroll
-      for (int w = 0; w < XA_WAVES; ++w) rt = max(rt, tops[w][row]);
+      for (int w = 0; w < XA_WAVES; ++w) rs = join_span(rs, spans[w][row]);
       if (m0 + row < M && col < r8) {
-        const float t = col < r ? __builtin_amdgcn_ldexpf(sum[e], -top_shift(rt)) : 0.f;
+        const float t = col < r ? __builtin_amdgcn_ldexpf(sum[e], any_wide ? 0 : -top_shift(rs >> 16)) : 0.f;
         const uint16_t hi = f32_to_bf16_rn(t), lo = f32_to_bf16_rn(t - bf16_to_f32(hi));
         limbs[(m0 + row) * 2 * r8 + col] = hi;
         limbs[(m0 + row) * 2 * r8 + r8 + col] = lo;
@@ -244,14 +327,25 @@ __global__ __launch_bounds__(64 * XA_WAVES) void x_to_f16_branch_kernel(const ui
 struct WTable {
   uint32_t lo, hi;
 };
-__device__ __forceinline__ WTable weight_table(uint16_t dbits) {
-  const _Float16 d = __builtin_bit_cast(_Float16, dbits);
-  const uint32_t v = dbits, v2 = __builtin_bit_cast(uint16_t, (_Float16)(d + d));
+// Of the weight with 16-bit pattern v and its double v2 (the code 3).
+__device__ __forceinline__ WTable weight_table(uint32_t v, uint32_t v2) {
   const uint32_t pair = v | (v2 << 16);                  // bytes lo, hi, lo2, hi2
   WTable t;
   t.lo = __builtin_amdgcn_perm(pair, pair, 0x02000C00u);                       // lo, 0, lo, lo2
   t.hi = __builtin_amdgcn_perm(pair, pair, 0x03010C01u) ^ 0x00000080u;         // -hi, 0, hi, hi2
   return t;
+}
+__device__ __forceinline__ WTable weight_table(uint16_t dbits) {
+  const _Float16 d = __builtin_bit_cast(_Float16, dbits);
+  return weight_table(dbits, __builtin_bit_cast(uint16_t, (_Float16)(d + d)));
+}
+// The two bf16 values that add up to the weight.
+__device__ __forceinline__ void weight_tables_bf16(uint16_t dbits, WTable& hi, WTable& lo) {
+  const float d = f16_to_f32(dbits);
+  const float dh = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, d) & 0xFFFF0000u), dl = d - dh;
+  auto top = [](float v) { return __builtin_bit_cast(uint32_t, v) >> 16; };
+  hi = weight_table(top(dh), top(dh + dh));
+  lo = weight_table(top(dl), top(dl + dl));
 }
 // K step t (0..3) of a 64-wide half block from the lane's two code dwords.
 template <int T>
@@ -352,11 +446,12 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
                                                (uint32_t)hs * 128u, 0, 0);
     }
   };
-  int row_exp = 0;
-  if (tid < FX_BM) {
-    const int64_t m = std::min<int64_t>(m0 + tid, rt.mend - 1);
-    row_exp = rexp[a.row_index ? source_row(a, m) : m];
-  }
+  // Exponents of the rows, lane l's of rows l and l + 64 (past the last row: its own), and which rows are wide.
+  auto load_exp = [&](int row) {
+    const int64_t m = std::min<int64_t>(m0 + std::min(row, FX_BM - 1), rt.mend - 1);
+    return rexp[a.row_index ? source_row(a, m) : m];
+  };
+  const int exp_lo = load_exp(lane), exp_hi = load_exp(64 + lane);
   int aoff[4];
 #pragma unroll
   for (int t = 0; t < 4; ++t) aoff[t] = c * 128 + (((4 * h + t) ^ ((c >> 1) & 7)) << 4);
@@ -364,15 +459,15 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
   // Codes: piece q holds columns 16 q .. + 15, lane l column l / 4 of them and
   // 16-byte position l % 4, which holds unit (l % 4) ^ (column / 4 % 4).
   const __amdgpu_buffer_rsrc_t rw = buf_rsrc(a.w + rt.expert * a.N * (K / 4), (uint32_t)(a.N * (K / 4)));
-  uint32_t woff[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    woff[q] = (uint32_t)(wcol(16 * q + (lane >> 2)) * (K / 4)) + (uint32_t)(((lane & 3) ^ ((lane >> 4) & 3)) << 4);
+  const int unit = (lane & 3) ^ ((lane >> 4) & 3);
+  auto code_off = [&](int q) { return (uint32_t)(wcol(16 * q + (lane >> 2)) * (K / 4)) + 16u * unit; };
+  const uint32_t woff0 = code_off(0), woff1 = code_off(1), woff2 = code_off(2), woff3 = code_off(3);
   auto copy_codes = [&](int set, int q) {                // past the last set: that one again, never used
-    const uint32_t wo = q == 0 ? woff[0] : q == 1 ? woff[1] : q == 2 ? woff[2] : woff[3];
+    const uint32_t wo = q == 0 ? woff0 : q == 1 ? woff1 : q == 2 ? woff2 : woff3;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         rw, (lds_void*)(smem + FX_OFF_W + ((set & 1) * 4 + wv) * FX_WBUF + q * 1024), 16,
-        wo - unit_back(set, KB, 2, (lane & 3) ^ ((lane >> 4) & 3)), unit_start(set, KB, 2), 0, 0);
+        wo - unit_back(set, KB, 2, unit),
+        unit_start(set, KB, 2), 0, 0);
   };
   const uint8_t* const wbase = smem + FX_OFF_W + wv * FX_WBUF + c * 64 + 8 * h;
   auto read_codes = [&](int hs, q2_u32x2 (&w)[2]) {
@@ -398,13 +493,7 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
-  // Operands of a step and of the one before it, whose products are still to come:
-  // zeros at first.
   q2_u32x2 w[2] = {};
-  q2_u32x4 av[2][MT], bf[2][2];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) av[1][i] = q2_u32x4{0u, 0u, 0u, 0u};
-  bf[1][0] = bf[1][1] = q2_u32x4{0u, 0u, 0u, 0u};
   uint64_t scn[2];
   load_scales(0, scn);
 #pragma unroll
@@ -413,21 +502,30 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
   copy_rows(0, 0);
   __builtin_amdgcn_s_waitcnt(0);
   read_codes(0, w);
-  for (int quad = 0; 4 * quad < KB; ++quad) {
-   const uint64_t sc[2] = {scn[0], scn[1]};
-   load_scales(quad + 1, scn);                           // past the end: the last four again, never used
-   const int b0 = min(4 * quad, KB - 4), bend = min(4 * quad + 4, KB);
-   for (int blk = 4 * quad; blk < bend; ++blk) {
-    const int sh = 16 * (blk - b0);
-    const WTable tab[2] = {weight_table((uint16_t)(sc[0] >> sh)), weight_table((uint16_t)(sc[1] >> sh))};
+  const uint64_t wide_lo = __builtin_amdgcn_ballot_w64(exp_lo == ROW_WIDE);
+  const uint64_t wide_hi = __builtin_amdgcn_ballot_w64(exp_hi == ROW_WIDE);
+  if ((wide_lo | wide_hi) == 0) {
+    // Operands of a step and of the one before it, whose products are still to come:
+    // zeros at first.
+    q2_u32x4 av[2][MT], bf[2][2];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int hs = 2 * blk + half;
-      stage_barrier<0>();
-      copy_codes((hs + 1) / 4 + 1, (hs + 1) & 3);
-      copy_rows(hs + 1 < NH ? hs + 1 : NH - 1, half ^ 1);          // past the end: the last one again, never read
-      const uint8_t* st = smem + half * FX_HALF;
-      q2_u32x2 wn[2];
+    for (int i = 0; i < MT; ++i) av[1][i] = q2_u32x4{0u, 0u, 0u, 0u};
+    bf[1][0] = bf[1][1] = q2_u32x4{0u, 0u, 0u, 0u};
+    for (int quad = 0; 4 * quad < KB; ++quad) {
+      const uint64_t sc[2] = {scn[0], scn[1]};
+      load_scales(quad + 1, scn);                        // past the end: the last four again, never used
+      const int b0 = min(4 * quad, KB - 4), bend = min(4 * quad + 4, KB);
+      for (int blk = 4 * quad; blk < bend; ++blk) {
+        const int sh = 16 * (blk - b0);
+        const WTable tab[2] = {weight_table((uint16_t)(sc[0] >> sh)), weight_table((uint16_t)(sc[1] >> sh))};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int hs = 2 * blk + half;
+          stage_barrier<0>();
+          copy_codes((hs + 1) / 4 + 1, (hs + 1) & 3);
+          copy_rows(hs + 1 < NH ? hs + 1 : NH - 1, half ^ 1);      // past the end: the last one again, never read
+          const uint8_t* st = smem + half * FX_HALF;
+          q2_u32x2 wn[2];
 #define Q2_STEP(T)                                                                                     \
   {                                                                                                    \
     constexpr int P = (T) & 1;                                                                         \
@@ -449,21 +547,95 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
   }
       Q2_STEP(0) Q2_STEP(1) Q2_STEP(2) Q2_STEP(3)
 #undef Q2_STEP
-      w[0] = wn[0];
-      w[1] = wn[1];
+          w[0] = wn[0];
+          w[1] = wn[1];
+        }
+      }
     }
-   }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] = mfma32(av[1][i], bf[1][j], acc[i][j]);
+  } else {
+    // A tile with a wide row: all its rows as bf16, the others' f16 values exactly, in
+    // the same order of steps; twice the products, four times the vector instructions.
+    // M = 1536, K = 4096, N = 12288: 276 us for 143 when every tile holds a wide row,
+    // 255 when one row of tiles does (it ends last); M = 4093, K = 12288, N = 4096 with
+    // rank 32: 748 for 398.
+    uint32_t kept[MT];                                   // all ones where row 32 i + c is bf16 already; a branch would cost more
+#pragma unroll
+    for (int i = 0; i < MT; ++i) kept[i] = 0u - ((uint32_t)((i < 2 ? wide_lo : wide_hi) >> (32 * (i & 1))) >> c & 1u);
+    q2_u32x4 av[2][MT], bh[2][2], bl[2][2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) av[1][i] = q2_u32x4{0u, 0u, 0u, 0u};
+    bh[1][0] = bh[1][1] = bl[1][0] = bl[1][1] = q2_u32x4{0u, 0u, 0u, 0u};
+    for (int quad = 0; 4 * quad < KB; ++quad) {
+      const uint64_t sc[2] = {scn[0], scn[1]};
+      load_scales(quad + 1, scn);                        // past the end: the last four again, never used
+      const int b0 = min(4 * quad, KB - 4), bend = min(4 * quad + 4, KB);
+      for (int blk = 4 * quad; blk < bend; ++blk) {
+        const int sh = 16 * (blk - b0);
+        WTable hi[2], lo[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) weight_tables_bf16((uint16_t)(sc[j] >> sh), hi[j], lo[j]);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int hs = 2 * blk + half;
+          stage_barrier<0>();
+          copy_codes((hs + 1) / 4 + 1, (hs + 1) & 3);
+          copy_rows(hs + 1 < NH ? hs + 1 : NH - 1, half ^ 1);      // past the end: the last one again, never read
+          const uint8_t* st = smem + half * FX_HALF;
+          q2_u32x2 wn[2];
+#define Q2_STEP(T)                                                                                     \
+  {                                                                                                    \
+    constexpr int P = (T) & 1;                                                                         \
+    if ((T) == 1) read_codes(hs + 1, wn);                                                              \
+    _Pragma("unroll") for (int i = 0; i < MT; ++i) {                                                   \
+      av[P][i] = *reinterpret_cast<const q2_u32x4*>(st + i * 4096 + aoff[T]);                          \
+      _Pragma("unroll") for (int d = 0; d < 4; ++d)                                                    \
+          av[P][i][d] = (av[P][i][d] & kept[i]) | (f16x2_bf16_hi(av[P][i][d]) & ~kept[i]);             \
+    }                                                                                                  \
+    _Pragma("unroll") for (int j = 0; j < 2; ++j) {                                                    \
+      bh[P][j] = decode_step<T>(w[j], hi[j]);                                                          \
+      bl[P][j] = decode_step<T>(w[j], lo[j]);                                                          \
+    }                                                                                                  \
+    _Pragma("unroll") for (int i = 0; i < MT; ++i)                                                     \
+        _Pragma("unroll") for (int j = 0; j < 2; ++j)                                                  \
+            acc[i][j] = mfma32_bf16(av[P ^ 1][i], bh[P ^ 1][j], acc[i][j]);                            \
+    _Pragma("unroll") for (int i = 0; i < MT; ++i)                                                     \
+        _Pragma("unroll") for (int j = 0; j < 2; ++j)                                                  \
+            acc[i][j] = mfma32_bf16(av[P ^ 1][i], bl[P ^ 1][j], acc[i][j]);                            \
+    __builtin_amdgcn_sched_group_barrier(0x100, MT + 2, 0);  /* LDS reads */                           \
+    _Pragma("unroll") for (int i = 0; i < 4 * MT; ++i) {                                               \
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);     /* product */                             \
+      __builtin_amdgcn_sched_group_barrier(0x002, 7, 0);     /* conversion and decode */               \
+    }                                                                                                  \
+    __builtin_amdgcn_sched_barrier(0);                                                                 \
   }
+          Q2_STEP(0) Q2_STEP(1) Q2_STEP(2) Q2_STEP(3)
+#undef Q2_STEP
+          w[0] = wn[0];
+          w[1] = wn[1];
+        }
+      }
+    }
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = mfma32(av[1][i], bf[1][j], acc[i][j]);
+      for (int j = 0; j < 2; ++j) {
+        acc[i][j] = mfma32_bf16(av[1][i], bh[1][j], acc[i][j]);
+        acc[i][j] = mfma32_bf16(av[1][i], bl[1][j], acc[i][j]);
+      }
+  }
   __builtin_amdgcn_s_waitcnt(0);                         // no copy may still write this workgroup's LDS
   __syncthreads();
 
   // The rows' powers of two: element 4 q + e of a tile is row 8 q + 4 h + e.
   int* const exps = reinterpret_cast<int*>(smem);
-  if (tid < FX_BM) exps[tid] = row_exp;
+  if (tid < FX_BM) {                                     // row 64 wv + lane; a wide row was not scaled
+    const int e = wv == 0 ? exp_lo : exp_hi;
+    exps[tid] = e == ROW_WIDE ? 0 : e;
+  }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < MT; ++i)

@@ -188,6 +188,99 @@ def test_many_rows(m, n, k, r, gated):
     check(y[:, sel], z, "gelu", gated, bias[torch.from_numpy(rows).to(DEV)], gate[sel], res[:, sel])
 
 
+def wide_rows(seed, m, k):
+    """bf16 bits of rows whose elements differ by up to 2^200 in size, among ordinary ones, and float64 values.
+    Every thirteenth row each: one large input; large inputs in the first block only; sizes spread over the whole range;
+    two sizes 2^45 apart; the smallest numbers, subnormal ones among them, beside 1; a row of zeros but for the ends."""
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((m, k))
+    x[1::13, 5] = 2.0 ** 41
+    x[2::13, :128] *= 2.0 ** 60
+    x[3::13] *= np.ldexp(1.0, rng.integers(-100, 101, x[3::13].shape))
+    x[4::13] *= np.where(rng.random(x[4::13].shape) < 0.02, 2.0 ** 45, 1.0)
+    x[5::13] = rng.integers(-300, 301, x[5::13].shape) * 2.0 ** -133
+    x[5::13, 7] = 1.0
+    x[6::13] = 0.0
+    x[6::13, [0, k - 1]] = 2.0 ** 90, 2.0 ** -90
+    xb = I.f32_to_bf16_bits(x.astype(np.float32))
+    return xb, O.bf16_to_f64(xb)
+
+
+def wide_weights(seed, n, k):
+    """Device weight, codes and scales: every fifth column has no weight at the large inputs of wide_rows, scales go
+    from the smallest subnormal f16 to 2^14."""
+    codes = np.random.default_rng(seed).integers(0, 3, (n, k)).astype(np.uint8)
+    codes[::5, :128] = 1
+    rng = np.random.default_rng(seed + 1)
+    scales = np.ldexp(1.0 + rng.integers(0, 1024, (n, k // 128)) / 1024.0, rng.integers(-14, 14, (n, 1)))
+    scales[::7] = rng.integers(1, 1024, scales[::7].shape) * 2.0 ** -24
+    scales = scales.astype(np.float32)
+    return q2.q2_pack(dev_u8(codes), torch.from_numpy(scales).to(DEV)), codes, scales
+
+
+def own_terms(x, w, a=None, b=None):
+    """x W^T (+ (x A^T) B^T) and the RMS sum of every element's own terms."""
+    z, size = x @ w.T, (x * x) @ (w * w).T
+    if a is not None:
+        z, size = z + (x @ a.T) @ b.T, size + ((x * x) @ (a * a).T) @ (b * b).T
+    return z, np.sqrt(size)
+
+
+# sizes that the kernel for many rows takes, the one between, and the plain one
+WIDE = [(1000, 5000, 640, 0), (1100, 4100, 12416, 0), (1100, 4100, 12416, 32), (1100, 4100, 4224, 12),
+        (700, 8200, 1152, 24), (300, 16400, 512, 64), (1100, 4100, 512, 100), (60, 9000, 640, 8),
+        (200, 3000, 384, 8)]
+
+
+@pytest.mark.parametrize("m,n,k,r", WIDE)
+def test_rows_whose_elements_differ_in_size(m, n, k, r):
+    """Every output is held to its own terms: where a weight is zero the input adds nothing, however large it is.
+    Products are exact and sums are in fp32, so K 2^-24 of the terms' sum would do; the branch's x A^T has 16 bits.
+    Terms below fp32's normal numbers may be lost: K of them.  (Other kernels than the one for many rows take a block's
+    sum of x off again, so an input of 2^60 covers the rest of its own block: rows 1 to 5 modulo 13 are left out.)"""
+    (p, s), codes, scales = wide_weights(361, n, k)
+    cols, _ = sample(n, False, 361)
+    w = (codes[cols].astype(np.float64) - 1) * np.repeat(scales[cols].astype(np.float64), 128, axis=1)
+    xb, x = wide_rows(361, m, k)
+    A = B = a = b = None
+    if r:
+        ab, bb = I.lowrank_factors(361, r, k, n, std=0.05)
+        ab[:, :128] = 0                                     # the branch sees none of the first block's large inputs
+        A, B = dev_bits(ab, torch.float16), dev_bits(bb, torch.float16)
+        a, b = O.f16_to_f64(ab), O.f16_to_f64(bb[cols])
+    z, size = own_terms(x, w, a, b)
+    got = q2.q2_linear_fused(dev_bits(xb, torch.bfloat16), p, s, A, B)
+    assert torch.equal(got, q2.q2_linear_fused(dev_bits(xb, torch.bfloat16), p, s, A, B))
+    g = host(got[:, torch.from_numpy(cols).to(DEV)])
+    assert np.isfinite(g).all()
+    bad = np.abs(g - z) > 1e-3 * size + k * 2.0 ** -126
+    if not (n >= 1536 and k >= 512 and m >= 300):
+        for i in range(1, 6):
+            bad[i::13] = False
+    assert not bad.any(), f"{bad.sum()} of {bad.size} outside, in rows {np.unique(np.argwhere(bad)[:, 0] % 13)} modulo 13"
+
+
+@pytest.mark.parametrize("counts,n,k", [([400, 0, 500], 10010, 640), ([1, 700, 64], 13000, 512)])
+@pytest.mark.parametrize("gather", [False, True])
+def test_grouped_rows_whose_elements_differ_in_size(counts, n, k, gather):
+    e, rows = len(counts), sum(counts)
+    (p, s), codes, scales = wide_weights(362, e * n, k)
+    cols, _ = sample(n, False, 362)
+    pick = (np.arange(e)[:, None] * n + cols).ravel()
+    w = ((codes[pick].astype(np.float64) - 1) * np.repeat(scales[pick].astype(np.float64), 128, axis=1)).reshape(e, len(cols), k)
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    xb, x = wide_rows(362, 500 if gather else rows, k)
+    index = np.random.default_rng(363).integers(-1, 501, rows).astype(np.int32) if gather else None
+    y = q2.q2_linear_grouped(dev_bits(xb, torch.bfloat16), torch.from_numpy(offsets).to(DEV), p.view(e, n, -1),
+                             s.view(e, n, -1), row_index=None if index is None else torch.from_numpy(index).to(DEV))
+    g = host(y[:, torch.from_numpy(cols).to(DEV)])
+    z = F.grouped_products(x, w, offsets, index)
+    size = np.sqrt(F.grouped_products(x * x, w * w, offsets, index))
+    bad = np.abs(g - z) > 1e-3 * size + k * 2.0 ** -126
+    assert np.isfinite(g).all()
+    assert not bad.any(), f"{bad.sum()} of {bad.size} outside, first {np.argwhere(bad)[0]}"
+
+
 # The tile of the kernel between few and many rows goes by the number of rows and columns.
 TILES = [(40, 500), (40, 9000), (100, 7000), (100, 10000), (100, 16000), (100, 19000), (100, 21010), (130, 13000)]
 
