@@ -283,7 +283,7 @@ int q4_linear(const uint16_t* x_bf16, const uint8_t* packed4, const uint16_t* sc
 /* Activations of q2_epilogue. */
 typedef enum {
   Q2_ACT_NONE = 0,      /* v                                                        */
-  Q2_ACT_RELU = 1,      /* max(v, 0)                                                */
+  Q2_ACT_RELU = 1,      /* max(v, 0), NaN for NaN                                   */
   Q2_ACT_GELU = 2,      /* v (1 + erf(v / sqrt 2)) / 2                              */
   Q2_ACT_GELU_TANH = 3, /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2        */
   Q2_ACT_SILU = 4       /* v / (1 + exp(-v))                                        */

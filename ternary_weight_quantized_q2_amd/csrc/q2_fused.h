@@ -109,7 +109,7 @@ __device__ __forceinline__ float logistic(float v) { return __builtin_amdgcn_rcp
 
 __device__ __forceinline__ float activate(int act, float v) {
   switch (act) {
-    case Q2_ACT_RELU: return fmaxf(v, 0.0f);
+    case Q2_ACT_RELU: return v < 0.0f ? 0.0f : v;         // a NaN stays one (fmaxf would drop it)
     case Q2_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
     // (1 + tanh u) / 2 is the logistic function of 2 u
     case Q2_ACT_GELU_TANH: return v * logistic(1.5957691216057308f * (v + 0.044715f * v * v * v));

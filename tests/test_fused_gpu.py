@@ -642,6 +642,23 @@ def test_non_finite_rows_stay_alone(fmt, m, n, k):
 
 
 @pytest.mark.parametrize("fmt", ["q2", "q4"])
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m,n,k", [(3, 200, 512), (40, 8206, 640), (100, 16000, 640), (100, 2002, 256), (900, 8200, 512)])
+def test_activations_keep_a_nan(fmt, act, m, n, k):
+    """A row of x with a NaN is NaN in every output, behind every activation, gated or not, in either column order."""
+    dev, _ = weights(fmt, 344, n, k)
+    _, x = acts(344, m, k)
+    x[2, k - 1] = np.nan
+    for gated in (False, True):
+        for out in (torch.float32, torch.bfloat16):
+            y = fused(fmt)(x, *dev, activation=act, gated=gated, out_dtype=out)
+            assert torch.isnan(y[2]).all() and torch.isfinite(y[:2]).all() and torch.isfinite(y[3:]).all()
+    off = torch.tensor([0, 2, m], dtype=torch.int32, device=DEV)
+    y = grouped(fmt)(x, off, *(torch.stack([t, t]) for t in dev), activation=act)
+    assert torch.isnan(y[2]).all() and torch.isfinite(y[:2]).all() and torch.isfinite(y[3:]).all()
+
+
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
 @pytest.mark.parametrize("rows,k", [(3, 128), (3, 640), (60, 256), (200, 640), (1100, 512)])
 def test_grouped_without_a_row_of_x(fmt, rows, k):
     """An index into no rows: every product is empty, the epilogue remains."""
