@@ -105,12 +105,32 @@ __device__ __forceinline__ BranchB branch_bfrag(const FusedArgs& a, int64_t n, i
 // exp and the reciprocal are the hardware's (about one ulp each); both GELU and
 // SiLU are v times a logistic or normal distribution function, so a large |v|
 // gives v or a zero, never inf / inf.
+// The normal distribution function of -a, a >= 0, is exp(-a^2 / 2) q(1 / (1 + 0.23 a))
+// with a polynomial q fitted on 0 <= a <= 13.3 for the least relative error, 4.8e-8:
+// relative, as the rest of a gated pair multiplies it, where (1 + erf) / 2 keeps
+// nothing below 2^-25.  It takes less time too (M = 1536, K = 4096, N = 12288: 151.6 us, 159.7).
+__device__ __forceinline__ float normal_tail(float a) {
+  const float s = __builtin_amdgcn_rcpf(__builtin_fmaf(0.23f, a, 1.0f));
+  float q = -0.078409999609f;
+  q = __builtin_fmaf(q, s, 0.290122002363f);
+  q = __builtin_fmaf(q, s, -0.277491927147f);
+  q = __builtin_fmaf(q, s, 0.300703167915f);
+  q = __builtin_fmaf(q, s, -0.032352376729f);
+  q = __builtin_fmaf(q, s, 0.119253337383f);
+  q = __builtin_fmaf(q, s, 0.085835561156f);
+  q = __builtin_fmaf(q, s, 0.092367239296f);
+  q = __builtin_fmaf(q, s, -2.7028827390e-05f);
+  return q * __builtin_amdgcn_exp2f(-0.72134752044448170f * (a * a));        // log2(e) / 2
+}
 __device__ __forceinline__ float logistic(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
 
 __device__ __forceinline__ float activate(int act, float v) {
   switch (act) {
     case Q2_ACT_RELU: return v < 0.0f ? 0.0f : v;         // a NaN stays one (fmaxf would drop it)
-    case Q2_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    case Q2_ACT_GELU: {
+      const float tail = normal_tail(fabsf(v));
+      return v * (v < 0.0f ? tail : 1.0f - tail);
+    }
     // (1 + tanh u) / 2 is the logistic function of 2 u
     case Q2_ACT_GELU_TANH: return v * logistic(1.5957691216057308f * (v + 0.044715f * v * v * v));
     case Q2_ACT_SILU: return v * logistic(v);

@@ -6,8 +6,11 @@ Tolerance of an output: the product z is held to the linears' bar, |err z| <=
 (finfo.eps / 2 relative).  The epilogue's own fp32 arithmetic is a few ulps of
 its terms, 2^-20 of them is allowed.
 """
+import math
+
 import numpy as np
 import pytest
+import scipy.special
 import torch
 
 import oracle.fused_oracle as F
@@ -639,6 +642,33 @@ def test_non_finite_rows_stay_alone(fmt, m, n, k):
     keep = torch.ones(m, dtype=torch.bool, device=DEV)
     keep[1:3] = False
     assert torch.equal(got[keep], want[keep]) and torch.isfinite(want).all()
+
+
+# of an activation: the range on which its value is a normal number, the exact value, and the size of the argument of its
+# exponential, whose rounding the value takes over
+TAILS = {"gelu": (13.0, lambda v: v * scipy.special.ndtr(v), lambda v: v * v / 2),
+         "gelu_tanh": (9.5, lambda v: v * scipy.special.expit(math.sqrt(8 / math.pi) * (v + 0.044715 * v ** 3)),
+                       lambda v: math.sqrt(8 / math.pi) * np.abs(v + 0.044715 * v ** 3)),
+         "silu": (80.0, lambda v: v * scipy.special.expit(v), np.abs)}
+
+
+@pytest.mark.parametrize("act", TAILS)
+@pytest.mark.parametrize("m,n,k", [(2, 16000, 128), (40, 16000, 640), (100, 16001, 256), (900, 16000, 512)])
+def test_activations_relative_to_their_values(act, m, n, k):
+    """The bias alone (x is 0): every value to a few ulps of itself, also where it is tiny, as a gated factor multiplies
+    it.  Of an exponential of argument u four roundings of u (three in u, one in the exponential's base) add
+    4 |u| 2^-24; the exponential, a reciprocal, a polynomial of positive value and four products sixteen more."""
+    most, exact, argument = TAILS[act]
+    dev, _ = weights("q2", 345, 2 * n, k)
+    v = torch.linspace(-most, most, n)
+    bias = torch.cat([v, torch.full((n,), 3.0)]).to(DEV)
+    x = torch.zeros((m, k), dtype=torch.bfloat16, device=DEV)
+    vd = v.double().numpy()
+    tol = 2.0 ** -24 * (4 * argument(vd) + 16) * np.abs(exact(vd)) + 2.0 ** -126
+    got = host(q2.q2_linear_fused(x, *dev, bias=bias, activation=act, gated=True)[-1])
+    assert (np.abs(got / 3 - exact(vd)) <= tol).all()
+    got = host(q2.q2_linear_fused(x, *(t[:n] for t in dev), bias=bias[:n].contiguous(), activation=act)[-1])
+    assert (np.abs(got - exact(vd)) <= tol).all()
 
 
 @pytest.mark.parametrize("fmt", ["q2", "q4"])
