@@ -333,6 +333,17 @@ __device__ __forceinline__ void store_strip(const FusedArgs& a, const float* bia
   }
 }
 
+// ---- grids -----------------------------------------------------------------------
+// A launch of 2^32 or more threads along one dimension runs without an error, but
+// not all of it.  Workgroups past GRID_X go along the second dimension, which may
+// reach past the last one.
+constexpr int GRID_X = 1 << 21;
+inline dim3 grid_of(int64_t workgroups) {
+  return workgroups <= GRID_X ? dim3((unsigned)workgroups)
+                              : dim3(GRID_X, (unsigned)((workgroups + GRID_X - 1) / GRID_X));
+}
+__device__ __forceinline__ int workgroup_id() { return (int)(blockIdx.x + blockIdx.y * (unsigned)GRID_X); }
+
 // ---- row groups ----------------------------------------------------------------
 // Offsets are clamped to [0, M] and to not decrease within a group, so whatever
 // they hold, the rows lie inside x and y.
@@ -363,11 +374,13 @@ __device__ __forceinline__ int group_tiles(const FusedArgs& a, int64_t e, int bm
 // Every wave of the workgroup calls it together; the results are scalars
 // (readlane), so that buffer resources built on them stay in scalar registers.
 __device__ __forceinline__ bool find_tile(const FusedArgs& a, int bm, int tiles_n, int group_m, RowTile& rt, int& tn) {
+  const int wg = workgroup_id();
   rt.expert = 0;
   rt.mend = a.M;
   if (a.offsets == nullptr) {
     const int tiles_m = a.M <= bm ? 1 : (int)((a.M + bm - 1) / bm);
-    const int tile = xcd_tile((int)blockIdx.x, tiles_m * tiles_n);
+    if (wg >= tiles_m * tiles_n) return false;
+    const int tile = xcd_tile(wg, tiles_m * tiles_n);
     if (tiles_m == 1) {
       rt.m0 = 0;
       tn = tile;
@@ -389,9 +402,9 @@ __device__ __forceinline__ bool find_tile(const FusedArgs& a, int bm, int tiles_
   for (int d = 32; d; d >>= 1) total += __shfl_xor(total, d);
   total = __builtin_amdgcn_readfirstlane(total);
   // bad offsets can count more tiles than the launch covers
-  const int tiles = (int)min((int64_t)total * tiles_n, (int64_t)gridDim.x);
-  if ((int)blockIdx.x >= tiles) return false;
-  const int tile = xcd_tile((int)blockIdx.x, tiles);
+  const int tiles = (int)min((int64_t)total * tiles_n, (int64_t)min(gridDim.x * gridDim.y, 0x7fffffffu));
+  if (wg >= tiles) return false;
+  const int tile = xcd_tile(wg, tiles);
   int slot = tile / tiles_n;
   tn = tile - slot * tiles_n;
   for (int64_t e0 = 0; e0 < a.E; e0 += 64) {             // slot < total: found before the last group's end

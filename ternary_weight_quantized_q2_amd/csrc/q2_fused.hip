@@ -167,7 +167,7 @@ hipError_t launch_fused(const FusedArgs& a, int fmt, void* ws, hipStream_t strea
   const int64_t cols = a.gated ? F_BN / 2 : F_BN;
   const int64_t tiles_n = (fused_n_out(a) + cols - 1) / cols, slots = max_row_tiles(a, F_BM);
   if (tiles_n > 0x7fffffff || slots > 0x7fffffff / tiles_n) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)(slots * tiles_n));
+  const dim3 grid = grid_of(slots * tiles_n);
   if (fmt == 0) hipLaunchKernelGGL((fused_tile_kernel<0>), grid, dim3(256), 0, stream, a, (int)tiles_n);
   else hipLaunchKernelGGL((fused_tile_kernel<1>), grid, dim3(256), 0, stream, a, (int)tiles_n);
   return hipGetLastError();

@@ -751,7 +751,7 @@ hipError_t launch_fused_f16(const FusedArgs& a, void* ws, hipStream_t stream) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int group_m = tile_group_rows(slots, tiles_n, 2.0 * bm * (double)K, (double)FX_BN * K * 0.265625, 64);
-  const dim3 grid((unsigned)(slots * tiles_n));
+  const dim3 grid = grid_of(slots * tiles_n);
 #define Q2_FX(MT) \
   hipLaunchKernelGGL((fused_f16_kernel<MT>), grid, dim3(256), 0, stream, a, x16, rexp, (int)tiles_n, group_m)
   if (bm == 96) Q2_FX(3);

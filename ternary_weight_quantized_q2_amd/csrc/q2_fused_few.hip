@@ -258,7 +258,7 @@ static hipError_t run_few(const FusedArgs& a, int bm, int64_t slots, int64_t til
   while (kg > 1 && rows * few_row_bytes(kg * FEW_BLOCKS) > 64 * 1024) --kg;
   const size_t lds = std::max<size_t>((size_t)rows * few_row_bytes(kg * FEW_BLOCKS),
                                       (size_t)kg * 16 * (FEW_COLS + 1) * 4);
-  hipLaunchKernelGGL((fused_few_kernel<FMT, SHORT, BRANCH>), dim3((unsigned)wgs), dim3(64 * kg), lds, stream, a, bm,
+  hipLaunchKernelGGL((fused_few_kernel<FMT, SHORT, BRANCH>), grid_of(wgs), dim3(64 * kg), lds, stream, a, bm,
                      (int)tiles_n);
   return hipGetLastError();
 }

@@ -352,7 +352,7 @@ static hipError_t run_mid(const FusedArgs& a, hipStream_t stream) {
   if (tiles_n > 0x7fffffff || slots > 0x7fffffff / tiles_n) return hipErrorInvalidValue;
   const int group_m = tile_group_rows(slots, tiles_n, 2.0 * BM * (double)a.K,
                                       (double)BN * a.K * (FMT == 0 ? 0.265625 : 0.53125), KG > 2 ? 32 : 64);
-  hipLaunchKernelGGL((fused_mid_kernel<FMT, MT, NT, NW, KG, OCC>), dim3((unsigned)(slots * tiles_n)), dim3(64 * NW * KG), 0,
+  hipLaunchKernelGGL((fused_mid_kernel<FMT, MT, NT, NW, KG, OCC>), grid_of(slots * tiles_n), dim3(64 * NW * KG), 0,
                      stream, a, (int)tiles_n, group_m);
   return hipGetLastError();
 }

@@ -416,7 +416,7 @@ __device__ __forceinline__ Eight load8(const void* p, int64_t i, int bf16) {
 __global__ __launch_bounds__(256) void combine_kernel(const void* z, int z_bf16, int64_t R, const int32_t* slot,
                                                       const float* weight, const void* residual, int res_bf16, void* y,
                                                       int out_bf16, int64_t T, int k, int64_t N, int64_t chunks) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t id = (int64_t)workgroup_id() * 256 + threadIdx.x;
   const int64_t t = id / chunks;
   if (t >= T) return;
   const int64_t n0 = (id - t * chunks) * CB_COLS;
@@ -492,7 +492,7 @@ __global__ __launch_bounds__(64 * CR_WAVES) void combine_ragged_kernel(const voi
                                                                        int64_t chunks) {
   typedef uint16_t half_w __attribute__((ext_vector_type(W)));
   typedef float float_w __attribute__((ext_vector_type(W)));
-  const int64_t id = (int64_t)blockIdx.x * CR_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t id = (int64_t)workgroup_id() * CR_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = id / chunks;
   if (t >= T) return;
   const int64_t n = (id - t * chunks) * (64 * W * CR_STEPS) + (threadIdx.x & 63) * W, left = N - n;
@@ -537,7 +537,7 @@ hipError_t launch_combine(const void* z, int z_bf16, int64_t R, const int32_t* s
   const int64_t per = vec ? 256 : CR_WAVES, blocks = (T * chunks + per - 1) / per;
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
 #define Q2_COMBINE(KERNEL)                                                                                            \
-  hipLaunchKernelGGL(KERNEL, dim3((unsigned)blocks), dim3(256), 0, stream, z, z_bf16, R, slot, weight, residual,      \
+  hipLaunchKernelGGL(KERNEL, grid_of(blocks), dim3(256), 0, stream, z, z_bf16, R, slot, weight, residual,      \
                      res_bf16, y, out_bf16, T, k, N, chunks)
   if (vec) Q2_COMBINE(combine_kernel);
   else if (pairs) Q2_COMBINE((combine_ragged_kernel<2>));

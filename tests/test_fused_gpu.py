@@ -510,6 +510,36 @@ def test_offsets_beyond_32_bits(fmt):
     check(y[torch.from_numpy(rows).to(DEV)], z)
 
 
+def test_more_than_32_bits_of_threads_one_row():
+    """2^24 workgroups of 256 threads and a few more: every column is the sum of x or its negative."""
+    n, k = 2 ** 29 + 70, 128
+    p = torch.full((n, k // 4), 0xAA, dtype=torch.uint8, device=DEV)          # codes 2
+    p[n // 2:] = 0                                                            # codes 0
+    x = torch.ones((1, k), device=DEV, dtype=torch.bfloat16)
+    y = torch.zeros((1, n), device=DEV)
+    q2.q2_linear_fused(x, p, torch.ones((n, 1), device=DEV, dtype=torch.float16), y=y)
+    assert (y[0, :n // 2] == k).all() and (y[0, n // 2:] == -k).all()
+    del p, y
+    torch.cuda.empty_cache()
+
+
+def test_more_than_32_bits_of_threads_many_rows():
+    """More than 2^24 tiles of 32 x 64."""
+    m, n, k = 2 ** 20 + 40, 2 ** 15, 128
+    dev, w = weights("q2", 346, n, k)
+    xb, x = acts(346, 4096, k)
+    row = torch.arange(m, device=DEV) % 4096
+    y = torch.full((m, n), 7.0, device=DEV, dtype=torch.bfloat16)
+    q2.q2_linear_fused(x[row], *dev, y=y)
+    want = y[:4096].clone()
+    check(want[:64], O.bf16_to_f64(xb[:64]) @ w.T)
+    for lo in range(0, m, 4096):
+        part = y[lo:lo + 4096]
+        assert torch.equal(part, want[:len(part)])
+    del y
+    torch.cuda.empty_cache()
+
+
 # ---------------------------------------------------------------------------
 # grouped
 # ---------------------------------------------------------------------------

@@ -213,6 +213,19 @@ def test_combine_beyond_32_bits():
     assert (y[0] == 7).all() and (y[1] == 1.5).all()
 
 
+@pytest.mark.parametrize("t,n,out", [(2 ** 26 + 9, 1, torch.float32), (2 ** 26 + 9, 2, torch.bfloat16),
+                                     (2 ** 23 + 1, 4096, torch.bfloat16)])
+def test_combine_of_more_than_32_bits_of_threads(t, n, out):
+    """Every token's row is its weight, all of them written."""
+    weight = (torch.arange(t, device=DEV) % 251).float().view(t, 1)
+    y = torch.full((t, n), -1.0, device=DEV, dtype=out)
+    q2.q2_combine(torch.ones((1, n), device=DEV), torch.zeros((t, 1), device=DEV, dtype=torch.int32), weight, y=y)
+    for lo in range(0, t, 2 ** 20):                         # whole numbers below 2^8 are exact in bf16
+        assert (y[lo:lo + 2 ** 20] == weight[lo:lo + 2 ** 20]).all()
+    del y
+    torch.cuda.empty_cache()
+
+
 # ---------------------------------------------------------------------------
 # together: an expert layer with its router, from logits to the residual stream
 # ---------------------------------------------------------------------------
