@@ -388,8 +388,8 @@ __device__ __forceinline__ bool find_tile(const FusedArgs& a, int bm, int tiles_
     }
     const int grp = tile / (group_m * tiles_n), gi = tile - grp * group_m * tiles_n;
     const int gm = min(group_m, tiles_m - grp * group_m);
-    rt.m0 = (int64_t)(grp * group_m + gi % gm) * bm;
     tn = gi / gm;
+    rt.m0 = (int64_t)(grp * group_m + (gi + tn) % gm) * bm;
     return true;
   }
   const int lane = threadIdx.x & 63;

@@ -559,9 +559,11 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
   } else {
     // A tile with a wide row: all its rows as bf16, the others' f16 values exactly, in
     // the same order of steps; twice the products, four times the vector instructions.
-    // M = 1536, K = 4096, N = 12288: 276 us for 143 when every tile holds a wide row,
-    // 255 when one row of tiles does (it ends last); M = 4093, K = 12288, N = 4096 with
-    // rank 32: 748 for 398.
+    // M = 1536, K = 4096, N = 12288: 270 us for 141 when every tile holds a wide row,
+    // 198 when one row of tiles does (first in its CU, as it ends last, and spread over
+    // the CUs by find_tile's order: 252 without either); M = 4093, K = 12288, N = 4096
+    // with rank 32: 732 for 392.
+    __builtin_amdgcn_s_setprio(3);
     uint32_t kept[MT];                                   // all ones where row 32 i + c is bf16 already; a branch would cost more
 #pragma unroll
     for (int i = 0; i < MT; ++i) kept[i] = 0u - ((uint32_t)((i < 2 ? wide_lo : wide_hi) >> (32 * (i & 1))) >> c & 1u);
@@ -626,6 +628,7 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
         acc[i][j] = mfma32_bf16(av[1][i], bh[1][j], acc[i][j]);
         acc[i][j] = mfma32_bf16(av[1][i], bl[1][j], acc[i][j]);
       }
+    __builtin_amdgcn_s_setprio(0);
   }
   __builtin_amdgcn_s_waitcnt(0);                         // no copy may still write this workgroup's LDS
   __syncthreads();
