@@ -341,8 +341,8 @@ int q2_linear_fused(const uint16_t* x_bf16, const uint8_t* packed, const uint16_
                     void* y, int64_t M, int64_t N, int64_t K,
                     void* workspace, size_t workspace_bytes, hipStream_t stream);
 
-/* q2_linear_fused_workspace_bytes - device bytes q2_linear_fused needs; 0 for
- * sizes that it refuses or that need none. */
+/* q2_linear_fused_workspace_bytes - device bytes q2_linear_fused needs; for
+ * sizes that it refuses, 0 or the bytes of the branch (M rows, rank r) alone. */
 size_t q2_linear_fused_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r);
 
 /*

@@ -369,8 +369,9 @@ __device__ __forceinline__ int group_tiles(const FusedArgs& a, int64_t e, int bm
 // The tile of this workgroup; false when there is none for it (the launch covers
 // the most tiles that the offsets can make).  Each XCD gets a contiguous range
 // of tile numbers.  Without groups they run over blocks of group_m row tiles,
-// row-fastest inside (see tile_group_rows); with groups over the column tiles
-// of a row tile, so an XCD meets few experts and reads their weights once.
+// row-fastest inside (see tile_group_rows) and from another row in each column, so
+// that a row's tiles are not all on the same CUs of an XCD; with groups over the
+// column tiles of a row tile, so an XCD meets few experts and reads their weights once.
 // Every wave of the workgroup calls it together; the results are scalars
 // (readlane), so that buffer resources built on them stay in scalar registers.
 __device__ __forceinline__ bool find_tile(const FusedArgs& a, int bm, int tiles_n, int group_m, RowTile& rt, int& tn) {

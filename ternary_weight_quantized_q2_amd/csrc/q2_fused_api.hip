@@ -111,8 +111,9 @@ int grouped_entry(int fmt, const uint16_t* x, int64_t x_rows, const int32_t* row
   return launch(a, fmt, need ? workspace : nullptr, stream, "grouped linear launch");
 }
 
+// Sizes that a linear takes, for the workspace queries: no error, no message.
 bool sizes_ok(int64_t M, int64_t N, int64_t K) {
-  return M > 0 && N > 0 && K > 0 && check_sizes(M, N, K) == Q2_OK && check_linear_k(K) == Q2_OK;
+  return M > 0 && N > 0 && K > 0 && K % 128 == 0 && K <= kMostK && sizes_fit(M, N, K);
 }
 
 bool route_sizes_ok(int64_t T, int64_t E, int64_t k) {
@@ -144,7 +145,7 @@ int q4_linear_fused(const uint16_t* x_bf16, const uint8_t* packed4, const uint16
 }
 
 size_t q2_linear_grouped_workspace_bytes(int64_t R, int64_t E, int64_t N, int64_t K) {
-  if (E <= 0 || E > 65536 || R > 0x7fffffff || !sizes_ok(R, N, K)) return 0;
+  if (E <= 0 || E > 65536 || R > 0x7fffffff || !sizes_ok(R, N, K) || !sizes_fit(0, E * N, K)) return 0;
   return q2dev::fused_workspace_bytes(R, N, K, E, 0);
 }
 

@@ -34,22 +34,25 @@ inline int check_ptr(const void* p, bool nonempty, size_t align, const char* nam
   return Q2_OK;
 }
 
+// keep every element index inside int64 with room to spare
+inline bool sizes_fit(int64_t M, int64_t N, int64_t K) {
+  const int64_t lim = (int64_t)1 << 46;
+  return M <= lim && N <= lim && K <= lim && (M <= 0 || (K <= lim / M && N <= lim / M)) && (N <= 0 || K <= lim / N);
+}
+
 inline int check_sizes(int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N < 0 || K < 0) return fail(Q2_ERR_ARG, "negative size (M=%lld N=%lld K=%lld)", (long long)M,
                                            (long long)N, (long long)K);
   if (K % 128 != 0) return fail(Q2_ERR_SHAPE, "K=%lld is not a multiple of 128", (long long)K);
-  // keep every element index inside int64 with room to spare
-  const int64_t lim = (int64_t)1 << 46;
-  if (M > lim || N > lim || K > lim || (M > 0 && K > lim / M) || (N > 0 && K > lim / N) ||
-      (M > 0 && N > lim / M))
-    return fail(Q2_ERR_ARG, "sizes too large");
+  if (!sizes_fit(M, N, K)) return fail(Q2_ERR_ARG, "sizes too large");
   return Q2_OK;
 }
 
 // The linear kernels address one tile's activation rows and weight columns
 // with 32-bit offsets; K up to 2^24 keeps them in range for every tile shape.
+constexpr int64_t kMostK = (int64_t)1 << 24;
 inline int check_linear_k(int64_t K) {
-  if (K > ((int64_t)1 << 24)) return fail(Q2_ERR_SHAPE, "K=%lld exceeds 16777216", (long long)K);
+  if (K > kMostK) return fail(Q2_ERR_SHAPE, "K=%lld exceeds 16777216", (long long)K);
   return Q2_OK;
 }
 

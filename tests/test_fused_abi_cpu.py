@@ -174,3 +174,15 @@ def test_route_workgroups_hold_few_enough_tokens_for_their_counts(lib):
     for t in (65, 70001, 1023 * 65536, 1023 * 65536 + 1, 2 ** 26 - 1, 2 ** 26):
         groups = lib.q2_route_workspace_bytes(t, 1024, 1) // 2048
         assert groups * 65535 >= t, t
+
+
+def test_workspace_queries_leave_the_message(lib):
+    """A query is no failed call, whatever its sizes."""
+    f, g = lib.q2_linear_fused_workspace_bytes, lib.q2_linear_grouped_workspace_bytes
+    assert lib.q2_linear(None, None, None, None, -1, 1, 128, None) == q2.Q2_ERR_ARG
+    detail = lib.q2_last_error()
+    assert b"negative" in detail
+    for k in (100, (1 << 24) + 128, -128):
+        assert f(4, 8, k, 0) == 0 and f(4096, 8192, k, 0) == 0 and g(4096, 4, 8192, k) == 0
+    assert f(1 << 40, 1 << 20, 128, 0) == 0 and f(4, 1 << 46, 128, 0) == 0 and g(1 << 20, 1 << 16, 1 << 30, 1 << 20) == 0
+    assert lib.q2_last_error() == detail
