@@ -35,6 +35,10 @@
  *    are checked before any HIP call, so argument errors are reported even on
  *    a host without a GPU.  q2_pack is the exception: it synchronizes on
  *    `stream` to report bad codes or scales.
+ *  - q2_linear and its lowrank, ex, a8 and 4-bit forms, and the rank-r branch
+ *    of q2_linear_fused, launch at most 2^32 - 1 threads and refuse sizes
+ *    beyond (Q2_ERR_HIP): from about 2^24 rows (a8), 2^26 rows (rank r) or
+ *    2^28 weight rows (16 rows of x or fewer) on.
  *  - Errors are negative q2_status values; nothing is thrown across the ABI.
  *    q2_strerror() names a status, q2_last_error() gives the calling thread's
  *    detail message for its most recent failed call.

@@ -114,7 +114,7 @@ __global__ __launch_bounds__(QZ8_THREADS) void quantize_rows_i8_kernel(const uin
 
 hipError_t launch_quantize_rows_i8(const uint16_t* x, uint8_t* xq, float* row_scale, int64_t M, int64_t K,
                                    hipStream_t stream) {
-  if (M > 0x7fffffff) return hipErrorInvalidValue;
+  if (!grid_fits(M, QZ8_THREADS)) return hipErrorInvalidValue;
   hipLaunchKernelGGL(quantize_rows_i8_kernel, dim3((unsigned)M), dim3(QZ8_THREADS), 0, stream, x, xq, row_scale, K);
   return hipGetLastError();
 }
@@ -535,7 +535,7 @@ static hipError_t run_a8(const A8Args& a, int ksplit, hipStream_t stream) {
   if (ksplit != 1 && ksplit != 2) return hipErrorInvalidValue;
   const int kpart = (ksplit == 2) ? (int)((KB + 1) / 2) : 0;
   const int64_t grid = tiles_m * tiles_n * (kpart > 0 ? 2 : 1);
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  if (!grid_fits(grid, 256 * KG)) return hipErrorInvalidValue;
   if (kpart > 0) {
     const hipError_t e = launch_zero_y(a.y, a.M * a.N, stream);
     if (e != hipSuccess) return e;

@@ -5,6 +5,10 @@
 
 namespace q2dev {
 
+// Whether a launch takes that many workgroups along one dimension: of 2^32 threads
+// and more it runs a part and returns without an error.
+inline bool grid_fits(int64_t workgroups, int threads) { return workgroups <= 0xffffffffll / threads; }
+
 // One linear call: x [M, K] bf16, weights in format fmt (0 = Q2_0, 1 = 4-bit),
 // y [M, N] fp32.  lr_t / lr_b / r describe an optional low-rank term the
 // kernels add into their accumulators (lr_t = bf16 limbs [M, 2r] of x A^T,

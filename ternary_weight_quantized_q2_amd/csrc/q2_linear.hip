@@ -1526,7 +1526,7 @@ static hipError_t run_gemm(const LinearArgs& a, hipStream_t stream) {
   const int64_t tiles_m = (a.M + BM - 1) / BM;
   const int64_t tiles_n = (a.N + BN - 1) / BN;
   const int64_t tiles = tiles_m * tiles_n;
-  if (tiles > 0x7fffffff) return hipErrorInvalidValue;
+  if (!grid_fits(tiles, 256)) return hipErrorInvalidValue;
   const int vec = lowrank_vec(a);
   // The low-rank branch only exists for Q2_0 weights.
   if constexpr (FMT == 0) {
@@ -1548,7 +1548,7 @@ static hipError_t launch_gemv(const LinearArgs& a, int64_t cb, hipStream_t strea
   const size_t red = (size_t)WAVES * 64 * 16;
   if (bytes < red) bytes = red;
   const int64_t grid = (a.N + 15) / 16;
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  if (!grid_fits(grid, WAVES * 64)) return hipErrorInvalidValue;
   hipLaunchKernelGGL((gemv_kernel<FMT, QMAX, WAVES>), dim3((unsigned)grid), dim3(WAVES * 64), bytes, stream, a,
                      (int)cb, lowrank_vec(a));
   return hipGetLastError();
@@ -1642,7 +1642,7 @@ static hipError_t run_gemm_kgroup(const LinearArgs& a, int ksplit, hipStream_t s
     return hipErrorInvalidValue;
   const int kpart = (ksplit == 2) ? (int)((KB + 1) / 2) : 0;
   const int64_t grid = tiles * (kpart > 0 ? 2 : 1);
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  if (!grid_fits(grid, 256 * KG)) return hipErrorInvalidValue;
   if (kpart > 0) {
     const hipError_t e = launch_zero_y(a.y, a.M * a.N, stream);
     if (e != hipSuccess) return e;
@@ -1778,7 +1778,7 @@ hipError_t launch_lowrank_t(const uint16_t* x, const uint16_t* A, uint16_t* tl, 
                             hipStream_t stream) {
   const int64_t gx = (M + 15) / 16;
   const int gy = (lr_pad(r) + 15) / 16;
-  if (gx > 0x7fffffff || gy > 65535) return hipErrorInvalidValue;
+  if (!grid_fits(gx, LR_WAVES * 64) || gy > 65535) return hipErrorInvalidValue;
   hipLaunchKernelGGL(lowrank_t_kernel, dim3((unsigned)gx, (unsigned)gy), dim3(LR_WAVES * 64), 0, stream, x, A, tl, M,
                      K, r);
   return hipGetLastError();
