@@ -411,6 +411,61 @@ def test_residual_in_place(fmt, out, m):
     check(y, O.bf16_to_f64(xb) @ w.T, "relu", residual=r0)
 
 
+# one size for each kernel beyond the one for few tiles, the first two with rows of whole 16-byte pieces and without
+KERNELS = [(60, 9000, 640), (60, 9002, 640), (900, 8200, 512), (900, 8206, 512), (200, 3000, 384)]
+
+
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
+@pytest.mark.parametrize("regime", I.ACT_REGIMES)
+@pytest.mark.parametrize("m,n,k", KERNELS)
+def test_activation_regimes_of_every_kernel(fmt, regime, m, n, k):
+    dev, w = weights(fmt, 347, n, k)
+    cols, rows = sample(n, False, 347)
+    xb = I.activations_regime_bf16(347, m, k, regime)
+    y = fused(fmt)(dev_bits(xb, torch.bfloat16), *dev)
+    check(y[:, torch.from_numpy(cols).to(DEV)], O.bf16_to_f64(xb) @ w[rows].T, what=regime)
+
+
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m,n,k", KERNELS)
+def test_epilogue_in_place_of_every_kernel(fmt, gated, act, m, n, k):
+    dev, w = weights(fmt, 348, n, k)
+    cols, rows = sample(n, gated, 348)
+    sel, wsel = torch.from_numpy(cols).to(DEV), torch.from_numpy(rows).to(DEV)
+    n_out = n // 2 if gated else n
+    xb, x = acts(348, m, k)
+    z = O.bf16_to_f64(xb) @ w[rows].T
+    bias, gate, res = rnd(1, n).to(DEV), rnd(2, n_out).to(DEV), rnd(3, m, n_out).to(DEV)
+    for out in (torch.float32, torch.bfloat16):
+        r0 = res.to(out)
+        y = r0.clone()
+        assert fused(fmt)(x, *dev, bias=bias, gate=gate, activation=act, gated=gated, residual=y, y=y) is y
+        check(y[:, sel], z, act, gated, bias[wsel], gate[sel], r0[:, sel], what="in place")
+        other = torch.bfloat16 if out == torch.float32 else torch.float32
+        assert torch.equal(y, fused(fmt)(x, *dev, bias=bias, gate=gate, activation=act, gated=gated, residual=r0,
+                                         out_dtype=out))
+        y = fused(fmt)(x, *dev, activation=act, gated=gated, residual=res.to(other), out_dtype=out)
+        check(y[:, sel], z, act, gated, residual=res.to(other)[:, sel], what="mixed types")
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("m,n,k,r", [(200, 3000, 384, 5), (300, 2502, 128, 40), (500, 1300, 256, 200)])
+def test_branch_of_the_plain_kernel(gated, m, n, k, r):
+    """K below four blocks and more tiles than the kernel for few of them takes."""
+    (p, s), w = weights("q2", 349, n, k)
+    xb, x = acts(349, m, k)
+    a, b = I.lowrank_factors(349, r, k, n, std=0.05)
+    xd = O.bf16_to_f64(xb)
+    z = xd @ w.T + (xd @ O.f16_to_f64(a).T) @ O.f16_to_f64(b).T
+    bias, res = rnd(4, n).to(DEV), rnd(5, m, n // 2 if gated else n).to(DEV)
+    for out in (torch.float32, torch.bfloat16):
+        y = q2.q2_linear_fused(x, p, s, dev_bits(a, torch.float16), dev_bits(b, torch.float16), bias=bias, residual=res,
+                               activation="silu", gated=gated, out_dtype=out)
+        check(y, z, "silu", gated, bias=bias, residual=res, what=f"r={r}")
+
+
 @pytest.mark.parametrize("fmt", ["q2", "q4"])
 @pytest.mark.parametrize("m", [1, 7, 40, 200])
 @pytest.mark.parametrize("n,k", [(75, 256), (75, 640), (8200, 512)])
