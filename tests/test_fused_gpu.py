@@ -194,7 +194,7 @@ def test_many_rows(m, n, k, r, gated):
 def wide_rows(seed, m, k):
     """bf16 bits of rows whose elements differ by up to 2^200 in size, among ordinary ones, and float64 values.
     Every thirteenth row each: one large input; large inputs in the first block only; sizes spread over the whole range;
-    two sizes 2^45 apart; the smallest numbers, subnormal ones among them, beside 1; a row of zeros but for the ends."""
+    two sizes 2^45 apart; the smallest numbers, subnormal ones among them, beside 1; a row of zeros but for the ends; subnormal ones alone."""
     rng = np.random.default_rng(seed)
     x = rng.standard_normal((m, k))
     x[1::13, 5] = 2.0 ** 41
@@ -205,6 +205,7 @@ def wide_rows(seed, m, k):
     x[5::13, 7] = 1.0
     x[6::13] = 0.0
     x[6::13, [0, k - 1]] = 2.0 ** 90, 2.0 ** -90
+    x[7::13] = rng.integers(-127, 128, x[7::13].shape) * 2.0 ** -133
     xb = I.f32_to_bf16_bits(x.astype(np.float32))
     return xb, O.bf16_to_f64(xb)
 
