@@ -9,11 +9,14 @@
 // accumulators with exact products, without a block's start value, row sums or
 // a rescale per block; the power of two is taken back by an exact ldexp.
 //
-// A row with smaller elements (a wide row) stays bf16, and a tile that holds one
-// runs on the bf16 matrix cores with each weight as the exact sum of two bf16
-// values, at twice the products.  Rounding those elements instead would cost at
-// most 2^-40 of the row's largest one, but that is the whole result of an output
-// whose weights at the larger elements are zero.
+// What the conversion rounds off smaller elements is at most 2^-40 of the row's
+// largest one, but that is the whole result of an output whose weights at the larger
+// elements are zero.  So a row that loses something in one element has that
+// element's place and remainder listed, and its outputs get the remainder times
+// their weight at the end (of 5e7 normal numbers every tenth matrix has such an
+// element).  A row that loses in more (a wide row) stays bf16, and a tile that holds
+// one runs on the bf16 matrix cores with each weight as the exact sum of two bf16
+// values, at twice the products.
 #include "q2_fused.h"
 #include "q2_internal.h"
 #include <algorithm>
@@ -34,7 +37,7 @@ __device__ __forceinline__ q2_f32x16 mfma32_bf16(q2_u32x4 a, q2_u32x4 b, q2_f32x
 }
 
 // ============================================================================
-// x as f16: row i of the output is row i of x times 2^-rexp[i]
+// x as f16: row i of the output is row i of x times 2^-(rowinfo[i] >> 2)
 // ============================================================================
 // Each group of 16 elements is stored as a transposed 4 x 4 matrix (position
 // 4 j + b holds element 4 b + j), the order in which a dword of sixteen codes
@@ -62,14 +65,34 @@ __device__ __forceinline__ uint32_t join_span(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(
       uint32_t, __builtin_elementwise_max(__builtin_bit_cast(q2_u16x2, a), __builtin_bit_cast(q2_u16x2, b)));
 }
-// A wide row: its smallest nonzero element lies below 2^-32 times the power of two
-// of its largest.  (Every bf16 is a multiple of 2^-133, which is exact as long as the
-// largest element lies below 2^-93.)
-__device__ __forceinline__ bool is_wide(uint32_t span) {
+// Whether a row may lose something: its smallest nonzero element lies below 2^-32
+// times the power of two of its largest.  (Every bf16 is a multiple of 2^-133, which
+// is exact as long as the largest element lies below 2^-93.)
+__device__ __forceinline__ bool may_lose(uint32_t span) {
   const int limit = (int)(span >> 23) - 32;              // exponent of 2^-32 times the largest
   return limit > 1 && span >> 16 < 0x7F80u && 0x10000u - (span & 0xFFFFu) < (uint32_t)limit << 7;
 }
-constexpr int ROW_WIDE = 1 << 16;                        // in the place of its exponent
+// What a row's info word says below its exponent.
+constexpr int ROW_LOST = 1, ROW_WIDE = 2;
+__device__ __forceinline__ int row_word(int shift, int lost) { return lost > 1 ? ROW_WIDE : -4 * shift | lost; }
+// The input and the remainder of a row with ROW_LOST.
+struct Lost {
+  int32_t k;
+  float r;
+};
+// Adds up how many of sixteen elements from input k on the conversion rounds; the last of them is kept.
+__device__ __forceinline__ void find_lost(const q2_u32x4& v0, const q2_u32x4& v1, int shift, int k, int& n, Lost& l) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t w = (i < 8 ? v0[(i & 7) >> 1] : v1[(i & 7) >> 1]);
+    const float x = __builtin_bit_cast(float, (i & 1) ? w & 0xFFFF0000u : w << 16);
+    const float r = x - __builtin_amdgcn_ldexpf((float)(_Float16)__builtin_amdgcn_ldexpf(x, shift), -shift);
+    if (r != 0.f) {
+      ++n;
+      l = Lost{k + i, r};
+    }
+  }
+}
 
 // The shift that puts the largest into [2^15, 2^16): floor(log2 |x|) from the bits (a
 // subnormal bf16 is bits * 2^-133); 0 for a row of zeros.
@@ -113,7 +136,7 @@ __device__ __forceinline__ void keep_bf16(const q2_u32x4& v0, const q2_u32x4& v1
 constexpr int CV_ROWS = 4;
 
 template <int NCH>
-__global__ __launch_bounds__(64 * CV_ROWS) void x_to_f16_kernel(const uint16_t* x, uint16_t* out, int32_t* rexp,
+__global__ __launch_bounds__(64 * CV_ROWS) void x_to_f16_kernel(const uint16_t* x, uint16_t* out, int32_t* rowinfo, Lost* lost,
                                                                 int64_t M, int64_t K) {
   const int lane = threadIdx.x & 63;
   const int64_t m = (int64_t)blockIdx.x * CV_ROWS + (threadIdx.x >> 6);
@@ -122,7 +145,7 @@ __global__ __launch_bounds__(64 * CV_ROWS) void x_to_f16_kernel(const uint16_t* 
   q2_u32x4* const dst = reinterpret_cast<q2_u32x4*>(out + m * K);
   if (m == M) {
     for (int64_t q = lane; q < 2 * chunks; q += 64) dst[q] = q2_u32x4{0u, 0u, 0u, 0u};
-    if (lane == 0) rexp[m] = 0;
+    if (lane == 0) rowinfo[m] = 0;
     return;
   }
   const q2_u32x4* const xr = reinterpret_cast<const q2_u32x4*>(x + m * K);
@@ -148,17 +171,25 @@ __global__ __launch_bounds__(64 * CV_ROWS) void x_to_f16_kernel(const uint16_t* 
 #pragma unroll
   for (int d = 32; d; d >>= 1) span = join_span(span, (uint32_t)__shfl_xor((int)span, d));
   const int shift = top_shift(span >> 16);
-  const bool wide = __builtin_amdgcn_readfirstlane(is_wide(span));
-  if (lane == 0) rexp[m] = wide ? ROW_WIDE : -shift;
   uint32_t h[8];
-  if (wide) {                                            // rare: from memory again, in a short loop
+  if (__builtin_amdgcn_readfirstlane((int)may_lose(span)) != 0) {        // rare: from memory again, in short loops
+    int n = 0;
+    Lost l = {};
+#pragma unroll 1
+    for (int64_t q = lane; q < chunks; q += 64) find_lost(xr[2 * q], xr[2 * q + 1], shift, (int)(16 * q), n, l);
+    const uint64_t lanes = __builtin_amdgcn_ballot_w64(n > 0);
+    const bool wide = __builtin_popcountll(lanes) > 1 || __builtin_amdgcn_ballot_w64(n > 1) != 0;
+    if (n == 1 && !wide) lost[m] = l;
+    if (lane == 0) rowinfo[m] = row_word(shift, wide ? 2 : lanes != 0);
 #pragma unroll 1
     for (int64_t q = lane; q < chunks; q += 64) {
-      keep_bf16(xr[2 * q], xr[2 * q + 1], h);
+      if (wide) keep_bf16(xr[2 * q], xr[2 * q + 1], h);
+      else to_f16(xr[2 * q], xr[2 * q + 1], shift, h);
       store_f16(dst + 2 * q, h);
     }
     return;
   }
+  if (lane == 0) rowinfo[m] = row_word(shift, 0);
   if constexpr (NCH > 0) {
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
@@ -193,10 +224,11 @@ __device__ __forceinline__ q2_f32x4 mfma16_f16(q2_u32x4 a, q2_u32x4 b, q2_f32x4 
 
 template <int CT>
 __global__ __launch_bounds__(64 * XA_WAVES) void x_to_f16_branch_kernel(const uint16_t* x, const uint16_t* A,
-                                                                        uint16_t* out, int32_t* rexp, uint16_t* limbs,
-                                                                        int64_t M, int64_t K, int r) {
+                                                                        uint16_t* out, int32_t* rowinfo, Lost* lost,
+                                                                        uint16_t* limbs, int64_t M, int64_t K, int r) {
   constexpr int XA_RUNS = CT <= 2 ? 12 : 8;              // of a wave, in registers
   __shared__ uint32_t spans[XA_WAVES][16];
+  __shared__ int lost_n[16];
   __shared__ q2_f32x4 red[XA_WAVES][CT][64];
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -232,10 +264,27 @@ __global__ __launch_bounds__(64 * XA_WAVES) void x_to_f16_branch_kernel(const ui
 #pragma unroll
   for (int w = 0; w < XA_WAVES; ++w) span = join_span(span, spans[w][c]);
   const int shift = top_shift(span >> 16);
-  const bool wide = is_wide(span);
-  const bool any_wide =                                  // among the sixteen rows; readfirstlane: a scalar branch
-      __builtin_amdgcn_readfirstlane((int)(__builtin_amdgcn_ballot_w64(wide) != 0)) != 0;
-  if (wv == 0 && g == 0 && live) rexp[m] = wide ? ROW_WIDE : -shift;
+  const bool any =                                       // of the sixteen rows; readfirstlane: a scalar branch
+      __builtin_amdgcn_readfirstlane((int)(__builtin_amdgcn_ballot_w64(may_lose(span)) != 0)) != 0;
+  bool wide = false;
+  if (any) {
+    if (threadIdx.x < 16) lost_n[threadIdx.x] = 0;
+    __syncthreads();
+    int n = 0;
+    Lost l = {};
+    if (may_lose(span)) {
+#pragma unroll 1
+      for (int s = wv; s < runs; s += XA_WAVES) {
+        const q2_u32x4* p = reinterpret_cast<const q2_u32x4*>(xr + (int64_t)s * 64);
+        find_lost(p[0], p[1], shift, s * 64 + 16 * g, n, l);
+      }
+    }
+    if (n > 0) atomicAdd(&lost_n[c], n);
+    __syncthreads();
+    wide = lost_n[c] > 1;
+    if (n == 1 && !wide && live) lost[m] = l;            // one lane of the workgroup holds it
+  }
+  if (wv == 0 && g == 0 && live) rowinfo[m] = row_word(shift, any ? lost_n[c] : 0);
 
   const uint16_t* ar[CT];
 #pragma unroll
@@ -243,12 +292,12 @@ __global__ __launch_bounds__(64 * XA_WAVES) void x_to_f16_branch_kernel(const ui
   q2_f32x4 acc[CT];
 #pragma unroll
   for (int t = 0; t < CT; ++t) acc[t] = q2_f32x4{0.f, 0.f, 0.f, 0.f};
-  // With a wide row among them, all sixteen are multiplied as bf16, A as two bf16 values.
-  auto product = [&](auto any, int s, const q2_u32x4& v0, const q2_u32x4& v1) {
+  // With a row among them that loses something, all sixteen are multiplied as bf16, A as two bf16 values.
+  auto product = [&](auto as_bf16, int s, const q2_u32x4& v0, const q2_u32x4& v1) {
     uint32_t h[8], raw[8];
     to_f16(v0, v1, shift, h);
     q2_u32x4* const dst = reinterpret_cast<q2_u32x4*>(out + m * K + (int64_t)s * 64 + 16 * g);
-    if constexpr (decltype(any)::value) {
+    if constexpr (decltype(as_bf16)::value) {
       keep_bf16(v0, v1, raw);
 #pragma unroll
       for (int i = 0; i < 8; ++i) raw[i] = wide ? raw[i] : h[i];
@@ -259,7 +308,7 @@ __global__ __launch_bounds__(64 * XA_WAVES) void x_to_f16_branch_kernel(const ui
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
       const q2_u32x4* p = reinterpret_cast<const q2_u32x4*>(ar[t] + (int64_t)s * 64);
-      if constexpr (decltype(any)::value) {
+      if constexpr (decltype(as_bf16)::value) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const q2_u32x4 av = p[i], xv = i ? v1 : v0;
@@ -278,11 +327,11 @@ __global__ __launch_bounds__(64 * XA_WAVES) void x_to_f16_branch_kernel(const ui
       }
     }
   };
-  auto reread = [&](auto any, int s) {
+  auto reread = [&](auto as_bf16, int s) {
     const q2_u32x4* p = reinterpret_cast<const q2_u32x4*>(xr + (int64_t)s * 64);
-    product(any, s, p[0], p[1]);
+    product(as_bf16, s, p[0], p[1]);
   };
-  if (!any_wide) {
+  if (!any) {
 #pragma unroll
     for (int i = 0; i < XA_RUNS; ++i) {
       const int s = wv + XA_WAVES * i;
@@ -309,7 +358,7 @@ __global__ __launch_bounds__(64 * XA_WAVES) void x_to_f16_branch_kernel(const ui
 #pragma unroll
       for (int w = 0; w < XA_WAVES; ++w) rs = join_span(rs, spans[w][row]);
       if (m0 + row < M && col < r8) {
-        const float t = col < r ? __builtin_amdgcn_ldexpf(sum[e], any_wide ? 0 : -top_shift(rs >> 16)) : 0.f;
+        const float t = col < r ? __builtin_amdgcn_ldexpf(sum[e], any ? 0 : -top_shift(rs >> 16)) : 0.f;
         const uint16_t hi = f32_to_bf16_rn(t), lo = f32_to_bf16_rn(t - bf16_to_f32(hi));
         limbs[(m0 + row) * 2 * r8 + col] = hi;
         limbs[(m0 + row) * 2 * r8 + r8 + col] = lo;
@@ -396,8 +445,8 @@ constexpr int FX_STRIP = 64 + 4;                         // floats per row of a 
 // vector instructions, one LDS read in turn: 2 - 4 % less time than reading and
 // decoding ahead of a step's products.
 template <int MT>
-__global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const uint16_t* x16, const int32_t* rexp,
-                                                           int tiles_n, int group_m) {
+__global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const uint16_t* x16, const int32_t* rowinfo,
+                                                           const Lost* lost, int tiles_n, int group_m) {
   constexpr int FX_BM = 32 * MT;                         // rows of a workgroup
   constexpr int FX_HALF = FX_BM * 128;                   // bytes of a 64-wide half block of the rows
   constexpr int FX_OFF_W = 2 * FX_HALF;
@@ -446,12 +495,12 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
                                                (uint32_t)hs * 128u, 0, 0);
     }
   };
-  // Exponents of the rows, lane l's of rows l and l + 64 (past the last row: its own), and which rows are wide.
-  auto load_exp = [&](int row) {
+  // Info words of the rows, lane l's of rows l and l + 64 (past the last row: its own).
+  auto load_info = [&](int row) {
     const int64_t m = std::min<int64_t>(m0 + std::min(row, FX_BM - 1), rt.mend - 1);
-    return rexp[a.row_index ? source_row(a, m) : m];
+    return rowinfo[a.row_index ? source_row(a, m) : m];
   };
-  const int exp_lo = load_exp(lane), exp_hi = load_exp(64 + lane);
+  const int info_lo = load_info(lane), info_hi = load_info(64 + lane);
   int aoff[4];
 #pragma unroll
   for (int t = 0; t < 4; ++t) aoff[t] = c * 128 + (((4 * h + t) ^ ((c >> 1) & 7)) << 4);
@@ -502,8 +551,10 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
   copy_rows(0, 0);
   __builtin_amdgcn_s_waitcnt(0);
   read_codes(0, w);
-  const uint64_t wide_lo = __builtin_amdgcn_ballot_w64(exp_lo == ROW_WIDE);
-  const uint64_t wide_hi = __builtin_amdgcn_ballot_w64(exp_hi == ROW_WIDE);
+  const uint64_t wide_lo = __builtin_amdgcn_ballot_w64((info_lo & ROW_WIDE) != 0);
+  const uint64_t wide_hi = __builtin_amdgcn_ballot_w64((info_hi & ROW_WIDE) != 0);
+  const uint64_t lost_lo = __builtin_amdgcn_ballot_w64((info_lo & ROW_LOST) != 0);
+  const uint64_t lost_hi = __builtin_amdgcn_ballot_w64((info_hi & ROW_LOST) != 0);
   if ((wide_lo | wide_hi) == 0) {
     // Operands of a step and of the one before it, whose products are still to come:
     // zeros at first.
@@ -635,10 +686,7 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
 
   // The rows' powers of two: element 4 q + e of a tile is row 8 q + 4 h + e.
   int* const exps = reinterpret_cast<int*>(smem);
-  if (tid < FX_BM) {                                     // row 64 wv + lane; a wide row was not scaled
-    const int e = wv == 0 ? exp_lo : exp_hi;
-    exps[tid] = e == ROW_WIDE ? 0 : e;
-  }
+  if (tid < FX_BM) exps[tid] = (wv == 0 ? info_lo : info_hi) >> 2;        // row 64 wv + lane
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < MT; ++i)
@@ -687,6 +735,21 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
         strip[(8 * (e >> 2) + 4 * h + (e & 3)) * FX_STRIP + 32 * j + c] = acc[i][j][e];
     __builtin_amdgcn_wave_barrier();
     const int rows = (int)std::min<int64_t>(rt.mend - m0 - 32 * i, 32);
+    // Remainders of rows that lost something in one element; lane l's column is l.
+    // Nothing to see with one such row (M = 1536, K = 4096, N = 12288: 152 us), 251 us
+    // with every row: 128 cache lines of codes and scales for a wave and row, whatever
+    // the order of the loads.
+    for (uint32_t left = (uint32_t)((i < 2 ? lost_lo : lost_hi) >> (32 * (i & 1))); left != 0; left &= left - 1) {
+      const int row = __builtin_ctz(left);
+      if (row >= rows) break;
+      const int64_t m = m0 + 32 * i + row;
+      const Lost l = lost[a.row_index ? source_row(a, m) : m];
+      const int64_t wr = rt.expert * a.N + wcol(lane);
+      const int code = a.w[wr * (K / 4) + (l.k >> 2)] >> (2 * (l.k & 3)) & 3;
+      const float w = (float)(code - 1) * f16_to_f32(a.s[wr * KB + l.k / BLOCK_K]);
+      strip[row * FX_STRIP + lane] = __builtin_fmaf(l.r, w, strip[row * FX_STRIP + lane]);
+    }
+    __builtin_amdgcn_wave_barrier();
     store_strip(a, bias, n_out, strip, FX_STRIP, 32, a.gated ? 32 : 64, m0 + 32 * i, rows, n0, lane);
     __builtin_amdgcn_wave_barrier();
   }
@@ -697,10 +760,12 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
 // ============================================================================
 static size_t pad256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-// `rows` rows of x and their exponents.  The last tile's rows run up to FX_MAX_BM - 1
-// past them, a row index needs one row of zeros behind them.
+// `rows` rows of x, their info words and what they lost.  The last tile's rows run up
+// to FX_MAX_BM - 1 past them, a row index needs one row of zeros behind them.
+static size_t x16_bytes(int64_t rows, int64_t K) { return pad256((size_t)(rows + FX_MAX_BM) * (size_t)K * 2); }
+static size_t info_bytes(int64_t rows) { return pad256((size_t)(rows + FX_MAX_BM) * 4); }
 size_t f16_workspace_bytes(int64_t rows, int64_t K) {
-  return pad256((size_t)(rows + FX_MAX_BM) * (size_t)K * 2) + pad256((size_t)(rows + FX_MAX_BM) * 4);
+  return x16_bytes(rows, K) + info_bytes(rows) + pad256((size_t)rows * sizeof(Lost));
 }
 
 // Rows of x are addressed with 32 bits from a tile's first row, and with a row
@@ -727,8 +792,10 @@ static int rows_per_tile(const FusedArgs& a, int64_t cols) {
 
 hipError_t launch_fused_f16(const FusedArgs& a, void* ws, hipStream_t stream) {
   const int64_t rows = a.x_rows, K = a.K;
-  uint16_t* x16 = static_cast<uint16_t*>(ws);
-  int32_t* rexp = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + pad256((size_t)(a.M + FX_MAX_BM) * (size_t)K * 2));
+  uint8_t* const w8 = static_cast<uint8_t*>(ws);
+  uint16_t* x16 = reinterpret_cast<uint16_t*>(w8);
+  int32_t* rowinfo = reinterpret_cast<int32_t*>(w8 + x16_bytes(a.M, K));
+  Lost* lost = reinterpret_cast<Lost*>(w8 + x16_bytes(a.M, K) + info_bytes(a.M));
   const int64_t cols = a.gated ? FX_BN / 2 : FX_BN;
   const int bm = rows_per_tile(a, cols);
   const int64_t tiles_n = (fused_n_out(a) + cols - 1) / cols, slots = max_row_tiles(a, bm);
@@ -736,15 +803,15 @@ hipError_t launch_fused_f16(const FusedArgs& a, void* ws, hipStream_t stream) {
   if (a.r > 0 && a.r <= XA_MAX_RANK) {
     const dim3 grid((unsigned)((rows + 15) / 16)), block(64 * XA_WAVES);
 #define Q2_XA(CT)                                                                                                  \
-  hipLaunchKernelGGL((x_to_f16_branch_kernel<CT>), grid, block, 0, stream, a.x, a.lr_a, x16, rexp, a.lr_t, rows, K, \
-                     a.r)
+  hipLaunchKernelGGL((x_to_f16_branch_kernel<CT>), grid, block, 0, stream, a.x, a.lr_a, x16, rowinfo, lost, a.lr_t, \
+                     rows, K, a.r)
     if (a.r <= 16) Q2_XA(1);
     else if (a.r <= 32) Q2_XA(2);
     else Q2_XA(4);
 #undef Q2_XA
   } else {
     const dim3 grid((unsigned)(rows / CV_ROWS + 1)), block(64 * CV_ROWS);
-#define Q2_CV(NCH) hipLaunchKernelGGL((x_to_f16_kernel<NCH>), grid, block, 0, stream, a.x, x16, rexp, rows, K)
+#define Q2_CV(NCH) hipLaunchKernelGGL((x_to_f16_kernel<NCH>), grid, block, 0, stream, a.x, x16, rowinfo, lost, rows, K)
     if (K <= 2048) Q2_CV(2);
     else if (K <= 4096) Q2_CV(4);
     else if (K <= 12288) Q2_CV(12);
@@ -756,7 +823,7 @@ hipError_t launch_fused_f16(const FusedArgs& a, void* ws, hipStream_t stream) {
   const int group_m = tile_group_rows(slots, tiles_n, 2.0 * bm * (double)K, (double)FX_BN * K * 0.265625, 64);
   const dim3 grid = grid_of(slots * tiles_n);
 #define Q2_FX(MT) \
-  hipLaunchKernelGGL((fused_f16_kernel<MT>), grid, dim3(256), 0, stream, a, x16, rexp, (int)tiles_n, group_m)
+  hipLaunchKernelGGL((fused_f16_kernel<MT>), grid, dim3(256), 0, stream, a, x16, rowinfo, lost, (int)tiles_n, group_m)
   if (bm == 96) Q2_FX(3);
   else Q2_FX(4);
 #undef Q2_FX

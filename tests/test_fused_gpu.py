@@ -194,7 +194,8 @@ def test_many_rows(m, n, k, r, gated):
 def wide_rows(seed, m, k):
     """bf16 bits of rows whose elements differ by up to 2^200 in size, among ordinary ones, and float64 values.
     Every thirteenth row each: one large input; large inputs in the first block only; sizes spread over the whole range;
-    two sizes 2^45 apart; the smallest numbers, subnormal ones among them, beside 1; a row of zeros but for the ends; subnormal ones alone."""
+    two sizes 2^45 apart; the smallest numbers, subnormal ones among them, beside 1; zeros but for the ends; subnormal ones
+    alone; two small inputs beside a large one; one that the scale of the large one keeps in part; one among ordinary ones."""
     rng = np.random.default_rng(seed)
     x = rng.standard_normal((m, k))
     x[1::13, 5] = 2.0 ** 41
@@ -206,6 +207,12 @@ def wide_rows(seed, m, k):
     x[6::13] = 0.0
     x[6::13, [0, k - 1]] = 2.0 ** 90, 2.0 ** -90
     x[7::13] = rng.integers(-127, 128, x[7::13].shape) * 2.0 ** -133
+    x[8::13] = 0.0
+    x[8::13, [200, 300, 301]] = 2.0 ** 60, 1.5 * 2.0 ** -20, 1.25 * 2.0 ** -20
+    x[9::13] = 0.0
+    x[9::13, [300, 200]] = -1.0, 255.0 * 2.0 ** -44           # eight bits, four of them below 2^-40
+    if k > 400:
+        x[10::13, 400] = 1e-30
     xb = I.f32_to_bf16_bits(x.astype(np.float32))
     return xb, O.bf16_to_f64(xb)
 
@@ -215,6 +222,9 @@ def wide_weights(seed, n, k):
     from the smallest subnormal f16 to 2^14."""
     codes = np.random.default_rng(seed).integers(0, 3, (n, k)).astype(np.uint8)
     codes[::5, :128] = 1
+    for i, (c0, c1) in zip((200, 300, 400), ((1, 2), (0, 1), (2, 0))):        # nothing at one of two inputs of a row
+        if i < k:
+            codes[::3, i], codes[1::3, i] = c0, c1
     rng = np.random.default_rng(seed + 1)
     scales = np.ldexp(1.0 + rng.integers(0, 1024, (n, k // 128)) / 1024.0, rng.integers(-14, 14, (n, 1)))
     scales[::7] = rng.integers(1, 1024, scales[::7].shape) * 2.0 ** -24
