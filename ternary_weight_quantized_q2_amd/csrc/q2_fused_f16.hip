@@ -13,8 +13,8 @@
 // largest one, but that is the whole result of an output whose weights at the larger
 // elements are zero.  So a row that loses something in one element has that
 // element's place and remainder listed, and its outputs get the remainder times
-// their weight at the end (of 5e7 normal numbers every tenth matrix has such an
-// element).  A row that loses in more (a wide row) stays bf16, and a tile that holds
+// their weight at the end (among 5e7 normal numbers there is such an element now and
+// then).  A row that loses in more (a wide row) stays bf16, and a tile that holds
 // one runs on the bf16 matrix cores with each weight as the exact sum of two bf16
 // values, at twice the products.
 #include "q2_fused.h"
@@ -131,7 +131,8 @@ __device__ __forceinline__ void keep_bf16(const q2_u32x4& v0, const q2_u32x4& v1
 
 // Rows without a branch: one wave per row, which stays in registers up to
 // 1024 NCH elements between the search for its largest element and the
-// conversion (NCH = 0: longer rows, read twice).  Row M (of M + 1) is a row of
+// conversion (NCH = 0: longer rows, read twice).  Rows between 4096 and 12288 take
+// the form for 12288, which loads their last elements again in the rest of its places.  Row M (of M + 1) is a row of
 // zeros that indexes outside x are pointed to.
 constexpr int CV_ROWS = 4;
 
@@ -213,8 +214,9 @@ __global__ __launch_bounds__(64 * CV_ROWS) void x_to_f16_kernel(const uint16_t* 
 // and multiplied by A (f16 as it is: exact products) while it is in registers;
 // the waves' sums of x A^T meet in LDS and leave as the branch's bf16 limbs.
 // Reading x once for both took a call at M = 4093, K = 12288, N = 4096, r = 32
-// from 487 us to 445; this kernel is 60 us of it, 200 MB at 3.4 TB/s: sixteen
-// rows fill a CU's registers, so its loads and its stores take turns.
+// from 487 us to 445; this kernel is 70 us of it, 200 MB at 2.9 TB/s: sixteen
+// rows fill a CU's registers, so its loads and its stores take turns.  There is one
+// form per rank: shorter rows load their last run again in the places they do not fill.
 constexpr int XA_WAVES = 16, XA_MAX_RANK = 64;
 
 __device__ __forceinline__ q2_f32x4 mfma16_f16(q2_u32x4 a, q2_u32x4 b, q2_f32x4 c) {

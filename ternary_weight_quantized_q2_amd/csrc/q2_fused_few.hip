@@ -4,8 +4,8 @@
 // What counts here is the read of the packed weights and the latency of one
 // pass: every wave has all loads of its blocks in flight before it computes on
 // any of them, in pieces of at least 64 bytes of a weight row.  One row, K = 2560,
-// N = 2 x 9728: 10 us Q2_0 (13 MB, 1.3 TB/s), 13 us 4-bit (26 MB, 2.0 TB/s) with the
-// weights from memory; 16 rows, K = 4096, N = 4096: 10.6 us.
+// N = 2 x 9728: 10 us Q2_0 (13 MB, 1.3 TB/s), 11.9 us 4-bit (26 MB, 2.2 TB/s) with the
+// weights from memory; 16 rows, K = 4096, N = 4096: 10.2 us.
 #include "q2_fused.h"
 #include <algorithm>
 

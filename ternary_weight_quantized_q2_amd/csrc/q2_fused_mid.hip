@@ -1,6 +1,6 @@
-// q2_fused_mid.hip - the fused and grouped linears between a few rows and the
-// f16 kernel's many, and for every row count above 16 of the 4-bit format,
-// whose weights (q - z) s have no exact f16 value.
+// q2_fused_mid.hip - the fused and grouped linears between few tiles and the f16
+// kernel's many rows, and of the 4-bit format, whose weights (q - z) s have no exact
+// f16 value, everything beyond few tiles.
 //
 // Weights decode to bf16 1 + c / 4 or 1 + q / 16 (q2_device.h); per 128-wide
 // block the row sums of x take the 1 back and one FMA per output applies the
@@ -23,7 +23,8 @@ __device__ __forceinline__ int mid_swz(int r) { return ((r >> 2) & 3) | ((r & 3)
 // for them.  Codes of the next unit are loaded to registers of their own while
 // this one is computed (ROLL = false), or, in tiles of 64 rows, which have no
 // room for them, column tile by column tile as this one's are decoded: 64 x 160
-// tiles then fit 256 registers, and 64 x 128 ones gained 3 %, 32-row ones lost 4 %.
+// tiles then fit 256 registers but for three of Q2_0 and one of 4-bit, spilled outside
+// the loop, and 64 x 128 ones gained 3 %, 32-row ones lost 4 %.
 // x and the codes are addressed with a scalar block offset (buffer loads): 8 % less
 // time for 20 rows per expert than 64-bit addresses.  Each wave sums its rows on the matrix cores itself (a quarter of
 // its products; sharing the sums would need a second barrier).
@@ -368,7 +369,8 @@ bool fused_mid_takes(const FusedArgs& a, int fmt) {
 // The tile.  K split over four or eight groups of waves makes a workgroup take a
 // CU for itself, so 256 of them are a round; two of K split over two share a CU.
 // Of the sizes below the one with the least rounds times the time of a round is
-// taken (K = 2560, 4-bit, us per round: 32 x 64 over eight groups 12.6; over four
+// taken, as measured at one K in one format; other K and Q2_0 are taken to stretch all
+// of them alike (K = 2560, 4-bit, us per round: 32 x 64 over eight groups 12.6; over four
 // 32 x 96 14.5, 64 x 64 17.0, 64 x 96 20.5, 64 x 128 23.4, 64 x 160 26.4; over two
 // 64 x 128 28 up to 256 workgroups and 36 up to 512).  So 128 rows, N = 2 x 9728
 // take 64 x 160 (29 us, 36 with 64 x 128 over two), N = 8192 64 x 64, N = 2560
