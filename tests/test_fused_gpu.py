@@ -195,7 +195,8 @@ def wide_rows(seed, m, k):
     """bf16 bits of rows whose elements differ by up to 2^200 in size, among ordinary ones, and float64 values.
     Every thirteenth row each: one large input; large inputs in the first block only; sizes spread over the whole range;
     two sizes 2^45 apart; the smallest numbers, subnormal ones among them, beside 1; zeros but for the ends; subnormal ones
-    alone; two small inputs beside a large one; one that the scale of the large one keeps in part; one among ordinary ones."""
+    alone; two small inputs beside a large one; one that the scale of the large one keeps in part; one among ordinary ones;
+    ordinary ones 2^30 below a large one."""
     rng = np.random.default_rng(seed)
     x = rng.standard_normal((m, k))
     x[1::13, 5] = 2.0 ** 41
@@ -213,6 +214,8 @@ def wide_rows(seed, m, k):
     x[9::13, [300, 200]] = -1.0, 255.0 * 2.0 ** -44           # eight bits, four of them below 2^-40
     if k > 400:
         x[10::13, 400] = 1e-30
+    x[11::13] *= 2.0 ** -30
+    x[11::13, 5] = 1.0
     xb = I.f32_to_bf16_bits(x.astype(np.float32))
     return xb, O.bf16_to_f64(xb)
 
@@ -251,7 +254,8 @@ def test_rows_whose_elements_differ_in_size(m, n, k, r):
     """Every output is held to its own terms: where a weight is zero the input adds nothing, however large it is.
     Products are exact and sums are in fp32, so K 2^-24 of the terms' sum would do; the branch's x A^T has 16 bits.
     Terms below fp32's normal numbers may be lost: K of them.  (Other kernels than the one for many rows take a block's
-    sum of x off again, so an input of 2^60 covers the rest of its own block: rows 1 to 5 modulo 13 are left out.)"""
+    sum of x off again, so an input of 2^60 covers the rest of its own block: rows 1 to 5 and 11
+    modulo 13 are left out.)"""
     (p, s), codes, scales = wide_weights(361, n, k)
     cols, _ = sample(n, False, 361)
     w = (codes[cols].astype(np.float64) - 1) * np.repeat(scales[cols].astype(np.float64), 128, axis=1)
@@ -269,9 +273,32 @@ def test_rows_whose_elements_differ_in_size(m, n, k, r):
     assert np.isfinite(g).all()
     bad = np.abs(g - z) > 1e-3 * size + k * 2.0 ** -126
     if not (n >= 1536 and k >= 512 and m >= 300):
-        for i in range(1, 6):
+        for i in (1, 2, 3, 4, 5, 11):
             bad[i::13] = False
     assert not bad.any(), f"{bad.sum()} of {bad.size} outside, in rows {np.unique(np.argwhere(bad)[:, 0] % 13)} modulo 13"
+
+
+@pytest.mark.parametrize("m,n,k,r", [(1100, 8200, 640, 0), (400, 16400, 512, 20)])
+def test_gated_rows_whose_elements_differ_in_size(m, n, k, r):
+    """Both factors of an output held to their own terms."""
+    (p, s), codes, scales = wide_weights(364, n, k)
+    cols, rows = sample(n, True, 364)
+    w = (codes[rows].astype(np.float64) - 1) * np.repeat(scales[rows].astype(np.float64), 128, axis=1)
+    xb, x = wide_rows(364, m, k)
+    A = B = a = b = None
+    if r:
+        ab, bb = I.lowrank_factors(364, r, k, n, std=0.05)
+        ab[:, :128] = 0
+        A, B = dev_bits(ab, torch.float16), dev_bits(bb, torch.float16)
+        a, b = O.f16_to_f64(ab), O.f16_to_f64(bb[rows])
+    z, size = own_terms(x, w, a, b)
+    err, h = 1e-3 * size + k * 2.0 ** -126, len(cols)
+    got = host(q2.q2_linear_fused(dev_bits(xb, torch.bfloat16), p, s, A, B, gated=True)[:, torch.from_numpy(cols).to(DEV)])
+    ref = z[:, :h] * z[:, h:]
+    tol = err[:, :h] * np.abs(z[:, h:]) + err[:, h:] * (np.abs(z[:, :h]) + err[:, :h]) + 2.0 ** -126
+    inside = np.abs(ref) + tol < 3e38                       # the others may overflow
+    bad = (np.abs(got - ref) > tol)[inside]
+    assert inside.mean() > 0.5 and not bad.any(), f"{bad.sum()} of {bad.size} outside"
 
 
 @pytest.mark.parametrize("counts,n,k", [([400, 0, 500], 10010, 640), ([1, 700, 64], 13000, 512)])
