@@ -60,7 +60,7 @@ extern "C" {
 typedef enum {
   Q2_OK = 0,
   Q2_ERR_ARG = -1,       /* NULL pointer for a non-empty buffer, negative size      */
-  Q2_ERR_SHAPE = -2,     /* K not a multiple of 128                                 */
+  Q2_ERR_SHAPE = -2,     /* K not a multiple of 128, or sizes beyond a call's limits */
   Q2_ERR_ALIGN = -3,     /* pointer not aligned as stated above                     */
   Q2_ERR_CODE = -4,      /* q2_pack: a code above 2                                 */
   Q2_ERR_SCALE = -5,     /* q2_pack: scale not exactly representable in f16, or NaN/inf */

@@ -152,7 +152,7 @@ const char* q2_strerror(int status) {
   switch (status) {
     case Q2_OK: return "Q2_OK";
     case Q2_ERR_ARG: return "Q2_ERR_ARG: invalid argument";
-    case Q2_ERR_SHAPE: return "Q2_ERR_SHAPE: K must be a multiple of 128";
+    case Q2_ERR_SHAPE: return "Q2_ERR_SHAPE: sizes that the call does not take";
     case Q2_ERR_ALIGN: return "Q2_ERR_ALIGN: misaligned pointer";
     case Q2_ERR_CODE: return "Q2_ERR_CODE: code outside {0,1,2}";
     case Q2_ERR_SCALE: return "Q2_ERR_SCALE: scale not exactly representable in f16";

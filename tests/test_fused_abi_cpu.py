@@ -186,3 +186,12 @@ def test_workspace_queries_leave_the_message(lib):
         assert f(4, 8, k, 0) == 0 and f(4096, 8192, k, 0) == 0 and g(4096, 4, 8192, k) == 0
     assert f(1 << 40, 1 << 20, 128, 0) == 0 and f(4, 1 << 46, 128, 0) == 0 and g(1 << 20, 1 << 16, 1 << 30, 1 << 20) == 0
     assert lib.q2_last_error() == detail
+
+
+def test_shape_errors_say_what_is_wrong(lib):
+    """A refused size that is no K is not reported as one."""
+    assert lib.q2_route(FAKE, 4, 1025, 2, 0, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 30, None) == q2.Q2_ERR_SHAPE
+    assert lib.q2_linear_fused(FAKE, FAKE, FAKE, None, None, 0, epi(flags=q2.Q2_EPI_GATED), FAKE, 4, 7, 128, None, 0,
+                               None) == q2.Q2_ERR_SHAPE
+    name = lib.q2_strerror(q2.Q2_ERR_SHAPE)
+    assert name.startswith(b"Q2_ERR_SHAPE") and b"128" not in name and b"halves" in lib.q2_last_error()
