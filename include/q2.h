@@ -329,7 +329,8 @@ typedef struct {
  *   epi        host pointer, read before the call returns; NULL is the plain
  *              product in f32
  *   y          f32 or bf16 [M, n_out], overwritten; apart from the residual it
- *              must not overlap an input
+ *              must not overlap an input (x: Q2_ERR_ARG, as for a residual that
+ *              overlaps y without being it)
  *   workspace  device scratch of >= q2_linear_fused_workspace_bytes(M, N, K, r)
  *              bytes, 256-byte aligned (may be NULL when that is 0), owned by
  *              the caller; overwritten
@@ -372,7 +373,7 @@ int q4_linear_fused(const uint16_t* x_bf16, const uint8_t* packed4, const uint16
  *              Q2_0 weights one after the other                      (in)
  *   epi        as q2_linear_fused, with bias [E, N]; gate and residual must be
  *              NULL (Q2_ERR_ARG): the experts' rows are joined by q2_combine
- *   y          f32 or bf16 [R, n_out]
+ *   y          f32 or bf16 [R, n_out]; must not overlap x (Q2_ERR_ARG)
  *   workspace  device scratch of >= q2_linear_grouped_workspace_bytes(R, E, N, K)
  *              bytes, 256-byte aligned (may be NULL when that is 0)
  * E <= 65536, R and x_rows < 2^31.  The counts stay on the device: the launch
@@ -444,7 +445,7 @@ size_t q2_route_workspace_bytes(int64_t T, int64_t E, int64_t k);
  *   weight    f32 [T, k]                                               (in)
  *   residual  f32 or bf16 [T, N], or NULL (0); may be y itself (same
  *             address and type)                                         (in)
- *   y         f32 or bf16 [T, N]; must not overlap z                     (out)
+ *   y         f32 or bf16 [T, N]; must not overlap z (Q2_ERR_ARG)         (out)
  * Pointers aligned to their element.  k <= 64 (Q2_ERR_SHAPE otherwise), k == 0
  * copies the residual; R < 2^31.  Asynchronous.
  */

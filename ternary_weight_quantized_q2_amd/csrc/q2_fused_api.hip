@@ -41,6 +41,22 @@ int check_workspace(const void* ws, size_t bytes, size_t need) {
   return Q2_OK;
 }
 
+bool overlap(const void* p, int64_t bytes_p, const void* q, int64_t bytes_q) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return bytes_p > 0 && bytes_q > 0 && (a < b ? b - a < (uintptr_t)bytes_p : a - b < (uintptr_t)bytes_q);
+}
+
+// y of `count` elements against an input that other workgroups read, and against
+// the residual, which may be y itself.
+int check_overlap(const void* y, int y_bf16, int64_t count, const void* in, int64_t in_bytes, const char* name,
+                  const void* residual, int res_bf16) {
+  const int64_t bytes = count * (y_bf16 ? 2 : 4);
+  if (in && overlap(y, bytes, in, in_bytes)) return fail(Q2_ERR_ARG, "y overlaps %s", name);
+  if (residual && !(residual == y && res_bf16 == y_bf16) && overlap(y, bytes, residual, count * (res_bf16 ? 2 : 4)))
+    return fail(Q2_ERR_ARG, "y overlaps the residual without being it, address and type");
+  return Q2_OK;
+}
+
 int launch(const q2dev::FusedArgs& a, int fmt, void* ws, hipStream_t stream, const char* what) {
   return hip_status(q2dev::launch_fused(a, fmt, ws, stream), what);
 }
@@ -63,6 +79,9 @@ int fused_entry(int fmt, const uint16_t* x, const uint8_t* w, const uint16_t* s,
   if (M == 0 || N == 0) return ok();
   const size_t need = fmt == 0 ? q2_linear_fused_workspace_bytes(M, N, K, r) : 0;
   if ((st = check_workspace(workspace, workspace_bytes, need))) return st;
+  const bool out16 = (e.flags & Q2_EPI_OUT_BF16) != 0, res16 = (e.flags & Q2_EPI_RESIDUAL_BF16) != 0;
+  const int64_t n_out = (e.flags & Q2_EPI_GATED) ? N / 2 : N;
+  if ((st = check_overlap(y, out16, M * n_out, x, M * K * 2, "x", e.residual, res16))) return st;
   if ((st = check_device())) return st;
   const size_t limbs = r > 0 ? q2_lowrank_workspace_bytes(M, r) : 0;
   q2dev::FusedArgs a = {};
@@ -102,6 +121,8 @@ int grouped_entry(int fmt, const uint16_t* x, int64_t x_rows, const int32_t* row
   if (!work) return ok();
   const size_t need = fmt == 0 ? q2_linear_grouped_workspace_bytes(R, E, N, K) : 0;
   if ((st = check_workspace(workspace, workspace_bytes, need))) return st;
+  const int64_t n_out = (e.flags & Q2_EPI_GATED) ? N / 2 : N;
+  if ((st = check_overlap(y, (e.flags & Q2_EPI_OUT_BF16) != 0, R * n_out, x, x_rows * K * 2, "x", nullptr, 0))) return st;
   if ((st = check_device())) return st;
   q2dev::FusedArgs a = {};
   a.x = x; a.x_rows = x_rows; a.row_index = row_index; a.w = w; a.s = s; a.z = z; a.offsets = offsets;
@@ -212,6 +233,10 @@ int q2_combine(const void* z, int64_t R, const int32_t* slot, const float* weigh
       (st = check_ptr(y, ne, (flags & Q2_COMBINE_OUT_BF16) ? 2 : 4, "y")))
     return st;
   if (!ne) return ok();
+  if ((st = check_overlap(y, (flags & Q2_COMBINE_OUT_BF16) != 0, T * N, k > 0 ? z : nullptr,
+                          R * N * ((flags & Q2_COMBINE_Z_BF16) ? 2 : 4), "z", residual,
+                          (flags & Q2_COMBINE_RESIDUAL_BF16) != 0)))
+    return st;
   if ((st = check_device())) return st;
   return hip_status(q2dev::launch_combine(z, (flags & Q2_COMBINE_Z_BF16) ? 1 : 0, R, slot, weight, residual,
                                           (flags & Q2_COMBINE_RESIDUAL_BF16) ? 1 : 0, y,

@@ -195,3 +195,28 @@ def test_shape_errors_say_what_is_wrong(lib):
                                None) == q2.Q2_ERR_SHAPE
     name = lib.q2_strerror(q2.Q2_ERR_SHAPE)
     assert name.startswith(b"Q2_ERR_SHAPE") and b"128" not in name and b"halves" in lib.q2_last_error()
+
+
+def test_outputs_that_overlap_what_others_read_are_refused(lib):
+    """y over x, a residual that starts elsewhere in y or has another type, z."""
+    m = n = k = 128
+    far = FAKE + (1 << 20)
+
+    def L(x=FAKE, y=far, **kw):
+        return lib.q2_linear_fused(x, far << 4, far << 4, None, None, 0, epi(**kw), y, m, n, k, None, 0, None)
+
+    bf = q2.Q2_EPI_OUT_BF16
+    for y in (FAKE, FAKE + 2 * m * k - 4, FAKE - 4 * m * n + 4):
+        assert L(y=y) == q2.Q2_ERR_ARG and b"overlaps x" in lib.q2_last_error()
+    assert L(y=FAKE, residual=FAKE, flags=bf | q2.Q2_EPI_RESIDUAL_BF16) == q2.Q2_ERR_ARG      # x itself updated in place
+    for res, flags in ((far + 4, 0), (far - 4, 0), (far, q2.Q2_EPI_RESIDUAL_BF16), (far, bf)):
+        assert L(residual=res, flags=flags) == q2.Q2_ERR_ARG and b"residual" in lib.q2_last_error()
+    assert lib.q4_linear_fused(FAKE, far, far, far, None, FAKE, m, n, k, None) == q2.Q2_ERR_ARG
+    assert lib.q2_linear_grouped(FAKE, m, None, far, far, far, None, FAKE + 256, m, 1, n, k, None, 0, None) == q2.Q2_ERR_ARG
+    assert lib.q4_linear_grouped(FAKE, m, None, far, far, far, far, None, FAKE, m, 1, n, k, None) == q2.Q2_ERR_ARG
+
+    def C(y, res=None, fl=0):
+        return lib.q2_combine(FAKE, 64, far << 2, far << 2, res, y, 16, 2, 64, fl, None)
+
+    assert C(FAKE) == q2.Q2_ERR_ARG and C(FAKE + 4 * 64 * 64 - 4) == q2.Q2_ERR_ARG and b"overlaps z" in lib.q2_last_error()
+    assert C(far, far + 8) == q2.Q2_ERR_ARG and C(far, far, q2.Q2_COMBINE_OUT_BF16) == q2.Q2_ERR_ARG

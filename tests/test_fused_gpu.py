@@ -434,6 +434,23 @@ def test_rank_r_branch(m, n, k, r, gated):
         check(y, z, "silu", gated, bias=bias, what=f"r={r}")
 
 
+@pytest.mark.parametrize("m", [1, 70, 900])
+def test_outputs_beside_x(m):
+    """x, y and the residual one behind the other in one buffer; over each other they are refused."""
+    k = n = 4096
+    (p, s), _ = weights("q2", 350, n, k)
+    buf = rnd(1, 3 * m, n).to(DEV).bfloat16()
+    x, y, res = buf[m:2 * m], buf[:m], buf[2 * m:]
+    want = q2.q2_linear_fused(x.clone(), p, s, residual=res.clone(), out_dtype=torch.bfloat16)
+    assert torch.equal(q2.q2_linear_fused(x, p, s, residual=res, y=y), want)
+    assert torch.equal(q2.q2_linear_fused(x, p, s, residual=res, y=res), want)
+    keep = buf.clone()
+    for y in (x, buf.view(-1)[8:8 + m * n].view(m, n)):
+        with pytest.raises(q2.Q2Error, match="overlaps"):
+            q2.q2_linear_fused(x, p, s, residual=x, y=y)
+    assert torch.equal(buf, keep)
+
+
 @pytest.mark.parametrize("fmt", ["q2", "q4"])
 @pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("m", [1, 13, 70, 200])
