@@ -337,8 +337,9 @@ typedef struct {
  * K == 0 is the empty sum: the epilogue of z = 0.  Products and sums as in
  * q2_linear: exact products, fp32 sums in a fixed order, so a call is run-to-run
  * bitwise deterministic.  The order goes by the sizes and, over many rows, by
- * whether a row near by holds elements more than 2^32 apart.  Errors: those of q2_linear_lowrank; an odd N with
- * Q2_EPI_GATED is Q2_ERR_SHAPE, an unknown activation or flag Q2_ERR_ARG.
+ * whether a row near by holds elements more than 2^32 apart.  Errors: those of
+ * q2_linear_lowrank; an odd N with Q2_EPI_GATED is Q2_ERR_SHAPE, an unknown
+ * activation or flag Q2_ERR_ARG.
  * Asynchronous; calls that share a workspace must be ordered on one stream.
  */
 int q2_linear_fused(const uint16_t* x_bf16, const uint8_t* packed, const uint16_t* scales_f16,

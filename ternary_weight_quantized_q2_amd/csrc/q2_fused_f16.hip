@@ -132,13 +132,13 @@ __device__ __forceinline__ void keep_bf16(const q2_u32x4& v0, const q2_u32x4& v1
 // Rows without a branch: one wave per row, which stays in registers up to
 // 1024 NCH elements between the search for its largest element and the
 // conversion (NCH = 0: longer rows, read twice).  Rows between 4096 and 12288 take
-// the form for 12288, which loads their last elements again in the rest of its places.  Row M (of M + 1) is a row of
-// zeros that indexes outside x are pointed to.
+// the form for 12288, which loads their last elements again in the rest of its
+// places.  Row M (of M + 1) is a row of zeros that indexes outside x are pointed to.
 constexpr int CV_ROWS = 4;
 
 template <int NCH>
-__global__ __launch_bounds__(64 * CV_ROWS) void x_to_f16_kernel(const uint16_t* x, uint16_t* out, int32_t* rowinfo, Lost* lost,
-                                                                int64_t M, int64_t K) {
+__global__ __launch_bounds__(64 * CV_ROWS) void x_to_f16_kernel(const uint16_t* x, uint16_t* out, int32_t* rowinfo,
+                                                                Lost* lost, int64_t M, int64_t K) {
   const int lane = threadIdx.x & 63;
   const int64_t m = (int64_t)blockIdx.x * CV_ROWS + (threadIdx.x >> 6);
   if (m > M) return;
@@ -517,8 +517,7 @@ __global__ __launch_bounds__(256, 2) void fused_f16_kernel(FusedArgs a, const ui
     const uint32_t wo = q == 0 ? woff0 : q == 1 ? woff1 : q == 2 ? woff2 : woff3;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         rw, (lds_void*)(smem + FX_OFF_W + ((set & 1) * 4 + wv) * FX_WBUF + q * 1024), 16,
-        wo - unit_back(set, KB, 2, unit),
-        unit_start(set, KB, 2), 0, 0);
+        wo - unit_back(set, KB, 2, unit), unit_start(set, KB, 2), 0, 0);
   };
   const uint8_t* const wbase = smem + FX_OFF_W + wv * FX_WBUF + c * 64 + 8 * h;
   auto read_codes = [&](int hs, q2_u32x2 (&w)[2]) {

@@ -26,8 +26,9 @@ __device__ __forceinline__ int mid_swz(int r) { return ((r >> 2) & 3) | ((r & 3)
 // tiles then fit 256 registers but for three of Q2_0 and one of 4-bit, spilled outside
 // the loop, and 64 x 128 ones gained 3 %, 32-row ones lost 4 %.
 // x and the codes are addressed with a scalar block offset (buffer loads): 8 % less
-// time for 20 rows per expert than 64-bit addresses.  Each wave sums its rows on the matrix cores itself (a quarter of
-// its products; sharing the sums would need a second barrier).
+// time for 20 rows per expert than 64-bit addresses.  Each wave sums its rows on the
+// matrix cores itself (a quarter of its products; sharing the sums would need a second
+// barrier).
 template <int FMT, int MT, int NT, int NW, int KG, int OCC>
 __global__ __launch_bounds__(64 * NW * KG, OCC) void fused_mid_kernel(FusedArgs a, int tiles_n, int group_m) {
   constexpr int W = NW * KG, BM = 16 * MT, BN = 16 * NT * NW;
