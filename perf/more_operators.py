@@ -234,7 +234,7 @@ def run(state):
         return _run_linear(state) if c["op"] == "linear" else _run_sample(state)
     import ternary_weight_quantized_q2_amd as q2
     if c["op"] == "linear":
-        return q2.q4g_linear(state["x"], state["packed"], state["scale"], state["zero"], bias=state["bias"],
+        return q2.q4_matvec(state["x"], state["packed"], state["scale"], state["zero"], bias=state["bias"],
                              activation=c["act"], gated=c["gated"], residual=state["residual"],
                              out_dtype=DTYPES[c["out"]])
     return tuple(q2.q2_sample(state["logits"], state["u"], **state["settings"]))
