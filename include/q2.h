@@ -453,6 +453,73 @@ size_t q2_route_workspace_bytes(int64_t T, int64_t E, int64_t k);
 int q2_combine(const void* z, int64_t R, const int32_t* slot, const float* weight, const void* residual, void* y,
                int64_t T, int64_t k, int64_t N, uint32_t flags, hipStream_t stream);
 
+/* Flags of q4_matvec. */
+#define Q4_ZERO_CODES 0x1u /* zero holds 4-bit codes, else f16 */
+
+/*
+ * q4_matvec - a linear over 4-bit weights whose scales and zero points hold for
+ * groups of inputs, with an epilogue; made for few rows (single tokens, decode
+ * batches, a vocabulary's logits), right for any number.
+ *   x_bf16     u16 [M, K]                                            (in)
+ *   packed4    u8  [N, K/2], two codes per byte, low nibble = even k  (in)
+ *   scale_f16  u16 [N, K/group]                                      (in)
+ *   zero       the zero points in code units: NULL (8 everywhere), u16 [N, K/group]
+ *              f16, or with Q4_ZERO_CODES u8 [N, ceil(K/group/2)], two codes per
+ *              byte, low nibble = even group                             (in)
+ *   group      32, 64 or a multiple of 128, dividing K (Q2_ERR_SHAPE otherwise)
+ *   epi, y     as q2_linear_fused, with z = x W^T, W[n, k] = (code - zero) * scale
+ * Products are exact, sums in fp32 in an order that goes by the sizes, so a call is
+ * run-to-run bitwise deterministic; weights that are all zero in a group add
+ * exactly nothing.  Scales are finite, and sum |x| over 128 inputs stays below
+ * 2^126.  K == 0 is the empty sum.  Errors: those of q4_linear_fused.
+ * Asynchronous.
+ */
+int q4_matvec(const uint16_t* x_bf16, const uint8_t* packed4, const uint16_t* scale_f16, const void* zero,
+              int64_t group, uint32_t flags, const q2_epilogue* epi, void* y,
+              int64_t M, int64_t N, int64_t K, hipStream_t stream);
+
+/* Flags of q2_sample. */
+#define Q2_SAMPLE_LOGITS_BF16 0x1u /* logits are bf16, else f32 */
+
+/* Settings of q2_sample: for every row the value, or, where it is not NULL, the
+ * array's element of the row (device, [B]). */
+typedef struct q2_sampling {
+  float temperature;  /* not above 0 or NaN: the best token, with probability 1 */
+  int32_t top_k;      /* not above 0: off                                       */
+  float top_p;        /* 1 and above or NaN: off; not above 0: the best token    */
+  float min_p;        /* not above 0 or NaN: off; above 1: the best token        */
+  const float* temperature_rows;
+  const int32_t* top_k_rows;
+  const float* top_p_rows;
+  const float* min_p_rows;
+} q2_sampling;
+
+/*
+ * q2_sample - one token drawn from each of B rows of V logits, from given random
+ * numbers.  The tokens of a row are ordered by logit, largest first, equal logits
+ * (+0 and -0 are) by lower token first; a logit of -inf or NaN is a masked token
+ * and never drawn.  With p_i = exp((logit_i - best) / temperature), 1 for a logit
+ * equal to the best (also +inf), in this order
+ *   min_p  leaves the tokens with p_i >= min_p,
+ *   top_k  of those the first top_k,
+ *   top_p  of those the shortest beginning whose sum reaches top_p * their sum,
+ * and the token drawn is the first one whose cumulative p exceeds u * the sum of
+ * what is left.
+ *   logits    f32 or bf16, row b at element b * ld; ld >= V               (in)
+ *   settings  host pointer, read before the call returns (its arrays are device
+ *             memory); NULL draws from the whole distribution at temperature 1
+ *   u         f32 [B], uniform in [0, 1); below 0 or NaN counts as 0, 1 and
+ *             above draws the last token that is left                      (in)
+ *   token     i32 [B]; -1 for a row whose tokens are all masked            (out)
+ *   prob      f32 [B]: the token's p over the sum of what is left; 0 with -1  (out)
+ * Sums are in units of 2^-S of the best token's p, S = 62 - ceil(log2 V) and at most
+ * 51, each p rounded once: exact, the same in any order, run-to-run deterministic.  A p
+ * below half a unit counts as 0.  1 <= V <= 2^24, B <= 2^30 (Q2_ERR_SHAPE
+ * otherwise).  Asynchronous.
+ */
+int q2_sample(const void* logits, int64_t B, int64_t V, int64_t ld, uint32_t flags, const q2_sampling* settings,
+              const float* u, int32_t* token, float* prob, hipStream_t stream);
+
 /*
  * q2_dequant - test export: w[n, k] = (q - 1) * d as float32 [N, K], exact;
  * a zero weight is written as +0.  Same layout rules as q2_linear.  Asynchronous.

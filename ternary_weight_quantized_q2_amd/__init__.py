@@ -35,7 +35,7 @@ EXPORTS = ("q2_pack", "q2_import_gemlite", "q2_linear", "q2_lowrank_workspace_by
            "q2_a8_workspace_bytes", "q2_linear_a8",
            "q2_linear_fused", "q2_linear_fused_workspace_bytes", "q4_linear_fused",
            "q2_linear_grouped", "q2_linear_grouped_workspace_bytes", "q4_linear_grouped",
-           "q2_route", "q2_route_workspace_bytes", "q2_combine",
+           "q2_route", "q2_route_workspace_bytes", "q2_combine", "q4_matvec", "q2_sample",
            "q4_linear", "q2_dequant", "q2_set_dispatch", "q2_strerror", "q2_last_error")
 
 # q2_epilogue: activations by name, and flags
@@ -43,12 +43,21 @@ ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 Q2_EPI_GATED, Q2_EPI_OUT_BF16, Q2_EPI_RESIDUAL_BF16 = 0x1, 0x2, 0x4
 Q2_ROUTE_LOGITS_BF16, Q2_ROUTE_RENORM = 0x1, 0x2
 Q2_COMBINE_Z_BF16, Q2_COMBINE_OUT_BF16, Q2_COMBINE_RESIDUAL_BF16 = 0x1, 0x2, 0x4
+Q4_ZERO_CODES = 0x1
+Q2_SAMPLE_LOGITS_BF16 = 0x1
 
 
 class Epilogue(ctypes.Structure):
     """The C ABI's q2_epilogue."""
     _fields_ = [("activation", ctypes.c_uint32), ("flags", ctypes.c_uint32), ("bias", ctypes.c_void_p),
                 ("gate", ctypes.c_void_p), ("residual", ctypes.c_void_p)]
+
+
+class Sampling(ctypes.Structure):
+    """The C ABI's q2_sampling."""
+    _fields_ = [("temperature", ctypes.c_float), ("top_k", ctypes.c_int32), ("top_p", ctypes.c_float),
+                ("min_p", ctypes.c_float), ("temperature_rows", ctypes.c_void_p), ("top_k_rows", ctypes.c_void_p),
+                ("top_p_rows", ctypes.c_void_p), ("min_p_rows", ctypes.c_void_p)]
 
 
 _lib = None
@@ -91,6 +100,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "q2_route": ([p, i64, i64, i64, ctypes.c_uint32, p, p, p, p, p, p, sz, p], ctypes.c_int),
         "q2_route_workspace_bytes": ([i64, i64, i64], sz),
         "q2_combine": ([p, i64, p, p, p, p, i64, i64, i64, ctypes.c_uint32, p], ctypes.c_int),
+        "q4_matvec": ([p, p, p, p, i64, ctypes.c_uint32, p, p, i64, i64, i64, p], ctypes.c_int),
+        "q2_sample": ([p, i64, i64, i64, ctypes.c_uint32, p, p, p, p, p], ctypes.c_int),
         "q4_linear": ([p, p, p, p, p, i64, i64, i64, p], ctypes.c_int),
         "q2_dequant": ([p, p, p, i64, i64, p], ctypes.c_int),
         "q2_set_dispatch": ([ctypes.c_char_p, ctypes.c_char_p, ctypes.c_int], ctypes.c_int),
@@ -554,6 +565,90 @@ def q2_combine(z, slot, weight, residual=None, out_dtype=torch.float32, y=None) 
         _have(y, out_dtype, (t, n), "y", dev)
     _check(lib.q2_combine(_ptr(z), r, _ptr(slot), _ptr(weight), _ptr(residual), _ptr(y), t, k, n, flags, _stream()))
     return y
+
+
+def q4_matvec(x, packed4, scale, zero=None, bias=None, activation="none", gated=False, gate=None, residual=None,
+              out_dtype=torch.float32, y=None) -> torch.Tensor:
+    """y = residual + gate * act(x W^T + bias) for 4-bit weights (code - zero) * scale with a scale per group of
+    K / G inputs: packed4 u8 [N, K/2] (low nibble = even k), scale f16 [N, G].  Groups are of 32, 64 or a multiple
+    of 128 inputs.
+
+    zero: None (8 everywhere), f16 [N, G] in code units, or u8 [N, ceil(G / 2)], two codes per byte (low nibble =
+    even group).  Made for few rows, right for any number.  The epilogue is q2_linear_fused's."""
+    lib = load()
+    dev = _here()
+    m, k = x.shape
+    n, groups = scale.shape
+    _have(x, torch.bfloat16, (m, k), "x", dev)
+    _have(packed4, torch.uint8, (n, k // 2), "packed4", dev)
+    _have(scale, torch.float16, (n, groups), "scale", dev)
+    if k and (groups == 0 or k % groups):
+        raise ValueError(f"scale: {groups} groups do not divide {k} inputs")
+    flags = 0
+    if zero is not None:
+        if zero.dtype is torch.uint8:
+            flags = Q4_ZERO_CODES
+            _have(zero, torch.uint8, (n, (groups + 1) // 2), "zero", dev)
+        else:
+            _have(zero, torch.float16, (n, groups), "zero", dev)
+    epi, y = _epilogue(n, m, (n,), bias, activation, gated, gate, residual, out_dtype, y, x, dev)
+    _check(lib.q4_matvec(_ptr(x), _ptr(packed4), _ptr(scale), _ptr(zero), k // groups if k else 32, flags,
+                         ctypes.addressof(epi), _ptr(y), m, n, k, _stream()))
+    return y
+
+
+class Sample(NamedTuple):
+    """q2_sample's draw."""
+    token: torch.Tensor       # i32 [B], -1 for a row whose tokens are all masked
+    prob: torch.Tensor        # f32 [B], the token's probability among those left to draw from
+
+
+def _setting(value, dtype, shape, name, dev):
+    """(value for all rows, address of the rows' values) of a sampling setting."""
+    if isinstance(value, torch.Tensor):
+        _have(value, dtype, shape, name, dev)
+        return 0, _ptr(value)
+    return value, None
+
+
+def q2_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, token=None, prob=None) -> Sample:
+    """One token of each row of logits [B, V] (f32 or bf16; rows may lie apart, as in a slice) from the random numbers
+    u f32 [B] in [0, 1): the first token in descending order of its logit (equal logits: the lower token first; -inf
+    and NaN are masked tokens) whose cumulative probability exceeds u.
+
+    temperature divides the logits (0: the largest logit); then min_p leaves the tokens with at least min_p times the
+    largest probability, top_k of those the first top_k (0: all), top_p of those the fewest whose sum reaches top_p of
+    theirs (1: all).  Each is a number, or a tensor [B] with one per row (top_k i32, the others f32)."""
+    lib = load()
+    dev = _here()
+    b, v = logits.shape
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"logits are float32 or bfloat16, not {logits.dtype}")
+    if logits.numel():
+        if logits.get_device() != dev:
+            raise ValueError(f"logits are on {logits.device}, not on the current device cuda:{dev}")
+        if v > 1 and logits.stride(1) != 1:
+            raise ValueError("logits: the logits of a row must lie next to each other")
+    _have(u, torch.float32, (b,), "u", dev)
+    t, tp = _setting(temperature, torch.float32, (b,), "temperature", dev)
+    k, kp = _setting(top_k, torch.int32, (b,), "top_k", dev)
+    k = max(0, min(int(k), 0x7fffffff))
+    p, pp = _setting(top_p, torch.float32, (b,), "top_p", dev)
+    m, mp = _setting(min_p, torch.float32, (b,), "min_p", dev)
+    new = _maker(logits, dev)
+    if token is None:
+        token = new((b,), dtype=torch.int32)
+    else:
+        _have(token, torch.int32, (b,), "token", dev)
+    if prob is None:
+        prob = new((b,), dtype=torch.float32)
+    else:
+        _have(prob, torch.float32, (b,), "prob", dev)
+    settings = Sampling(t, k, p, m, tp, kp, pp, mp)
+    _check(lib.q2_sample(_ptr(logits), b, v, logits.stride(0) if b > 1 else v,
+                         Q2_SAMPLE_LOGITS_BF16 if logits.dtype == torch.bfloat16 else 0, ctypes.addressof(settings),
+                         _ptr(u), _ptr(token), _ptr(prob), _stream()))
+    return Sample(token, prob)
 
 
 def q2_dequant(packed, scales, w=None) -> torch.Tensor:

@@ -1,0 +1,492 @@
+"""GPU tests of the 4-bit products with scales per group and of the sampler against the float64 oracle, and of a run of
+them together, from a hidden row to the token.
+
+Products: the linears' bar (tests/test_fused_gpu.py).  Draws: the token is equal.  A probability is a quotient of one p,
+right to a few units of 2^-52, and a sum whose V terms are each off by up to half a unit of 2^-S of a sum that is at least
+one, rounded once to fp32: relative 2^-24 + V 2^-(S + 1) + 2^-48.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle.q2_oracle as O
+import oracle.token_oracle as T
+import ternary_weight_quantized_q2_amd as q2
+from tests.test_fused_gpu import ACTS, check, host, rnd
+from tests.test_parity_gpu import DEV, acts
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    assert torch.cuda.is_available(), "GPU parity tests need a GPU; they must not be skipped silently"
+    torch.cuda.set_device(0)
+    q2.load()
+    yield
+
+
+# ---------------------------------------------------------------------------
+# products
+# ---------------------------------------------------------------------------
+
+ZEROS = ["none", "codes", "f16"]
+
+
+def weights(seed, n, k, group, zero):
+    """(device arguments, float64 weight)."""
+    g = np.random.default_rng([0, seed, n, k])
+    packed = g.integers(0, 256, (n, k // 2)).astype(np.uint8)
+    scale = (np.abs(g.standard_normal((n, k // group))) * 0.02).astype(np.float16)
+    z = None
+    if zero == "codes":
+        z = g.integers(0, 256, (n, (k // group + 1) // 2)).astype(np.uint8)
+    elif zero == "f16":
+        z = (g.random((n, k // group)) * 15).astype(np.float16)
+    dev = [torch.from_numpy(packed).to(DEV), torch.from_numpy(scale).to(DEV), None if z is None else torch.from_numpy(z).to(DEV)]
+    return dev, T.weight(packed, scale, z)
+
+
+# K with and without whole 128-input blocks, one group and many, one column to several tiles
+SHAPES = [(64, 32, 32), (1, 32, 64), (37, 32, 96), (100, 32, 416), (513, 32, 1120), (70, 32, 9696), (33, 32, 2560),
+          (64, 64, 64), (5, 64, 192), (130, 64, 2560), (1000, 64, 320), (200, 64, 9664),
+          (48, 128, 128), (99, 128, 1152), (17, 256, 512), (257, 256, 2560), (40, 384, 1152), (31, 640, 640), (65, 2560, 2560)]
+
+
+@pytest.mark.parametrize("n,group,k", SHAPES)
+@pytest.mark.parametrize("zero", ZEROS)
+@pytest.mark.parametrize("m", [1, 3, 6, 16, 17, 40, 64, 65, 150])
+def test_sizes(n, group, k, zero, m):
+    dev, w = weights(401, n, k, group, zero)
+    xb, x = acts(401, m, k)
+    y = q2.q4_matvec(x, *dev)
+    assert y.dtype == torch.float32
+    check(y, O.bf16_to_f64(xb) @ w.T, what=f"{m} {n} {k} {group} {zero}")
+    assert torch.equal(q2.q4_matvec(x, *dev, out_dtype=torch.bfloat16), y.to(torch.bfloat16))
+    assert torch.equal(q2.q4_matvec(x, *dev), y)
+
+
+@pytest.mark.parametrize("m", [1, 16, 50])
+@pytest.mark.parametrize("zero", ZEROS)
+@pytest.mark.parametrize("n,group,k", [(9001, 32, 2560), (33000, 64, 1280), (20480, 128, 2560)])
+def test_wide(n, group, k, zero, m):
+    """Many tiles: sampled columns."""
+    g = np.random.default_rng(402)
+    cols = np.unique(np.concatenate([np.arange(40), n - 1 - np.arange(40), g.choice(n, 100)]))
+    groups = k // group
+    packed = torch.randint(0, 256, (n, k // 2), dtype=torch.uint8, generator=torch.Generator().manual_seed(1))
+    scale = (rnd(2, n, groups).abs() * 0.02).half()
+    z = None
+    if zero == "codes":
+        z = torch.randint(0, 256, (n, (groups + 1) // 2), dtype=torch.uint8, generator=torch.Generator().manual_seed(3))
+    elif zero == "f16":
+        z = (torch.rand((n, groups), generator=torch.Generator().manual_seed(3)) * 15).half()
+    w = T.weight(packed.numpy()[cols], scale.numpy()[cols], None if z is None else z.numpy()[cols])
+    xb, x = acts(402, m, k)
+    y = q2.q4_matvec(x, packed.to(DEV), scale.to(DEV), None if z is None else z.to(DEV))
+    check(y[:, torch.from_numpy(cols).to(DEV)], O.bf16_to_f64(xb) @ w.T)
+
+
+@pytest.mark.parametrize("m", [1, 5, 33])
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("n", [80, 74])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_epilogue(m, act, gated, n, out):
+    k, zero = 320, ZEROS[m % 3]
+    dev, w = weights(403, n, k, 64 if gated else 32, zero)
+    xb, x = acts(403, m, k)
+    n_out = n // 2 if gated else n
+    bias, gate, res = rnd(1, n).to(DEV), rnd(2, n_out).to(DEV), rnd(3, m, n_out).to(DEV)
+    z = O.bf16_to_f64(xb) @ w.T
+    for b in (None, bias):
+        for g in (None, gate):
+            for r in (None, res, res.bfloat16()):
+                y = q2.q4_matvec(x, *dev, bias=b, activation=act, gated=gated, gate=g, residual=r, out_dtype=out)
+                check(y, z, act, gated, b, g, r)
+
+
+def test_residual_in_place_and_unaligned_output():
+    m, n, k = 9, 75, 288
+    dev, w = weights(404, n, k, 32, "codes")
+    xb, x = acts(404, m, k)
+    res = rnd(4, m, n).to(DEV)
+    want = q2.q4_matvec(x, *dev, residual=res)
+    flat = torch.full((m * n + 9,), 7.0, device=DEV)
+    y = flat[1:1 + m * n].view(m, n)
+    y.copy_(res)
+    assert q2.q4_matvec(x, *dev, residual=y, y=y) is y
+    assert torch.equal(y, want) and (flat[:1] == 7).all() and (flat[1 + m * n:] == 7).all()
+    check(want, O.bf16_to_f64(xb) @ w.T, residual=res)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128, 256])
+@pytest.mark.parametrize("zero", ZEROS)
+@pytest.mark.parametrize("m", [1, 16, 40])
+def test_zero_weights_add_nothing(group, zero, m):
+    """A whole weight of zeros gives zeros bit for bit, zero groups among others add exactly nothing."""
+    n, k = 70, 1280
+    g = np.random.default_rng(405)
+    groups = k // group
+    zc = g.integers(0, 16, (n, groups)) if zero != "none" else np.full((n, groups), 8)
+    q = np.repeat(zc, group, axis=1)
+    dead = np.ones((n, groups), bool)
+    dead[1::2] = g.random(dead[1::2].shape) < 0.5             # every other column has live groups
+    q = np.where(np.repeat(dead, group, axis=1), q, g.integers(0, 16, (n, k)))
+    packed = (q[:, 0::2] | q[:, 1::2] << 4).astype(np.uint8)
+    scale = (g.random((n, groups)) * 0.02 + 0.01).astype(np.float16)
+    if zero == "none":
+        z = None
+    elif zero == "f16":
+        z = zc.astype(np.float16)
+    else:
+        zc = np.concatenate([zc, zc[:, :1]], axis=1) if groups % 2 else zc
+        z = (zc[:, 0::2] | zc[:, 1::2] << 4).astype(np.uint8)
+    dev = [torch.from_numpy(packed).to(DEV), torch.from_numpy(scale).to(DEV), None if z is None else torch.from_numpy(z).to(DEV)]
+    xb, x = acts(405, m, k)
+    big = x.clone()
+    big[:, ::7] *= 2.0 ** 60
+    assert (q2.q4_matvec(big, *dev)[:, 0::2] == 0).all()
+    # inputs at dead groups of column 1 change nothing of it
+    y = q2.q4_matvec(x, *dev)
+    x2 = x.clone()
+    at = torch.from_numpy(np.repeat(dead[1], group)).to(DEV)
+    x2[:, at] = x2[:, at] * 3 + 1
+    assert torch.equal(q2.q4_matvec(x2, *dev)[:, 1], y[:, 1])
+    check(y[:, 1::2], O.bf16_to_f64(xb) @ T.weight(packed, scale, z)[1::2].T)
+
+
+@pytest.mark.parametrize("group,k", [(32, 1120), (64, 2560), (128, 1280)])
+@pytest.mark.parametrize("zero", ZEROS)
+def test_scales_and_zero_points_of_every_size(group, k, zero):
+    """Subnormal and large f16 scales, negative ones, zero points outside the codes and not whole."""
+    n, m = 50, 7
+    g = np.random.default_rng(406)
+    packed = g.integers(0, 256, (n, k // 2)).astype(np.uint8)
+    scale = np.ldexp(g.random((n, k // group)) + 0.5, g.integers(-20, 12, (n, 1))).astype(np.float16)
+    scale[::3] *= -1
+    scale[1] = 0
+    z = None
+    if zero == "codes":
+        z = g.integers(0, 256, (n, (k // group + 1) // 2)).astype(np.uint8)
+    elif zero == "f16":
+        z = (g.standard_normal((n, k // group)) * 100).astype(np.float16)
+    dev = [torch.from_numpy(packed).to(DEV), torch.from_numpy(scale).to(DEV), None if z is None else torch.from_numpy(z).to(DEV)]
+    xb, x = acts(406, m, k)
+    xd, w = O.bf16_to_f64(xb), T.weight(packed, scale, z)
+    y = host(q2.q4_matvec(x, *dev))
+    bad = np.abs(y - xd @ w.T) > 1e-3 * np.sqrt((xd * xd) @ (w * w).T)     # every output by its own terms
+    assert not bad.any() and (y[:, 1] == 0).all()
+
+
+@pytest.mark.parametrize("m", [2, 20])
+def test_rows_do_not_meet(m):
+    """A row that holds an infinity or a NaN leaves the others as they are."""
+    dev, _ = weights(407, 90, 640, 64, "f16")
+    _, x = acts(407, m, 640)
+    want = q2.q4_matvec(x, *dev)
+    x2 = x.clone()
+    x2[1, 5], x2[1, 100] = float("inf"), float("nan")
+    got = q2.q4_matvec(x2, *dev)
+    keep = [i for i in range(m) if i != 1]
+    assert torch.equal(got[keep], want[keep]) and not got[1].isfinite().all()
+
+
+@pytest.mark.parametrize("zero", ZEROS)
+def test_empty_sizes(zero):
+    dev, _ = weights(408, 12, 64, 32, zero)
+    assert q2.q4_matvec(torch.empty((0, 64), dtype=torch.bfloat16, device=DEV), *dev).shape == (0, 12)
+    bias, res = rnd(1, 12).to(DEV), rnd(2, 3, 12).to(DEV)
+    e = [torch.empty((12, 0), dtype=t, device=DEV) for t in (torch.uint8, torch.float16)]
+    ez = {"none": None, "codes": e[0], "f16": e[1]}[zero]
+    x = torch.empty((3, 0), dtype=torch.bfloat16, device=DEV)
+    assert torch.equal(q2.q4_matvec(x, e[0], e[1], ez, bias=bias, residual=res), bias + res)
+    none = [torch.empty((0, 32), dtype=torch.uint8, device=DEV), torch.empty((0, 2), dtype=torch.float16, device=DEV)]
+    assert q2.q4_matvec(torch.zeros((3, 64), dtype=torch.bfloat16, device=DEV), *none).shape == (3, 0)
+
+
+def test_matvec_refusals():
+    dev, _ = weights(409, 8, 128, 32, "f16")
+    x = torch.zeros((2, 128), dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError, match="x: expected"):
+        q2.q4_matvec(x.float(), *dev)
+    with pytest.raises(ValueError, match="contiguous"):
+        q2.q4_matvec(x.expand(2, 2, 128)[:, 0], dev[0], dev[1].t().contiguous().t())
+    with pytest.raises(q2.Q2Error, match="group"):
+        q2.q4_matvec(x, dev[0], dev[1].repeat(1, 2))          # groups of 16
+    with pytest.raises(ValueError, match="unknown activation"):
+        q2.q4_matvec(x, *dev, activation="tanh")
+
+
+# ---------------------------------------------------------------------------
+# draws
+# ---------------------------------------------------------------------------
+
+def check_sample(logits, u, what="", dev=None, **settings):
+    """Draws of rows of logits (host tensor; dev: the device tensor to pass in its place)."""
+    v = logits.shape[1]
+    on = {k: s.to(DEV) if isinstance(s, torch.Tensor) else s for k, s in settings.items()}
+    got = q2.q2_sample(logits.to(DEV) if dev is None else dev, u.to(DEV), **on)
+    f32 = {k: host(s) if isinstance(s, torch.Tensor) else float(np.float32(s)) for k, s in settings.items()}
+    token, prob = T.sample(logits.double().numpy(), u.double().numpy(), **f32)
+    g = got.token.cpu().numpy()
+    bad = g != token
+    assert not bad.any(), f"{what} {bad.sum()} of {bad.size} tokens, row {np.argwhere(bad)[0]}: {g[bad][0]} for {token[bad][0]}"
+    unit = min(62 - int(np.ceil(np.log2(max(v, 1)))), 51)
+    tol = prob * (2.0 ** -24 + v * 2.0 ** -(unit + 1) + 2.0 ** -48) + 2.0 ** -149
+    assert (np.abs(got.prob.cpu().double().numpy() - prob) <= tol).all(), what
+    return got
+
+
+def uniform(seed, n):
+    return torch.rand(n, generator=torch.Generator().manual_seed(seed))
+
+
+VOCAB = [1, 2, 3, 31, 64, 100, 257, 1000, 1024, 1025, 4099, 8192, 50021, 128009]
+SETTINGS = [dict(), dict(temperature=0.7), dict(top_k=5), dict(top_p=0.9), dict(min_p=0.05), dict(temperature=0.0),
+            dict(temperature=1.3, top_k=50, top_p=0.95), dict(top_k=300, min_p=0.001), dict(top_p=0.3, min_p=0.3),
+            dict(temperature=2.0, top_k=2000, top_p=0.99, min_p=1e-4)]
+
+
+@pytest.mark.parametrize("v", VOCAB)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sample(v, dtype):
+    b = 9
+    logits = (rnd(v, b, v) * 3).to(dtype)
+    for i, s in enumerate(SETTINGS):
+        check_sample(logits, uniform(i, b), f"{s}", **s)
+
+
+@pytest.mark.parametrize("v", [5, 700, 3001, 40000])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_settings_of_their_own(v, dtype):
+    b = 40
+    g = torch.Generator().manual_seed(v)
+
+    def pick(values, t):
+        return torch.tensor(values, dtype=t)[torch.randint(0, len(values), (b,), generator=g)]
+
+    s = dict(temperature=pick([0.0, 0.3, 1.0, 1.7, -2.0], torch.float32), top_k=pick([0, -4, 1, 3, 100, 2 ** 31 - 1], torch.int32),
+             top_p=pick([1.0, 0.9, 0.5, 0.01, 2.0, 0.0], torch.float32), min_p=pick([0.0, 0.1, 1.0, 1.5, -1.0], torch.float32))
+    logits = (rnd(v, b, v) * 3).to(dtype)
+    logits[torch.rand((b, v), generator=g) < 0.3] = -np.inf
+    check_sample(logits, uniform(1, b), **s)
+    for name in s:
+        check_sample(logits, uniform(2, b), name, **{name: s[name]})
+
+
+@pytest.mark.parametrize("v", [6, 300, 5000, 30000])
+@pytest.mark.parametrize("levels", [1, 2, 7, 200])
+def test_ties(v, levels):
+    """Few distinct logits, each of many tokens: the lower token first, borders inside the ties."""
+    b = 24
+    logits = torch.randint(0, levels, (b, v), generator=torch.Generator().manual_seed(v)).float() / 8
+    logits[0, ::2] = -0.0
+    for i, s in enumerate([dict(), dict(top_k=4), dict(top_k=v // 2), dict(top_p=0.5), dict(top_k=v // 3 + 1, top_p=0.37),
+                           dict(min_p=0.9), dict(temperature=0.0), dict(temperature=30.0, top_p=0.77)]):
+        u = uniform(i, b)
+        u[:4] = torch.tensor([0.0, 0.5, 0.25, 1 - 2.0 ** -24])
+        check_sample(logits, u, f"{s}", **s)
+        check_sample(logits.bfloat16(), u, f"bf16 {s}", **s)
+
+
+@pytest.mark.parametrize("v", [2000, 40000])
+def test_logits_one_step_apart(v):
+    """All of them within one part of the first histogram, neighbours in fp32, and one range inside the other."""
+    b = 6
+    steps = torch.stack([torch.randperm(v, generator=torch.Generator().manual_seed(i)) for i in range(b)])
+    logits = (1.0 + steps * 2.0 ** -23).float()
+    logits[1] += 40
+    logits[2, : v // 2] -= 0.25
+    logits[3] = torch.where(steps[3] % 3 == 0, logits[3], torch.tensor(1.0))
+    logits[4] = steps[4].float() * 1e-30
+    for i, s in enumerate([dict(), dict(top_k=700), dict(top_p=0.6), dict(top_k=1900, top_p=0.9), dict(min_p=0.9999)]):
+        check_sample(logits, uniform(i, b), f"{s}", **s)
+
+
+def test_borders_of_the_random_number():
+    """u at, below and above every border of eight equal tokens; outside [0, 1)."""
+    u = torch.cat([torch.arange(9) / 8, torch.arange(1, 9) / 8 - 2.0 ** -24, torch.tensor([-1.0, 2.0, np.nan, np.inf, -np.inf])])
+    logits = torch.full((len(u), 12), -np.inf)
+    logits[:, 2:10] = 3.0
+    got = check_sample(logits, u)
+    assert got.token[:8].tolist() == list(range(2, 10)) and got.token[8:17].tolist() == [9] + list(range(2, 10))
+    assert got.token[17:].tolist() == [2, 9, 2, 9, 2]
+
+
+@pytest.mark.parametrize("v", [40, 3000])
+def test_masks_and_extremes(v):
+    b = 16
+    logits = rnd(5, b, v) * 4
+    low, high = torch.finfo(torch.float32).min, torch.finfo(torch.float32).max
+    logits[0] = -np.inf
+    logits[1] = np.nan
+    logits[2] = -np.inf
+    logits[2, v - 1] = -5.0
+    logits[3] = low                                           # the type's lowest value is a logit like any other
+    logits[4, 1:] = low
+    logits[5, 7] = high
+    logits[6, [3, 9]] = np.inf
+    logits[7, ::3] = np.nan
+    logits[8, ::2] = -np.inf
+    logits[9] = high
+    logits[10] = low
+    logits[10, 5] = -np.inf
+    logits[11] = torch.linspace(-90, 0, v)                    # most of them too unlikely to be drawn
+    logits[12] = torch.linspace(-31, 0, v)
+    logits[13] = 0.0
+    logits[13, 11] = 60.0
+    logits[14] *= 1e30
+    logits[15] *= 1e-30
+    for i, s in enumerate(SETTINGS + [dict(temperature=1e-30), dict(temperature=1e30), dict(temperature=np.inf),
+                                      dict(temperature=np.inf, top_k=5)]):
+        got = check_sample(logits, uniform(i, b), f"{s}", **s)
+        assert got.token[:2].tolist() == [-1, -1] and got.prob[:2].tolist() == [0, 0] and got.token[2] == v - 1
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("v,ld,at", [(1001, 1007, 0), (1001, 1007, 1), (5000, 5001, 3), (64, 200, 7), (3, 9, 2), (20000, 20003, 5)])
+def test_rows_apart_and_unaligned(dtype, v, ld, at):
+    """Rows of a wider tensor, from any column on; what lies between them is never read as a logit."""
+    b = 7
+    wide = torch.full((b, ld + 8), 90.0).to(dtype)
+    wide[:, at:at + v] = (rnd(v, b, v) * 3).to(dtype)
+    dev = wide.to(DEV)
+    for i, s in enumerate([dict(), dict(top_k=20, top_p=0.9), dict(temperature=0.0)]):
+        check_sample(wide[:, at:at + v], uniform(i, b), dev=dev[:, at:at + v], **s)
+
+
+def test_last_positions_of_a_batch_of_texts():
+    """logits[:, -1] of [B, S, V]."""
+    full = rnd(1, 5, 3, 700).to(DEV)
+    check_sample(full[:, -1].cpu(), uniform(1, 5), dev=full[:, -1], top_p=0.8)
+
+
+def test_large_vocabulary():
+    v = (1 << 24) - 3
+    logits = torch.zeros((1, v), device=DEV, dtype=torch.bfloat16)
+    logits[0, v - 1] = 1.0
+    u = torch.tensor([0.75], device=DEV)
+    got = q2.q2_sample(logits, u)
+    e = float(np.exp(1.0))
+    want = int(np.floor(0.75 * (v - 1 + e) - e))
+    assert got.token.item() == want and abs(got.prob.item() * (v - 1 + e) - 1) < 1e-6
+    assert q2.q2_sample(logits, u, top_k=1001).token.item() == int(np.floor(0.75 * (1000 + e) - e))
+    assert q2.q2_sample(logits, u, temperature=0.0).token.item() == v - 1
+    with pytest.raises(q2.Q2Error, match="2\\^24"):
+        q2.q2_sample(torch.empty((1, (1 << 24) + 1), device=DEV, dtype=torch.bfloat16), u)
+
+
+def test_rows_beyond_32_bits():
+    """Row offsets past 2^31 elements."""
+    ld, b = 1 << 23, 300
+    big = torch.empty((b, ld), device=DEV, dtype=torch.bfloat16)
+    big[:, :100] = (rnd(1, b, 100) * 3).bfloat16().to(DEV)
+    check_sample(big[:, :100].cpu(), uniform(1, b), dev=big[:, :100], top_k=10)
+    del big
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("b", [200, 513, 5000])
+def test_many_rows(b):
+    logits = rnd(b, b, 300) * 3
+    check_sample(logits, uniform(b, b), top_k=40, top_p=0.95)
+    check_sample(logits, uniform(b, b))
+
+
+def test_frequencies():
+    """Every token of a small distribution as often as its probability says: evenly spaced u hit each within one."""
+    logits, n = rnd(3, 1, 50) * 2, 20000
+    got = q2.q2_sample(logits.to(DEV).repeat(n, 1), ((torch.arange(n) + 0.5) / n).to(DEV), temperature=0.8)
+    p = torch.softmax(logits[0].double() / np.float32(0.8), 0)
+    count = torch.bincount(got.token.cpu().long(), minlength=50).double()
+    assert (count - n * p).abs().max() <= 1.01
+
+
+def test_sample_outputs_given_and_empty():
+    logits, u = rnd(1, 4, 100).to(DEV), uniform(1, 4).to(DEV)
+    token, prob = torch.full((4,), -7, device=DEV, dtype=torch.int32), torch.zeros(4, device=DEV)
+    got = q2.q2_sample(logits, u, token=token, prob=prob)
+    assert got.token is token and got.prob is prob and torch.equal(token, q2.q2_sample(logits, u).token)
+    none = q2.q2_sample(torch.empty((0, 9), device=DEV), torch.empty(0, device=DEV))
+    assert none.token.shape == (0,) and none.token.is_cuda
+
+
+def test_sample_refusals():
+    logits, u = torch.zeros((4, 100), device=DEV), torch.zeros(4, device=DEV)
+    with pytest.raises(ValueError, match="next to each other"):
+        q2.q2_sample(torch.zeros((100, 4), device=DEV).t(), u)
+    with pytest.raises(q2.Q2Error, match="ld"):
+        q2.q2_sample(torch.zeros((1, 100), device=DEV).expand(4, 100), u)
+    with pytest.raises(q2.Q2Error):
+        q2.q2_sample(torch.zeros((4, 0), device=DEV), u)
+    with pytest.raises(ValueError, match="device tensor"):
+        q2.q2_sample(logits, u.cpu())
+    with pytest.raises(ValueError, match="temperature"):
+        q2.q2_sample(logits, u, temperature=torch.ones(3, device=DEV))
+    with pytest.raises(ValueError, match="current device"):
+        q2.q2_sample(logits.cpu(), u)
+
+
+# ---------------------------------------------------------------------------
+# together: from hidden rows to tokens
+# ---------------------------------------------------------------------------
+
+def step(x, gated, down, head, u, **settings):
+    """A gated layer onto the residual stream x, the vocabulary's logits and the draw."""
+    h = q2.q4_matvec(x, *gated, activation="silu", gated=True, out_dtype=torch.bfloat16)
+    x = q2.q4_matvec(h, *down, residual=x, out_dtype=torch.bfloat16)
+    logits = q2.q4_matvec(x, *head)
+    return h, x, logits, q2.q2_sample(logits, u, **settings)
+
+
+def model(hidden=256, inner=320, vocab=5003):
+    return (weights(421, 2 * inner, hidden, 64, "f16"), weights(422, hidden, inner, 32, "none"),
+            weights(423, vocab, hidden, 128, "codes"))
+
+
+@pytest.mark.parametrize("m", [1, 7, 30])
+def test_from_rows_to_tokens(m):
+    (gd, gw), (dd, dw), (hd, hw) = model()
+    xb, x = acts(420, m, 256)
+    u = uniform(5, m)
+    h, x1, logits, got = step(x, gd, dd, hd, u.to(DEV), temperature=0.8, top_k=100, top_p=0.9)
+    check(h, O.bf16_to_f64(xb) @ gw.T, "silu", True)
+    check(x1, host(h) @ dw.T, residual=x)
+    check(logits, host(x1) @ hw.T)
+    token, _ = T.sample(host(logits), u.double().numpy(), float(np.float32(0.8)), 100, float(np.float32(0.9)))
+    assert np.array_equal(got.token.cpu().numpy(), token)
+
+
+@pytest.mark.parametrize("m", [1, 7])
+def test_in_a_graph_and_on_a_busy_stream(m):
+    (gd, _), (dd, _), (hd, _) = model()
+    _, x = acts(424, m, 256)
+    u = uniform(6, m).to(DEV)
+    settings = dict(temperature=torch.full((m,), 0.9, device=DEV), top_k=50, top_p=0.9, min_p=0.01)
+    step(x, gd, dd, hd, u, **settings)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            out = step(x, gd, dd, hd, u, **settings)
+    for i in range(4):
+        x.copy_(acts(430 + i, m, 256)[1])
+        u.copy_(uniform(7 + i, m))
+        settings["temperature"].fill_(0.5 + 0.3 * i)
+        want = step(x, gd, dd, hd, u, **settings)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[2], want[2]) and all(torch.equal(a, b) for a, b in zip(out[3], want[3])), f"replay {i}"
+    # written late on another stream, read there
+    late = torch.zeros_like(x)
+    with torch.cuda.stream(side):
+        big = torch.randn((4096, 4096), device=DEV)
+        for _ in range(10):
+            big = big @ big * 1e-3
+        late.copy_(x)
+        got = step(late, gd, dd, hd, u, **settings)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got[3], want[3]))
