@@ -1,19 +1,14 @@
-// q4_matvec.hip - products with 4-bit weights whose scales (and zero points) hold for
-// groups of inputs: single tokens, decode batches, a vocabulary's logits.
-//
-// y = epilogue(x W^T), w = (q - z) s with one s and z per group of 32, 64 or a
-// multiple of 128 inputs.  A code decodes to bf16 1 + q / 16 (q2_device.h); per group
-// sum x (1 + q / 16) - (1 + z / 16) sum x = sum x (q - z) / 16 on the matrix cores,
-// exact products and fp32 sums, and one FMA per output applies the group's scale.
-#include "q2_token.h"
-#include <algorithm>
+// q4_matvec.hip - the launch of the 4-bit products with scales per group, and the plain
+// kernel for weights of few inputs.
+#include "q4_matvec.h"
 
 namespace q2dev {
 
 constexpr int MV_BM = 16, MV_BN = 64;
 
 // A workgroup owns 16 rows x 64 weight columns; each of its four waves 16 of the
-// columns, 32 inputs at a time, straight from global memory.
+// columns, 32 inputs at a time, straight from global memory.  For what the other
+// kernel's loads and grid do not take: one row, K = 2560, N = 2 x 9728 took 40 us here.
 __global__ __launch_bounds__(256) void matvec_tile_kernel(MatvecArgs m, int tiles_n) {
   const FusedArgs& a = m.f;
   __shared__ float out[MV_BM][MV_BN + 4];
@@ -72,11 +67,17 @@ __global__ __launch_bounds__(256) void matvec_tile_kernel(MatvecArgs m, int tile
 }
 
 hipError_t launch_q4_matvec(const MatvecArgs& m, hipStream_t stream) {
-  const int64_t cols = m.f.gated ? MV_BN / 2 : MV_BN;
-  const int64_t tiles_n = (fused_n_out(m.f) + cols - 1) / cols, tiles_m = max_row_tiles(m.f, MV_BM);
-  if (tiles_n > 0x7fffffff || tiles_m > 0x7fffffff / tiles_n) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(matvec_tile_kernel, grid_of(tiles_m * tiles_n), dim3(256), 0, stream, m, (int)tiles_n);
-  return hipGetLastError();
+  // less than a unit of inputs, more rows than the grid's second dimension, columns beyond 32 bits
+  if (m.f.K < 256 || m.f.N > 0x7fffffff || m.f.M > 65535 * MV_ROWS) {
+    const int64_t cols = m.f.gated ? MV_BN / 2 : MV_BN;
+    const int64_t tiles_n = (fused_n_out(m.f) + cols - 1) / cols, tiles_m = max_row_tiles(m.f, MV_BM);
+    if (tiles_n > 0x7fffffff || tiles_m > 0x7fffffff / tiles_n) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(matvec_tile_kernel, grid_of(tiles_m * tiles_n), dim3(256), 0, stream, m, (int)tiles_n);
+    return hipGetLastError();
+  }
+  if (m.group == 32) return launch_matvec<GROUP_32>(m, stream);
+  if (m.group == 64) return launch_matvec<GROUP_64>(m, stream);
+  return launch_matvec<GROUP_128>(m, stream);
 }
 
 }  // namespace q2dev

@@ -87,6 +87,48 @@ def test_wide(n, group, k, zero, m):
     check(y[:, torch.from_numpy(cols).to(DEV)], O.bf16_to_f64(xb) @ w.T)
 
 
+@pytest.mark.parametrize("m", [1, 4, 9, 20, 64])
+@pytest.mark.parametrize("zero", ZEROS)
+@pytest.mark.parametrize("group,k", [(32, 8224), (64, 20480), (128, 16512), (256, 9984)])
+def test_long_inputs_of_few_columns(m, zero, group, k):
+    """Few strips of many units, x in parts, gated and plain."""
+    dev, w = weights(410, 18, k, group, zero)
+    xb, x = acts(410, m, k)
+    z = O.bf16_to_f64(xb) @ w.T
+    check(q2.q4_matvec(x, *dev), z)
+    check(q2.q4_matvec(x, *dev, gated=True), z, gated=True)
+
+
+def test_largest_k():
+    k, n = 1 << 24, 3
+    g = np.random.default_rng(411)
+    packed = g.integers(0, 256, (n, k // 2)).astype(np.uint8)
+    scale = (g.random((n, k // 32)) * 0.02).astype(np.float16)
+    dev = [torch.from_numpy(t).to(DEV) for t in (packed, scale)]
+    xb, x = acts(411, 2, k)
+    xd = O.bf16_to_f64(xb)
+    for m in (1, 2, 64):
+        y = q2.q4_matvec(x[:1] if m == 1 else x if m == 2 else x.repeat(32, 1), *dev)
+        for i in range(n):
+            w = T.nibbles(packed[i:i + 1], k)[0].astype(np.float64) - 8
+            w *= np.repeat(scale[i].astype(np.float64), 32)
+            for r in range(min(m, 2)):
+                assert abs(y[r, i].item() - xd[r] @ w) <= 1e-3 * np.sqrt((xd[r] ** 2) @ (w * w))
+            if m == 64:
+                assert torch.equal(y[2:, i], y[:2, i].repeat(31))
+
+
+def test_rows_beyond_the_grid():
+    """More blocks of rows than a grid's second dimension takes."""
+    m, k = 65535 * 64 + 70, 256
+    dev, w = weights(412, 2, k, 64, "codes")
+    xb, x = acts(412, 50, k)
+    y = q2.q4_matvec(x.repeat(m // 50 + 1, 1)[:m].contiguous(), *dev)
+    check(y[:50], O.bf16_to_f64(xb) @ w.T)
+    whole = y[:m // 50 * 50].view(-1, 50, 2)
+    assert (whole == whole[0]).all() and torch.equal(y[m // 50 * 50:], y[:m % 50])
+
+
 @pytest.mark.parametrize("m", [1, 5, 33])
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("gated", [False, True])
