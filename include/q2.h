@@ -512,13 +512,21 @@ typedef struct q2_sampling {
  *             above draws the last token that is left                      (in)
  *   token     i32 [B]; -1 for a row whose tokens are all masked            (out)
  *   prob      f32 [B]: the token's p over the sum of what is left; 0 with -1  (out)
+ *   workspace device scratch of >= q2_sample_workspace_bytes(B, V) bytes, 256-byte
+ *             aligned (may be NULL when that is 0); overwritten
  * Sums are in units of 2^-S of the best token's p, S = 62 - ceil(log2 V) and at most
  * 51, each p rounded once: exact, the same in any order, run-to-run deterministic.  A p
  * below half a unit counts as 0.  1 <= V <= 2^24, B <= 2^30 (Q2_ERR_SHAPE
- * otherwise).  Asynchronous.
+ * otherwise).  Asynchronous; calls that share a workspace must be ordered on one
+ * stream.
  */
 int q2_sample(const void* logits, int64_t B, int64_t V, int64_t ld, uint32_t flags, const q2_sampling* settings,
-              const float* u, int32_t* token, float* prob, hipStream_t stream);
+              const float* u, int32_t* token, float* prob, void* workspace, size_t workspace_bytes,
+              hipStream_t stream);
+
+/* q2_sample_workspace_bytes - device bytes q2_sample needs; 0 for sizes that it
+ * refuses or that need none. */
+size_t q2_sample_workspace_bytes(int64_t B, int64_t V);
 
 /*
  * q2_dequant - test export: w[n, k] = (q - 1) * d as float32 [N, K], exact;

@@ -35,7 +35,7 @@ EXPORTS = ("q2_pack", "q2_import_gemlite", "q2_linear", "q2_lowrank_workspace_by
            "q2_a8_workspace_bytes", "q2_linear_a8",
            "q2_linear_fused", "q2_linear_fused_workspace_bytes", "q4_linear_fused",
            "q2_linear_grouped", "q2_linear_grouped_workspace_bytes", "q4_linear_grouped",
-           "q2_route", "q2_route_workspace_bytes", "q2_combine", "q4_matvec", "q2_sample",
+           "q2_route", "q2_route_workspace_bytes", "q2_combine", "q4_matvec", "q2_sample", "q2_sample_workspace_bytes",
            "q4_linear", "q2_dequant", "q2_set_dispatch", "q2_strerror", "q2_last_error")
 
 # q2_epilogue: activations by name, and flags
@@ -101,7 +101,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "q2_route_workspace_bytes": ([i64, i64, i64], sz),
         "q2_combine": ([p, i64, p, p, p, p, i64, i64, i64, ctypes.c_uint32, p], ctypes.c_int),
         "q4_matvec": ([p, p, p, p, i64, ctypes.c_uint32, p, p, i64, i64, i64, p], ctypes.c_int),
-        "q2_sample": ([p, i64, i64, i64, ctypes.c_uint32, p, p, p, p, p], ctypes.c_int),
+        "q2_sample": ([p, i64, i64, i64, ctypes.c_uint32, p, p, p, p, p, sz, p], ctypes.c_int),
+        "q2_sample_workspace_bytes": ([i64, i64], sz),
         "q4_linear": ([p, p, p, p, p, i64, i64, i64, p], ctypes.c_int),
         "q2_dequant": ([p, p, p, i64, i64, p], ctypes.c_int),
         "q2_set_dispatch": ([ctypes.c_char_p, ctypes.c_char_p, ctypes.c_int], ctypes.c_int),
@@ -597,6 +598,11 @@ def q4_matvec(x, packed4, scale, zero=None, bias=None, activation="none", gated=
     return y
 
 
+def sample_workspace_bytes(b: int, v: int) -> int:
+    """Workspace bytes of q2_sample for b rows of v logits."""
+    return int(load().q2_sample_workspace_bytes(b, v))
+
+
 class Sample(NamedTuple):
     """q2_sample's draw."""
     token: torch.Tensor       # i32 [B], -1 for a row whose tokens are all masked
@@ -611,7 +617,8 @@ def _setting(value, dtype, shape, name, dev):
     return value, None
 
 
-def q2_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, token=None, prob=None) -> Sample:
+def q2_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, token=None, prob=None,
+              workspace=None) -> Sample:
     """One token of each row of logits [B, V] (f32 or bf16; rows may lie apart, as in a slice) from the random numbers
     u f32 [B] in [0, 1): the first token in descending order of its logit (equal logits: the lower token first; -inf
     and NaN are masked tokens) whose cumulative probability exceeds u.
@@ -645,9 +652,10 @@ def q2_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, token=N
     else:
         _have(prob, torch.float32, (b,), "prob", dev)
     settings = Sampling(t, k, p, m, tp, kp, pp, mp)
+    ws, ws_bytes = _scratch(lib.q2_sample_workspace_bytes(b, v), workspace, dev)
     _check(lib.q2_sample(_ptr(logits), b, v, logits.stride(0) if b > 1 else v,
                          Q2_SAMPLE_LOGITS_BF16 if logits.dtype == torch.bfloat16 else 0, ctypes.addressof(settings),
-                         _ptr(u), _ptr(token), _ptr(prob), _stream()))
+                         _ptr(u), _ptr(token), _ptr(prob), _ptr(ws), ws_bytes, _stream()))
     return Sample(token, prob)
 
 

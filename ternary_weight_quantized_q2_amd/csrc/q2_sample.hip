@@ -3,9 +3,10 @@
 //
 // Order: logits descending, equal ones by lower token; p_i = exp((l_i - best) / T).
 // Every filter leaves the first tokens of that order, and the draw is the first token
-// whose cumulative p exceeds u times the sum, so nothing is sorted: each of the three
-// borders is the place where a cumulative count or sum reaches a target, found by a
-// histogram over the logits' distance from the best one.
+// whose cumulative p exceeds u times the sum, so nothing is sorted as a whole: each of
+// the three borders is the place where a cumulative count or sum reaches a target.  A
+// histogram over the logits' distance from the best one says in which of 4096 parts it
+// lies, and only the tokens of those parts are gathered and sorted.
 //
 // A token's p is held as a whole number of 2^-S, S = 62 - ceil(log2 V) (at most 51),
 // rounded once from 64-bit floating point.  Sums of whole numbers do not depend on
@@ -14,12 +15,15 @@
 // a per cent of a token's width.  A p below half a unit, 2^-46 at V = 2^17, is never drawn.
 #include "q2_token.h"
 #include <algorithm>
+#include <cstddef>
 
 namespace q2dev {
 
 constexpr int SM_THREADS = 1024, SM_WAVES = SM_THREADS / 64;
-constexpr int SM_BUCKETS = 2048, SM_PER = SM_BUCKETS / SM_THREADS;
-constexpr int SM_LIST = 256;                             // elements of a bucket that are compared with each other
+constexpr int SM_BUCKETS = 4096, SM_PER = SM_BUCKETS / SM_THREADS;
+constexpr int SM_LIST = 2048;                            // tokens that are sorted
+constexpr int SM_PARTS = 64;                             // of a row, at most
+constexpr int SM_FEW = 256;                              // tokens that are compared with each other
 
 __device__ __forceinline__ uint32_t logit_key(float v) { // order-preserving, 0 for a masked token
   const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f);              // -0 counts as +0
@@ -29,82 +33,135 @@ __device__ __forceinline__ float key_logit(uint32_t o) {
   return __builtin_bit_cast(float, o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-// f(logit, token) for the row's tokens, 16 bytes at a time between the first and the
-// last aligned address.
-template <class F>
-__device__ __forceinline__ void each_logit(const void* row, int bf16, int V, F f) {
-  const int size = bf16 ? 2 : 4, per = 16 / size;
+// f(logit, token) for tokens t0 .. t1 - 1 of a row, 16 bytes at a time between the first
+// and the last aligned address, four loads of a thread ahead.  ONCE: f's code appears
+// once (a launch starts with cold instruction caches, about a microsecond per KB).
+template <bool ONCE, class F>
+__device__ __forceinline__ void each_logit(const void* whole, int bf16, int t0, int t1, F f) {
+  const int size = bf16 ? 2 : 4, per = 16 / size, V = t1 - t0;
+  const uint8_t* const row = static_cast<const uint8_t*>(whole) + (int64_t)t0 * size;
   const int head = min(V, (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / size);
-  const int body = (V - head) / per;
-  auto one = [&](int i) {
-    f(bf16 ? bf16_to_f32(static_cast<const uint16_t*>(row)[i]) : static_cast<const float*>(row)[i], i);
+  const int body = (V - head) / per, rest = V - body * per;              // up to per - 1 tokens in front and behind
+  const q2_u32x4* const p = reinterpret_cast<const q2_u32x4*>(row + head * size);
+  constexpr int AHEAD = 4;
+  q2_u32x4 v[AHEAD], next[AHEAD];
+  auto load = [&](int i) {
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) next[k] = p[min(i + k * SM_THREADS, body - 1)];
   };
-  if ((int)threadIdx.x < head) one(threadIdx.x);
-  const q2_u32x4* p = reinterpret_cast<const q2_u32x4*>(static_cast<const uint8_t*>(row) + head * size);
-  for (int i = threadIdx.x; i < body; i += SM_THREADS) {
-    const q2_u32x4 v = p[i];
-    const int at = head + i * per;
-    if (bf16) {
+  if (body > 0) load(threadIdx.x);
+  const int steps = (body + AHEAD * SM_THREADS - 1) / (AHEAD * SM_THREADS);
+#pragma unroll 1
+  for (int step = 0; step <= steps; ++step) {            // the last one: the rest, a token per thread
+    const bool last = step == steps;
+    const int i = step * AHEAD * SM_THREADS + threadIdx.x;
 #pragma unroll
-      for (int d = 0; d < 8; ++d)
-        f(__builtin_bit_cast(float, (d & 1) ? v[d >> 1] & 0xFFFF0000u : v[d >> 1] << 16), at + d);
-    } else {
+    for (int k = 0; k < AHEAD; ++k) v[k] = next[k];
+    if (!last) load(i + AHEAD * SM_THREADS);             // past the end: the last piece again
+    const int one = (int)threadIdx.x < head ? (int)threadIdx.x : body * per + (int)threadIdx.x;
+    if (last) {
+      if ((int)threadIdx.x >= rest) break;
+      v[0][0] = bf16 ? (uint32_t)reinterpret_cast<const uint16_t*>(row)[one] : reinterpret_cast<const uint32_t*>(row)[one];
+    }
+#pragma unroll 1
+    for (int k = 0; k < (last ? 1 : AHEAD); ++k) {
+      const int piece = i + k * SM_THREADS;
+      if (!last && piece >= body) break;
+      const int at = t0 + (last ? one : head + piece * per);
+      if constexpr (ONCE) {
+        const int n = last ? 1 : per;
+#pragma unroll 1
+        for (int d = 0; d < n; ++d) {
+          const uint32_t w = v[0][0];
+          f(__builtin_bit_cast(float, bf16 ? w << 16 : w), at + d);
+          if (bf16 && !(d & 1)) v[0][0] = w >> 16;
+          else v[0][0] = v[0][1], v[0][1] = v[0][2], v[0][2] = v[0][3];
+        }
+      } else if (last) {
+        const uint32_t w = v[0][0];
+        f(__builtin_bit_cast(float, bf16 ? w << 16 : w), at);
+      } else {
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const uint32_t b = v[d];                         // a bit cast of the vector's element itself reads element 0
-        f(__builtin_bit_cast(float, b), at + d);
+        for (int d = 0; d < 4; ++d) {
+          const uint32_t w = v[0][d];                    // a bit cast of the vector's element itself reads element 0
+          if (bf16) {
+            f(__builtin_bit_cast(float, w << 16), at + 2 * d);
+            f(__builtin_bit_cast(float, w & 0xFFFF0000u), at + 2 * d + 1);
+          } else {
+            f(__builtin_bit_cast(float, w), at + d);
+          }
+        }
       }
+#pragma unroll
+      for (int q = 1; q < AHEAD; ++q) v[q - 1] = v[q];
     }
   }
-  const int tail = head + body * per + threadIdx.x;
-  if (tail < V) one(tail);
 }
 
+// A kernel that needs only the beginning of it allocates that.
 struct SampleShared {
-  uint64_t sum[2][SM_BUCKETS];                           // [0] over all tokens, [1] over a range of one bucket
-  uint32_t count[2][SM_BUCKETS];
   uint64_t wsum[SM_WAVES];
   uint32_t wcount[SM_WAVES];
-  uint64_t best, base_s, list_w[SM_LIST];
-  uint32_t list[SM_LIST];
-  uint32_t base_n, bucket, n, fill, lo, hi, key;
+  float wbest[SM_WAVES];
+  uint64_t base_s, total;
+  uint32_t base_n, bucket, n, fill, lo, hi, key, unused;
+  uint64_t sum[SM_BUCKETS];                              // over all tokens
+  uint32_t count[SM_BUCKETS];
+  uint64_t list[SM_LIST];
+  uint64_t sum2[SM_BUCKETS];                             // over a range of one bucket, or of the list
+  uint32_t count2[SM_BUCKETS];
+  uint64_t start[SM_BUCKETS];
 };
 
 // What a row's tokens are measured by.
 struct Measure {
-  float best;
-  uint32_t best_key;
-  double inv_t, unit, min_p;                             // 1 / T, 2^S
-  float per_logit;                                       // buckets per unit of the logit
+  float best, cut;                                       // no token further than cut from the best has a weight
+  double scale, unit, min_p, per_octave;                 // log2(e) / T, 2^S, buckets per halving of p
 
-  __device__ __forceinline__ double p(uint32_t key) const {
-    if (key == best_key) return 1.0;
-    const double d = ((double)best - (double)key_logit(key)) * inv_t;
-    return d >= 0.0 ? exp(-d) : 0.0;                     // inf * 0 is NaN: no probability
+  // log2 of 1 / p.  NaN (of infinity times zero) has no probability.
+  __device__ __forceinline__ double octaves(float v) const {
+    return v == best ? 0.0 : ((double)best - (double)v) * scale;
   }
-  // Whole number of units; 0 for a token that is masked, below min-p or too unlikely.
-  __device__ __forceinline__ uint64_t weight(uint32_t key) const {
-    if (key == 0) return 0;
-    const double q = p(key);
+  // 2^-y: the power series of 2^r, |r| <= 1/2, to r^11 (off by 7e-15 at most).
+  __device__ __forceinline__ static double p_of(double y) {
+    if (!(y < 1000.0)) return 0.0;
+    const double n = __builtin_rint(y), r = (n - y) * 0.69314718055994530942;
+    double q = 1.0 / 39916800;
+    q = __builtin_fma(q, r, 1.0 / 3628800);
+    q = __builtin_fma(q, r, 1.0 / 362880);
+    q = __builtin_fma(q, r, 1.0 / 40320);
+    q = __builtin_fma(q, r, 1.0 / 5040);
+    q = __builtin_fma(q, r, 1.0 / 720);
+    q = __builtin_fma(q, r, 1.0 / 120);
+    q = __builtin_fma(q, r, 1.0 / 24);
+    q = __builtin_fma(q, r, 1.0 / 6);
+    q = __builtin_fma(q, r, 0.5);
+    q = __builtin_fma(q, r, 1.0);
+    q = __builtin_fma(q, r, 1.0);
+    return __builtin_ldexp(q, -(int)n);
+  }
+  // Whole number of units; 0 for a token that is below min-p or too unlikely.
+  __device__ __forceinline__ uint64_t weight(double y) const {
+    const double q = p_of(y);
     if (!(q >= min_p)) return 0;
     return __builtin_bit_cast(uint64_t, q * unit + 0x1p52) - __builtin_bit_cast(uint64_t, 0x1p52);
   }
-  // Does not fall as the logit falls: subtraction and product round monotonically.
-  __device__ __forceinline__ int bucket(uint32_t key) const {
-    if (key == best_key) return 0;
-    const float t = (best - key_logit(key)) * per_logit;
-    return t < (float)(SM_BUCKETS - 1) ? (int)t : SM_BUCKETS - 1;
+  // Does not fall as the logit falls: the difference and the products round monotonically.
+  __device__ __forceinline__ int bucket(double y) const {
+    const double t = y * per_octave;
+    return t < SM_BUCKETS - 1 ? (int)t : SM_BUCKETS - 1;
   }
+  __device__ __forceinline__ bool near(float v) const { return !(best - v > cut) && v > -__builtin_inff(); }
 };
 
-// Exclusive sums over the buckets before this thread's (SM_PER each), and the totals.
-__device__ __forceinline__ void scan_buckets(SampleShared& s, int h, uint64_t& before_s, uint32_t& before_n,
-                                             uint64_t& total_s, uint32_t& total_n) {
+// Sums before this thread's SM_PER buckets, and the totals.
+__device__ __forceinline__ void scan_buckets(SampleShared& s, const uint64_t* sum, const uint32_t* count, uint64_t& before_s,
+                                             uint32_t& before_n, uint64_t& total_s, uint32_t& total_n) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   uint64_t vs = 0;
   uint32_t vn = 0;
 #pragma unroll
-  for (int i = 0; i < SM_PER; ++i) vs += s.sum[h][SM_PER * threadIdx.x + i], vn += s.count[h][SM_PER * threadIdx.x + i];
+  for (int i = 0; i < SM_PER; ++i) vs += sum[SM_PER * threadIdx.x + i], vn += count[SM_PER * threadIdx.x + i];
   uint64_t is = vs;
   uint32_t in = vn;
 #pragma unroll
@@ -120,6 +177,7 @@ __device__ __forceinline__ void scan_buckets(SampleShared& s, int h, uint64_t& b
   before_n = in - vn;
   total_s = 0;
   total_n = 0;
+#pragma unroll
   for (int w = 0; w < SM_WAVES; ++w) {
     if (w < wv) before_s += s.wsum[w], before_n += s.wcount[w];
     total_s += s.wsum[w];
@@ -129,30 +187,35 @@ __device__ __forceinline__ void scan_buckets(SampleShared& s, int h, uint64_t& b
 
 // The first place of the order where the cumulative count (by_count) or weight reaches
 // target, which lies between 1 and the total: the logit's key, what lies before tokens
-// of that logit, and how many of these it takes.
+// of that logit, and how many of these it takes.  For parts of the histogram with more
+// tokens than the list holds: one pass over the row per step, each with a histogram of
+// its own over the range of keys that is left.
 struct Place {
   uint32_t key, before_n, ties;
   uint64_t before_s, w;
 };
 
-__device__ Place locate(SampleShared& s, const Measure& me, const void* row, int bf16, int V, bool by_count,
-                        uint64_t target) {
+__device__ __noinline__ Place locate(SampleShared& s, const Measure& me, const void* row, int bf16, int V, bool by_count,
+                                     uint64_t target) {
   Place p;
   uint32_t lo = 1, hi = 0xFFFFFFFFu;                     // keys of the range
   int bucket = -1;
   uint64_t base_s = 0;
   uint32_t base_n = 0;
+  uint64_t* const list_w = s.list + SM_FEW;
   for (int h = 0;; h = 1) {
     uint64_t bs, ts;
     uint32_t bn, tn;
-    scan_buckets(s, h, bs, bn, ts, tn);
+    const uint64_t* const sum = h ? s.sum2 : s.sum;
+    const uint32_t* const count = h ? s.count2 : s.count;
+    scan_buckets(s, sum, count, bs, bn, ts, tn);
     bs += base_s;
     bn += base_n;
 #pragma unroll
     for (int i = 0; i < SM_PER; ++i) {
       const int b = SM_PER * threadIdx.x + i;
-      const uint64_t vs = s.sum[h][b];
-      const uint32_t vn = s.count[h][b];
+      const uint64_t vs = sum[b];
+      const uint32_t vn = count[b];
       const uint64_t from = by_count ? bn : bs, to = by_count ? bn + vn : bs + vs;
       if (from < target && target <= to) {
         s.bucket = b;
@@ -177,31 +240,37 @@ __device__ Place locate(SampleShared& s, const Measure& me, const void* row, int
       lo = (uint32_t)std::max<int64_t>((int64_t)lo, (int64_t)(top - per + 1));
       hi = (uint32_t)top;
     }
-    auto mine = [&](uint32_t key) { return key >= lo && key <= hi && me.bucket(key) == bucket; };
-    if (n <= SM_LIST) {
-      each_logit(row, bf16, V, [&](float v, int) {
+    // tokens of the range that have a weight, with their keys
+    auto each = [&](auto f) {
+      each_logit<true>(row, bf16, 0, V, [&](float v, int) {
+        if (!me.near(v)) return;
         const uint32_t key = logit_key(v);
-        if (key == 0 || !mine(key)) return;
-        const uint64_t w = me.weight(key);
-        if (w == 0) return;
+        const double y = me.octaves(v);
+        if (key < lo || key > hi || me.bucket(y) != bucket) return;
+        const uint64_t w = me.weight(y);
+        if (w != 0) f(key, w);
+      });
+    };
+    if (n <= SM_FEW) {
+      each([&](uint32_t key, uint64_t w) {
         const uint32_t at = atomicAdd(&s.fill, 1u);
         s.list[at] = key;
-        s.list_w[at] = w;
+        list_w[at] = w;
       });
       __syncthreads();
       if (threadIdx.x < n) {
-        const uint32_t key = s.list[threadIdx.x];
+        const uint64_t key = s.list[threadIdx.x];
         uint64_t gs = base_s;
         uint32_t gn = base_n, eq = 0;
         for (uint32_t j = 0; j < n; ++j) {
-          const uint32_t k = s.list[j];
-          if (k > key) gs += s.list_w[j], ++gn;
+          const uint64_t k = s.list[j];
+          if (k > key) gs += list_w[j], ++gn;
           eq += k == key;
         }
-        const uint64_t w = s.list_w[threadIdx.x];
+        const uint64_t w = list_w[threadIdx.x];
         const uint64_t from = by_count ? gn : gs, step = by_count ? 1 : w;
         if (from < target && target <= from + eq * step) {               // the same from every token of that logit
-          s.key = key;
+          s.key = (uint32_t)key;
           s.base_s = gs;
           s.base_n = gn;
         }
@@ -214,35 +283,28 @@ __device__ Place locate(SampleShared& s, const Measure& me, const void* row, int
       p.key = lo;
       break;
     }
-    // too many: the range of their keys, in a histogram of its own
     __syncthreads();
     if (threadIdx.x == 0) s.lo = 0xFFFFFFFFu, s.hi = 0;
-    for (int i = threadIdx.x; i < SM_BUCKETS; i += SM_THREADS) s.sum[1][i] = 0, s.count[1][i] = 0;
+    for (int i = threadIdx.x; i < SM_BUCKETS; i += SM_THREADS) s.sum2[i] = 0, s.count2[i] = 0;
     __syncthreads();
     uint32_t klo = 0xFFFFFFFFu, khi = 0;
-    each_logit(row, bf16, V, [&](float v, int) {
-      const uint32_t key = logit_key(v);
-      if (key != 0 && mine(key) && me.weight(key) != 0) klo = min(klo, key), khi = max(khi, key);
-    });
+    each([&](uint32_t key, uint64_t) { klo = min(klo, key), khi = max(khi, key); });
 #pragma unroll
     for (int d = 32; d; d >>= 1) klo = min(klo, __shfl_xor(klo, d)), khi = max(khi, __shfl_xor(khi, d));
     if ((threadIdx.x & 63) == 0) atomicMin(&s.lo, klo), atomicMax(&s.hi, khi);
     __syncthreads();
-    lo = s.lo;
-    hi = s.hi;
-    const uint64_t per = ((uint64_t)hi - lo + SM_BUCKETS) / SM_BUCKETS;
-    each_logit(row, bf16, V, [&](float v, int) {
-      const uint32_t key = logit_key(v);
-      if (key == 0 || !mine(key)) return;
-      const uint64_t w = me.weight(key);
-      if (w == 0) return;
-      const int i = (int)((hi - key) / per);
-      atomicAdd(reinterpret_cast<unsigned long long*>(&s.sum[1][i]), (unsigned long long)w);
-      atomicAdd(&s.count[1][i], 1u);
+    const uint32_t new_lo = s.lo, new_hi = s.hi;
+    const uint64_t per = ((uint64_t)new_hi - new_lo + SM_BUCKETS) / SM_BUCKETS;
+    each([&](uint32_t key, uint64_t w) {
+      const int i = (int)((new_hi - key) / per);
+      atomicAdd(reinterpret_cast<unsigned long long*>(&s.sum2[i]), (unsigned long long)w);
+      atomicAdd(&s.count2[i], 1u);
     });
+    lo = new_lo;
+    hi = new_hi;
     __syncthreads();
   }
-  p.w = me.weight(p.key);
+  p.w = me.weight(me.octaves(key_logit(p.key)));
   p.before_s = s.base_s;
   p.before_n = s.base_n;
   p.ties = (uint32_t)(by_count ? target - p.before_n : (target - p.before_s + p.w - 1) / p.w);
@@ -250,84 +312,39 @@ __device__ Place locate(SampleShared& s, const Measure& me, const void* row, int
   return p;
 }
 
-// A workgroup per row.
-__global__ __launch_bounds__(SM_THREADS) void sample_kernel(SampleArgs a, int shift) {
-  __shared__ SampleShared s;
-  const int64_t r = blockIdx.x + (int64_t)blockIdx.y * GRID_X;
-  if (r >= a.B) return;
-  const int V = (int)a.V, lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const void* row = static_cast<const uint8_t*>(a.logits) + r * a.ld * (a.bf16 ? 2 : 4);
-  const float temperature = a.temperature ? a.temperature[r] : a.temperature_all;
-  const int32_t top_k = a.top_k ? a.top_k[r] : a.top_k_all;
-  const float top_p = a.top_p ? a.top_p[r] : a.top_p_all;
-  const float min_p = a.min_p ? a.min_p[r] : a.min_p_all;
+// ceil(part * whole) as a target: 1 .. whole.
+__device__ __forceinline__ uint64_t part_of(float part, uint64_t whole) {
+  const double x = (double)part * (double)whole;
+  uint64_t t = (uint64_t)x;
+  t += (double)t < x;
+  return std::min(std::max<uint64_t>(t, 1), whole);
+}
+// The cumulative weight that the draw reaches first: more than u of the total.
+__device__ __forceinline__ uint64_t draw_target(float u, uint64_t total) {
+  const uint64_t t = u > 0.f ? (uint64_t)std::min((double)u * (double)total, (double)total) : 0;
+  return std::min(t, total - 1) + 1;
+}
 
-  uint64_t best = 0;
-  each_logit(row, a.bf16, V, [&](float v, int i) {
-    const uint32_t key = logit_key(v);
-    const uint64_t both = (uint64_t)key << 32 | (uint32_t)~i;
-    if (key != 0 && both > best) best = both;
-  });
-#pragma unroll
-  for (int d = 32; d; d >>= 1) {
-    const uint64_t o = __shfl_xor(best, d);
-    best = o > best ? o : best;
-  }
-  if (lane == 0) s.wsum[wv] = best;
-  for (int i = threadIdx.x; i < SM_BUCKETS; i += SM_THREADS) s.sum[0][i] = 0, s.count[0][i] = 0;
-  __syncthreads();
-  for (int w = 0; w < SM_WAVES; ++w) best = s.wsum[w] > best ? s.wsum[w] : best;
-  // nothing to draw from, or one token left
-  if (best == 0 || !(temperature > 0.f) || top_k == 1 || top_p <= 0.f || min_p > 1.f) {
-    if (threadIdx.x == 0) {
-      a.token[r] = best == 0 ? -1 : (int32_t)~(uint32_t)best;
-      a.prob[r] = best == 0 ? 0.f : 1.f;
-    }
-    return;
-  }
-  Measure me;
-  me.best_key = (uint32_t)(best >> 32);
-  me.best = key_logit(me.best_key);
-  me.inv_t = 1.0 / (double)temperature;
-  me.unit = __builtin_bit_cast(double, (uint64_t)(1023 + shift) << 52);
-  me.min_p = min_p > 0.f ? (double)min_p : 0.0;
-  me.per_logit = (float)(SM_BUCKETS / ((shift + 1) * 0.6931471805599453) * me.inv_t);
-
-  each_logit(row, a.bf16, V, [&](float v, int) {
-    const uint32_t key = logit_key(v);
-    const uint64_t w = me.weight(key);
-    if (w == 0) return;
-    const int b = me.bucket(key);
-    atomicAdd(reinterpret_cast<unsigned long long*>(&s.sum[0][b]), (unsigned long long)w);
-    atomicAdd(&s.count[0][b], 1u);
-  });
-  __syncthreads();
-  uint64_t bs, total;
-  uint32_t bn, count;
-  scan_buckets(s, 0, bs, bn, total, count);
+// The row's borders by passes over it, whatever the histogram's parts hold.
+__device__ __noinline__ void sample_slow(SampleShared& s, const Measure& me, const void* row, int bf16, int V, int top_k,
+                                         float top_p, float u, uint64_t total, uint32_t count, int32_t* token, float* prob) {
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   if (top_k > 0 && (uint32_t)top_k < count) {
-    const Place p = locate(s, me, row, a.bf16, V, true, (uint64_t)top_k);
+    const Place p = locate(s, me, row, bf16, V, true, (uint64_t)top_k);
     total = p.before_s + p.ties * p.w;
   }
   if (top_p < 1.f) {
-    const double x = (double)top_p * (double)total;
-    uint64_t target = (uint64_t)x;
-    target += (double)target < x;
-    target = std::min(std::max<uint64_t>(target, 1), total);
-    const Place p = locate(s, me, row, a.bf16, V, false, target);
+    const Place p = locate(s, me, row, bf16, V, false, part_of(top_p, total));
     total = p.before_s + p.ties * p.w;
   }
-  const float u = a.u[r];
-  const uint64_t target = u > 0.f ? (uint64_t)std::min((double)u * (double)total, (double)total) : 0;
-  const Place p = locate(s, me, row, a.bf16, V, false, std::min(target, total - 1) + 1);
-
+  const Place p = locate(s, me, row, bf16, V, false, draw_target(u, total));
   // the token: the ties-th one that has the logit
   const int per = (V + SM_THREADS - 1) / SM_THREADS, lo = min(V, (int)threadIdx.x * per), hi = min(V, lo + per);
-  auto logit = [&](int i) {
-    return logit_key(a.bf16 ? bf16_to_f32(static_cast<const uint16_t*>(row)[i]) : static_cast<const float*>(row)[i]);
+  auto key = [&](int i) {
+    return logit_key(bf16 ? bf16_to_f32(static_cast<const uint16_t*>(row)[i]) : static_cast<const float*>(row)[i]);
   };
   uint32_t n = 0;
-  for (int i = lo; i < hi; ++i) n += logit(i) == p.key;
+  for (int i = lo; i < hi; ++i) n += key(i) == p.key;
   uint32_t in = n;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -341,16 +358,431 @@ __global__ __launch_bounds__(SM_THREADS) void sample_kernel(SampleArgs a, int sh
     uint32_t left = p.ties - (in - n);
     int i = lo;
     for (; i < hi; ++i)
-      if (logit(i) == p.key && --left == 0) break;
-    a.token[r] = i;
-    a.prob[r] = (float)(me.p(p.key) * me.unit / (double)total);
+      if (key(i) == p.key && --left == 0) break;
+    *token = i;
+    *prob = (float)(me.p_of(me.octaves(key_logit(p.key))) * me.unit / (double)total);
   }
 }
 
-hipError_t launch_sample(const SampleArgs& a, hipStream_t stream) {
+// ---- a row's steps -----------------------------------------------------------------
+struct Settings {
+  float temperature, top_p, min_p, u;
+  int32_t top_k;
+  __device__ __forceinline__ bool greedy() const { // the first token of the order, whatever its p
+    return !(temperature > 0.f) || top_k == 1 || top_p <= 0.f || min_p > 1.f;
+  }
+};
+__device__ __forceinline__ Settings settings_of(const SampleArgs& a, int64_t r) {
+  return Settings{a.temperature ? a.temperature[r] : a.temperature_all, a.top_p ? a.top_p[r] : a.top_p_all,
+                  a.min_p ? a.min_p[r] : a.min_p_all, a.u[r], a.top_k ? a.top_k[r] : a.top_k_all};
+}
+__device__ __forceinline__ Measure measure_of(const Settings& c, float best, int shift) {
+  Measure me;
+  me.best = best;
+  me.scale = 1.4426950408889634 / (double)c.temperature;
+  me.unit = __builtin_bit_cast(double, (uint64_t)(1023 + shift) << 52);
+  me.min_p = c.min_p > 0.f ? (double)c.min_p : 0.0;
+  me.per_octave = (double)SM_BUCKETS / (shift + 1);
+  // Half a unit is 2^-(S + 1); min-p cuts nearer.  A little further out: the exact tests come behind it.
+  double reach = shift + 1.01;
+  if (c.min_p > 0.f) reach = std::min(reach, 0.01 - (double)log2f(c.min_p));
+  me.cut = (float)(reach / me.scale * 1.000001);
+  return me;
+}
+
+// The largest of the range's logits, in all threads.
+__device__ __forceinline__ float best_of(SampleShared& s, const void* row, int bf16, int t0, int t1) {
+  float best = -__builtin_inff();
+  each_logit<false>(row, bf16, t0, t1, [&](float v, int) { best = fmaxf(best, v); });         // a NaN is dropped
+#pragma unroll
+  for (int d = 32; d; d >>= 1) best = fmaxf(best, __shfl_xor(best, d));
+  if ((threadIdx.x & 63) == 0) s.wbest[threadIdx.x >> 6] = best;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < SM_WAVES; ++w) best = fmaxf(best, s.wbest[w]);
+  return best;
+}
+// The range's first token that has the largest logit, ~0 without one, by wave.
+__device__ __forceinline__ uint32_t first_of(const void* row, int bf16, int t0, int t1, float best) {
+  uint32_t at = 0xFFFFFFFFu;
+  each_logit<false>(row, bf16, t0, t1, [&](float v, int i) {
+    if (v == best) at = min(at, (uint32_t)i);
+  });
+#pragma unroll
+  for (int d = 32; d; d >>= 1) at = min(at, __shfl_xor(at, d));
+  return at;
+}
+// The range's tokens into the histogram in s.
+__device__ __forceinline__ void fill_histogram(SampleShared& s, const Measure& me, const void* row, int bf16, int t0, int t1) {
+  each_logit<true>(row, bf16, t0, t1, [&](float v, int) {
+    if (!me.near(v)) return;
+    const double y = me.octaves(v);
+    const uint64_t w = me.weight(y);
+    if (w == 0) return;
+    const int b = me.bucket(y);
+    atomicAdd(reinterpret_cast<unsigned long long*>(&s.sum[b]), (unsigned long long)w);
+    atomicAdd(&s.count[b], 1u);
+  });
+}
+
+// The parts of the histogram where the borders lie.  Until the tokens of top-k's part
+// are looked at, the sum of what it leaves is known to within that part, and so on: a
+// range of parts for each border.
+struct Borders {
+  bool by_k, by_p;
+  int k_part, p_lo, p_hi, d_lo, d_hi;
+  uint64_t total, before_s;                              // the sum of all; before this thread's buckets
+  uint32_t count, before_n;
+  uint32_t chosen_count;                                 // tokens in the parts
+
+  __device__ __forceinline__ bool chosen(int b) const {
+    return b == k_part || (b >= p_lo && b <= p_hi) || (b >= d_lo && b <= d_hi);
+  }
+};
+__device__ __forceinline__ Borders borders_of(SampleShared& s, const Settings& c, const uint64_t* sum, const uint32_t* count) {
+  Borders o;
+  scan_buckets(s, sum, count, o.before_s, o.before_n, o.total, o.count);
+  o.by_k = c.top_k > 0 && (uint32_t)c.top_k < o.count;
+  o.by_p = c.top_p < 1.f;
+  auto find = [&](bool by_count, uint64_t target) {      // the part that reaches it, what lies before, its own sum
+    uint64_t bs = o.before_s;
+    uint32_t bn = o.before_n;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < SM_PER; ++i) {
+      const int b = SM_PER * threadIdx.x + i;
+      const uint64_t vs = sum[b];
+      const uint32_t vn = count[b];
+      const uint64_t from = by_count ? bn : bs, to = by_count ? bn + vn : bs + vs;
+      if (from < target && target <= to) s.bucket = b, s.base_s = bs, s.total = vs;
+      bs += vs;
+      bn += vn;
+    }
+    __syncthreads();
+    return (int)s.bucket;
+  };
+  o.k_part = -1, o.p_lo = 0, o.p_hi = -1;
+  uint64_t least = o.total, most = o.total;              // bounds of the sum of what is left
+  if (o.by_k) {
+    o.k_part = find(true, (uint64_t)c.top_k);
+    least = s.base_s + 1;
+    most = s.base_s + s.total;
+  }
+  if (o.by_p) {
+    o.p_lo = find(false, part_of(c.top_p, least));
+    least = s.base_s + 1;
+    o.p_hi = find(false, part_of(c.top_p, most));
+    most = s.base_s + s.total;
+  }
+  o.d_lo = find(false, draw_target(c.u, least));
+  o.d_hi = find(false, draw_target(c.u, most));
+  if (threadIdx.x == 0) s.fill = 0;
+  __syncthreads();
+  uint32_t n = 0;
+#pragma unroll
+  for (int i = 0; i < SM_PER; ++i)
+    if (o.chosen(SM_PER * threadIdx.x + i)) n += count[SM_PER * threadIdx.x + i];
+  if (n) atomicAdd(&s.fill, n);
+  __syncthreads();
+  o.chosen_count = s.fill;
+  return o;
+}
+// The range's tokens of the parts, key above the complement of the token.
+template <class F>
+__device__ __forceinline__ void each_chosen(const Measure& me, const Borders& o, const void* row, int bf16, int t0, int t1, F f) {
+  each_logit<true>(row, bf16, t0, t1, [&](float v, int i) {
+    if (!me.near(v)) return;
+    const double y = me.octaves(v);
+    if (o.chosen(me.bucket(y)) && me.weight(y) != 0) f((uint64_t)logit_key(v) << 32 | (uint32_t)~i);
+  });
+}
+
+// The draw from the n tokens of the parts, in s.list in any order (n <= SM_LIST); the
+// histogram's sums and counts at sum, count.
+__device__ __forceinline__ void draw(SampleShared& s, const Settings& c, const Measure& me, const Borders& o, const uint64_t* sum,
+                                     const uint32_t* count, uint32_t n, int32_t* token, float* prob) {
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  int size = 64;
+  while (size < (int)n) size <<= 1;
+  for (int i = (int)n + threadIdx.x; i < size; i += SM_THREADS) s.list[i] = 0;
+  __syncthreads();
+  for (int span = 2; span <= size; span <<= 1)           // largest first
+    for (int step = span >> 1; step; step >>= 1) {
+      for (int i = threadIdx.x; i < size / 2; i += SM_THREADS) {
+        const int lo = ((i & ~(step - 1)) << 1) | (i & (step - 1)), hi = lo | step;
+        const uint64_t x = s.list[lo], z = s.list[hi];
+        if ((x < z) == ((lo & span) == 0)) s.list[lo] = z, s.list[hi] = x;
+      }
+      __syncthreads();
+    }
+  // What lies before each: within its part the sum over the list, before it the histogram's.
+  constexpr int OWN = SM_LIST / SM_THREADS;              // list entries of a thread, one after the other
+  uint64_t w[OWN], vs = 0;
+  int part[OWN], first[OWN], vf = 0;
+  uint32_t key[OWN];
+#pragma unroll
+  for (int q = 0; q < OWN; ++q) {
+    const int i = OWN * threadIdx.x + q;
+    w[q] = 0, part[q] = -1, key[q] = 0;
+    if (i < (int)n) {
+      key[q] = (uint32_t)(s.list[i] >> 32);
+      const double y = me.octaves(key_logit(key[q]));
+      w[q] = me.weight(y);
+      part[q] = me.bucket(y);
+      if (i == 0 || me.bucket(me.octaves(key_logit((uint32_t)(s.list[i - 1] >> 32)))) != part[q]) vf = i;
+    }
+    first[q] = vf;                                       // where its part begins, if among this thread's
+    vs += w[q];
+  }
+  uint64_t is = vs;
+  int mf = vf;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint64_t os = __shfl_up(is, d);
+    const int of = __shfl_up(mf, d);
+    if (lane >= d) is += os, mf = max(mf, of);
+  }
+  __syncthreads();
+  if (lane == 63) s.wsum[wv] = is, s.wcount[wv] = (uint32_t)mf;
+  __syncthreads();
+  uint64_t run = is - vs;
+  int from = __shfl_up(mf, 1);
+  if (lane == 0) from = 0;
+  for (int k = 0; k < wv; ++k) run += s.wsum[k], from = max(from, (int)s.wcount[k]);
+  uint64_t* const sums = s.sum2;                       // over the list before each entry
+  uint64_t before[OWN];
+#pragma unroll
+  for (int q = 0; q < OWN; ++q) {
+    before[q] = run;
+    sums[OWN * threadIdx.x + q] = run;
+    run += w[q];
+    first[q] = max(first[q], from);
+  }
+  // the histogram's sums and counts before each of the parts
+  uint32_t* const part_n = s.count2;
+  uint64_t bs = o.before_s;
+  uint32_t bn = o.before_n;
+#pragma unroll
+  for (int i = 0; i < SM_PER; ++i) {
+    const int b = SM_PER * threadIdx.x + i;
+    const uint64_t own = sum[b];
+    if (o.chosen(b)) {
+      s.start[b] = bs;
+      part_n[b] = bn;
+    }
+    bs += own;
+    bn += count[b];
+  }
+  __syncthreads();
+  uint32_t before_n[OWN];
+#pragma unroll
+  for (int q = 0; q < OWN; ++q) {
+    before_n[q] = 0;
+    if (part[q] < 0) continue;
+    before[q] += s.start[part[q]] - sums[first[q]];
+    before_n[q] = part_n[part[q]] + (OWN * threadIdx.x + q - first[q]);
+  }
+  uint64_t total = o.total;
+  if (o.by_k) {
+#pragma unroll
+    for (int q = 0; q < OWN; ++q)
+      if (part[q] >= 0 && before_n[q] + 1 == (uint32_t)c.top_k) s.total = before[q] + w[q];
+    __syncthreads();
+    total = s.total;
+    __syncthreads();
+  }
+  if (o.by_p) {
+    const uint64_t target = part_of(c.top_p, total);
+#pragma unroll
+    for (int q = 0; q < OWN; ++q)
+      if (part[q] >= 0 && before[q] < target && target <= before[q] + w[q]) s.total = before[q] + w[q];
+    __syncthreads();
+    total = s.total;
+  }
+  const uint64_t target = draw_target(c.u, total);
+#pragma unroll
+  for (int q = 0; q < OWN; ++q)
+    if (part[q] >= 0 && before[q] < target && target <= before[q] + w[q]) {
+      *token = (int32_t)~(uint32_t)s.list[OWN * threadIdx.x + q];
+      *prob = (float)(me.p_of(me.octaves(key_logit(key[q]))) * me.unit / (double)total);
+    }
+}
+
+__device__ __forceinline__ const void* row_of(const SampleArgs& a, int64_t r) {
+  return static_cast<const uint8_t*>(a.logits) + r * a.ld * (a.bf16 ? 2 : 4);
+}
+
+// ---- a workgroup per row ------------------------------------------------------------
+__global__ __launch_bounds__(SM_THREADS) void sample_kernel(SampleArgs a, int shift) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  SampleShared& s = *reinterpret_cast<SampleShared*>(smem);
+  const int64_t r = blockIdx.x + (int64_t)blockIdx.y * GRID_X;
+  if (r >= a.B) return;
+  const int V = (int)a.V;
+  const void* const row = row_of(a, r);
+  const Settings c = settings_of(a, r);
+  for (int i = threadIdx.x; i < SM_BUCKETS; i += SM_THREADS) s.sum[i] = 0, s.count[i] = 0;
+  if (threadIdx.x == 0) s.lo = 0xFFFFFFFFu;
+  const float best = best_of(s, row, a.bf16, 0, V);
+  if (!(best > -__builtin_inff())) {                     // nothing to draw from
+    if (threadIdx.x == 0) a.token[r] = -1, a.prob[r] = 0.f;
+    return;
+  }
+  if (c.greedy()) {
+    const uint32_t at = first_of(row, a.bf16, 0, V, best);
+    if ((threadIdx.x & 63) == 0) atomicMin(&s.lo, at);
+    __syncthreads();
+    if (threadIdx.x == 0) a.token[r] = (int32_t)s.lo, a.prob[r] = 1.f;
+    return;
+  }
+  const Measure me = measure_of(c, best, shift);
+  fill_histogram(s, me, row, a.bf16, 0, V);
+  __syncthreads();
+  const Borders o = borders_of(s, c, s.sum, s.count);
+  if (o.chosen_count > SM_LIST) {
+    sample_slow(s, me, row, a.bf16, V, c.top_k, c.top_p, c.u, o.total, o.count, a.token + r, a.prob + r);
+    return;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) s.fill = 0;
+  __syncthreads();
+  each_chosen(me, o, row, a.bf16, 0, V, [&](uint64_t e) { s.list[atomicAdd(&s.fill, 1u)] = e; });
+  __syncthreads();
+  draw(s, c, me, o, s.sum, s.count, o.chosen_count, a.token + r, a.prob + r);
+}
+
+// ---- several workgroups per row -------------------------------------------------------
+// Few rows leave most CUs idle, and one CU takes 35 us for the exponentials of 2^17
+// logits.  Here a row's tokens are cut into parts, and what the workgroups of a row
+// tell each other goes through the workspace from one launch to the next: each part's best
+// logit, the histogram, the list of the tokens to sort.
+struct RowSpace {
+  uint64_t sum[SM_BUCKETS];
+  uint64_t list[SM_LIST];
+  uint32_t count[SM_BUCKETS];
+  float best[SM_PARTS];
+  uint32_t fill, first;
+};
+
+struct Part {
+  int64_t r;
+  int t0, t1;
+  const void* row;
+};
+__device__ __forceinline__ Part part_of_row(const SampleArgs& a, int per) {
+  Part p;
+  p.r = blockIdx.y;
+  p.t0 = blockIdx.x * per;
+  p.t1 = min(p.t0 + per, (int)a.V);
+  p.row = row_of(a, p.r);
+  return p;
+}
+__device__ __forceinline__ float row_best(const RowSpace& sp, int parts) {
+  float best = sp.best[0];
+  for (int i = 1; i < parts; ++i) best = fmaxf(best, sp.best[i]);
+  return best;
+}
+
+__global__ __launch_bounds__(SM_THREADS) void sample_best_kernel(SampleArgs a, int per, RowSpace* ws) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const Part p = part_of_row(a, per);
+  RowSpace& sp = ws[p.r];
+  for (int i = blockIdx.x * SM_THREADS + threadIdx.x; i < SM_BUCKETS; i += gridDim.x * SM_THREADS) sp.sum[i] = 0, sp.count[i] = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) sp.fill = 0, sp.first = 0xFFFFFFFFu;
+  const float best = best_of(*reinterpret_cast<SampleShared*>(smem), p.row, a.bf16, p.t0, p.t1);
+  if (threadIdx.x == 0) sp.best[blockIdx.x] = best;
+}
+
+__global__ __launch_bounds__(SM_THREADS) void sample_histogram_kernel(SampleArgs a, int per, int shift, RowSpace* ws) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  SampleShared& s = *reinterpret_cast<SampleShared*>(smem);
+  const Part p = part_of_row(a, per);
+  RowSpace& sp = ws[p.r];
+  const Settings c = settings_of(a, p.r);
+  const float best = row_best(sp, gridDim.x);
+  if (!(best > -__builtin_inff())) return;
+  if (c.greedy()) {
+    const uint32_t at = first_of(p.row, a.bf16, p.t0, p.t1, best);
+    if ((threadIdx.x & 63) == 0 && at != 0xFFFFFFFFu) atomicMin(&sp.first, at);
+    return;
+  }
+  for (int i = threadIdx.x; i < SM_BUCKETS; i += SM_THREADS) s.sum[i] = 0, s.count[i] = 0;
+  __syncthreads();
+  fill_histogram(s, measure_of(c, best, shift), p.row, a.bf16, p.t0, p.t1);
+  __syncthreads();
+  for (int i = threadIdx.x; i < SM_BUCKETS; i += SM_THREADS) {
+    if (s.count[i] == 0) continue;
+    atomicAdd(reinterpret_cast<unsigned long long*>(&sp.sum[i]), (unsigned long long)s.sum[i]);
+    atomicAdd(&sp.count[i], s.count[i]);
+  }
+}
+
+__global__ __launch_bounds__(SM_THREADS) void sample_gather_kernel(SampleArgs a, int per, int shift, RowSpace* ws) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  SampleShared& s = *reinterpret_cast<SampleShared*>(smem);
+  const Part p = part_of_row(a, per);
+  RowSpace& sp = ws[p.r];
+  const Settings c = settings_of(a, p.r);
+  const float best = row_best(sp, gridDim.x);
+  if (!(best > -__builtin_inff()) || c.greedy()) return;
+  const Borders o = borders_of(s, c, sp.sum, sp.count);
+  if (o.chosen_count > SM_LIST) return;
+  each_chosen(measure_of(c, best, shift), o, p.row, a.bf16, p.t0, p.t1, [&](uint64_t e) {
+    const uint32_t at = atomicAdd(&sp.fill, 1u);
+    if (at < SM_LIST) sp.list[at] = e;
+  });
+}
+
+__global__ __launch_bounds__(SM_THREADS) void sample_draw_kernel(SampleArgs a, int parts, int shift, RowSpace* ws) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  SampleShared& s = *reinterpret_cast<SampleShared*>(smem);
+  const int64_t r = blockIdx.x;
+  const RowSpace& sp = ws[r];
+  const Settings c = settings_of(a, r);
+  const float best = row_best(sp, parts);
+  if (!(best > -__builtin_inff()) || c.greedy()) {
+    const bool none = !(best > -__builtin_inff());
+    if (threadIdx.x == 0) a.token[r] = none ? -1 : (int32_t)sp.first, a.prob[r] = none ? 0.f : 1.f;
+    return;
+  }
+  const Measure me = measure_of(c, best, shift);
+  const Borders o = borders_of(s, c, sp.sum, sp.count);
+  if (o.chosen_count > SM_LIST) {
+    for (int i = threadIdx.x; i < SM_BUCKETS; i += SM_THREADS) s.sum[i] = sp.sum[i], s.count[i] = sp.count[i];
+    __syncthreads();
+    sample_slow(s, me, row_of(a, r), a.bf16, (int)a.V, c.top_k, c.top_p, c.u, o.total, o.count, a.token + r, a.prob + r);
+    return;
+  }
+  for (int i = threadIdx.x; i < (int)o.chosen_count; i += SM_THREADS) s.list[i] = sp.list[i];
+  draw(s, c, me, o, sp.sum, sp.count, o.chosen_count, a.token + r, a.prob + r);
+}
+
+// Tokens of a part; 0 where a workgroup takes whole rows: few tokens, or rows enough for the CUs.
+static int part_tokens(int64_t B, int64_t V) {
+  if (V <= 8192 || B > 128) return 0;
+  const int64_t parts = std::min<int64_t>({(256 + B - 1) / B, (V + 4095) / 4096, SM_PARTS});
+  return parts > 1 ? (int)(((V + parts - 1) / parts + 1023) / 1024 * 1024) : 0;
+}
+
+size_t sample_workspace_bytes(int64_t B, int64_t V) {
+  return part_tokens(B, V) ? (size_t)B * sizeof(RowSpace) : 0;
+}
+
+hipError_t launch_sample(const SampleArgs& a, void* workspace, hipStream_t stream) {
   int bits = 0;
   while (((int64_t)1 << bits) < a.V) ++bits;
-  hipLaunchKernelGGL(sample_kernel, grid_of(a.B), dim3(SM_THREADS), 0, stream, a, std::min(62 - bits, 51));
+  const int shift = std::min(62 - bits, 51), per = part_tokens(a.B, a.V);
+  constexpr size_t LDS = sizeof(SampleShared), SMALL = offsetof(SampleShared, sum), HIST = offsetof(SampleShared, list);
+  if (per == 0) {
+    hipLaunchKernelGGL(sample_kernel, grid_of(a.B), dim3(SM_THREADS), LDS, stream, a, shift);
+    return hipGetLastError();
+  }
+  RowSpace* const ws = static_cast<RowSpace*>(workspace);
+  const dim3 grid((unsigned)((a.V + per - 1) / per), (unsigned)a.B);
+  hipLaunchKernelGGL(sample_best_kernel, grid, dim3(SM_THREADS), SMALL, stream, a, per, ws);
+  hipLaunchKernelGGL(sample_histogram_kernel, grid, dim3(SM_THREADS), HIST, stream, a, per, shift, ws);
+  hipLaunchKernelGGL(sample_gather_kernel, grid, dim3(SM_THREADS), SMALL, stream, a, per, shift, ws);
+  hipLaunchKernelGGL(sample_draw_kernel, dim3((unsigned)a.B), dim3(SM_THREADS), LDS, stream, a, (int)grid.x, shift, ws);
   return hipGetLastError();
 }
 

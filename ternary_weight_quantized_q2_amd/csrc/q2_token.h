@@ -33,6 +33,7 @@ struct SampleArgs {
   int32_t* token;
   float* prob;
 };
-hipError_t launch_sample(const SampleArgs& a, hipStream_t stream);
+size_t sample_workspace_bytes(int64_t B, int64_t V);
+hipError_t launch_sample(const SampleArgs& a, void* workspace, hipStream_t stream);
 
 }  // namespace q2dev

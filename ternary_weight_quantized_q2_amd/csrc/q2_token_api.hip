@@ -6,8 +6,12 @@
 #include "q2_token.h"
 
 namespace {
+
 using namespace q2host;
-}
+
+bool sample_sizes_ok(int64_t B, int64_t V) { return B >= 0 && B <= (1 << 30) && V >= 1 && V <= (1 << 24); }
+
+}  // namespace
 
 extern "C" {
 
@@ -50,11 +54,15 @@ int q4_matvec(const uint16_t* x_bf16, const uint8_t* packed4, const uint16_t* sc
   return hip_status(q2dev::launch_q4_matvec(a, stream), "4-bit product launch");
 }
 
+size_t q2_sample_workspace_bytes(int64_t B, int64_t V) {
+  return B > 0 && sample_sizes_ok(B, V) ? q2dev::sample_workspace_bytes(B, V) : 0;
+}
+
 int q2_sample(const void* logits, int64_t B, int64_t V, int64_t ld, uint32_t flags, const q2_sampling* settings,
-              const float* u, int32_t* token, float* prob, hipStream_t stream) {
+              const float* u, int32_t* token, float* prob, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   if (B < 0 || V < 0) return fail(Q2_ERR_ARG, "negative size (B=%lld V=%lld)", (long long)B, (long long)V);
   if (flags & ~Q2_SAMPLE_LOGITS_BF16) return fail(Q2_ERR_ARG, "unknown sample flag bits 0x%x", flags & ~Q2_SAMPLE_LOGITS_BF16);
-  if (V < 1 || V > (1 << 24) || B > (1 << 30)) return fail(Q2_ERR_SHAPE, "B=%lld V=%lld: 1 <= V <= 2^24, B <= 2^30",
+  if (!sample_sizes_ok(B, V)) return fail(Q2_ERR_SHAPE, "B=%lld V=%lld: 1 <= V <= 2^24, B <= 2^30",
                                                            (long long)B, (long long)V);
   if (B > 1 && (ld < V || ld > ((int64_t)1 << 46) / B))
     return fail(Q2_ERR_ARG, "ld=%lld: rows of V=%lld logits overlap or lie too far apart", (long long)ld, (long long)V);
@@ -68,6 +76,7 @@ int q2_sample(const void* logits, int64_t B, int64_t V, int64_t ld, uint32_t fla
       (st = check_ptr(token, B > 0, 4, "token")) || (st = check_ptr(prob, B > 0, 4, "prob")))
     return st;
   if (B == 0) return ok();
+  if ((st = check_workspace(workspace, workspace_bytes, q2_sample_workspace_bytes(B, V)))) return st;
   if ((st = check_device())) return st;
   q2dev::SampleArgs a = {};
   a.logits = logits;
@@ -80,7 +89,7 @@ int q2_sample(const void* logits, int64_t B, int64_t V, int64_t ld, uint32_t fla
   a.min_p = c.min_p_rows; a.min_p_all = c.min_p;
   a.token = token;
   a.prob = prob;
-  return hip_status(q2dev::launch_sample(a, stream), "sample launch");
+  return hip_status(q2dev::launch_sample(a, workspace, stream), "sample launch");
 }
 
 }  // extern "C"

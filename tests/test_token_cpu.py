@@ -48,9 +48,9 @@ def test_matvec_argument_errors(lib):
 
 
 def test_sample_argument_errors(lib):
-    def S(lg=FAKE, b=4, v=100, ld=100, fl=0, u=FAKE, t=FAKE, p=FAKE, **c):
+    def S(lg=FAKE, b=4, v=100, ld=100, fl=0, u=FAKE, t=FAKE, p=FAKE, ws=FAKE, wb=1 << 40, **c):
         s = q2.Sampling(1.0, 0, 1.0, 0.0, *(c.get(n) for n in ("tr", "kr", "pr", "mr")))
-        return lib.q2_sample(lg, b, v, ld, fl, ctypes.addressof(s), u, t, p, None)
+        return lib.q2_sample(lg, b, v, ld, fl, ctypes.addressof(s), u, t, p, ws, wb, None)
 
     assert S(b=-1) == q2.Q2_ERR_ARG and S(v=-1) == q2.Q2_ERR_ARG and S(fl=2) == q2.Q2_ERR_ARG
     assert S(v=0) == q2.Q2_ERR_SHAPE and S(v=(1 << 24) + 1, ld=1 << 25) == q2.Q2_ERR_SHAPE
@@ -63,6 +63,13 @@ def test_sample_argument_errors(lib):
     for name in ("tr", "kr", "pr", "mr"):
         assert S(**{name: FAKE + 2}) == q2.Q2_ERR_ALIGN, name
     assert S(b=0, lg=None, u=None, t=None, p=None) == q2.Q2_OK
+    need = q2.sample_workspace_bytes(4, 100000)
+    assert need > 0 and q2.sample_workspace_bytes(4, 100) == 0 and q2.sample_workspace_bytes(4, (1 << 24) + 1) == 0
+    assert q2.sample_workspace_bytes(0, 100000) == 0 and q2.sample_workspace_bytes(-1, 100000) == 0
+    assert q2.sample_workspace_bytes(2 ** 63 - 1, 2 ** 63 - 1) == 0 and q2.sample_workspace_bytes(-2 ** 63, 5) == 0
+    big = dict(v=100000, ld=100000)
+    assert S(wb=need - 1, **big) == q2.Q2_ERR_WORKSPACE and S(ws=None, **big) == q2.Q2_ERR_ARG
+    assert S(ws=FAKE + 64, **big) == q2.Q2_ERR_ALIGN
 
 
 # ---------------------------------------------------------------------------
