@@ -33,12 +33,14 @@ __device__ __forceinline__ float key_logit(uint32_t o) {
   return __builtin_bit_cast(float, o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-// f(logit, token) for tokens t0 .. t1 - 1 of a row, 16 bytes at a time between the first
-// and the last aligned address, four loads of a thread ahead.  ONCE: f's code appears
-// once (a launch starts with cold instruction caches, about a microsecond per KB).
-template <bool ONCE, class F>
-__device__ __forceinline__ void each_logit(const void* whole, int bf16, int t0, int t1, F f) {
-  const int size = bf16 ? 2 : 4, per = 16 / size, V = t1 - t0;
+// f(four logits, the first one's token, the step between their tokens) for tokens t0 ..
+// t1 - 1 of a row; NaN, which is a masked logit, in places that are none.  16 bytes at a
+// time between the first and the last aligned address, four loads of a thread ahead.
+// f's code appears once: a launch starts with cold instruction caches and pays about a
+// microsecond per KB that it meets for the first time.
+template <class F>
+__device__ __forceinline__ void each_four(const void* whole, int bf16, int t0, int t1, F f) {
+  const int size = bf16 ? 2 : 4, per = 16 / size, V = t1 - t0, threads = blockDim.x;
   const uint8_t* const row = static_cast<const uint8_t*>(whole) + (int64_t)t0 * size;
   const int head = min(V, (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / size);
   const int body = (V - head) / per, rest = V - body * per;              // up to per - 1 tokens in front and behind
@@ -47,55 +49,51 @@ __device__ __forceinline__ void each_logit(const void* whole, int bf16, int t0, 
   q2_u32x4 v[AHEAD], next[AHEAD];
   auto load = [&](int i) {
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) next[k] = p[min(i + k * SM_THREADS, body - 1)];
+    for (int k = 0; k < AHEAD; ++k) next[k] = p[min(i + k * threads, body - 1)];
   };
   if (body > 0) load(threadIdx.x);
-  const int steps = (body + AHEAD * SM_THREADS - 1) / (AHEAD * SM_THREADS);
+  const int steps = (body + AHEAD * threads - 1) / (AHEAD * threads);
 #pragma unroll 1
   for (int step = 0; step <= steps; ++step) {            // the last one: the rest, a token per thread
     const bool last = step == steps;
-    const int i = step * AHEAD * SM_THREADS + threadIdx.x;
+    const int i = step * AHEAD * threads + threadIdx.x;
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) v[k] = next[k];
-    if (!last) load(i + AHEAD * SM_THREADS);             // past the end: the last piece again
-    const int one = (int)threadIdx.x < head ? (int)threadIdx.x : body * per + (int)threadIdx.x;
+    if (step + 1 < steps) load(i + AHEAD * threads);     // past the end: the last piece again
+    int one = 0;
     if (last) {
       if ((int)threadIdx.x >= rest) break;
-      v[0][0] = bf16 ? (uint32_t)reinterpret_cast<const uint16_t*>(row)[one] : reinterpret_cast<const uint32_t*>(row)[one];
+      one = (int)threadIdx.x < head ? (int)threadIdx.x : body * per + (int)threadIdx.x;
+      const uint32_t w = bf16 ? (uint32_t)reinterpret_cast<const uint16_t*>(row)[one] << 16 : reinterpret_cast<const uint32_t*>(row)[one];
+      v[0] = q2_u32x4{w, 0x7FC00000u, 0x7FC00000u, 0x7FC00000u};
     }
 #pragma unroll 1
     for (int k = 0; k < (last ? 1 : AHEAD); ++k) {
-      const int piece = i + k * SM_THREADS;
+      const int piece = i + k * threads;
       if (!last && piece >= body) break;
       const int at = t0 + (last ? one : head + piece * per);
-      if constexpr (ONCE) {
-        const int n = last ? 1 : per;
+      const int halves = bf16 && !last ? 2 : 1;
 #pragma unroll 1
-        for (int d = 0; d < n; ++d) {
-          const uint32_t w = v[0][0];
-          f(__builtin_bit_cast(float, bf16 ? w << 16 : w), at + d);
-          if (bf16 && !(d & 1)) v[0][0] = w >> 16;
-          else v[0][0] = v[0][1], v[0][1] = v[0][2], v[0][2] = v[0][3];
-        }
-      } else if (last) {
-        const uint32_t w = v[0][0];
-        f(__builtin_bit_cast(float, bf16 ? w << 16 : w), at);
-      } else {
+      for (int h = 0; h < halves; ++h) {
+        float x[4];
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
           const uint32_t w = v[0][d];                    // a bit cast of the vector's element itself reads element 0
-          if (bf16) {
-            f(__builtin_bit_cast(float, w << 16), at + 2 * d);
-            f(__builtin_bit_cast(float, w & 0xFFFF0000u), at + 2 * d + 1);
-          } else {
-            f(__builtin_bit_cast(float, w), at + d);
-          }
+          x[d] = __builtin_bit_cast(float, halves == 1 ? w : h ? w & 0xFFFF0000u : w << 16);
         }
+        f(x, at + h, halves);
       }
 #pragma unroll
       for (int q = 1; q < AHEAD; ++q) v[q - 1] = v[q];
     }
   }
+}
+template <class F>
+__device__ __forceinline__ void each_logit(const void* row, int bf16, int t0, int t1, F f) {
+  each_four(row, bf16, t0, t1, [&](const float(&x)[4], int at, int by) {
+#pragma unroll 1
+    for (int d = 0; d < 4; ++d) f(d == 0 ? x[0] : d == 1 ? x[1] : d == 2 ? x[2] : x[3], at + d * by);
+  });
 }
 
 // A kernel that needs only the beginning of it allocates that.
@@ -103,6 +101,10 @@ struct SampleShared {
   uint64_t wsum[SM_WAVES];
   uint32_t wcount[SM_WAVES];
   float wbest[SM_WAVES];
+  struct {
+    uint64_t before, own;
+    int part;
+  } find[6];
   uint64_t base_s, total;
   uint32_t base_n, bucket, n, fill, lo, hi, key, unused;
   uint64_t sum[SM_BUCKETS];                              // over all tokens
@@ -118,13 +120,13 @@ struct Measure {
   float best, cut;                                       // no token further than cut from the best has a weight
   double scale, unit, min_p, per_octave;                 // log2(e) / T, 2^S, buckets per halving of p
 
-  // log2 of 1 / p.  NaN (of infinity times zero) has no probability.
+  // log2 of 1 / p, at most 1000, where p is 0 in units: also of a masked logit, and of
+  // infinity times zero.
   __device__ __forceinline__ double octaves(float v) const {
-    return v == best ? 0.0 : ((double)best - (double)v) * scale;
+    return v == best ? 0.0 : __builtin_fmin(((double)best - (double)v) * scale, 1000.0);
   }
   // 2^-y: the power series of 2^r, |r| <= 1/2, to r^11 (off by 7e-15 at most).
   __device__ __forceinline__ static double p_of(double y) {
-    if (!(y < 1000.0)) return 0.0;
     const double n = __builtin_rint(y), r = (n - y) * 0.69314718055994530942;
     double q = 1.0 / 39916800;
     q = __builtin_fma(q, r, 1.0 / 3628800);
@@ -143,25 +145,26 @@ struct Measure {
   // Whole number of units; 0 for a token that is below min-p or too unlikely.
   __device__ __forceinline__ uint64_t weight(double y) const {
     const double q = p_of(y);
-    if (!(q >= min_p)) return 0;
-    return __builtin_bit_cast(uint64_t, q * unit + 0x1p52) - __builtin_bit_cast(uint64_t, 0x1p52);
+    const uint64_t w = __builtin_bit_cast(uint64_t, q * unit + 0x1p52) - __builtin_bit_cast(uint64_t, 0x1p52);
+    return q >= min_p ? w : 0;
   }
   // Does not fall as the logit falls: the difference and the products round monotonically.
   __device__ __forceinline__ int bucket(double y) const {
     const double t = y * per_octave;
     return t < SM_BUCKETS - 1 ? (int)t : SM_BUCKETS - 1;
   }
-  __device__ __forceinline__ bool near(float v) const { return !(best - v > cut) && v > -__builtin_inff(); }
+  // Whether the logit may have a weight; the exact test is weight() != 0.
+  __device__ __forceinline__ bool near(float v) const { return !(best - v > cut); }
 };
 
 // Sums before this thread's SM_PER buckets, and the totals.
-__device__ __forceinline__ void scan_buckets(SampleShared& s, const uint64_t* sum, const uint32_t* count, uint64_t& before_s,
-                                             uint32_t& before_n, uint64_t& total_s, uint32_t& total_n) {
+__device__ __forceinline__ void scan_buckets(SampleShared& s, const uint64_t (&own_s)[SM_PER], const uint32_t (&own_n)[SM_PER],
+                                             uint64_t& before_s, uint32_t& before_n, uint64_t& total_s, uint32_t& total_n) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   uint64_t vs = 0;
   uint32_t vn = 0;
 #pragma unroll
-  for (int i = 0; i < SM_PER; ++i) vs += sum[SM_PER * threadIdx.x + i], vn += count[SM_PER * threadIdx.x + i];
+  for (int i = 0; i < SM_PER; ++i) vs += own_s[i], vn += own_n[i];
   uint64_t is = vs;
   uint32_t in = vn;
 #pragma unroll
@@ -206,16 +209,21 @@ __device__ __noinline__ Place locate(SampleShared& s, const Measure& me, const v
   for (int h = 0;; h = 1) {
     uint64_t bs, ts;
     uint32_t bn, tn;
-    const uint64_t* const sum = h ? s.sum2 : s.sum;
-    const uint32_t* const count = h ? s.count2 : s.count;
-    scan_buckets(s, sum, count, bs, bn, ts, tn);
+    uint64_t own_s[SM_PER];
+    uint32_t own_n[SM_PER];
+#pragma unroll
+    for (int i = 0; i < SM_PER; ++i) {
+      own_s[i] = (h ? s.sum2 : s.sum)[SM_PER * threadIdx.x + i];
+      own_n[i] = (h ? s.count2 : s.count)[SM_PER * threadIdx.x + i];
+    }
+    scan_buckets(s, own_s, own_n, bs, bn, ts, tn);
     bs += base_s;
     bn += base_n;
 #pragma unroll
     for (int i = 0; i < SM_PER; ++i) {
       const int b = SM_PER * threadIdx.x + i;
-      const uint64_t vs = sum[b];
-      const uint32_t vn = count[b];
+      const uint64_t vs = own_s[i];
+      const uint32_t vn = own_n[i];
       const uint64_t from = by_count ? bn : bs, to = by_count ? bn + vn : bs + vs;
       if (from < target && target <= to) {
         s.bucket = b;
@@ -242,7 +250,7 @@ __device__ __noinline__ Place locate(SampleShared& s, const Measure& me, const v
     }
     // tokens of the range that have a weight, with their keys
     auto each = [&](auto f) {
-      each_logit<true>(row, bf16, 0, V, [&](float v, int) {
+      each_logit(row, bf16, 0, V, [&](float v, int) {
         if (!me.near(v)) return;
         const uint32_t key = logit_key(v);
         const double y = me.octaves(v);
@@ -393,7 +401,9 @@ __device__ __forceinline__ Measure measure_of(const Settings& c, float best, int
 // The largest of the range's logits, in all threads.
 __device__ __forceinline__ float best_of(SampleShared& s, const void* row, int bf16, int t0, int t1) {
   float best = -__builtin_inff();
-  each_logit<false>(row, bf16, t0, t1, [&](float v, int) { best = fmaxf(best, v); });         // a NaN is dropped
+  each_four(row, bf16, t0, t1, [&](const float(&x)[4], int, int) {                     // a NaN is dropped
+    best = fmaxf(best, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+  });
 #pragma unroll
   for (int d = 32; d; d >>= 1) best = fmaxf(best, __shfl_xor(best, d));
   if ((threadIdx.x & 63) == 0) s.wbest[threadIdx.x >> 6] = best;
@@ -404,24 +414,34 @@ __device__ __forceinline__ float best_of(SampleShared& s, const void* row, int b
 }
 // The range's first token that has the largest logit, ~0 without one, by wave.
 __device__ __forceinline__ uint32_t first_of(const void* row, int bf16, int t0, int t1, float best) {
-  uint32_t at = 0xFFFFFFFFu;
-  each_logit<false>(row, bf16, t0, t1, [&](float v, int i) {
-    if (v == best) at = min(at, (uint32_t)i);
+  uint32_t first = 0xFFFFFFFFu;
+  each_four(row, bf16, t0, t1, [&](const float(&x)[4], int at, int by) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+      if (x[d] == best) first = min(first, (uint32_t)(at + d * by));
   });
 #pragma unroll
-  for (int d = 32; d; d >>= 1) at = min(at, __shfl_xor(at, d));
-  return at;
+  for (int d = 32; d; d >>= 1) first = min(first, __shfl_xor(first, d));
+  return first;
 }
 // The range's tokens into the histogram in s.
 __device__ __forceinline__ void fill_histogram(SampleShared& s, const Measure& me, const void* row, int bf16, int t0, int t1) {
-  each_logit<true>(row, bf16, t0, t1, [&](float v, int) {
-    if (!me.near(v)) return;
-    const double y = me.octaves(v);
-    const uint64_t w = me.weight(y);
-    if (w == 0) return;
-    const int b = me.bucket(y);
-    atomicAdd(reinterpret_cast<unsigned long long*>(&s.sum[b]), (unsigned long long)w);
-    atomicAdd(&s.count[b], 1u);
+  each_four(row, bf16, t0, t1, [&](const float(&x)[4], int, int) {
+    if (!(me.near(x[0]) || me.near(x[1]) || me.near(x[2]) || me.near(x[3]))) return;
+    uint64_t w[4];
+    int b[4];
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {                        // four chains at once: one waits for every step
+      const double y = me.octaves(x[d]);
+      w[d] = me.weight(y);
+      b[d] = me.bucket(y);
+    }
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+      if (w[d] != 0) {
+        atomicAdd(reinterpret_cast<unsigned long long*>(&s.sum[b[d]]), (unsigned long long)w[d]);
+        atomicAdd(&s.count[b[d]], 1u);
+      }
   });
 }
 
@@ -430,109 +450,148 @@ __device__ __forceinline__ void fill_histogram(SampleShared& s, const Measure& m
 // range of parts for each border.
 struct Borders {
   bool by_k, by_p;
-  int k_part, p_lo, p_hi, d_lo, d_hi;
-  uint64_t total, before_s;                              // the sum of all; before this thread's buckets
-  uint32_t count, before_n;
+  int lo[3], hi[3];                                      // parts of top-k, top-p, the draw
+  uint64_t total;                                        // the sum of all
+  uint32_t count;
   uint32_t chosen_count;                                 // tokens in the parts
 
   __device__ __forceinline__ bool chosen(int b) const {
-    return b == k_part || (b >= p_lo && b <= p_hi) || (b >= d_lo && b <= d_hi);
+    return (b >= lo[0] && b <= hi[0]) || (b >= lo[1] && b <= hi[1]) || (b >= lo[2] && b <= hi[2]);
   }
 };
-__device__ __forceinline__ Borders borders_of(SampleShared& s, const Settings& c, const uint64_t* sum, const uint32_t* count) {
+// start_s, start_n, where given: for the chosen parts, what lies before them.
+__device__ __forceinline__ Borders borders_of(SampleShared& s, const Settings& c, const uint64_t* sum, const uint32_t* count,
+                                              uint64_t* start_s, uint32_t* start_n) {
   Borders o;
-  scan_buckets(s, sum, count, o.before_s, o.before_n, o.total, o.count);
+  uint64_t vs[SM_PER], bs0;
+  uint32_t vn[SM_PER], bn0;
+#pragma unroll
+  for (int i = 0; i < SM_PER; ++i) vs[i] = sum[SM_PER * threadIdx.x + i], vn[i] = count[SM_PER * threadIdx.x + i];
+  scan_buckets(s, vs, vn, bs0, bn0, o.total, o.count);
   o.by_k = c.top_k > 0 && (uint32_t)c.top_k < o.count;
   o.by_p = c.top_p < 1.f;
-  auto find = [&](bool by_count, uint64_t target) {      // the part that reaches it, what lies before, its own sum
-    uint64_t bs = o.before_s;
-    uint32_t bn = o.before_n;
-    __syncthreads();
+  o.lo[0] = o.lo[1] = o.lo[2] = 0;
+  o.hi[0] = o.hi[1] = o.hi[2] = -1;
+  uint64_t least = o.total, most = o.total;              // bounds of the sum of what is left
+  if (threadIdx.x == 0) s.fill = 0;
+#pragma unroll 1
+  for (int border = o.by_k ? 0 : o.by_p ? 1 : 2; border < 3; border = border == 0 && !o.by_p ? 2 : border + 1) {
+    const uint64_t first = border == 0 ? (uint64_t)c.top_k : border == 1 ? part_of(c.top_p, least) : draw_target(c.u, least);
+    const uint64_t second = border == 0 ? first : border == 1 ? part_of(c.top_p, most) : draw_target(c.u, most);
+    uint64_t bs = bs0, bn = bn0;
 #pragma unroll
-    for (int i = 0; i < SM_PER; ++i) {
-      const int b = SM_PER * threadIdx.x + i;
-      const uint64_t vs = sum[b];
-      const uint32_t vn = count[b];
-      const uint64_t from = by_count ? bn : bs, to = by_count ? bn + vn : bs + vs;
-      if (from < target && target <= to) s.bucket = b, s.base_s = bs, s.total = vs;
-      bs += vs;
-      bn += vn;
+    for (int i = 0; i < SM_PER; ++i) {                   // the part that reaches a target, what lies before it, its own sum
+      const uint64_t before = border == 0 ? bn : bs, reach = before + (border == 0 ? vn[i] : vs[i]);
+      if (before < first && first <= reach) s.find[2 * border] = {bs, vs[i], SM_PER * (int)threadIdx.x + i};
+      if (before < second && second <= reach) s.find[2 * border + 1] = {bs, vs[i], SM_PER * (int)threadIdx.x + i};
+      bs += vs[i];
+      bn += vn[i];
     }
     __syncthreads();
-    return (int)s.bucket;
-  };
-  o.k_part = -1, o.p_lo = 0, o.p_hi = -1;
-  uint64_t least = o.total, most = o.total;              // bounds of the sum of what is left
-  if (o.by_k) {
-    o.k_part = find(true, (uint64_t)c.top_k);
-    least = s.base_s + 1;
-    most = s.base_s + s.total;
+    const int lo = s.find[2 * border].part, hi = s.find[2 * border + 1].part;
+    least = s.find[2 * border].before + 1;
+    most = s.find[2 * border + 1].before + s.find[2 * border + 1].own;
+    if (border == 0) o.lo[0] = lo, o.hi[0] = hi;
+    else if (border == 1) o.lo[1] = lo, o.hi[1] = hi;
+    else o.lo[2] = lo, o.hi[2] = hi;
   }
-  if (o.by_p) {
-    o.p_lo = find(false, part_of(c.top_p, least));
-    least = s.base_s + 1;
-    o.p_hi = find(false, part_of(c.top_p, most));
-    most = s.base_s + s.total;
-  }
-  o.d_lo = find(false, draw_target(c.u, least));
-  o.d_hi = find(false, draw_target(c.u, most));
-  if (threadIdx.x == 0) s.fill = 0;
-  __syncthreads();
   uint32_t n = 0;
 #pragma unroll
-  for (int i = 0; i < SM_PER; ++i)
-    if (o.chosen(SM_PER * threadIdx.x + i)) n += count[SM_PER * threadIdx.x + i];
+  for (int i = 0; i < SM_PER; ++i) {
+    const int b = SM_PER * threadIdx.x + i;
+    if (o.chosen(b)) {
+      n += vn[i];
+      if (start_s) start_s[b] = bs0, start_n[b] = bn0;
+    }
+    bs0 += vs[i];
+    bn0 += vn[i];
+  }
   if (n) atomicAdd(&s.fill, n);
   __syncthreads();
   o.chosen_count = s.fill;
   return o;
 }
-// The range's tokens of the parts, key above the complement of the token.
+
+// The range's tokens of the parts, key above the complement of the token.  The logits of
+// a border's parts lie in a range of distances from the best one, and rounding does not
+// turn an order round, so distances in 32 bits drop nearly all others: first by the one
+// range that holds the three.  Distances are not negative and are compared by their bits.
 template <class F>
 __device__ __forceinline__ void each_chosen(const Measure& me, const Borders& o, const void* row, int bf16, int t0, int t1, F f) {
-  each_logit<true>(row, bf16, t0, t1, [&](float v, int i) {
-    if (!me.near(v)) return;
-    const double y = me.octaves(v);
-    if (o.chosen(me.bucket(y)) && me.weight(y) != 0) f((uint64_t)logit_key(v) << 32 | (uint32_t)~i);
+  const double step = 1.0 / (me.per_octave * me.scale);
+  uint32_t from[3], over[3], lo = 0xFFFFFFFFu, hi = 0;
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {                          // a little wider: the exact test comes behind it
+    const bool none = o.lo[j] > o.hi[j], all = !(me.best < __builtin_inff());          // its own distance is no number
+    const uint32_t first = all ? 0u : __builtin_bit_cast(uint32_t, (float)(o.lo[j] * step * (1 - 1e-6)));
+    const uint32_t last = all || o.hi[j] == SM_BUCKETS - 1 ? 0xFFFFFFFFu : __builtin_bit_cast(uint32_t, (float)((o.hi[j] + 1) * step * (1 + 1e-6)));
+    from[j] = none ? 0xFFFFFFFFu : first;
+    over[j] = none ? 0u : last - first;
+    if (!none) lo = min(lo, first), hi = max(hi, last);
+  }
+  each_four(row, bf16, t0, t1, [&](const float(&x)[4], int at, int by) {
+    uint32_t away[4];
+#pragma unroll
+    for (int d = 0; d < 4; ++d) away[d] = __builtin_bit_cast(uint32_t, me.best - x[d]);
+    if (min(min(away[0] - lo, away[1] - lo), min(away[2] - lo, away[3] - lo)) > hi - lo) return;
+#pragma unroll 1
+    for (int d = 0; d < 4; ++d) {
+      const uint32_t w = d == 0 ? away[0] : d == 1 ? away[1] : d == 2 ? away[2] : away[3];
+      if (w - from[0] > over[0] && w - from[1] > over[1] && w - from[2] > over[2]) continue;
+      const float v = d == 0 ? x[0] : d == 1 ? x[1] : d == 2 ? x[2] : x[3];
+      const double y = me.octaves(v);
+      if (o.chosen(me.bucket(y)) && me.weight(y) != 0) f((uint64_t)logit_key(v) << 32 | (uint32_t)~(at + d * by));
+    }
   });
 }
 
-// The draw from the n tokens of the parts, in s.list in any order (n <= SM_LIST); the
-// histogram's sums and counts at sum, count.
-__device__ __forceinline__ void draw(SampleShared& s, const Settings& c, const Measure& me, const Borders& o, const uint64_t* sum,
-                                     const uint32_t* count, uint32_t n, int32_t* token, float* prob) {
+// The draw from the n tokens of the parts, in s.list in any order (n <= SM_LIST);
+// start_s, start_n: what lies before the parts.
+template <int THREADS>
+__device__ __forceinline__ void draw(SampleShared& s, const Settings& c, const Measure& me, bool by_k, bool by_p, uint64_t total,
+                                     const uint64_t* start_s, const uint32_t* start_n, uint32_t n, int32_t* token, float* prob) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   int size = 64;
   while (size < (int)n) size <<= 1;
-  for (int i = (int)n + threadIdx.x; i < size; i += SM_THREADS) s.list[i] = 0;
-  __syncthreads();
-  for (int span = 2; span <= size; span <<= 1)           // largest first
-    for (int step = span >> 1; step; step >>= 1) {
-      for (int i = threadIdx.x; i < size / 2; i += SM_THREADS) {
-        const int lo = ((i & ~(step - 1)) << 1) | (i & (step - 1)), hi = lo | step;
-        const uint64_t x = s.list[lo], z = s.list[hi];
-        if ((x < z) == ((lo & span) == 0)) s.list[lo] = z, s.list[hi] = x;
+  if (size <= THREADS) {
+    // Largest first: an entry's place is the number of larger ones.  All are different.
+    __syncthreads();
+    const uint64_t mine = threadIdx.x < n ? s.list[threadIdx.x] : 0;
+    int place = 0;
+    if ((int)threadIdx.x < (int)((n + 63) & ~63u)) {     // whole waves
+#pragma unroll 4
+      for (int j = 0; j < (int)n; ++j) place += s.list[j] > mine;
+    }
+    __syncthreads();
+    if (threadIdx.x < n) s.list[place] = mine;
+    __syncthreads();
+  } else {
+    for (int i = (int)n + threadIdx.x; i < size; i += THREADS) s.list[i] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int span = 2; span <= size; span <<= 1)
+#pragma unroll 1
+      for (int step = span >> 1; step; step >>= 1) {
+#pragma unroll 1
+        for (int i = threadIdx.x; i < size / 2; i += THREADS) {
+          const int lo = ((i & ~(step - 1)) << 1) | (i & (step - 1)), hi = lo | step;
+          const uint64_t x = s.list[lo], z = s.list[hi];
+          if ((x < z) == ((lo & span) == 0)) s.list[lo] = z, s.list[hi] = x;
+        }
+        __syncthreads();
       }
-      __syncthreads();
-    }
-  // What lies before each: within its part the sum over the list, before it the histogram's.
-  constexpr int OWN = SM_LIST / SM_THREADS;              // list entries of a thread, one after the other
-  uint64_t w[OWN], vs = 0;
-  int part[OWN], first[OWN], vf = 0;
-  uint32_t key[OWN];
-#pragma unroll
-  for (int q = 0; q < OWN; ++q) {
-    const int i = OWN * threadIdx.x + q;
-    w[q] = 0, part[q] = -1, key[q] = 0;
-    if (i < (int)n) {
-      key[q] = (uint32_t)(s.list[i] >> 32);
-      const double y = me.octaves(key_logit(key[q]));
-      w[q] = me.weight(y);
-      part[q] = me.bucket(y);
-      if (i == 0 || me.bucket(me.octaves(key_logit((uint32_t)(s.list[i - 1] >> 32)))) != part[q]) vf = i;
-    }
-    first[q] = vf;                                       // where its part begins, if among this thread's
-    vs += w[q];
+  }
+  // What lies before each entry: the sum over the list, less where its part begins, and
+  // what lies before the part.  A thread takes `own` entries, one after the other.
+  const int own = (size + THREADS - 1) / THREADS, i0 = own * threadIdx.x, i1 = min(i0 + own, (int)n);
+  auto octaves = [&](int i) { return me.octaves(key_logit((uint32_t)(s.list[i] >> 32))); };
+  uint64_t vs = 0;
+  int vf = 0;
+#pragma unroll 1
+  for (int i = i0; i < i1; ++i) {
+    const double y = octaves(i);
+    vs += me.weight(y);
+    if (i == 0 || me.bucket(octaves(i - 1)) != me.bucket(y)) vf = i;
   }
   uint64_t is = vs;
   int mf = vf;
@@ -542,70 +601,50 @@ __device__ __forceinline__ void draw(SampleShared& s, const Settings& c, const M
     const int of = __shfl_up(mf, d);
     if (lane >= d) is += os, mf = max(mf, of);
   }
-  __syncthreads();
   if (lane == 63) s.wsum[wv] = is, s.wcount[wv] = (uint32_t)mf;
   __syncthreads();
   uint64_t run = is - vs;
-  int from = __shfl_up(mf, 1);
-  if (lane == 0) from = 0;
-  for (int k = 0; k < wv; ++k) run += s.wsum[k], from = max(from, (int)s.wcount[k]);
-  uint64_t* const sums = s.sum2;                       // over the list before each entry
-  uint64_t before[OWN];
-#pragma unroll
-  for (int q = 0; q < OWN; ++q) {
-    before[q] = run;
-    sums[OWN * threadIdx.x + q] = run;
-    run += w[q];
-    first[q] = max(first[q], from);
-  }
-  // the histogram's sums and counts before each of the parts
-  uint32_t* const part_n = s.count2;
-  uint64_t bs = o.before_s;
-  uint32_t bn = o.before_n;
-#pragma unroll
-  for (int i = 0; i < SM_PER; ++i) {
-    const int b = SM_PER * threadIdx.x + i;
-    const uint64_t own = sum[b];
-    if (o.chosen(b)) {
-      s.start[b] = bs;
-      part_n[b] = bn;
-    }
-    bs += own;
-    bn += count[b];
+  int first = __shfl_up(mf, 1);
+  if (lane == 0) first = 0;
+  for (int k = 0; k < wv; ++k) run += s.wsum[k], first = max(first, (int)s.wcount[k]);
+  const uint64_t run0 = run;
+  const int first0 = first;
+#pragma unroll 1
+  for (int i = i0; i < i1; ++i) {
+    s.sum2[i] = run;
+    run += me.weight(octaves(i));
   }
   __syncthreads();
-  uint32_t before_n[OWN];
-#pragma unroll
-  for (int q = 0; q < OWN; ++q) {
-    before_n[q] = 0;
-    if (part[q] < 0) continue;
-    before[q] += s.start[part[q]] - sums[first[q]];
-    before_n[q] = part_n[part[q]] + (OWN * threadIdx.x + q - first[q]);
-  }
-  uint64_t total = o.total;
-  if (o.by_k) {
-#pragma unroll
-    for (int q = 0; q < OWN; ++q)
-      if (part[q] >= 0 && before_n[q] + 1 == (uint32_t)c.top_k) s.total = before[q] + w[q];
-    __syncthreads();
-    total = s.total;
-    __syncthreads();
-  }
-  if (o.by_p) {
-    const uint64_t target = part_of(c.top_p, total);
-#pragma unroll
-    for (int q = 0; q < OWN; ++q)
-      if (part[q] >= 0 && before[q] < target && target <= before[q] + w[q]) s.total = before[q] + w[q];
-    __syncthreads();
-    total = s.total;
-  }
-  const uint64_t target = draw_target(c.u, total);
-#pragma unroll
-  for (int q = 0; q < OWN; ++q)
-    if (part[q] >= 0 && before[q] < target && target <= before[q] + w[q]) {
-      *token = (int32_t)~(uint32_t)s.list[OWN * threadIdx.x + q];
-      *prob = (float)(me.p_of(me.octaves(key_logit(key[q]))) * me.unit / (double)total);
+  // f(entry, the number and weight of what lies before it, its own weight, 1 / p in octaves)
+  auto each = [&](auto f) {
+    uint64_t at = run0;
+    int from = first0;
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) {
+      const double y = octaves(i);
+      const int part = me.bucket(y);
+      const uint64_t w = me.weight(y);
+      if (i == 0 || me.bucket(octaves(i - 1)) != part) from = i;
+      f(i, start_n[part] + (i - from), start_s[part] + at - s.sum2[from], w, y);
+      at += w;
     }
+  };
+#pragma unroll 1
+  for (int step = by_k ? 0 : by_p ? 1 : 2; step < 3; step = step == 0 && !by_p ? 2 : step + 1) {
+    const uint64_t target = step == 0 ? 0 : step == 1 ? part_of(c.top_p, total) : draw_target(c.u, total);
+    each([&](int i, uint32_t before_n, uint64_t before, uint64_t w, double y) {
+      if (step == 0 ? before_n + 1 != (uint32_t)c.top_k : before >= target || target > before + w) return;
+      if (step < 2) {
+        s.total = before + w;
+      } else {
+        *token = (int32_t)~(uint32_t)s.list[i];
+        *prob = (float)(me.p_of(y) * me.unit / (double)total);
+      }
+    });
+    __syncthreads();
+    if (step < 2) total = s.total;
+    __syncthreads();
+  }
 }
 
 __device__ __forceinline__ const void* row_of(const SampleArgs& a, int64_t r) {
@@ -638,7 +677,7 @@ __global__ __launch_bounds__(SM_THREADS) void sample_kernel(SampleArgs a, int sh
   const Measure me = measure_of(c, best, shift);
   fill_histogram(s, me, row, a.bf16, 0, V);
   __syncthreads();
-  const Borders o = borders_of(s, c, s.sum, s.count);
+  const Borders o = borders_of(s, c, s.sum, s.count, s.start, s.count2);
   if (o.chosen_count > SM_LIST) {
     sample_slow(s, me, row, a.bf16, V, c.top_k, c.top_p, c.u, o.total, o.count, a.token + r, a.prob + r);
     return;
@@ -648,7 +687,7 @@ __global__ __launch_bounds__(SM_THREADS) void sample_kernel(SampleArgs a, int sh
   __syncthreads();
   each_chosen(me, o, row, a.bf16, 0, V, [&](uint64_t e) { s.list[atomicAdd(&s.fill, 1u)] = e; });
   __syncthreads();
-  draw(s, c, me, o, s.sum, s.count, o.chosen_count, a.token + r, a.prob + r);
+  draw<SM_THREADS>(s, c, me, o.by_k, o.by_p, o.total, s.start, s.count2, o.chosen_count, a.token + r, a.prob + r);
 }
 
 // ---- several workgroups per row -------------------------------------------------------
@@ -659,9 +698,12 @@ __global__ __launch_bounds__(SM_THREADS) void sample_kernel(SampleArgs a, int sh
 struct RowSpace {
   uint64_t sum[SM_BUCKETS];
   uint64_t list[SM_LIST];
+  uint64_t start_s[SM_BUCKETS];
   uint32_t count[SM_BUCKETS];
+  uint32_t start_n[SM_BUCKETS];
   float best[SM_PARTS];
-  uint32_t fill, first;
+  uint64_t total;
+  uint32_t fill, first, all, chosen, by_k, by_p;
 };
 
 struct Part {
@@ -678,8 +720,11 @@ __device__ __forceinline__ Part part_of_row(const SampleArgs& a, int per) {
   return p;
 }
 __device__ __forceinline__ float row_best(const RowSpace& sp, int parts) {
-  float best = sp.best[0];
-  for (int i = 1; i < parts; ++i) best = fmaxf(best, sp.best[i]);
+  static_assert(SM_PARTS == 64, "a lane for each part");
+  const int lane = threadIdx.x & 63;
+  float best = sp.best[min(lane, parts - 1)];
+#pragma unroll
+  for (int d = 32; d; d >>= 1) best = fmaxf(best, __shfl_xor(best, d));
   return best;
 }
 
@@ -725,13 +770,17 @@ __global__ __launch_bounds__(SM_THREADS) void sample_gather_kernel(SampleArgs a,
   const Settings c = settings_of(a, p.r);
   const float best = row_best(sp, gridDim.x);
   if (!(best > -__builtin_inff()) || c.greedy()) return;
-  const Borders o = borders_of(s, c, sp.sum, sp.count);
+  const bool lead = blockIdx.x == 0;                     // tells the draw what it found
+  const Borders o = borders_of(s, c, sp.sum, sp.count, lead ? sp.start_s : nullptr, lead ? sp.start_n : nullptr);
+  if (lead && threadIdx.x == 0) sp.total = o.total, sp.all = o.count, sp.chosen = o.chosen_count, sp.by_k = o.by_k, sp.by_p = o.by_p;
   if (o.chosen_count > SM_LIST) return;
   each_chosen(measure_of(c, best, shift), o, p.row, a.bf16, p.t0, p.t1, [&](uint64_t e) {
     const uint32_t at = atomicAdd(&sp.fill, 1u);
     if (at < SM_LIST) sp.list[at] = e;
   });
 }
+
+constexpr int SM_DRAW = 256;                             // threads that sort a row's list: fewer wait less for each other
 
 __global__ __launch_bounds__(SM_THREADS) void sample_draw_kernel(SampleArgs a, int parts, int shift, RowSpace* ws) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -740,21 +789,22 @@ __global__ __launch_bounds__(SM_THREADS) void sample_draw_kernel(SampleArgs a, i
   const RowSpace& sp = ws[r];
   const Settings c = settings_of(a, r);
   const float best = row_best(sp, parts);
-  if (!(best > -__builtin_inff()) || c.greedy()) {
-    const bool none = !(best > -__builtin_inff());
+  const bool none = !(best > -__builtin_inff());
+  if (none || c.greedy()) {
     if (threadIdx.x == 0) a.token[r] = none ? -1 : (int32_t)sp.first, a.prob[r] = none ? 0.f : 1.f;
     return;
   }
   const Measure me = measure_of(c, best, shift);
-  const Borders o = borders_of(s, c, sp.sum, sp.count);
-  if (o.chosen_count > SM_LIST) {
+  const uint32_t n = sp.chosen;
+  if (n > SM_LIST) {
     for (int i = threadIdx.x; i < SM_BUCKETS; i += SM_THREADS) s.sum[i] = sp.sum[i], s.count[i] = sp.count[i];
     __syncthreads();
-    sample_slow(s, me, row_of(a, r), a.bf16, (int)a.V, c.top_k, c.top_p, c.u, o.total, o.count, a.token + r, a.prob + r);
+    sample_slow(s, me, row_of(a, r), a.bf16, (int)a.V, c.top_k, c.top_p, c.u, sp.total, sp.all, a.token + r, a.prob + r);
     return;
   }
-  for (int i = threadIdx.x; i < (int)o.chosen_count; i += SM_THREADS) s.list[i] = sp.list[i];
-  draw(s, c, me, o, sp.sum, sp.count, o.chosen_count, a.token + r, a.prob + r);
+  if (threadIdx.x >= SM_DRAW) return;                    // whole waves
+  for (int i = threadIdx.x; i < (int)n; i += SM_DRAW) s.list[i] = sp.list[i];
+  draw<SM_DRAW>(s, c, me, sp.by_k != 0, sp.by_p != 0, sp.total, sp.start_s, sp.start_n, n, a.token + r, a.prob + r);
 }
 
 // Tokens of a part; 0 where a workgroup takes whole rows: few tokens, or rows enough for the CUs.
