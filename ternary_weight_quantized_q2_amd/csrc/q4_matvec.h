@@ -54,6 +54,9 @@ __global__ __launch_bounds__(RT > 2 ? 512 : 1024) void matvec_kernel(MatvecArgs 
   constexpr int NS = 2 * GPB;                            // scales of a unit and column
   constexpr int SW = GM == GROUP_128 ? 2 : NS / 2;       // dwords of scales and of f16 zero points
   constexpr int ZW = ZM == ZERO_F16 || GM == GROUP_128 ? SW : 1;
+  // Where 1 + z / 16 is a bf16 and a lane has several outputs, each step adds
+  // minus its products with x first, which leaves one FMA per output and group in place of two.
+  constexpr bool CHAIN = E > 1 && ZM != ZERO_F16;
   const FusedArgs& a = m.f;
   extern __shared__ __align__(16) uint8_t xs[];
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
@@ -65,7 +68,6 @@ __global__ __launch_bounds__(RT > 2 ? 512 : 1024) void matvec_kernel(MatvecArgs 
   const uint32_t n_out = (uint32_t)a.N >> a.gated;
   const int half = a.gated & si, tile = si >> a.gated;
   float* const red = reinterpret_cast<float*>(xs + sh.sums);
-  int first_u = 0;                                       // first unit of the inputs in use
   const NatConsts kc = q4_nat_consts();
 
   // Rows of x from unit u0 on, 512 inputs per copy.  Piece q of a row lies at
@@ -190,32 +192,27 @@ __global__ __launch_bounds__(RT > 2 ? 512 : 1024) void matvec_kernel(MatvecArgs 
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[i][e] = 0.f;
 #pragma unroll 1
-    for (int u = ki, end = 0;; u += kg) {
-      if (u >= end) {                                    // the same for all waves of the workgroup
-        if (end >= sh.units) break;
-        const int u0 = end;
-        end = min(u0 + sh.chunk_units, sh.units);
-        if (!staged) {
-          xb = xnext;
-          __builtin_amdgcn_s_waitcnt(0);
-          asm volatile("" ::: "memory");
-          clear_x(u0, xb);
-          stage_barrier<63>();                           // these are there, and the ones before are read
-          if (sh.keep) {
-            staged = true;
-          } else {
-            xnext = xs + (xb == xs ? sh.sums / 2 : 0);
-            if (end < sh.units) copy_x(end, xnext);
-            else if (tg + (int)gridDim.x < sh.tile_groups) copy_x(0, xnext);
-          }
+    for (int u0 = 0, end; u0 < sh.units; u0 = end) {     // the same for all waves of the workgroup
+      end = min(u0 + sh.chunk_units, sh.units);
+      if (!staged) {
+        xb = xnext;
+        __builtin_amdgcn_s_waitcnt(0);
+        asm volatile("" ::: "memory");
+        clear_x(u0, xb);
+        stage_barrier<63>();                             // these are there, and the ones before are read
+        if (sh.keep) {
+          staged = true;
+        } else {
+          xnext = xs + (xb == xs ? sh.sums / 2 : 0);
+          if (end < sh.units) copy_x(end, xnext);
+          else if (tg + (int)gridDim.x < sh.tile_groups) copy_x(0, xnext);
         }
-        first_u = u0;
-        u = u0 + ki - kg;
-        continue;
       }
+#pragma unroll 1
+    for (int u = u0 + ki; u < end; u += kg) {
       cur = next;
       load(next);
-      const int at = (u - first_u) * 512;
+      const int at = (u - u0) * 512;
       if constexpr (GM == GROUP_128) {
         if constexpr (ZM == ZERO_CODES) {
 #pragma unroll
@@ -232,6 +229,7 @@ __global__ __launch_bounds__(RT > 2 ? 512 : 1024) void matvec_kernel(MatvecArgs 
       };
       auto zero_of = [&](int i) -> float {
         if constexpr (ZM == ZERO_F16) return f16_to_f32((uint16_t)(GM == GROUP_128 ? cur.z[i] : cur.z[i / 2] >> (16 * (i & 1))));
+        else if constexpr (ZM == ZERO_8) return 8.f;
         else return (float)((GM == GROUP_128 ? cur.z[i] : cur.z[0] >> (4 * i)) & 15u);
       };
       // 16 bytes of a lane are 32 inputs of its column, piece g of the block.  Lane
@@ -260,7 +258,7 @@ __global__ __launch_bounds__(RT > 2 ? 512 : 1024) void matvec_kernel(MatvecArgs 
         }
       }
       auto reg = [](int gr, int t) { return GM == GROUP_32 ? gr : GM == GROUP_64 ? 2 * t + gr : t; };
-      if constexpr (ZM != ZERO_8) {
+      if constexpr (ZM != ZERO_8 || CHAIN) {
         // A group whose codes all equal its zero point is rare: look closer only where
         // the eight codes of some lane's dword are equal.
         uint64_t any = 0;
@@ -288,6 +286,13 @@ __global__ __launch_bounds__(RT > 2 ? 512 : 1024) void matvec_kernel(MatvecArgs 
         // which takes more registers than there are: with several row tiles one after the other.
         if constexpr (RT > 1) asm volatile("" ::: "memory");
         q2_f32x4 sum[RT], tmp[RT];
+        q2_u32x4 ones = sones;
+        if constexpr (CHAIN) {                           // - (1 + z / 16) in every place
+          uint32_t z = 0xBFC0BFC0u;
+          if constexpr (ZM == ZERO_CODES)
+            z = ((GM == GROUP_128 ? cur.z[k] : cur.z[0] >> (4 * k)) & 15u) * 0x00080008u | 0xBF80BF80u;
+          ones = q2_u32x4{z, z, z, z};
+        }
 #pragma unroll
         for (int t = 0; t < STEPS; ++t) {
           const int q = GM == GROUP_32 ? 4 * gr + g : GM == GROUP_64 ? 8 * gr + 4 * (g & 1) + 2 * t + (g >> 1) : 4 * g + t;
@@ -297,8 +302,8 @@ __global__ __launch_bounds__(RT > 2 ? 512 : 1024) void matvec_kernel(MatvecArgs 
           for (int i = 0; i < RT; ++i) {
             const q2_f32x4 none = q2_f32x4{0.f, 0.f, 0.f, 0.f};
             const q2_u32x4 av = *reinterpret_cast<const q2_u32x4*>(xb + xrow[i] + at + 256 * d + 16 * (q ^ swz[i]));
-            sum[i] = mfma(av, sones, t > 0 ? sum[i] : none);
-            tmp[i] = mfma(av, bf, t > 0 ? tmp[i] : none);
+            sum[i] = mfma(av, ones, t == 0 ? none : CHAIN ? tmp[i] : sum[i]);
+            tmp[i] = mfma(av, bf, CHAIN ? sum[i] : t == 0 ? none : tmp[i]);
           }
         }
         const float s = scale_of(k), k4 = ZM == ZERO_8 ? 1.f : 1.f + zero_of(k) * 0.0625f;
@@ -306,31 +311,40 @@ __global__ __launch_bounds__(RT > 2 ? 512 : 1024) void matvec_kernel(MatvecArgs 
         for (int i = 0; i < RT; ++i)
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            float v = __builtin_fmaf(s, __builtin_fmaf(-k4, sum[i][e], tmp[i][e]), acc[i][e]);
+            float v = __builtin_fmaf(s, CHAIN ? tmp[i][e] : __builtin_fmaf(-k4, sum[i][e], tmp[i][e]), acc[i][e]);
             if constexpr (RT > 1) asm volatile("" : "+v"(v));
             acc[i][e] = v;
           }
       }
     }
-    // Partial sums through LDS, added in the waves' order; lane (c, g) holds rows 4 g .. (E == 1: row g).
-    constexpr int VALS = RT * E;
-#pragma unroll
-    for (int i = 0; i < VALS; ++i) red[(wv * VALS + i) * 64 + lane] = acc[i / E][i % E];
-    stage_barrier<63>();
+    }
+    // Partial sums through LDS, added in the waves' order, a row tile at a time: room that
+    // they take is x's.  Lane (c, g) holds rows 4 g .. (E == 1: row g).
 #pragma unroll 1
-    for (int i = wv; i < sh.tiles * VALS; i += waves) {
-      const int t = i / VALS, e = i % VALS, row = E == 1 ? g : 16 * (e / E) + 4 * g + e % E;
-      const uint32_t n = ((uint32_t)tg * sh.tiles + t) * 16 + c;
-      const float* p = red + ((t << a.gated) * kg * VALS + e) * 64 + lane;
-      float v = 0.f, u = 0.f;
-#pragma unroll 4
-      for (int q = 0; q < kg; ++q) v += p[q * 64 * VALS];
-      if (a.gated) {
-        p += kg * 64 * VALS;
-#pragma unroll 4
-        for (int q = 0; q < kg; ++q) u += p[q * 64 * VALS];
+    for (int rt = 0; rt < RT; ++rt) {
+      if (rt > 0) stage_barrier<63>();                   // the last ones are read
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        red[(wv * E + e) * 64 + lane] = acc[0][e];
+#pragma unroll
+        for (int i = 1; i < RT; ++i) acc[i - 1][e] = acc[i][e];
       }
-      if (row < rows && n < n_out) store_out(a, a.bias, n_out, m0 + row, n, v * 16.f, u * 16.f);
+      stage_barrier<63>();
+#pragma unroll 1
+      for (int i = wv; i < sh.tiles * E; i += waves) {
+        const int t = i / E, e = i % E, row = E == 1 ? g : 16 * rt + 4 * g + e;
+        const uint32_t n = ((uint32_t)tg * sh.tiles + t) * 16 + c;
+        const float* p = red + ((t << a.gated) * kg * E + e) * 64 + lane;
+        float v = 0.f, u = 0.f;
+#pragma unroll 4
+        for (int q = 0; q < kg; ++q) v += p[q * 64 * E];
+        if (a.gated) {
+          p += kg * 64 * E;
+#pragma unroll 4
+          for (int q = 0; q < kg; ++q) u += p[q * 64 * E];
+        }
+        if (row < rows && n < n_out) store_out(a, a.bias, n_out, m0 + row, n, v * 16.f, u * 16.f);
+      }
     }
     if (sh.keep && tg + (int)gridDim.x < sh.tile_groups) stage_barrier<63>();        // before the sums of the next tiles
   }
@@ -370,7 +384,7 @@ static hipError_t run_matvec(const MatvecArgs& m, hipStream_t stream) {
   const int ns = a.gated ? 2 * tiles : tiles;
   auto stride = [&](int units) { return (units * 256 + 511) / 512 * 1024; };
   // All of x in LDS where it fits, else two parts of it in turn.
-  const int sum_bytes = kg * ns * 256 * E * RT, part = (MV_LDS - sum_bytes) / 2;
+  const int sum_bytes = kg * ns * 256 * E, part = (MV_LDS - sum_bytes) / 2;
   const int64_t whole = (int64_t)rows * stride(sh.units);
   sh.keep = whole <= lds * 1024 && whole + sum_bytes <= MV_LDS;
   if (!sh.keep) {
