@@ -4,10 +4,10 @@
 // y = epilogue(x W^T), w = (q - z) s with one s and z per group of 32, 64 or a
 // multiple of 128 inputs.  A code decodes to bf16 1 + q / 16 (q2_device.h); per group
 // sum x (1 + q / 16) - (1 + z / 16) sum x = sum x (q - z) / 16 on the matrix cores,
-// exact products and fp32 sums, and one FMA per output applies the group's scale.
-// Without zero points the constant is 1.5 and the row sums run through the same
-// instructions as the products, so a group of codes 8 cancels bit for bit; with them a
-// group whose codes all equal a whole zero point takes a scale of 0.
+// exact products and fp32 sums, and one FMA per output applies the group's scale.  A
+// group whose codes all equal a whole zero point takes a scale of 0, so it adds exactly
+// nothing; where the sums with 1.5, which stands for 8 without zero points, run through
+// the same instructions as the products they cancel bit for bit by themselves.
 #pragma once
 #include "q2_token.h"
 #include <algorithm>
@@ -41,11 +41,12 @@ struct MatvecShape {
 // cold instruction caches, and code that runs once costs a wave about a microsecond per
 // KB: the loop's body appears once, and sizes come from the host.  Captured launches
 // back to back, weights from memory: one row, K = 2560, N = 2 x 9728 in groups of 64
-// 12.0 us (28 MB, 2.3 TB/s; at 4.9 TB/s between the first load and the last, the rest
-// is the launch, the first instructions and the last workgroups), N = 128009 46 us (184
-// MB, 4.0 TB/s); 13 rows, N = 6144 8.1 us; 61 rows, K = 2560, N = 9728 in groups of 128
-// 25 us; 32 rows, K = 4096, N = 128009 in groups of 32 140 us (320 MB), bound by vector
-// instructions: decode, and two FMAs per output and group.
+// 11.5 us (28 MB, 2.4 TB/s; at 4.9 TB/s between the first load and the last, the rest
+// is the launch, the first instructions and the last workgroups), N = 128009 44 us (184
+// MB, 4.2 TB/s); 13 rows, N = 6144 7.4 us; 61 rows, K = 2560, N = 9728 in groups of 128
+// 18.6 us, waits for x and for LDS with one workgroup per CU; 32 rows, K = 4096, N = 128009
+// in groups of 32 120 us (320 MB), bound by vector instructions: decode, and an FMA per
+// output and group.
 template <int GM, int ZM, int E, int RT>
 __global__ __launch_bounds__(RT > 2 ? 512 : 1024) void matvec_kernel(MatvecArgs m, MatvecShape sh) {
   constexpr int GPB = GM == GROUP_32 ? 4 : GM == GROUP_64 ? 2 : 1;        // groups per block
@@ -279,13 +280,36 @@ __global__ __launch_bounds__(RT > 2 ? 512 : 1024) void matvec_kernel(MatvecArgs 
           }
         }
       }
+      // Step j: its x was read a step before, and the sums of the group before are added
+      // up behind its first products: waits for LDS and for the matrix cores overlap.
+      // Left alone the compiler reads and multiplies all groups before it adds any up, which
+      // takes more registers than there are: with several row tiles the reads stay in order.
+      auto read = [&](int j, q2_u32x4(&v)[RT]) {
+        const int d = j / 4, gr = j % 4 / STEPS, t = j % STEPS;
+        const int q = GM == GROUP_32 ? 4 * gr + g : GM == GROUP_64 ? 8 * gr + 4 * (g & 1) + 2 * t + (g >> 1) : 4 * g + t;
 #pragma unroll
-      for (int k = 0; k < NS; ++k) {
-        const int d = k / GPB, gr = k % GPB;
-        // Left alone the compiler reads and multiplies all groups before it adds any up,
-        // which takes more registers than there are: with several row tiles one after the other.
+        for (int i = 0; i < RT; ++i) v[i] = *reinterpret_cast<const q2_u32x4*>(xb + xrow[i] + at + 256 * d + 16 * (q ^ swz[i]));
+      };
+      q2_f32x4 sum[2][RT], tmp[2][RT];
+      auto add_up = [&](int k) {
+        const float s = scale_of(k), k4 = ZM == ZERO_8 ? 1.f : 1.f + zero_of(k) * 0.0625f;
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float t = tmp[k & 1][i][e];
+            float v = __builtin_fmaf(s, CHAIN ? t : __builtin_fmaf(-k4, sum[k & 1][i][e], t), acc[i][e]);
+            if constexpr (RT > 1) asm volatile("" : "+v"(v));
+            acc[i][e] = v;
+          }
+      };
+      q2_u32x4 av[2][RT];
+      read(0, av[0]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int k = j / STEPS, t = j % STEPS, d = j / 4, gr = k % GPB;
         if constexpr (RT > 1) asm volatile("" ::: "memory");
-        q2_f32x4 sum[RT], tmp[RT];
+        if (j + 1 < 8) read(j + 1, av[(j + 1) & 1]);
         q2_u32x4 ones = sones;
         if constexpr (CHAIN) {                           // - (1 + z / 16) in every place
           uint32_t z = 0xBFC0BFC0u;
@@ -293,29 +317,18 @@ __global__ __launch_bounds__(RT > 2 ? 512 : 1024) void matvec_kernel(MatvecArgs 
             z = ((GM == GROUP_128 ? cur.z[k] : cur.z[0] >> (4 * k)) & 15u) * 0x00080008u | 0xBF80BF80u;
           ones = q2_u32x4{z, z, z, z};
         }
+        if constexpr (RT > 1) asm volatile("" : "+v"(cur.w[d][reg(gr, t)]));
+        const q2_u32x4 bf = q4_frag(cur.w[d][reg(gr, t)], kc);
 #pragma unroll
-        for (int t = 0; t < STEPS; ++t) {
-          const int q = GM == GROUP_32 ? 4 * gr + g : GM == GROUP_64 ? 8 * gr + 4 * (g & 1) + 2 * t + (g >> 1) : 4 * g + t;
-          if constexpr (RT > 1) asm volatile("" : "+v"(cur.w[d][reg(gr, t)]));
-          const q2_u32x4 bf = q4_frag(cur.w[d][reg(gr, t)], kc);
-#pragma unroll
-          for (int i = 0; i < RT; ++i) {
-            const q2_f32x4 none = q2_f32x4{0.f, 0.f, 0.f, 0.f};
-            const q2_u32x4 av = *reinterpret_cast<const q2_u32x4*>(xb + xrow[i] + at + 256 * d + 16 * (q ^ swz[i]));
-            sum[i] = mfma(av, ones, t == 0 ? none : CHAIN ? tmp[i] : sum[i]);
-            tmp[i] = mfma(av, bf, CHAIN ? sum[i] : t == 0 ? none : tmp[i]);
-          }
+        for (int i = 0; i < RT; ++i) {
+          const q2_f32x4 none = q2_f32x4{0.f, 0.f, 0.f, 0.f};
+          q2_f32x4 &su = sum[k & 1][i], &tm = tmp[k & 1][i];
+          su = mfma(av[j & 1][i], ones, t == 0 ? none : CHAIN ? tm : su);
+          tm = mfma(av[j & 1][i], bf, CHAIN ? su : t == 0 ? none : tm);
         }
-        const float s = scale_of(k), k4 = ZM == ZERO_8 ? 1.f : 1.f + zero_of(k) * 0.0625f;
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            float v = __builtin_fmaf(s, CHAIN ? tmp[i][e] : __builtin_fmaf(-k4, sum[i][e], tmp[i][e]), acc[i][e]);
-            if constexpr (RT > 1) asm volatile("" : "+v"(v));
-            acc[i][e] = v;
-          }
+        if (t == 0 && k > 0) add_up(k - 1);
       }
+      add_up(NS - 1);
     }
     }
     // Partial sums through LDS, added in the waves' order, a row tile at a time: room that
@@ -358,10 +371,12 @@ static hipError_t run_matvec(const MatvecArgs& m, hipStream_t stream) {
   MatvecShape sh = {};
   sh.units = (int)((a.K + 255) / 256);
   const int64_t out_tiles = (fused_n_out(a) + 15) / 16, strips = a.gated ? 2 * out_tiles : out_tiles;
+  const int64_t row_blocks = (a.M + ROWS - 1) / ROWS;
   // Waves.  One to four rows: about ten for each CU, where the strips are fewer by
   // sharing them; where they are more, two strips by two waves each per workgroup.  More
-  // waves pay more for their start, fewer leave memory idle.  Workgroups of sixteen for
-  // more rows, as few as one per CU: each has all of x in LDS.
+  // waves pay more for their start, fewer leave memory idle.  Workgroups of up to
+  // sixteen for more rows, one per CU, whose x goes to its LDS once: as many tiles for each
+  // as fill the fewest turns of the CUs.
   // One row, K = 2560: 1216 strips 12.3 us with two waves, 14.9 with one, 18.2 with five;
   // 8001 strips 46 in pairs of two waves, 93 with five.  8 rows, K = 4096, 768 strips: 13.0
   // three strips by four waves each, 18.6 one by eight.
@@ -373,11 +388,12 @@ static hipError_t run_matvec(const MatvecArgs& m, hipStream_t stream) {
     kg = strips > 1250 ? 2 : (int)std::clamp<int64_t>(2500 / strips, 1, a.gated ? WAVES / 2 : WAVES);
     lds = 64;
   } else {
-    tiles = (int)std::clamp<int64_t>((strips + 255) / 256, 1, RT > 1 ? WAVES : 8);
-    if (a.gated) tiles = std::max(1, tiles / 2);
+    const int widest = (RT > 1 ? WAVES : 8) / (a.gated ? 2 : 1);
+    most = std::max<int64_t>(1, 256 / row_blocks);
+    const int64_t turns = (out_tiles + most * widest - 1) / (most * widest);
+    tiles = (int)((out_tiles + most * turns - 1) / (most * turns));
     kg = WAVES / (a.gated ? 2 * tiles : tiles);
     lds = 140;
-    most = 256;
   }
   kg = std::min(kg, sh.units);
   kg = (sh.units + (sh.units + kg - 1) / kg - 1) / ((sh.units + kg - 1) / kg);          // the same number of units for all
@@ -410,7 +426,6 @@ static hipError_t run_matvec(const MatvecArgs& m, hipStream_t stream) {
   sh.per = (int)(m.group / BLOCK_K);
   sh.weight_row = (uint32_t)(a.K / 2);
   const int bytes = sh.sums + sum_bytes;
-  const int64_t row_blocks = (a.M + ROWS - 1) / ROWS;
   if (bytes > MV_LDS || kg * ns > WAVES || row_blocks > 65535) return hipErrorInvalidValue;
   hipLaunchKernelGGL((matvec_kernel<GM, ZM, E, RT>), dim3((unsigned)std::min<int64_t>(groups, most), (unsigned)row_blocks), dim3(64 * kg, ns),
                      bytes, stream, m, sh);
@@ -419,9 +434,15 @@ static hipError_t run_matvec(const MatvecArgs& m, hipStream_t stream) {
 
 template <int GM, int ZM>
 static hipError_t pick_matvec(const MatvecArgs& m, hipStream_t stream) {
-  if (m.f.M > 32) return run_matvec<GM, ZM, 4, 4>(m, stream);
-  if (m.f.M > 16) return run_matvec<GM, ZM, 4, 2>(m, stream);
-  return m.f.M > 4 ? run_matvec<GM, ZM, 4, 1>(m, stream) : run_matvec<GM, ZM, 1, 1>(m, stream);
+  if (m.f.M <= 4) return run_matvec<GM, ZM, 1, 1>(m, stream);
+  // More rows share a decoded weight as there is work for all CUs.  In tiles of 16 x 16
+  // outputs, with 16, 32 and 64 rows: 320 tiles (K = 2560) 7.1 / 11.2 us, 640 8.5 / 11.2 / 22.5,
+  // 1216 14.1 / 14.9; 1536 (K = 4096) 18.8 / 17.7, 2432 (K = 2560) 20.0 / 18.5 / 23.2;
+  // 16384 85 / 66 / 70, 32004 167 / 141 / 132.
+  const int64_t work = ((fused_n_out(m.f) + 15) / 16 << m.f.gated) * ((m.f.M + 15) / 16);
+  if (m.f.M <= 16 || work <= 1200) return run_matvec<GM, ZM, 4, 1>(m, stream);
+  if (m.f.M > 32 && work >= 24000) return run_matvec<GM, ZM, 4, 4>(m, stream);
+  return run_matvec<GM, ZM, 4, 2>(m, stream);
 }
 
 template <int GM>

@@ -87,6 +87,42 @@ def test_wide(n, group, k, zero, m):
     check(y[:, torch.from_numpy(cols).to(DEV)], O.bf16_to_f64(xb) @ w.T)
 
 
+@pytest.mark.parametrize("m,n", [(17, 9700), (32, 20010), (33, 20010), (150, 4000), (50, 100010), (130, 45000), (64, 96016)])
+@pytest.mark.parametrize("zero", ZEROS)
+@pytest.mark.parametrize("group,k", [(32, 288), (64, 2624), (128, 384), (384, 1152)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_rows_that_share_a_weight(m, n, group, k, zero, gated):
+    """16, 32 and 64 rows per decoded weight, one and several blocks of rows; sampled columns, and every fifth group of
+    codes equal to its zero point."""
+    groups = k // group
+    g = torch.Generator().manual_seed(412)
+    packed = torch.randint(0, 256, (n, k // 2), dtype=torch.uint8, generator=g)
+    scale = (rnd(2, n, groups).abs() * 0.02).half()
+    z = None
+    if zero == "codes":
+        z = torch.randint(0, 256, (n, (groups + 1) // 2), dtype=torch.uint8, generator=g)
+    elif zero == "f16":
+        z = (torch.rand((n, groups), generator=g) * 15).half()
+        z[:, ::5] = z[:, ::5].round()
+    for i in range(0, groups, 5):
+        c = 8 if z is None else (z[:, i // 2] >> (4 * (i % 2))) & 15 if zero == "codes" else z[:, i].to(torch.uint8)
+        part = torch.as_tensor(c * 17, dtype=torch.uint8)
+        packed[:, i * group // 2:(i + 1) * group // 2] = part if part.dim() == 0 else part[:, None]
+    half = n // 2 if gated else n
+    r = np.random.default_rng(412)
+    cols = np.unique(np.concatenate([np.arange(40), half - 1 - np.arange(40), r.choice(half, 100)]))
+    every = np.concatenate([cols, cols + half]) if gated else cols
+    w = T.weight(packed.numpy()[every], scale.numpy()[every], None if z is None else z.numpy()[every])
+    xb, x = acts(412, m, k)
+    dev = [packed.to(DEV), scale.to(DEV), None if z is None else z.to(DEV)]
+    y = q2.q4_matvec(x, *dev, gated=gated)
+    check(y[:, torch.from_numpy(cols).to(DEV)], O.bf16_to_f64(xb) @ w.T, gated=gated)
+    nothing = torch.zeros_like(scale)
+    nothing[:, ::5] = scale[:, ::5]
+    y = q2.q4_matvec(x, dev[0], nothing.to(DEV), dev[2], gated=gated)
+    assert not y.any()
+
+
 @pytest.mark.parametrize("m", [1, 4, 9, 20, 64])
 @pytest.mark.parametrize("zero", ZEROS)
 @pytest.mark.parametrize("group,k", [(32, 8224), (64, 20480), (128, 16512), (256, 9984)])
