@@ -101,12 +101,10 @@ struct SampleShared {
   uint64_t wsum[SM_WAVES];
   uint32_t wcount[SM_WAVES];
   float wbest[SM_WAVES];
-  struct {
-    uint64_t before, own;
-    int part;
-  } find[6];
   uint64_t base_s, total;
   uint32_t base_n, bucket, n, fill, lo, hi, key, unused;
+  int border_lo[3], border_hi[3];
+  uint32_t all, chosen;
   uint64_t sum[SM_BUCKETS];                              // over all tokens
   uint32_t count[SM_BUCKETS];
   uint64_t list[SM_LIST];
@@ -119,6 +117,7 @@ struct SampleShared {
 struct Measure {
   float best, cut;                                       // no token further than cut from the best has a weight
   double scale, unit, min_p, per_octave;                 // log2(e) / T, 2^S, buckets per halving of p
+  double step;                                           // a bucket's width as a distance of logits
 
   // log2 of 1 / p, at most 1000, where p is 0 in units: also of a masked logit, and of
   // infinity times zero.
@@ -157,6 +156,16 @@ struct Measure {
   __device__ __forceinline__ bool near(float v) const { return !(best - v > cut); }
 };
 
+// Inclusive sums over the lanes.
+__device__ __forceinline__ void scan_lanes(uint64_t& s, uint32_t& n) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint64_t os = __shfl_up(s, d);
+    const uint32_t on = __shfl_up(n, d);
+    if (lane >= d) s += os, n += on;
+  }
+}
 // Sums before this thread's SM_PER buckets, and the totals.
 __device__ __forceinline__ void scan_buckets(SampleShared& s, const uint64_t (&own_s)[SM_PER], const uint32_t (&own_n)[SM_PER],
                                              uint64_t& before_s, uint32_t& before_n, uint64_t& total_s, uint32_t& total_n) {
@@ -167,25 +176,18 @@ __device__ __forceinline__ void scan_buckets(SampleShared& s, const uint64_t (&o
   for (int i = 0; i < SM_PER; ++i) vs += own_s[i], vn += own_n[i];
   uint64_t is = vs;
   uint32_t in = vn;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint64_t os = __shfl_up(is, d);
-    const uint32_t on = __shfl_up(in, d);
-    if (lane >= d) is += os, in += on;
-  }
+  scan_lanes(is, in);
   __syncthreads();                                       // the waves' sums of an earlier scan are read
   if (lane == 63) s.wsum[wv] = is, s.wcount[wv] = in;
   __syncthreads();
+  uint64_t ws = lane < SM_WAVES ? s.wsum[lane] : 0;
+  uint32_t wn = lane < SM_WAVES ? s.wcount[lane] : 0;
+  scan_lanes(ws, wn);
+  total_s = __shfl(ws, 63);
+  total_n = __shfl(wn, 63);
   before_s = is - vs;
   before_n = in - vn;
-  total_s = 0;
-  total_n = 0;
-#pragma unroll
-  for (int w = 0; w < SM_WAVES; ++w) {
-    if (w < wv) before_s += s.wsum[w], before_n += s.wcount[w];
-    total_s += s.wsum[w];
-    total_n += s.wcount[w];
-  }
+  if (wv > 0) before_s += __shfl(ws, wv - 1), before_n += __shfl(wn, wv - 1);
 }
 
 // The first place of the order where the cumulative count (by_count) or weight reaches
@@ -373,6 +375,11 @@ __device__ __noinline__ void sample_slow(SampleShared& s, const Measure& me, con
 }
 
 // ---- a row's steps -----------------------------------------------------------------
+// What S, and with it the number of buckets per halving of p, comes to.
+struct SampleUnits {
+  double unit, per_octave, octaves_per;                  // 2^S; buckets and their inverse
+  float reach;                                           // octaves to half a unit
+};
 struct Settings {
   float temperature, top_p, min_p, u;
   int32_t top_k;
@@ -384,33 +391,37 @@ __device__ __forceinline__ Settings settings_of(const SampleArgs& a, int64_t r) 
   return Settings{a.temperature ? a.temperature[r] : a.temperature_all, a.top_p ? a.top_p[r] : a.top_p_all,
                   a.min_p ? a.min_p[r] : a.min_p_all, a.u[r], a.top_k ? a.top_k[r] : a.top_k_all};
 }
-__device__ __forceinline__ Measure measure_of(const Settings& c, float best, int shift) {
+__device__ __forceinline__ Measure measure_of(const Settings& c, float best, const SampleUnits& of) {
   Measure me;
+  const double half = 0.69314718055994530942 * (double)c.temperature;    // the distance that halves p
   me.best = best;
   me.scale = 1.4426950408889634 / (double)c.temperature;
-  me.unit = __builtin_bit_cast(double, (uint64_t)(1023 + shift) << 52);
+  me.unit = of.unit;
   me.min_p = c.min_p > 0.f ? (double)c.min_p : 0.0;
-  me.per_octave = (double)SM_BUCKETS / (shift + 1);
+  me.per_octave = of.per_octave;
+  me.step = half * of.octaves_per;
   // Half a unit is 2^-(S + 1); min-p cuts nearer.  A little further out: the exact tests come behind it.
-  double reach = shift + 1.01;
-  if (c.min_p > 0.f) reach = std::min(reach, 0.01 - (double)log2f(c.min_p));
-  me.cut = (float)(reach / me.scale * 1.000001);
+  float reach = of.reach;
+  if (c.min_p > 0.f) reach = fminf(reach, 0.01f - __builtin_amdgcn_logf(c.min_p));     // log2
+  me.cut = (float)(reach * half * 1.000001);
   return me;
 }
 
+__device__ __forceinline__ float max_of_lanes(float v) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
+  return v;
+}
 // The largest of the range's logits, in all threads.
 __device__ __forceinline__ float best_of(SampleShared& s, const void* row, int bf16, int t0, int t1) {
   float best = -__builtin_inff();
   each_four(row, bf16, t0, t1, [&](const float(&x)[4], int, int) {                     // a NaN is dropped
     best = fmaxf(best, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
   });
-#pragma unroll
-  for (int d = 32; d; d >>= 1) best = fmaxf(best, __shfl_xor(best, d));
+  best = max_of_lanes(best);
   if ((threadIdx.x & 63) == 0) s.wbest[threadIdx.x >> 6] = best;
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < SM_WAVES; ++w) best = fmaxf(best, s.wbest[w]);
-  return best;
+  return max_of_lanes(s.wbest[threadIdx.x & (SM_WAVES - 1)]);
 }
 // The range's first token that has the largest logit, ~0 without one, by wave.
 __device__ __forceinline__ uint32_t first_of(const void* row, int bf16, int t0, int t1, float best) {
@@ -459,56 +470,114 @@ struct Borders {
     return (b >= lo[0] && b <= hi[0]) || (b >= lo[1] && b <= hi[1]) || (b >= lo[2] && b <= hi[2]);
   }
 };
-// start_s, start_n, where given: for the chosen parts, what lies before them.
-__device__ __forceinline__ Borders borders_of(SampleShared& s, const Settings& c, const uint64_t* sum, const uint32_t* count,
+// The parts' sums and counts, SM_PER of each thread, are in s.sum and s.count.  start_s,
+// start_n, where given: for the chosen parts, what lies before them.  One wave looks for
+// the borders, while the fifteen others wait: sixteen that find the same take four turns of
+// each SIMD for it (5 us in place of 3).
+__device__ __forceinline__ Borders borders_of(SampleShared& s, const Settings& c, const uint64_t (&vs)[SM_PER], const uint32_t (&vn)[SM_PER],
                                               uint64_t* start_s, uint32_t* start_n) {
-  Borders o;
-  uint64_t vs[SM_PER], bs0;
-  uint32_t vn[SM_PER], bn0;
+  static_assert(SM_WAVES <= 64 && SM_PER <= 64 && SM_LIST >= SM_THREADS + SM_THREADS / 2, "one lane each, room in the list");
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  uint64_t* const upto_s = s.list;                       // a thread's parts and those before them in its wave
+  uint32_t* const upto_n = reinterpret_cast<uint32_t*>(s.list + SM_THREADS);
+  uint64_t is = 0;
+  uint32_t in = 0;
 #pragma unroll
-  for (int i = 0; i < SM_PER; ++i) vs[i] = sum[SM_PER * threadIdx.x + i], vn[i] = count[SM_PER * threadIdx.x + i];
-  scan_buckets(s, vs, vn, bs0, bn0, o.total, o.count);
+  for (int i = 0; i < SM_PER; ++i) is += vs[i], in += vn[i];
+  const uint64_t own_s = is;
+  const uint32_t own_n = in;
+  scan_lanes(is, in);
+  upto_s[threadIdx.x] = is;
+  upto_n[threadIdx.x] = in;
+  if (lane == 63) s.wsum[wv] = is, s.wcount[wv] = in;
+  __syncthreads();
+  if (wv == 0) {
+    const uint64_t wave_s = lane < SM_WAVES ? s.wsum[lane] : 0;
+    const uint32_t wave_n = lane < SM_WAVES ? s.wcount[lane] : 0;
+    uint64_t ws = wave_s;
+    uint32_t wn = wave_n;
+    scan_lanes(ws, wn);
+    const uint64_t total = __shfl(ws, 63);
+    const uint32_t all = __shfl(wn, 63);
+    const bool by_k = c.top_k > 0 && (uint32_t)c.top_k < all, by_p = c.top_p < 1.f;
+    uint64_t least = total, most = total;                // bounds of the sum of what is left
+    uint32_t chosen = 0, next_n = 0;
+#pragma unroll 1
+    for (int border = by_k ? 0 : by_p ? 1 : 2; border < 3; border = border == 0 && !by_p ? 2 : border + 1) {
+      uint64_t last_target = 0, before = 0, own = 0;
+      uint32_t before_n = 0, from_n = 0, own_parts = 0;
+      int part = 0;
+#pragma unroll 1
+      for (int end = 0; end < 2; ++end) {
+        const uint64_t left = end ? most : least;
+        const uint64_t target = border == 0 ? (uint64_t)c.top_k : border == 1 ? part_of(c.top_p, left) : draw_target(c.u, left);
+        if (end == 0 || target != last_target) {
+          // the part that reaches the target: its wave, its thread there, its place
+          const uint64_t w = __builtin_amdgcn_ballot_w64(lane < SM_WAVES && (border ? ws : (uint64_t)wn) >= target);
+          const int at = __builtin_ctzll(w);
+          const uint64_t base_s = __shfl(ws - wave_s, at);
+          const uint32_t base_n = __shfl(wn - wave_n, at);
+          const uint64_t ts = base_s + upto_s[64 * at + lane];
+          const uint32_t tn = base_n + upto_n[64 * at + lane];
+          const int th = __builtin_ctzll(__builtin_amdgcn_ballot_w64((border ? ts : (uint64_t)tn) >= target));
+          const int first = SM_PER * (64 * at + th);
+          before = th ? __shfl(ts, th - 1) : base_s;
+          before_n = th ? __shfl(tn, th - 1) : base_n;
+          part = first;
+#pragma unroll 1
+          for (;; ++part) {
+            own = s.sum[part];
+            own_parts = s.count[part];
+            if (part == first + SM_PER - 1 || (border ? before + own : (uint64_t)before_n + own_parts) >= target) break;
+            before += own;
+            before_n += own_parts;
+          }
+        }
+        if (end == 0) {
+          if (lane == 0) s.border_lo[border] = part;
+          least = before + 1;
+          from_n = before_n;
+        }
+        last_target = target;
+      }
+      if (lane == 0) s.border_hi[border] = part;
+      // The next border's bounds; `most` was this one's until here.  A later border's
+      // parts lie at or before this one's: what both hold counts once.
+      most = before + own;
+      const uint32_t to_n = before_n + own_parts;
+      const bool first_border = border == 0 || (border == 1 && !by_k) || (border == 2 && !by_k && !by_p);
+      chosen += first_border ? to_n - from_n : min(to_n, next_n) - min(from_n, next_n);
+      next_n = first_border ? from_n : min(next_n, from_n);
+    }
+    if (lane < SM_WAVES) s.wsum[lane] = ws - wave_s, s.wcount[lane] = wn - wave_n;
+    if (lane == 0) {
+      if (!by_k) s.border_lo[0] = 0, s.border_hi[0] = -1;
+      if (!by_p) s.border_lo[1] = 0, s.border_hi[1] = -1;
+      s.total = total;
+      s.all = all;
+      s.chosen = chosen;
+    }
+  }
+  __syncthreads();
+  Borders o;
+  o.total = s.total;
+  o.count = s.all;
+  o.chosen_count = s.chosen;
   o.by_k = c.top_k > 0 && (uint32_t)c.top_k < o.count;
   o.by_p = c.top_p < 1.f;
-  o.lo[0] = o.lo[1] = o.lo[2] = 0;
-  o.hi[0] = o.hi[1] = o.hi[2] = -1;
-  uint64_t least = o.total, most = o.total;              // bounds of the sum of what is left
-  if (threadIdx.x == 0) s.fill = 0;
-#pragma unroll 1
-  for (int border = o.by_k ? 0 : o.by_p ? 1 : 2; border < 3; border = border == 0 && !o.by_p ? 2 : border + 1) {
-    const uint64_t first = border == 0 ? (uint64_t)c.top_k : border == 1 ? part_of(c.top_p, least) : draw_target(c.u, least);
-    const uint64_t second = border == 0 ? first : border == 1 ? part_of(c.top_p, most) : draw_target(c.u, most);
-    uint64_t bs = bs0, bn = bn0;
 #pragma unroll
-    for (int i = 0; i < SM_PER; ++i) {                   // the part that reaches a target, what lies before it, its own sum
-      const uint64_t before = border == 0 ? bn : bs, reach = before + (border == 0 ? vn[i] : vs[i]);
-      if (before < first && first <= reach) s.find[2 * border] = {bs, vs[i], SM_PER * (int)threadIdx.x + i};
-      if (before < second && second <= reach) s.find[2 * border + 1] = {bs, vs[i], SM_PER * (int)threadIdx.x + i};
-      bs += vs[i];
-      bn += vn[i];
-    }
-    __syncthreads();
-    const int lo = s.find[2 * border].part, hi = s.find[2 * border + 1].part;
-    least = s.find[2 * border].before + 1;
-    most = s.find[2 * border + 1].before + s.find[2 * border + 1].own;
-    if (border == 0) o.lo[0] = lo, o.hi[0] = hi;
-    else if (border == 1) o.lo[1] = lo, o.hi[1] = hi;
-    else o.lo[2] = lo, o.hi[2] = hi;
-  }
-  uint32_t n = 0;
+  for (int j = 0; j < 3; ++j) o.lo[j] = s.border_lo[j], o.hi[j] = s.border_hi[j];
+  if (start_s) {
+    uint64_t before_s = s.wsum[wv] + is - own_s;
+    uint32_t before_n = s.wcount[wv] + in - own_n;
 #pragma unroll
-  for (int i = 0; i < SM_PER; ++i) {
-    const int b = SM_PER * threadIdx.x + i;
-    if (o.chosen(b)) {
-      n += vn[i];
-      if (start_s) start_s[b] = bs0, start_n[b] = bn0;
+    for (int i = 0; i < SM_PER; ++i) {
+      const int b = SM_PER * threadIdx.x + i;
+      if (o.chosen(b)) start_s[b] = before_s, start_n[b] = before_n;
+      before_s += vs[i];
+      before_n += vn[i];
     }
-    bs0 += vs[i];
-    bn0 += vn[i];
   }
-  if (n) atomicAdd(&s.fill, n);
-  __syncthreads();
-  o.chosen_count = s.fill;
   return o;
 }
 
@@ -518,13 +587,12 @@ __device__ __forceinline__ Borders borders_of(SampleShared& s, const Settings& c
 // range that holds the three.  Distances are not negative and are compared by their bits.
 template <class F>
 __device__ __forceinline__ void each_chosen(const Measure& me, const Borders& o, const void* row, int bf16, int t0, int t1, F f) {
-  const double step = 1.0 / (me.per_octave * me.scale);
   uint32_t from[3], over[3], lo = 0xFFFFFFFFu, hi = 0;
 #pragma unroll
   for (int j = 0; j < 3; ++j) {                          // a little wider: the exact test comes behind it
     const bool none = o.lo[j] > o.hi[j], all = !(me.best < __builtin_inff());          // its own distance is no number
-    const uint32_t first = all ? 0u : __builtin_bit_cast(uint32_t, (float)(o.lo[j] * step * (1 - 1e-6)));
-    const uint32_t last = all || o.hi[j] == SM_BUCKETS - 1 ? 0xFFFFFFFFu : __builtin_bit_cast(uint32_t, (float)((o.hi[j] + 1) * step * (1 + 1e-6)));
+    const uint32_t first = all || o.lo[j] == 0 ? 0u : __builtin_bit_cast(uint32_t, (float)(o.lo[j] * me.step * (1 - 1e-6)));
+    const uint32_t last = all || o.hi[j] == SM_BUCKETS - 1 ? 0xFFFFFFFFu : __builtin_bit_cast(uint32_t, (float)((o.hi[j] + 1) * me.step * (1 + 1e-6)));
     from[j] = none ? 0xFFFFFFFFu : first;
     over[j] = none ? 0u : last - first;
     if (!none) lo = min(lo, first), hi = max(hi, last);
@@ -582,63 +650,66 @@ __device__ __forceinline__ void draw(SampleShared& s, const Settings& c, const M
       }
   }
   // What lies before each entry: the sum over the list, less where its part begins, and
-  // what lies before the part.  A thread takes `own` entries, one after the other.
+  // what lies before the part.  A thread takes `own` entries, one after the other; their
+  // weights and parts lie where the histogram was.
   const int own = (size + THREADS - 1) / THREADS, i0 = own * threadIdx.x, i1 = min(i0 + own, (int)n);
   auto octaves = [&](int i) { return me.octaves(key_logit((uint32_t)(s.list[i] >> 32))); };
   uint64_t vs = 0;
-  int vf = 0;
 #pragma unroll 1
   for (int i = i0; i < i1; ++i) {
     const double y = octaves(i);
-    vs += me.weight(y);
-    if (i == 0 || me.bucket(octaves(i - 1)) != me.bucket(y)) vf = i;
+    const uint64_t w = me.weight(y);
+    s.sum[i] = w;
+    s.count[i] = (uint32_t)me.bucket(y);
+    vs += w;
   }
+  __syncthreads();
+  uint32_t vf = 0;                                       // the last entry that begins a part
+#pragma unroll 1
+  for (int i = max(i0, 1); i < i1; ++i)
+    if (s.count[i - 1] != s.count[i]) vf = i;
   uint64_t is = vs;
-  int mf = vf;
+  uint32_t mf = vf;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const uint64_t os = __shfl_up(is, d);
-    const int of = __shfl_up(mf, d);
+    const uint32_t of = __shfl_up(mf, d);
     if (lane >= d) is += os, mf = max(mf, of);
   }
-  if (lane == 63) s.wsum[wv] = is, s.wcount[wv] = (uint32_t)mf;
+  if (lane == 63) s.wsum[wv] = is, s.wcount[wv] = mf;
   __syncthreads();
   uint64_t run = is - vs;
-  int first = __shfl_up(mf, 1);
+  uint32_t first = __shfl_up(mf, 1);
   if (lane == 0) first = 0;
-  for (int k = 0; k < wv; ++k) run += s.wsum[k], first = max(first, (int)s.wcount[k]);
-  const uint64_t run0 = run;
-  const int first0 = first;
 #pragma unroll 1
-  for (int i = i0; i < i1; ++i) {
-    s.sum2[i] = run;
-    run += me.weight(octaves(i));
-  }
+  for (int k = 0; k < wv; ++k) run += s.wsum[k], first = max(first, s.wcount[k]);
+  const uint64_t run0 = run;
+#pragma unroll 1
+  for (int i = i0; i < i1; ++i) s.sum2[i] = run, run += s.sum[i];
   __syncthreads();
-  // f(entry, the number and weight of what lies before it, its own weight, 1 / p in octaves)
+  // f(entry, the number and weight of what lies before it, its own weight)
   auto each = [&](auto f) {
     uint64_t at = run0;
-    int from = first0;
+    uint32_t from = first;
 #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
-      const double y = octaves(i);
-      const int part = me.bucket(y);
-      const uint64_t w = me.weight(y);
-      if (i == 0 || me.bucket(octaves(i - 1)) != part) from = i;
-      f(i, start_n[part] + (i - from), start_s[part] + at - s.sum2[from], w, y);
+      const uint32_t part = s.count[i];
+      const uint64_t w = s.sum[i];
+      if (i > 0 && s.count[i - 1] != part) from = i;
+      f(i, start_n[part] + (i - from), start_s[part] + at - s.sum2[from], w);
       at += w;
     }
   };
 #pragma unroll 1
   for (int step = by_k ? 0 : by_p ? 1 : 2; step < 3; step = step == 0 && !by_p ? 2 : step + 1) {
     const uint64_t target = step == 0 ? 0 : step == 1 ? part_of(c.top_p, total) : draw_target(c.u, total);
-    each([&](int i, uint32_t before_n, uint64_t before, uint64_t w, double y) {
+    each([&](int i, uint32_t before_n, uint64_t before, uint64_t w) {
       if (step == 0 ? before_n + 1 != (uint32_t)c.top_k : before >= target || target > before + w) return;
       if (step < 2) {
         s.total = before + w;
       } else {
         *token = (int32_t)~(uint32_t)s.list[i];
-        *prob = (float)(me.p_of(y) * me.unit / (double)total);
+        *prob = (float)(me.p_of(octaves(i)) * me.unit / (double)total);
       }
     });
     __syncthreads();
@@ -652,7 +723,7 @@ __device__ __forceinline__ const void* row_of(const SampleArgs& a, int64_t r) {
 }
 
 // ---- a workgroup per row ------------------------------------------------------------
-__global__ __launch_bounds__(SM_THREADS) void sample_kernel(SampleArgs a, int shift) {
+__global__ __launch_bounds__(SM_THREADS) void sample_kernel(SampleArgs a, SampleUnits of) {
   extern __shared__ __align__(16) uint8_t smem[];
   SampleShared& s = *reinterpret_cast<SampleShared*>(smem);
   const int64_t r = blockIdx.x + (int64_t)blockIdx.y * GRID_X;
@@ -674,15 +745,18 @@ __global__ __launch_bounds__(SM_THREADS) void sample_kernel(SampleArgs a, int sh
     if (threadIdx.x == 0) a.token[r] = (int32_t)s.lo, a.prob[r] = 1.f;
     return;
   }
-  const Measure me = measure_of(c, best, shift);
+  const Measure me = measure_of(c, best, of);
   fill_histogram(s, me, row, a.bf16, 0, V);
   __syncthreads();
-  const Borders o = borders_of(s, c, s.sum, s.count, s.start, s.count2);
+  uint64_t vs[SM_PER];
+  uint32_t vn[SM_PER];
+#pragma unroll
+  for (int i = 0; i < SM_PER; ++i) vs[i] = s.sum[SM_PER * threadIdx.x + i], vn[i] = s.count[SM_PER * threadIdx.x + i];
+  const Borders o = borders_of(s, c, vs, vn, s.start, s.count2);
   if (o.chosen_count > SM_LIST) {
     sample_slow(s, me, row, a.bf16, V, c.top_k, c.top_p, c.u, o.total, o.count, a.token + r, a.prob + r);
     return;
   }
-  __syncthreads();
   if (threadIdx.x == 0) s.fill = 0;
   __syncthreads();
   each_chosen(me, o, row, a.bf16, 0, V, [&](uint64_t e) { s.list[atomicAdd(&s.fill, 1u)] = e; });
@@ -721,11 +795,7 @@ __device__ __forceinline__ Part part_of_row(const SampleArgs& a, int per) {
 }
 __device__ __forceinline__ float row_best(const RowSpace& sp, int parts) {
   static_assert(SM_PARTS == 64, "a lane for each part");
-  const int lane = threadIdx.x & 63;
-  float best = sp.best[min(lane, parts - 1)];
-#pragma unroll
-  for (int d = 32; d; d >>= 1) best = fmaxf(best, __shfl_xor(best, d));
-  return best;
+  return max_of_lanes(sp.best[min((int)threadIdx.x & 63, parts - 1)]);
 }
 
 __global__ __launch_bounds__(SM_THREADS) void sample_best_kernel(SampleArgs a, int per, RowSpace* ws) {
@@ -738,7 +808,7 @@ __global__ __launch_bounds__(SM_THREADS) void sample_best_kernel(SampleArgs a, i
   if (threadIdx.x == 0) sp.best[blockIdx.x] = best;
 }
 
-__global__ __launch_bounds__(SM_THREADS) void sample_histogram_kernel(SampleArgs a, int per, int shift, RowSpace* ws) {
+__global__ __launch_bounds__(SM_THREADS) void sample_histogram_kernel(SampleArgs a, int per, SampleUnits of, RowSpace* ws) {
   extern __shared__ __align__(16) uint8_t smem[];
   SampleShared& s = *reinterpret_cast<SampleShared*>(smem);
   const Part p = part_of_row(a, per);
@@ -753,7 +823,7 @@ __global__ __launch_bounds__(SM_THREADS) void sample_histogram_kernel(SampleArgs
   }
   for (int i = threadIdx.x; i < SM_BUCKETS; i += SM_THREADS) s.sum[i] = 0, s.count[i] = 0;
   __syncthreads();
-  fill_histogram(s, measure_of(c, best, shift), p.row, a.bf16, p.t0, p.t1);
+  fill_histogram(s, measure_of(c, best, of), p.row, a.bf16, p.t0, p.t1);
   __syncthreads();
   for (int i = threadIdx.x; i < SM_BUCKETS; i += SM_THREADS) {
     if (s.count[i] == 0) continue;
@@ -762,7 +832,7 @@ __global__ __launch_bounds__(SM_THREADS) void sample_histogram_kernel(SampleArgs
   }
 }
 
-__global__ __launch_bounds__(SM_THREADS) void sample_gather_kernel(SampleArgs a, int per, int shift, RowSpace* ws) {
+__global__ __launch_bounds__(SM_THREADS) void sample_gather_kernel(SampleArgs a, int per, SampleUnits of, RowSpace* ws) {
   extern __shared__ __align__(16) uint8_t smem[];
   SampleShared& s = *reinterpret_cast<SampleShared*>(smem);
   const Part p = part_of_row(a, per);
@@ -771,10 +841,18 @@ __global__ __launch_bounds__(SM_THREADS) void sample_gather_kernel(SampleArgs a,
   const float best = row_best(sp, gridDim.x);
   if (!(best > -__builtin_inff()) || c.greedy()) return;
   const bool lead = blockIdx.x == 0;                     // tells the draw what it found
-  const Borders o = borders_of(s, c, sp.sum, sp.count, lead ? sp.start_s : nullptr, lead ? sp.start_n : nullptr);
+  uint64_t vs[SM_PER];
+  uint32_t vn[SM_PER];
+#pragma unroll
+  for (int i = 0; i < SM_PER; ++i) {
+    const int b = SM_PER * threadIdx.x + i;
+    s.sum[b] = vs[i] = sp.sum[b];
+    s.count[b] = vn[i] = sp.count[b];
+  }
+  const Borders o = borders_of(s, c, vs, vn, lead ? sp.start_s : nullptr, lead ? sp.start_n : nullptr);
   if (lead && threadIdx.x == 0) sp.total = o.total, sp.all = o.count, sp.chosen = o.chosen_count, sp.by_k = o.by_k, sp.by_p = o.by_p;
   if (o.chosen_count > SM_LIST) return;
-  each_chosen(measure_of(c, best, shift), o, p.row, a.bf16, p.t0, p.t1, [&](uint64_t e) {
+  each_chosen(measure_of(c, best, of), o, p.row, a.bf16, p.t0, p.t1, [&](uint64_t e) {
     const uint32_t at = atomicAdd(&sp.fill, 1u);
     if (at < SM_LIST) sp.list[at] = e;
   });
@@ -782,7 +860,7 @@ __global__ __launch_bounds__(SM_THREADS) void sample_gather_kernel(SampleArgs a,
 
 constexpr int SM_DRAW = 256;                             // threads that sort a row's list: fewer wait less for each other
 
-__global__ __launch_bounds__(SM_THREADS) void sample_draw_kernel(SampleArgs a, int parts, int shift, RowSpace* ws) {
+__global__ __launch_bounds__(SM_THREADS) void sample_draw_kernel(SampleArgs a, int parts, SampleUnits of, RowSpace* ws) {
   extern __shared__ __align__(16) uint8_t smem[];
   SampleShared& s = *reinterpret_cast<SampleShared*>(smem);
   const int64_t r = blockIdx.x;
@@ -794,7 +872,7 @@ __global__ __launch_bounds__(SM_THREADS) void sample_draw_kernel(SampleArgs a, i
     if (threadIdx.x == 0) a.token[r] = none ? -1 : (int32_t)sp.first, a.prob[r] = none ? 0.f : 1.f;
     return;
   }
-  const Measure me = measure_of(c, best, shift);
+  const Measure me = measure_of(c, best, of);
   const uint32_t n = sp.chosen;
   if (n > SM_LIST) {
     for (int i = threadIdx.x; i < SM_BUCKETS; i += SM_THREADS) s.sum[i] = sp.sum[i], s.count[i] = sp.count[i];
@@ -822,17 +900,18 @@ hipError_t launch_sample(const SampleArgs& a, void* workspace, hipStream_t strea
   int bits = 0;
   while (((int64_t)1 << bits) < a.V) ++bits;
   const int shift = std::min(62 - bits, 51), per = part_tokens(a.B, a.V);
-  constexpr size_t LDS = sizeof(SampleShared), SMALL = offsetof(SampleShared, sum), HIST = offsetof(SampleShared, list);
+  const SampleUnits of = {(double)(1ull << shift), (double)SM_BUCKETS / (shift + 1), (shift + 1) / (double)SM_BUCKETS, shift + 1.01f};
+  constexpr size_t LDS = sizeof(SampleShared), SMALL = offsetof(SampleShared, sum), HIST = offsetof(SampleShared, list), LIST = offsetof(SampleShared, sum2);
   if (per == 0) {
-    hipLaunchKernelGGL(sample_kernel, grid_of(a.B), dim3(SM_THREADS), LDS, stream, a, shift);
+    hipLaunchKernelGGL(sample_kernel, grid_of(a.B), dim3(SM_THREADS), LDS, stream, a, of);
     return hipGetLastError();
   }
   RowSpace* const ws = static_cast<RowSpace*>(workspace);
   const dim3 grid((unsigned)((a.V + per - 1) / per), (unsigned)a.B);
   hipLaunchKernelGGL(sample_best_kernel, grid, dim3(SM_THREADS), SMALL, stream, a, per, ws);
-  hipLaunchKernelGGL(sample_histogram_kernel, grid, dim3(SM_THREADS), HIST, stream, a, per, shift, ws);
-  hipLaunchKernelGGL(sample_gather_kernel, grid, dim3(SM_THREADS), SMALL, stream, a, per, shift, ws);
-  hipLaunchKernelGGL(sample_draw_kernel, dim3((unsigned)a.B), dim3(SM_THREADS), LDS, stream, a, (int)grid.x, shift, ws);
+  hipLaunchKernelGGL(sample_histogram_kernel, grid, dim3(SM_THREADS), HIST, stream, a, per, of, ws);
+  hipLaunchKernelGGL(sample_gather_kernel, grid, dim3(SM_THREADS), LIST, stream, a, per, of, ws);
+  hipLaunchKernelGGL(sample_draw_kernel, dim3((unsigned)a.B), dim3(SM_THREADS), LDS, stream, a, (int)grid.x, of, ws);
   return hipGetLastError();
 }
 
