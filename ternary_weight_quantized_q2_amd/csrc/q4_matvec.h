@@ -210,126 +210,126 @@ __global__ __launch_bounds__(RT > 2 ? 512 : 1024) void matvec_kernel(MatvecArgs 
         }
       }
 #pragma unroll 1
-    for (int u = u0 + ki; u < end; u += kg) {
-      cur = next;
-      load(next);
-      const int at = (u - u0) * 512;
-      if constexpr (GM == GROUP_128) {
-        if constexpr (ZM == ZERO_CODES) {
+      for (int u = u0 + ki; u < end; u += kg) {
+        cur = next;
+        load(next);
+        const int at = (u - u0) * 512;
+        if constexpr (GM == GROUP_128) {
+          if constexpr (ZM == ZERO_CODES) {
 #pragma unroll
-          for (int d = 0; d < 2; ++d) cur.z[d] >>= 4 * (group_of(2 * u + d) & 1);
+            for (int d = 0; d < 2; ++d) cur.z[d] >>= 4 * (group_of(2 * u + d) & 1);
+          }
+        } else if (NS * (u + 1) > sh.last_group + 1) {     // the unit that the row ends in
+          const int n = NS * u - first_scale(u);
+          shift_halves(cur.s, n);
+          if constexpr (ZM == ZERO_F16) shift_halves(cur.z, n);
+          if constexpr (ZM == ZERO_CODES) cur.z[0] >>= 8 * (GPB * u - first_code(u));
         }
-      } else if (NS * (u + 1) > sh.last_group + 1) {     // the unit that the row ends in
-        const int n = NS * u - first_scale(u);
-        shift_halves(cur.s, n);
-        if constexpr (ZM == ZERO_F16) shift_halves(cur.z, n);
-        if constexpr (ZM == ZERO_CODES) cur.z[0] >>= 8 * (GPB * u - first_code(u));
-      }
-      auto scale_of = [&](int i) {
-        return f16_to_f32((uint16_t)(GM == GROUP_128 ? cur.s[i] : cur.s[i / 2] >> (16 * (i & 1))));
-      };
-      auto zero_of = [&](int i) -> float {
-        if constexpr (ZM == ZERO_F16) return f16_to_f32((uint16_t)(GM == GROUP_128 ? cur.z[i] : cur.z[i / 2] >> (16 * (i & 1))));
-        else if constexpr (ZM == ZERO_8) return 8.f;
-        else return (float)((GM == GROUP_128 ? cur.z[i] : cur.z[0] >> (4 * i)) & 15u);
-      };
-      // 16 bytes of a lane are 32 inputs of its column, piece g of the block.  Lane
-      // swaps bring the dwords of a group of 32 or 64 inputs into the same registers.
-#pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        uint32_t(&w)[4] = cur.w[d];
-        auto swap32 = [&](int p, int q) {
-          auto r = __builtin_amdgcn_permlane32_swap(w[p], w[q], false, false);
-          w[p] = r[0];
-          w[q] = r[1];
+        auto scale_of = [&](int i) {
+          return f16_to_f32((uint16_t)(GM == GROUP_128 ? cur.s[i] : cur.s[i / 2] >> (16 * (i & 1))));
         };
-        auto swap16 = [&](int p, int q) {
-          auto r = __builtin_amdgcn_permlane16_swap(w[p], w[q], false, false);
-          w[p] = r[0];
-          w[q] = r[1];
+        auto zero_of = [&](int i) -> float {
+          if constexpr (ZM == ZERO_F16) return f16_to_f32((uint16_t)(GM == GROUP_128 ? cur.z[i] : cur.z[i / 2] >> (16 * (i & 1))));
+          else if constexpr (ZM == ZERO_8) return 8.f;
+          else return (float)((GM == GROUP_128 ? cur.z[i] : cur.z[0] >> (4 * i)) & 15u);
         };
-        if constexpr (GM == GROUP_32) {
-          swap32(0, 2);
-          swap32(1, 3);
-          swap16(0, 1);
-          swap16(2, 3);
-        } else if constexpr (GM == GROUP_64) {
-          swap32(0, 1);
-          swap32(2, 3);
-        }
-      }
-      auto reg = [](int gr, int t) { return GM == GROUP_32 ? gr : GM == GROUP_64 ? 2 * t + gr : t; };
-      if constexpr (ZM != ZERO_8 || CHAIN) {
-        // A group whose codes all equal its zero point is rare: look closer only where
-        // the eight codes of some lane's dword are equal.
-        uint64_t any = 0;
+        // 16 bytes of a lane are 32 inputs of its column, piece g of the block.  Lane
+        // swaps bring the dwords of a group of 32 or 64 inputs into the same registers.
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          const uint32_t w0 = cur.w[i / GPB][reg(i % GPB, 0)];
-          any |= __builtin_amdgcn_ballot_w64(w0 == __builtin_amdgcn_alignbit(w0, w0, 4));
+        for (int d = 0; d < 2; ++d) {
+          uint32_t(&w)[4] = cur.w[d];
+          auto swap32 = [&](int p, int q) {
+            auto r = __builtin_amdgcn_permlane32_swap(w[p], w[q], false, false);
+            w[p] = r[0];
+            w[q] = r[1];
+          };
+          auto swap16 = [&](int p, int q) {
+            auto r = __builtin_amdgcn_permlane16_swap(w[p], w[q], false, false);
+            w[p] = r[0];
+            w[q] = r[1];
+          };
+          if constexpr (GM == GROUP_32) {
+            swap32(0, 2);
+            swap32(1, 3);
+            swap16(0, 1);
+            swap16(2, 3);
+          } else if constexpr (GM == GROUP_64) {
+            swap32(0, 1);
+            swap32(2, 3);
+          }
         }
-        if (any != 0) {
+        auto reg = [](int gr, int t) { return GM == GROUP_32 ? gr : GM == GROUP_64 ? 2 * t + gr : t; };
+        if constexpr (ZM != ZERO_8 || CHAIN) {
+          // A group whose codes all equal its zero point is rare: look closer only where
+          // the eight codes of some lane's dword are equal.
+          uint64_t any = 0;
 #pragma unroll
           for (int i = 0; i < NS; ++i) {
-            uint32_t part[STEPS];
+            const uint32_t w0 = cur.w[i / GPB][reg(i % GPB, 0)];
+            any |= __builtin_amdgcn_ballot_w64(w0 == __builtin_amdgcn_alignbit(w0, w0, 4));
+          }
+          if (any != 0) {
 #pragma unroll
-            for (int t = 0; t < STEPS; ++t) part[t] = cur.w[i / GPB][reg(i % GPB, t)];
-            const uint64_t dead = column_all(q4_part_zero(part, zero_of(i)));
-            if constexpr (GM == GROUP_128) cur.s[i] = zero_where(cur.s[i], dead);
-            else cur.s[i / 2] &= zero_where(0xFFFFu << (16 * (i & 1)), dead) | 0xFFFFu << (16 * (~i & 1));
+            for (int i = 0; i < NS; ++i) {
+              uint32_t part[STEPS];
+#pragma unroll
+              for (int t = 0; t < STEPS; ++t) part[t] = cur.w[i / GPB][reg(i % GPB, t)];
+              const uint64_t dead = column_all(q4_part_zero(part, zero_of(i)));
+              if constexpr (GM == GROUP_128) cur.s[i] = zero_where(cur.s[i], dead);
+              else cur.s[i / 2] &= zero_where(0xFFFFu << (16 * (i & 1)), dead) | 0xFFFFu << (16 * (~i & 1));
+            }
           }
         }
-      }
-      // Step j: its x was read a step before, and the sums of the group before are added
-      // up behind its first products: waits for LDS and for the matrix cores overlap.
-      // Left alone the compiler reads and multiplies all groups before it adds any up, which
-      // takes more registers than there are: with several row tiles the reads stay in order.
-      auto read = [&](int j, q2_u32x4(&v)[RT]) {
-        const int d = j / 4, gr = j % 4 / STEPS, t = j % STEPS;
-        const int q = GM == GROUP_32 ? 4 * gr + g : GM == GROUP_64 ? 8 * gr + 4 * (g & 1) + 2 * t + (g >> 1) : 4 * g + t;
+        // Step j: its x was read a step before, and the sums of the group before are added
+        // up behind its first products: waits for LDS and for the matrix cores overlap.
+        // Left alone the compiler reads and multiplies all groups before it adds any up, which
+        // takes more registers than there are: with several row tiles the reads stay in order.
+        auto read = [&](int j, q2_u32x4(&v)[RT]) {
+          const int d = j / 4, gr = j % 4 / STEPS, t = j % STEPS;
+          const int q = GM == GROUP_32 ? 4 * gr + g : GM == GROUP_64 ? 8 * gr + 4 * (g & 1) + 2 * t + (g >> 1) : 4 * g + t;
 #pragma unroll
-        for (int i = 0; i < RT; ++i) v[i] = *reinterpret_cast<const q2_u32x4*>(xb + xrow[i] + at + 256 * d + 16 * (q ^ swz[i]));
-      };
-      q2_f32x4 sum[2][RT], tmp[2][RT];
-      auto add_up = [&](int k) {
-        const float s = scale_of(k), k4 = ZM == ZERO_8 ? 1.f : 1.f + zero_of(k) * 0.0625f;
+          for (int i = 0; i < RT; ++i) v[i] = *reinterpret_cast<const q2_u32x4*>(xb + xrow[i] + at + 256 * d + 16 * (q ^ swz[i]));
+        };
+        q2_f32x4 sum[2][RT], tmp[2][RT];
+        auto add_up = [&](int k) {
+          const float s = scale_of(k), k4 = ZM == ZERO_8 ? 1.f : 1.f + zero_of(k) * 0.0625f;
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
+          for (int i = 0; i < RT; ++i)
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float t = tmp[k & 1][i][e];
-            float v = __builtin_fmaf(s, CHAIN ? t : __builtin_fmaf(-k4, sum[k & 1][i][e], t), acc[i][e]);
-            if constexpr (RT > 1) asm volatile("" : "+v"(v));
-            acc[i][e] = v;
+            for (int e = 0; e < E; ++e) {
+              const float t = tmp[k & 1][i][e];
+              float v = __builtin_fmaf(s, CHAIN ? t : __builtin_fmaf(-k4, sum[k & 1][i][e], t), acc[i][e]);
+              if constexpr (RT > 1) asm volatile("" : "+v"(v));
+              acc[i][e] = v;
+            }
+        };
+        q2_u32x4 av[2][RT];
+        read(0, av[0]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int k = j / STEPS, t = j % STEPS, d = j / 4, gr = k % GPB;
+          if constexpr (RT > 1) asm volatile("" ::: "memory");
+          if (j + 1 < 8) read(j + 1, av[(j + 1) & 1]);
+          q2_u32x4 ones = sones;
+          if constexpr (CHAIN) {                           // - (1 + z / 16) in every place
+            uint32_t z = 0xBFC0BFC0u;
+            if constexpr (ZM == ZERO_CODES)
+              z = ((GM == GROUP_128 ? cur.z[k] : cur.z[0] >> (4 * k)) & 15u) * 0x00080008u | 0xBF80BF80u;
+            ones = q2_u32x4{z, z, z, z};
           }
-      };
-      q2_u32x4 av[2][RT];
-      read(0, av[0]);
+          if constexpr (RT > 1) asm volatile("" : "+v"(cur.w[d][reg(gr, t)]));
+          const q2_u32x4 bf = q4_frag(cur.w[d][reg(gr, t)], kc);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int k = j / STEPS, t = j % STEPS, d = j / 4, gr = k % GPB;
-        if constexpr (RT > 1) asm volatile("" ::: "memory");
-        if (j + 1 < 8) read(j + 1, av[(j + 1) & 1]);
-        q2_u32x4 ones = sones;
-        if constexpr (CHAIN) {                           // - (1 + z / 16) in every place
-          uint32_t z = 0xBFC0BFC0u;
-          if constexpr (ZM == ZERO_CODES)
-            z = ((GM == GROUP_128 ? cur.z[k] : cur.z[0] >> (4 * k)) & 15u) * 0x00080008u | 0xBF80BF80u;
-          ones = q2_u32x4{z, z, z, z};
+          for (int i = 0; i < RT; ++i) {
+            const q2_f32x4 none = q2_f32x4{0.f, 0.f, 0.f, 0.f};
+            q2_f32x4 &su = sum[k & 1][i], &tm = tmp[k & 1][i];
+            su = mfma(av[j & 1][i], ones, t == 0 ? none : CHAIN ? tm : su);
+            tm = mfma(av[j & 1][i], bf, CHAIN ? su : t == 0 ? none : tm);
+          }
+          if (t == 0 && k > 0) add_up(k - 1);
         }
-        if constexpr (RT > 1) asm volatile("" : "+v"(cur.w[d][reg(gr, t)]));
-        const q2_u32x4 bf = q4_frag(cur.w[d][reg(gr, t)], kc);
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          const q2_f32x4 none = q2_f32x4{0.f, 0.f, 0.f, 0.f};
-          q2_f32x4 &su = sum[k & 1][i], &tm = tmp[k & 1][i];
-          su = mfma(av[j & 1][i], ones, t == 0 ? none : CHAIN ? tm : su);
-          tm = mfma(av[j & 1][i], bf, CHAIN ? su : t == 0 ? none : tm);
-        }
-        if (t == 0 && k > 0) add_up(k - 1);
+        add_up(NS - 1);
       }
-      add_up(NS - 1);
-    }
     }
     // Partial sums through LDS, added in the waves' order, a row tile at a time: room that
     // they take is x's.  Lane (c, g) holds rows 4 g .. (E == 1: row g).

@@ -434,6 +434,30 @@ def test_rows_apart_and_unaligned(dtype, v, ld, at):
         check_sample(wide[:, at:at + v], uniform(i, b), dev=dev[:, at:at + v], **s)
 
 
+def test_masks_and_extremes_of_long_rows():
+    """The same where several workgroups share a row."""
+    test_masks_and_extremes(20011)
+
+
+@pytest.mark.parametrize("b,v", [(128, 8192), (128, 8193), (129, 8193), (1, 8193), (3, 12289), (65, 16384), (17, 65537)])
+def test_rows_shared_by_workgroups(b, v):
+    """On both sides of the sizes from which several workgroups take a row; parts that end inside a piece."""
+    logits = rnd(b + v, b, v) * 3
+    logits[:, v - 1] = 9.0                                    # a likely token in the last, short part
+    for i, s in enumerate([dict(), dict(top_k=40, top_p=0.9), dict(temperature=0.0), dict(top_k=3000, temperature=3.0)]):
+        check_sample(logits, uniform(i, b), f"{s}", **s)
+
+
+@pytest.mark.parametrize("b,v", [(5, 300), (200, 300), (3, 5001), (2, 20011), (129, 9001)])
+def test_more_tokens_than_the_list_at_a_border(b, v):
+    """Thousands of tokens in the part of a border, among others, alike and not."""
+    logits = rnd(7, b, v)
+    logits[:, v // 8: v - v // 8] = 1.5
+    logits[0] = 2.0 + torch.arange(v) * 2.0 ** -22
+    for i, s in enumerate([dict(), dict(top_k=v // 2), dict(top_p=0.6), dict(top_k=2 * v // 3, top_p=0.7, temperature=0.6)]):
+        check_sample(logits, uniform(i, b), f"{s}", **s)
+
+
 def test_last_positions_of_a_batch_of_texts():
     """logits[:, -1] of [B, S, V]."""
     full = rnd(1, 5, 3, 700).to(DEV)
@@ -488,6 +512,61 @@ def test_sample_outputs_given_and_empty():
     assert got.token is token and got.prob is prob and torch.equal(token, q2.q2_sample(logits, u).token)
     none = q2.q2_sample(torch.empty((0, 9), device=DEV), torch.empty(0, device=DEV))
     assert none.token.shape == (0,) and none.token.is_cuda
+
+
+def test_workspace_of_the_caller():
+    logits, u = (rnd(1, 4, 30000) * 3).to(DEV), uniform(1, 4).to(DEV)
+    need = q2.sample_workspace_bytes(4, 30000)
+    assert need > 0 and q2.sample_workspace_bytes(4, 300) == 0 and q2.sample_workspace_bytes(1000, 30000) == 0
+    ws = torch.full((need + 256,), 0xA5, device=DEV, dtype=torch.uint8)
+    want = q2.q2_sample(logits, u, top_k=50)
+    for _ in range(2):                                        # whatever it holds
+        got = q2.q2_sample(logits, u, top_k=50, workspace=ws[:need])
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert (ws[need:] == 0xA5).all()
+    with pytest.raises(q2.Q2Error, match="workspace"):
+        q2.q2_sample(logits, u, workspace=ws[:need - 1])
+    with pytest.raises(q2.Q2Error, match="aligned"):
+        q2.q2_sample(logits, u, workspace=ws[8:])
+
+
+def test_two_calls_at_once():
+    """On two streams, each with a workspace of its own."""
+    logits = [(rnd(i, 3, 100003) * 3).to(DEV) for i in range(2)]
+    u = [uniform(i, 3).to(DEV) for i in range(2)]
+    want = [q2.q2_sample(logits[i], u[i], top_p=0.9) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(q2.q2_sample(logits[i], u[i], top_p=0.9))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for g in got[i] for a, b in zip(g, want[i]))
+
+
+def test_two_graphs_of_long_rows():
+    """Captured where several workgroups share a row, replayed in turn with eager calls between."""
+    logits, u = (rnd(1, 2, 50021) * 3).to(DEV), uniform(1, 2).to(DEV)
+    few = logits[:1, :9001]
+    graphs, outs = [], []
+    for f in (lambda: q2.q2_sample(logits, u, temperature=0.8, top_k=100), lambda: q2.q2_sample(few, u[:1], top_p=0.5)):
+        f()
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(f())
+    for i in range(5):
+        logits.copy_(rnd(10 + i, 2, 50021) * 3)
+        u.copy_(uniform(10 + i, 2))
+        want = q2.q2_sample(logits, u, temperature=0.8, top_k=100), q2.q2_sample(few, u[:1], top_p=0.5)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for out, w in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(out, w)), f"replay {i}"
 
 
 def test_sample_refusals():
