@@ -583,11 +583,12 @@ __device__ __forceinline__ Borders borders_of(SampleShared& s, const Settings& c
 
 // The range's tokens of the parts, key above the complement of the token.  The logits of
 // a border's parts lie in a range of distances from the best one, and rounding does not
-// turn an order round, so distances in 32 bits drop nearly all others: first by the one
-// range that holds the three.  Distances are not negative and are compared by their bits.
+// turn an order round, so distances in 32 bits drop nearly all others: first by the
+// draw's range and one that holds top-k's and top-p's.  Distances are not negative and are
+// compared by their bits.
 template <class F>
 __device__ __forceinline__ void each_chosen(const Measure& me, const Borders& o, const void* row, int bf16, int t0, int t1, F f) {
-  uint32_t from[3], over[3], lo = 0xFFFFFFFFu, hi = 0;
+  uint32_t from[3], over[3], lo = 0xFFFFFFFFu, hi = 0;   // lo, hi: of top-k and top-p
 #pragma unroll
   for (int j = 0; j < 3; ++j) {                          // a little wider: the exact test comes behind it
     const bool none = o.lo[j] > o.hi[j], all = !(me.best < __builtin_inff());          // its own distance is no number
@@ -595,13 +596,16 @@ __device__ __forceinline__ void each_chosen(const Measure& me, const Borders& o,
     const uint32_t last = all || o.hi[j] == SM_BUCKETS - 1 ? 0xFFFFFFFFu : __builtin_bit_cast(uint32_t, (float)((o.hi[j] + 1) * me.step * (1 + 1e-6)));
     from[j] = none ? 0xFFFFFFFFu : first;
     over[j] = none ? 0u : last - first;
-    if (!none) lo = min(lo, first), hi = max(hi, last);
+    if (!none && j < 2) lo = min(lo, first), hi = max(hi, last);
   }
   each_four(row, bf16, t0, t1, [&](const float(&x)[4], int at, int by) {
     uint32_t away[4];
 #pragma unroll
     for (int d = 0; d < 4; ++d) away[d] = __builtin_bit_cast(uint32_t, me.best - x[d]);
-    if (min(min(away[0] - lo, away[1] - lo), min(away[2] - lo, away[3] - lo)) > hi - lo) return;
+    auto least = [&](uint32_t n) { return min(min(away[0] - n, away[1] - n), min(away[2] - n, away[3] - n)); };
+    bool in = least(from[2]) <= over[2];
+    if (o.by_k || o.by_p) in |= least(lo) <= hi - lo;    // the same for all lanes
+    if (!in) return;
 #pragma unroll 1
     for (int d = 0; d < 4; ++d) {
       const uint32_t w = d == 0 ? away[0] : d == 1 ? away[1] : d == 2 ? away[2] : away[3];
@@ -841,6 +845,7 @@ __global__ __launch_bounds__(SM_THREADS) void sample_gather_kernel(SampleArgs a,
   const float best = row_best(sp, gridDim.x);
   if (!(best > -__builtin_inff()) || c.greedy()) return;
   const bool lead = blockIdx.x == 0;                     // tells the draw what it found
+  if (threadIdx.x == 0) s.fill = 0;
   uint64_t vs[SM_PER];
   uint32_t vn[SM_PER];
 #pragma unroll
@@ -852,10 +857,13 @@ __global__ __launch_bounds__(SM_THREADS) void sample_gather_kernel(SampleArgs a,
   const Borders o = borders_of(s, c, vs, vn, lead ? sp.start_s : nullptr, lead ? sp.start_n : nullptr);
   if (lead && threadIdx.x == 0) sp.total = o.total, sp.all = o.count, sp.chosen = o.chosen_count, sp.by_k = o.by_k, sp.by_p = o.by_p;
   if (o.chosen_count > SM_LIST) return;
-  each_chosen(measure_of(c, best, of), o, p.row, a.bf16, p.t0, p.t1, [&](uint64_t e) {
-    const uint32_t at = atomicAdd(&sp.fill, 1u);
-    if (at < SM_LIST) sp.list[at] = e;
-  });
+  each_chosen(measure_of(c, best, of), o, p.row, a.bf16, p.t0, p.t1, [&](uint64_t e) { s.list[atomicAdd(&s.fill, 1u)] = e; });
+  __syncthreads();
+  const uint32_t n = s.fill;                             // a wait for memory for all of them, not for each
+  if (threadIdx.x == 0 && n > 0) s.n = atomicAdd(&sp.fill, n);
+  __syncthreads();
+  for (uint32_t i = threadIdx.x; i < n; i += SM_THREADS)
+    if (s.n + i < SM_LIST) sp.list[s.n + i] = s.list[i];
 }
 
 constexpr int SM_DRAW = 256;                             // threads that sort a row's list: fewer wait less for each other
