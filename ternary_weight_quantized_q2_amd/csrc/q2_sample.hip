@@ -893,11 +893,17 @@ __global__ __launch_bounds__(SM_THREADS) void sample_draw_kernel(SampleArgs a, i
   draw<SM_DRAW>(s, c, me, sp.by_k != 0, sp.by_p != 0, sp.total, sp.start_s, sp.start_n, n, a.token + r, a.prob + r);
 }
 
-// Tokens of a part; 0 where a workgroup takes whole rows: few tokens, or rows enough for the CUs.
+// Tokens of a part; 0 where a workgroup takes whole rows.  As many parts as keep the
+// workgroups of all rows on the CUs at once, where what the parts spare, about half a
+// microsecond per 1024 tokens, is more than three launches and the ways through memory
+// cost, which grows with the rows.  By one workgroup and by parts: 1 row of 16384 20.7 / 21.8
+// us, of 20000 23.9 / 21.9; 32 of 16384 22.6 / 27.1, of 32768 32.6 / 32.3; 64 of 32768
+// 33.5 / 36.4, of 50021 45.1 / 38.1; 96 of 50021 46.5 / 44.8; 128 of 32768 35.7 / 40.8, of
+// 128009 97.8 / 85.0.  96 of 128009 94.9 / 75.6, in three parts, which do not fit at once, 97.7.
 static int part_tokens(int64_t B, int64_t V) {
-  if (V <= 8192 || B > 128) return 0;
-  const int64_t parts = std::min<int64_t>({(256 + B - 1) / B, (V + 4095) / 4096, SM_PARTS});
-  return parts > 1 ? (int)(((V + parts - 1) / parts + 1023) / 1024 * 1024) : 0;
+  const int64_t parts = std::min<int64_t>({256 / std::max<int64_t>(B, 1), (V + 4095) / 4096, SM_PARTS});
+  if (parts <= 1 || V - V / parts < 14000 + 100 * B) return 0;
+  return (int)(((V + parts - 1) / parts + 1023) / 1024 * 1024);
 }
 
 size_t sample_workspace_bytes(int64_t B, int64_t V) {

@@ -439,6 +439,33 @@ def test_masks_and_extremes_of_long_rows():
     test_masks_and_extremes(20011)
 
 
+def test_masks_and_extremes_over_workgroups():
+    """The same where several workgroups share a row, in parts of 4096 tokens and a shorter one."""
+    assert q2.sample_workspace_bytes(16, 30011) > 0
+    test_masks_and_extremes(30011)
+
+
+@pytest.mark.parametrize("b,v", [(1, 17500), (1, 18900), (8, 18500), (60, 30000), (64, 40001), (100, 60000), (128, 53500), (128, 53700),
+                                 (129, 53700), (17, 65537)])
+def test_rows_in_parts(b, v):
+    """Around the sizes from which a row is cut; the last part short, or one token long."""
+    logits = rnd(b + v, b, v) * 3
+    logits[:, v - 1] = 9.0
+    for i, s in enumerate([dict(), dict(top_k=40, top_p=0.9), dict(temperature=0.0), dict(top_k=3000, temperature=3.0)]):
+        check_sample(logits, uniform(i, b), f"{s}", **s)
+
+
+@pytest.mark.parametrize("b,v", [(2, 40011), (100, 50001)])
+def test_long_lists_of_rows_in_parts(b, v):
+    """More tokens at a border than the list holds, and as many as it nearly holds."""
+    assert q2.sample_workspace_bytes(b, v) > 0
+    test_more_tokens_than_the_list_at_a_border(b, v)
+    logits = rnd(8, b, v)
+    logits[:, 100:2140] = 5.0                                 # 2040 alike
+    for i, s in enumerate([dict(), dict(top_k=1000), dict(top_p=0.5)]):
+        check_sample(logits, uniform(i, b), f"{s}", **s)
+
+
 @pytest.mark.parametrize("b,v", [(128, 8192), (128, 8193), (129, 8193), (1, 8193), (3, 12289), (65, 16384), (17, 65537)])
 def test_rows_shared_by_workgroups(b, v):
     """On both sides of the sizes from which several workgroups take a row; parts that end inside a piece."""
