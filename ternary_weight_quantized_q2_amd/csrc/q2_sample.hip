@@ -727,6 +727,10 @@ __device__ __forceinline__ const void* row_of(const SampleArgs& a, int64_t r) {
 }
 
 // ---- a workgroup per row ------------------------------------------------------------
+// One row of 4099, top-k: 17 us, dependent steps of one workgroup (best 2.3, histogram 3.3,
+// borders 3.6, gathering 2.4, draw 3.6).  256 rows of 128009, min-p: 92 us for 131 MB;
+// the best logit 24 (5.4 TB/s), exponentials and LDS additions 24, gathering 16, the slowest
+// row 20 behind the median; vector instructions issue in 38 % of the cycles.
 __global__ __launch_bounds__(SM_THREADS) void sample_kernel(SampleArgs a, SampleUnits of) {
   extern __shared__ __align__(16) uint8_t smem[];
   SampleShared& s = *reinterpret_cast<SampleShared*>(smem);
@@ -769,10 +773,11 @@ __global__ __launch_bounds__(SM_THREADS) void sample_kernel(SampleArgs a, Sample
 }
 
 // ---- several workgroups per row -------------------------------------------------------
-// Few rows leave most CUs idle, and one CU takes 35 us for the exponentials of 2^17
-// logits.  Here a row's tokens are cut into parts, and what the workgroups of a row
-// tell each other goes through the workspace from one launch to the next: each part's best
-// logit, the histogram, the list of the tokens to sort.
+// Few rows leave most CUs idle: one row of 128009 takes one workgroup 87 us.  Here a row's
+// tokens are cut into parts, and what the workgroups of a row tell each other goes through
+// the workspace from one launch to the next: each part's best logit, the histogram, the
+// list of the tokens to sort.  One row of 128009 26 us, 32 rows 41, 64 rows bf16 64: the four
+// launches' dependent steps, then the 64-bit exponentials (8 and 13 us of the last two).
 struct RowSpace {
   uint64_t sum[SM_BUCKETS];
   uint64_t list[SM_LIST];
