@@ -101,10 +101,13 @@ struct SampleShared {
   uint64_t wsum[SM_WAVES];
   uint32_t wcount[SM_WAVES];
   float wbest[SM_WAVES];
-  uint64_t base_s, total;
-  uint32_t base_n, bucket, n, fill, lo, hi, key, unused;
-  int border_lo[3], border_hi[3];
-  uint32_t all, chosen;
+  uint64_t base_s, total, before_s[SM_WAVES];
+  uint32_t base_n, bucket, n, fill, lo, hi, key, all;
+  uint32_t before_n[SM_WAVES];
+  struct {
+    int part[2];                                         // where it begins, where it ends
+    uint32_t tokens[2];                                  // before the first part, up to the last
+  } border[3];
   uint64_t sum[SM_BUCKETS];                              // over all tokens
   uint32_t count[SM_BUCKETS];
   uint64_t list[SM_LIST];
@@ -471,9 +474,9 @@ struct Borders {
   }
 };
 // The parts' sums and counts, SM_PER of each thread, are in s.sum and s.count.  start_s,
-// start_n, where given: for the chosen parts, what lies before them.  One wave looks for
-// the borders, while the fifteen others wait: sixteen that find the same take four turns of
-// each SIMD for it (5 us in place of 3).
+// start_n, where given: for the chosen parts, what lies before them.  One wave looks for where
+// the borders begin and one for where they end, while the others wait: sixteen that find
+// the same take four turns of each SIMD for it (5 us in place of 3).
 __device__ __forceinline__ Borders borders_of(SampleShared& s, const Settings& c, const uint64_t (&vs)[SM_PER], const uint32_t (&vn)[SM_PER],
                                               uint64_t* start_s, uint32_t* start_n) {
   static_assert(SM_WAVES <= 64 && SM_PER <= 64 && SM_LIST >= SM_THREADS + SM_THREADS / 2, "one lane each, room in the list");
@@ -491,85 +494,66 @@ __device__ __forceinline__ Borders borders_of(SampleShared& s, const Settings& c
   upto_n[threadIdx.x] = in;
   if (lane == 63) s.wsum[wv] = is, s.wcount[wv] = in;
   __syncthreads();
-  if (wv == 0) {
+  if (wv < 2) {
     const uint64_t wave_s = lane < SM_WAVES ? s.wsum[lane] : 0;
     const uint32_t wave_n = lane < SM_WAVES ? s.wcount[lane] : 0;
     uint64_t ws = wave_s;
     uint32_t wn = wave_n;
     scan_lanes(ws, wn);
-    const uint64_t total = __shfl(ws, 63);
+    uint64_t left = __shfl(ws, 63);                      // the least or the most that the borders so far leave
     const uint32_t all = __shfl(wn, 63);
+    if (wv == 0) {
+      if (lane < SM_WAVES) s.before_s[lane] = ws - wave_s, s.before_n[lane] = wn - wave_n;
+      if (lane == 0) s.total = left, s.all = all;
+    }
     const bool by_k = c.top_k > 0 && (uint32_t)c.top_k < all, by_p = c.top_p < 1.f;
-    uint64_t least = total, most = total;                // bounds of the sum of what is left
-    uint32_t chosen = 0, next_n = 0;
 #pragma unroll 1
     for (int border = by_k ? 0 : by_p ? 1 : 2; border < 3; border = border == 0 && !by_p ? 2 : border + 1) {
-      uint64_t last_target = 0, before = 0, own = 0;
-      uint32_t before_n = 0, from_n = 0, own_parts = 0;
-      int part = 0;
+      const uint64_t target = border == 0 ? (uint64_t)c.top_k : border == 1 ? part_of(c.top_p, left) : draw_target(c.u, left);
+      // the part that reaches the target: its wave, its thread there, its place
+      const int at = __builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < SM_WAVES && (border ? ws : (uint64_t)wn) >= target));
+      const uint64_t base_s = __shfl(ws - wave_s, at);
+      const uint32_t base_n = __shfl(wn - wave_n, at);
+      const uint64_t ts = base_s + upto_s[64 * at + lane];
+      const uint32_t tn = base_n + upto_n[64 * at + lane];
+      const int th = __builtin_ctzll(__builtin_amdgcn_ballot_w64((border ? ts : (uint64_t)tn) >= target));
+      uint64_t before = th ? __shfl(ts, th - 1) : base_s, own;
+      uint32_t before_n = th ? __shfl(tn, th - 1) : base_n, own_n;
+      int part = SM_PER * (64 * at + th);
+      const int last = part + SM_PER - 1;
 #pragma unroll 1
-      for (int end = 0; end < 2; ++end) {
-        const uint64_t left = end ? most : least;
-        const uint64_t target = border == 0 ? (uint64_t)c.top_k : border == 1 ? part_of(c.top_p, left) : draw_target(c.u, left);
-        if (end == 0 || target != last_target) {
-          // the part that reaches the target: its wave, its thread there, its place
-          const uint64_t w = __builtin_amdgcn_ballot_w64(lane < SM_WAVES && (border ? ws : (uint64_t)wn) >= target);
-          const int at = __builtin_ctzll(w);
-          const uint64_t base_s = __shfl(ws - wave_s, at);
-          const uint32_t base_n = __shfl(wn - wave_n, at);
-          const uint64_t ts = base_s + upto_s[64 * at + lane];
-          const uint32_t tn = base_n + upto_n[64 * at + lane];
-          const int th = __builtin_ctzll(__builtin_amdgcn_ballot_w64((border ? ts : (uint64_t)tn) >= target));
-          const int first = SM_PER * (64 * at + th);
-          before = th ? __shfl(ts, th - 1) : base_s;
-          before_n = th ? __shfl(tn, th - 1) : base_n;
-          part = first;
-#pragma unroll 1
-          for (;; ++part) {
-            own = s.sum[part];
-            own_parts = s.count[part];
-            if (part == first + SM_PER - 1 || (border ? before + own : (uint64_t)before_n + own_parts) >= target) break;
-            before += own;
-            before_n += own_parts;
-          }
-        }
-        if (end == 0) {
-          if (lane == 0) s.border_lo[border] = part;
-          least = before + 1;
-          from_n = before_n;
-        }
-        last_target = target;
+      for (;; ++part) {
+        own = s.sum[part];
+        own_n = s.count[part];
+        if (part == last || (border ? before + own : (uint64_t)before_n + own_n) >= target) break;
+        before += own;
+        before_n += own_n;
       }
-      if (lane == 0) s.border_hi[border] = part;
-      // The next border's bounds; `most` was this one's until here.  A later border's
-      // parts lie at or before this one's: what both hold counts once.
-      most = before + own;
-      const uint32_t to_n = before_n + own_parts;
-      const bool first_border = border == 0 || (border == 1 && !by_k) || (border == 2 && !by_k && !by_p);
-      chosen += first_border ? to_n - from_n : min(to_n, next_n) - min(from_n, next_n);
-      next_n = first_border ? from_n : min(next_n, from_n);
-    }
-    if (lane < SM_WAVES) s.wsum[lane] = ws - wave_s, s.wcount[lane] = wn - wave_n;
-    if (lane == 0) {
-      if (!by_k) s.border_lo[0] = 0, s.border_hi[0] = -1;
-      if (!by_p) s.border_lo[1] = 0, s.border_hi[1] = -1;
-      s.total = total;
-      s.all = all;
-      s.chosen = chosen;
+      left = wv ? before + own : before + 1;
+      if (lane == 0) s.border[border].part[wv] = part, s.border[border].tokens[wv] = wv ? before_n + own_n : before_n;
     }
   }
   __syncthreads();
   Borders o;
   o.total = s.total;
   o.count = s.all;
-  o.chosen_count = s.chosen;
   o.by_k = c.top_k > 0 && (uint32_t)c.top_k < o.count;
   o.by_p = c.top_p < 1.f;
+  // A later border's parts lie at or before an earlier one's; what both hold counts once.
+  uint32_t counted = o.count;
+  o.chosen_count = 0;
 #pragma unroll
-  for (int j = 0; j < 3; ++j) o.lo[j] = s.border_lo[j], o.hi[j] = s.border_hi[j];
+  for (int j = 0; j < 3; ++j) {
+    const bool is = j == 0 ? o.by_k : j == 1 ? o.by_p : true;
+    o.lo[j] = is ? s.border[j].part[0] : 0;
+    o.hi[j] = is ? s.border[j].part[1] : -1;
+    const uint32_t from = is ? s.border[j].tokens[0] : counted, to = is ? s.border[j].tokens[1] : counted;
+    o.chosen_count += min(to, counted) - min(from, counted);
+    counted = min(from, counted);
+  }
   if (start_s) {
-    uint64_t before_s = s.wsum[wv] + is - own_s;
-    uint32_t before_n = s.wcount[wv] + in - own_n;
+    uint64_t before_s = s.before_s[wv] + is - own_s;
+    uint32_t before_n = s.before_n[wv] + in - own_n;
 #pragma unroll
     for (int i = 0; i < SM_PER; ++i) {
       const int b = SM_PER * threadIdx.x + i;
