@@ -23,6 +23,7 @@ constexpr int SM_THREADS = 1024, SM_WAVES = SM_THREADS / 64;
 constexpr int SM_BUCKETS = 4096, SM_PER = SM_BUCKETS / SM_THREADS;
 constexpr int SM_LIST = 2048;                            // tokens that are sorted
 constexpr int SM_PARTS = 64;                             // of a row, at most
+constexpr int SM_DRAW = 256;                             // threads that sort a row's list: fewer wait less for each other
 constexpr int SM_FEW = 256;                              // tokens that are compared with each other
 
 __device__ __forceinline__ uint32_t logit_key(float v) { // order-preserving, 0 for a masked token
@@ -602,14 +603,14 @@ __device__ __forceinline__ void each_chosen(const Measure& me, const Borders& o,
 }
 
 // The draw from the n tokens of the parts, in s.list in any order (n <= SM_LIST);
-// start_s, start_n: what lies before the parts.
-template <int THREADS>
+// start_s, start_n: what lies before the parts.  By the first SM_DRAW threads alone (one row of
+// 4099: 15.3 us in place of 16.5 by all).
 __device__ __forceinline__ void draw(SampleShared& s, const Settings& c, const Measure& me, bool by_k, bool by_p, uint64_t total,
                                      const uint64_t* start_s, const uint32_t* start_n, uint32_t n, int32_t* token, float* prob) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   int size = 64;
   while (size < (int)n) size <<= 1;
-  if (size <= THREADS) {
+  if (size <= SM_DRAW) {
     // Largest first: an entry's place is the number of larger ones.  All are different.
     __syncthreads();
     const uint64_t mine = threadIdx.x < n ? s.list[threadIdx.x] : 0;
@@ -622,14 +623,14 @@ __device__ __forceinline__ void draw(SampleShared& s, const Settings& c, const M
     if (threadIdx.x < n) s.list[place] = mine;
     __syncthreads();
   } else {
-    for (int i = (int)n + threadIdx.x; i < size; i += THREADS) s.list[i] = 0;
+    for (int i = (int)n + threadIdx.x; i < size; i += SM_DRAW) s.list[i] = 0;
     __syncthreads();
 #pragma unroll 1
     for (int span = 2; span <= size; span <<= 1)
 #pragma unroll 1
       for (int step = span >> 1; step; step >>= 1) {
 #pragma unroll 1
-        for (int i = threadIdx.x; i < size / 2; i += THREADS) {
+        for (int i = threadIdx.x; i < size / 2; i += SM_DRAW) {
           const int lo = ((i & ~(step - 1)) << 1) | (i & (step - 1)), hi = lo | step;
           const uint64_t x = s.list[lo], z = s.list[hi];
           if ((x < z) == ((lo & span) == 0)) s.list[lo] = z, s.list[hi] = x;
@@ -640,7 +641,7 @@ __device__ __forceinline__ void draw(SampleShared& s, const Settings& c, const M
   // What lies before each entry: the sum over the list, less where its part begins, and
   // what lies before the part.  A thread takes `own` entries, one after the other; their
   // weights and parts lie where the histogram was.
-  const int own = (size + THREADS - 1) / THREADS, i0 = own * threadIdx.x, i1 = min(i0 + own, (int)n);
+  const int own = (size + SM_DRAW - 1) / SM_DRAW, i0 = own * threadIdx.x, i1 = min(i0 + own, (int)n);
   auto octaves = [&](int i) { return me.octaves(key_logit((uint32_t)(s.list[i] >> 32))); };
   uint64_t vs = 0;
 #pragma unroll 1
@@ -711,8 +712,8 @@ __device__ __forceinline__ const void* row_of(const SampleArgs& a, int64_t r) {
 }
 
 // ---- a workgroup per row ------------------------------------------------------------
-// One row of 4099, top-k: 17 us, dependent steps of one workgroup (best 2.3, histogram 3.3,
-// borders 3.6, gathering 2.4, draw 3.6).  256 rows of 128009, min-p: 92 us for 131 MB;
+// One row of 4099, top-k: 15.3 us, dependent steps of one workgroup (best 2.4, histogram 3.4,
+// borders 3.0, gathering 2.5, draw 2.6).  256 rows of 128009, min-p: 91 us for 131 MB;
 // the best logit 24 (5.4 TB/s), exponentials and LDS additions 24, gathering 16, the slowest
 // row 20 behind the median; vector instructions issue in 38 % of the cycles.
 __global__ __launch_bounds__(SM_THREADS) void sample_kernel(SampleArgs a, SampleUnits of) {
@@ -753,14 +754,15 @@ __global__ __launch_bounds__(SM_THREADS) void sample_kernel(SampleArgs a, Sample
   __syncthreads();
   each_chosen(me, o, row, a.bf16, 0, V, [&](uint64_t e) { s.list[atomicAdd(&s.fill, 1u)] = e; });
   __syncthreads();
-  draw<SM_THREADS>(s, c, me, o.by_k, o.by_p, o.total, s.start, s.count2, o.chosen_count, a.token + r, a.prob + r);
+  if (threadIdx.x >= SM_DRAW) return;                    // whole waves
+  draw(s, c, me, o.by_k, o.by_p, o.total, s.start, s.count2, o.chosen_count, a.token + r, a.prob + r);
 }
 
 // ---- several workgroups per row -------------------------------------------------------
 // Few rows leave most CUs idle: one row of 128009 takes one workgroup 87 us.  Here a row's
 // tokens are cut into parts, and what the workgroups of a row tell each other goes through
 // the workspace from one launch to the next: each part's best logit, the histogram, the
-// list of the tokens to sort.  One row of 128009 26 us, 32 rows 41, 64 rows bf16 64: the four
+// list of the tokens to sort.  One row of 128009 25 us, 32 rows 42, 64 rows bf16 64: the four
 // launches' dependent steps, then the 64-bit exponentials (8 and 13 us of the last two).
 struct RowSpace {
   uint64_t sum[SM_BUCKETS];
@@ -855,8 +857,6 @@ __global__ __launch_bounds__(SM_THREADS) void sample_gather_kernel(SampleArgs a,
     if (s.n + i < SM_LIST) sp.list[s.n + i] = s.list[i];
 }
 
-constexpr int SM_DRAW = 256;                             // threads that sort a row's list: fewer wait less for each other
-
 __global__ __launch_bounds__(SM_THREADS) void sample_draw_kernel(SampleArgs a, int parts, SampleUnits of, RowSpace* ws) {
   extern __shared__ __align__(16) uint8_t smem[];
   SampleShared& s = *reinterpret_cast<SampleShared*>(smem);
@@ -879,7 +879,7 @@ __global__ __launch_bounds__(SM_THREADS) void sample_draw_kernel(SampleArgs a, i
   }
   if (threadIdx.x >= SM_DRAW) return;                    // whole waves
   for (int i = threadIdx.x; i < (int)n; i += SM_DRAW) s.list[i] = sp.list[i];
-  draw<SM_DRAW>(s, c, me, sp.by_k != 0, sp.by_p != 0, sp.total, sp.start_s, sp.start_n, n, a.token + r, a.prob + r);
+  draw(s, c, me, sp.by_k != 0, sp.by_p != 0, sp.total, sp.start_s, sp.start_n, n, a.token + r, a.prob + r);
 }
 
 // Tokens of a part; 0 where a workgroup takes whole rows.  As many parts as keep the
