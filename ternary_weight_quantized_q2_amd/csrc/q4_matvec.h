@@ -377,9 +377,10 @@ static hipError_t run_matvec(const MatvecArgs& m, hipStream_t stream) {
   // waves pay more for their start, fewer leave memory idle.  Workgroups of up to
   // sixteen for more rows, one per CU, whose x goes to its LDS once: as many tiles for each
   // as fill the fewest turns of the CUs.
-  // One row, K = 2560: 1216 strips 12.3 us with two waves, 14.9 with one, 18.2 with five;
-  // 8001 strips 46 in pairs of two waves, 93 with five.  8 rows, K = 4096, 768 strips: 13.0
-  // three strips by four waves each, 18.6 one by eight.
+  // One row, K = 2560: 1216 strips 11.1 us with two waves, 12.9 with one, 16.8 with five;
+  // 8001 strips 45 in pairs of two waves, 48 in pairs of one or singly, 81 with five.  160
+  // strips, K = 9728: 8.5 with thirteen waves, 9.4 with six.  13 rows, 384 strips: 7.2 two
+  // strips by five waves each, 8.1 one by ten, 9.4 four by four.
   constexpr int WAVES = RT > 2 ? 8 : 16;                 // of a workgroup, at most
   int kg, tiles, lds;
   int64_t most = 1 << 20;

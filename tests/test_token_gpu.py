@@ -468,7 +468,7 @@ def test_long_lists_of_rows_in_parts(b, v):
 
 @pytest.mark.parametrize("b,v", [(128, 8192), (128, 8193), (129, 8193), (1, 8193), (3, 12289), (65, 16384), (17, 65537)])
 def test_rows_shared_by_workgroups(b, v):
-    """On both sides of the sizes from which several workgroups take a row; parts that end inside a piece."""
+    """About 8192 and 16384 tokens, many rows and few; parts that end inside a piece."""
     logits = rnd(b + v, b, v) * 3
     logits[:, v - 1] = 9.0                                    # a likely token in the last, short part
     for i, s in enumerate([dict(), dict(top_k=40, top_p=0.9), dict(temperature=0.0), dict(top_k=3000, temperature=3.0)]):
