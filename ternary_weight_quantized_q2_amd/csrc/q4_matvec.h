@@ -4,8 +4,11 @@
 // y = epilogue(x W^T), w = (q - z) s with one s and z per group of 32, 64 or a
 // multiple of 128 inputs.  A code decodes to bf16 1 + q / 16 (q2_device.h); per group
 // sum x (1 + q / 16) - (1 + z / 16) sum x = sum x (q - z) / 16 on the matrix cores,
-// exact products and fp32 sums, and one FMA per output applies the group's scale.  A
-// group whose codes all equal a whole zero point takes a scale of 0, so it adds exactly
+// exact products and fp32 sums, and one FMA per output applies the group's scale.  Of an
+// f16 zero point below 2^-9 the sum 1 + z / 16 would lose bits: sum x goes off first,
+// then (z / 16) sum x (over 17 to 64 rows up to 6 % slower than the one FMA with 1 + z / 16;
+// both forms with a branch by what the unit's zero points need spill, up to 35 % slower).
+// A group whose codes all equal a whole zero point takes a scale of 0, so it adds exactly
 // nothing; where the sums with 1.5, which stands for 8 without zero points, run through
 // the same instructions as the products they cancel bit for bit by themselves.
 #pragma once
@@ -56,7 +59,7 @@ __global__ __launch_bounds__(RT > 2 ? 512 : 1024) void matvec_kernel(MatvecArgs 
   constexpr int SW = GM == GROUP_128 ? 2 : NS / 2;       // dwords of scales and of f16 zero points
   constexpr int ZW = ZM == ZERO_F16 || GM == GROUP_128 ? SW : 1;
   // Where 1 + z / 16 is a bf16 and a lane has several outputs, each step adds
-  // minus its products with x first, which leaves one FMA per output and group in place of two.
+  // minus its products with x first, which leaves one FMA per output and group.
   constexpr bool CHAIN = E > 1 && ZM != ZERO_F16;
   const FusedArgs& a = m.f;
   extern __shared__ __align__(16) uint8_t xs[];
@@ -292,13 +295,19 @@ __global__ __launch_bounds__(RT > 2 ? 512 : 1024) void matvec_kernel(MatvecArgs 
         };
         q2_f32x4 sum[2][RT], tmp[2][RT];
         auto add_up = [&](int k) {
-          const float s = scale_of(k), k4 = ZM == ZERO_8 ? 1.f : 1.f + zero_of(k) * 0.0625f;
+          const float s = scale_of(k), z16 = zero_of(k) * 0.0625f;
 #pragma unroll
           for (int i = 0; i < RT; ++i)
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-              const float t = tmp[k & 1][i][e];
-              float v = __builtin_fmaf(s, CHAIN ? t : __builtin_fmaf(-k4, sum[k & 1][i][e], t), acc[i][e]);
+              const float su = sum[k & 1][i][e];
+              float t = tmp[k & 1][i][e];
+              if constexpr (!CHAIN) {
+                if constexpr (ZM == ZERO_8) t -= su;
+                else if constexpr (ZM == ZERO_CODES) t = __builtin_fmaf(-(1.f + z16), su, t);
+                else t = __builtin_fmaf(-z16, su, t - su);
+              }
+              float v = __builtin_fmaf(s, t, acc[i][e]);
               if constexpr (RT > 1) asm volatile("" : "+v"(v));
               acc[i][e] = v;
             }

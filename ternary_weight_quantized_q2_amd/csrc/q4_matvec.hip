@@ -51,9 +51,9 @@ __global__ __launch_bounds__(256) void matvec_tile_kernel(MatvecArgs m, int tile
       sum = mfma(av, sones, sum);
     }
     const float d = f16_to_f32((uint16_t)zero_where(sp[gr], column_all(pz)));
-    const float k4 = m.zero == ZERO_8 ? 1.f : 1.f + z * 0.0625f;
+    const float z16 = m.zero == ZERO_8 ? 0.f : z * 0.0625f;   // ZERO_8: off with the sum already
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(d, __builtin_fmaf(-k4, sum[e], tmp[e]), acc[e]);
+    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(d, __builtin_fmaf(-z16, sum[e], tmp[e] - sum[e]), acc[e]);
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) out[4 * g + e][cb] = acc[e] * 16.f;
