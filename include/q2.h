@@ -470,8 +470,9 @@ int q2_combine(const void* z, int64_t R, const int32_t* slot, const float* weigh
  *   epi, y     as q2_linear_fused, with z = x W^T, W[n, k] = (code - zero) * scale
  * Products are exact, sums in fp32 in an order that goes by the sizes, so a call is
  * run-to-run bitwise deterministic; weights that are all zero in a group add
- * exactly nothing.  Scales are finite, and sum |x| over 128 inputs stays below
- * 2^126.  K == 0 is the empty sum.  Errors: those of q4_linear_fused.
+ * exactly nothing.  Scales and zero points are finite, and sum |x| over 128 inputs
+ * stays below 2^126, and so does sum |x| |zero| / 16 (which is less where zero points
+ * lie between -16 and 16).  K == 0 is the empty sum.  Errors: those of q4_linear_fused.
  * Asynchronous.
  */
 int q4_matvec(const uint16_t* x_bf16, const uint8_t* packed4, const uint16_t* scale_f16, const void* zero,

@@ -20,7 +20,9 @@ __global__ __launch_bounds__(256) void matvec_tile_kernel(MatvecArgs m, int tile
   const int64_t n_out = fused_n_out(a), K = a.K;
   const int out_cols = a.gated ? MV_BN / 2 : MV_BN;
   const int64_t n0 = (int64_t)tn * out_cols;
-  const int groups = (int)(K / m.group), steps = (int)(m.group / 32);
+  // Sums of x are of up to 128 inputs, of which a group may have many.
+  const int groups = (int)(K / m.group), blocks = m.group > BLOCK_K ? (int)(m.group / BLOCK_K) : 1;
+  const int steps = (int)(m.group / blocks / 32);
   const NatConsts kc = q4_nat_consts();
 
   const int cb = 16 * wv + c;
@@ -40,20 +42,22 @@ __global__ __launch_bounds__(256) void matvec_tile_kernel(MatvecArgs m, int tile
     float z = 8.f;
     if (m.zero == ZERO_CODES) z = (float)((m.zero_codes[n * ((groups + 1) / 2) + gr / 2] >> (4 * (gr & 1))) & 15);
     if (m.zero == ZERO_F16) z = f16_to_f32(a.z[n * groups + gr]);
-    q2_f32x4 tmp = q2_f32x4{0.f, 0.f, 0.f, 0.f}, sum = tmp;
-    uint64_t pz = ~0ull;
-    for (int t = 0; t < steps; ++t) {
-      const int64_t k0 = gr * m.group + 32 * t;
-      const uint32_t w[1] = {*reinterpret_cast<const uint32_t*>(wp + k0 / 2)};
-      const q2_u32x4 av = *reinterpret_cast<const q2_u32x4*>(xp + k0);
-      pz &= q4_part_zero(w, z);
-      tmp = mfma(av, q4_frag(w[0], kc), tmp);
-      sum = mfma(av, sones, sum);
-    }
-    const float d = f16_to_f32((uint16_t)zero_where(sp[gr], column_all(pz)));
     const float z16 = m.zero == ZERO_8 ? 0.f : z * 0.0625f;   // ZERO_8: off with the sum already
+    for (int b = 0; b < blocks; ++b) {
+      q2_f32x4 tmp = q2_f32x4{0.f, 0.f, 0.f, 0.f}, sum = tmp;
+      uint64_t pz = ~0ull;
+      for (int t = 0; t < steps; ++t) {
+        const int64_t k0 = gr * m.group + BLOCK_K * b + 32 * t;
+        const uint32_t w[1] = {*reinterpret_cast<const uint32_t*>(wp + k0 / 2)};
+        const q2_u32x4 av = *reinterpret_cast<const q2_u32x4*>(xp + k0);
+        pz &= q4_part_zero(w, z);
+        tmp = mfma(av, q4_frag(w[0], kc), tmp);
+        sum = mfma(av, sones, sum);
+      }
+      const float d = f16_to_f32((uint16_t)zero_where(sp[gr], column_all(pz)));
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(d, __builtin_fmaf(-z16, sum[e], tmp[e] - sum[e]), acc[e]);
+      for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(d, __builtin_fmaf(-z16, sum[e], tmp[e] - sum[e]), acc[e]);
+    }
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) out[4 * g + e][cb] = acc[e] * 16.f;

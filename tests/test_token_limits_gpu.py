@@ -57,3 +57,39 @@ def test_small_zero_points_of_wide_weights(group, m, n):
     xb, x = acts(502, m, 384)
     y = q2.q4_matvec(x, *(torch.from_numpy(t).to(DEV) for t in (packed, scale, zero)))
     check_terms(y[:, torch.from_numpy(cols).to(DEV)], O.bf16_to_f64(xb), T.weight(packed[cols], scale[cols], zero[cols]))
+
+
+def largest_inputs(m, k):
+    """bf16 rows whose sum of |x| over any 128 inputs is 0.99 2^126, as bits and on the device."""
+    g = np.random.default_rng([503, m, k])
+    xb = np.where(g.random((m, k)) < 0.9, 0x7AFD, 0xFAFD).astype(np.uint16)    # +-(1 + 125 / 128) 2^118
+    return xb, torch.from_numpy(xb.view(np.int16)).to(DEV).view(torch.bfloat16)
+
+
+@pytest.mark.parametrize("group,k", [(32, 96), (64, 64), (128, 128), (64, 1280), (128, 2560), (512, 1024), (1280, 2560)])
+@pytest.mark.parametrize("zero", [None, 15.0, 16.0])
+@pytest.mark.parametrize("m", [1, 9, 40])
+def test_largest_inputs(group, k, zero, m):
+    """The largest x that are promised to work."""
+    g = np.random.default_rng(504)
+    packed = g.integers(0, 256, (30, k // 2)).astype(np.uint8)
+    scale = ((g.random((30, k // group)) + 0.5) * 2.0 ** -12).astype(np.float16)
+    z = None if zero is None else np.full(scale.shape, zero, np.float16)
+    xb, x = largest_inputs(m, k)
+    y = q2.q4_matvec(x, *(None if t is None else torch.from_numpy(t).to(DEV) for t in (packed, scale, z)))
+    check_terms(y, O.bf16_to_f64(xb), T.weight(packed, scale, z))
+
+
+def test_largest_inputs_of_more_rows_than_the_grid():
+    """The same in one group of 512 inputs, whose sum of |x| is beyond fp32, for more rows than the grid's second
+    dimension takes."""
+    m, k = 65535 * 64 + 70, 512
+    g = np.random.default_rng(505)
+    packed = g.integers(0, 256, (2, k // 2)).astype(np.uint8)
+    scale = np.full((2, 1), 2.0 ** -12, np.float16)
+    xb, x = largest_inputs(50, k)
+    x = torch.abs(x).repeat(m // 50 + 1, 1)[:m].contiguous()
+    y = q2.q4_matvec(x, torch.from_numpy(packed).to(DEV), torch.from_numpy(scale).to(DEV))
+    check_terms(y[:50], O.bf16_to_f64(xb & 0x7FFF), T.weight(packed, scale, None))
+    whole = y[:m // 50 * 50].view(-1, 50, 2)
+    assert (whole == whole[0]).all() and torch.equal(y[m // 50 * 50:], y[:m % 50])
