@@ -518,7 +518,8 @@ typedef struct q2_sampling {
  * Sums are in units of 2^-S of the best token's p, S = 62 - ceil(log2 V) and at most
  * 51, each p rounded once: exact, the same in any order, run-to-run deterministic.  A p
  * below half a unit counts as 0.  1 <= V <= 2^24, B <= 2^30 (Q2_ERR_SHAPE
- * otherwise).  Outputs must not overlap the logits, the settings or each other.
+ * otherwise).  Outputs must not overlap the logits, the settings, each other or, without
+ * being it, u (Q2_ERR_ARG), nor the workspace.
  * Asynchronous; calls that share a workspace must be ordered on one stream.
  */
 int q2_sample(const void* logits, int64_t B, int64_t V, int64_t ld, uint32_t flags, const q2_sampling* settings,

@@ -625,7 +625,8 @@ def q2_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, token=N
 
     temperature divides the logits (0: the largest logit); then min_p leaves the tokens with at least min_p times the
     largest probability, top_k of those the first top_k (0: all), top_p of those the fewest whose sum reaches top_p of
-    theirs (1: all).  Each is a number, or a tensor [B] with one per row (top_k i32, the others f32)."""
+    theirs (1: all).  Each is a number, or a tensor [B] with one per row (top_k i32, the others f32).  A given token or
+    prob shares no memory with the other arguments, except that prob may be u."""
     lib = load()
     dev = _here()
     b, v = logits.shape

@@ -11,6 +11,35 @@ using namespace q2host;
 
 bool sample_sizes_ok(int64_t B, int64_t V) { return B >= 0 && B <= (1 << 30) && V >= 1 && V <= (1 << 24); }
 
+// An output of B 4-byte elements against B rows of row_bytes, pitch bytes apart: what lies
+// between the rows is not theirs.
+bool overlaps_rows(const void* out, int64_t B, const void* rows, int64_t row_bytes, int64_t pitch) {
+  if (!overlap(out, 4 * B, rows, (B - 1) * pitch + row_bytes)) return false;
+  const uintptr_t o = reinterpret_cast<uintptr_t>(out), r = reinterpret_cast<uintptr_t>(rows);
+  if (o < r) return true;                                // reaches the first row
+  const int64_t row = (int64_t)(o - r) / pitch, at = (int64_t)(o - r) % pitch;
+  return at < row_bytes || (row + 1 < B && at + 4 * B > pitch);
+}
+
+// Outputs are written while other rows' inputs are read.  u may be an output itself: a
+// row's is read before its token and probability are written.
+int check_outputs(const q2_sampling& c, const void* logits, int64_t row_bytes, int64_t pitch, int64_t B, const float* u,
+                  const int32_t* token, const float* prob) {
+  if (overlap(token, 4 * B, prob, 4 * B)) return fail(Q2_ERR_ARG, "token overlaps prob");
+  const struct {
+    const void* p;
+    const char* name;
+  } outs[] = {{token, "token"}, {prob, "prob"}},
+    ins[] = {{c.temperature_rows, "temperature"}, {c.top_k_rows, "top_k"}, {c.top_p_rows, "top_p"}, {c.min_p_rows, "min_p"}};
+  for (const auto& out : outs) {
+    if (overlaps_rows(out.p, B, logits, row_bytes, pitch)) return fail(Q2_ERR_ARG, "%s overlaps the logits", out.name);
+    if (out.p != u && overlap(out.p, 4 * B, u, 4 * B)) return fail(Q2_ERR_ARG, "%s overlaps u without being it", out.name);
+    for (const auto& in : ins)
+      if (in.p && overlap(out.p, 4 * B, in.p, 4 * B)) return fail(Q2_ERR_ARG, "%s overlaps %s", out.name, in.name);
+  }
+  return Q2_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -77,6 +106,8 @@ int q2_sample(const void* logits, int64_t B, int64_t V, int64_t ld, uint32_t fla
     return st;
   if (B == 0) return ok();
   if ((st = check_workspace(workspace, workspace_bytes, q2_sample_workspace_bytes(B, V)))) return st;
+  const int64_t size = bf16 ? 2 : 4;
+  if ((st = check_outputs(c, logits, V * size, (B > 1 ? ld : V) * size, B, u, token, prob))) return st;
   if ((st = check_device())) return st;
   q2dev::SampleArgs a = {};
   a.logits = logits;

@@ -7,8 +7,9 @@ import torch
 import oracle.q2_oracle as O
 import oracle.token_oracle as T
 import ternary_weight_quantized_q2_amd as q2
-from tests.test_fused_gpu import check_terms
+from tests.test_fused_gpu import check_terms, rnd
 from tests.test_parity_gpu import DEV, acts
+from tests.test_token_gpu import uniform
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +94,32 @@ def test_largest_inputs_of_more_rows_than_the_grid():
     check_terms(y[:50], O.bf16_to_f64(xb & 0x7FFF), T.weight(packed, scale, None))
     whole = y[:m // 50 * 50].view(-1, 50, 2)
     assert (whole == whole[0]).all() and torch.equal(y[m // 50 * 50:], y[:m % 50])
+
+
+@pytest.mark.parametrize("b,v", [(1, 300), (300, 300), (3, 50021), (100, 60000)])
+@pytest.mark.parametrize("settings", [dict(), dict(top_k=40, top_p=0.9), dict(temperature=0.0), dict(temperature=2.0, top_k=3000)])
+def test_random_numbers_in_an_output(b, v, settings):
+    """prob may be u, and token the memory of u."""
+    logits, u = (rnd(b, b, v) * 3).to(DEV), uniform(b, b).to(DEV)
+    want = q2.q2_sample(logits, u, **settings)
+    own = u.clone()
+    got = q2.q2_sample(logits, own, prob=own, **settings)
+    assert got.prob is own and all(torch.equal(a, c) for a, c in zip(got, want))
+    own = u.clone()
+    got = q2.q2_sample(logits, own, token=own.view(torch.int32), **settings)
+    assert all(torch.equal(a, c) for a, c in zip(got, want))
+    wide = torch.cat([u, u])
+    if b > 1:
+        with pytest.raises(q2.Q2Error, match="overlaps u"):
+            q2.q2_sample(logits, wide[:b], prob=wide[1:b + 1], **settings)
+    with pytest.raises(q2.Q2Error, match="overlaps the logits"):
+        q2.q2_sample(logits, u, prob=logits.view(-1)[-b:], **settings)
+
+
+def test_outputs_beside_the_logits():
+    """Outputs in the columns that rows of logits have behind them."""
+    wide = (rnd(5, 6, 320) * 3).to(DEV)
+    want = q2.q2_sample(wide[:, :300], uniform(5, 6).to(DEV), top_p=0.9)
+    token, prob = wide[2, 300:306].view(torch.int32), wide[4, 310:316]
+    got = q2.q2_sample(wide[:, :300], uniform(5, 6).to(DEV), top_p=0.9, token=token, prob=prob)
+    assert all(torch.equal(a, c) for a, c in zip(got, want)) and got.prob is prob
