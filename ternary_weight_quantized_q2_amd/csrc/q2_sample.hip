@@ -885,13 +885,16 @@ __global__ __launch_bounds__(SM_THREADS) void sample_draw_kernel(SampleArgs a, i
 // Tokens of a part; 0 where a workgroup takes whole rows.  As many parts as keep the
 // workgroups of all rows on the CUs at once, where what the parts spare, about half a
 // microsecond per 1024 tokens, is more than three launches and the ways through memory
-// cost, which grows with the rows.  By one workgroup and by parts: 1 row of 16384 20.7 / 21.8
-// us, of 20000 23.9 / 21.9; 32 of 16384 22.6 / 27.1, of 32768 32.6 / 32.3; 64 of 32768
-// 33.5 / 36.4, of 50021 45.1 / 38.1; 96 of 50021 46.5 / 44.8; 128 of 32768 35.7 / 40.8, of
-// 128009 97.8 / 85.0.  96 of 128009 94.9 / 75.6, in three parts, which do not fit at once, 97.7.
+// cost, which grows with the rows, quickly up to 32.  By one workgroup and by parts, f32 from the
+// whole distribution: 1 row of 16384 19.4 / 21.7 us, of 20000 22.5 / 21.6; 8 of 18000 22.4 / 23.5,
+// of 24000 25.7 / 24.0; 16 of 20000 24.2 / 25.1, of 24000 26.1 / 25.6; 32 of 24000 26.7 / 29.5, of 32768
+// 31.2 / 31.9, of 40000 36.8 / 32.7; 64 of 32768 32.0 / 36.3, of 40000 37.5 / 37.5, of 50021 43.6 / 38.0; 96
+// of 40000 38.3 / 41.7, of 50021 45.0 / 44.8, of 64000 51.6 / 48.6; 128 of 50021 45.5 / 48.8, of 64000 53.6 / 55.5,
+// of 128009 95.8 / 84.8.  With top-k and top-p, or bf16, the two meet up to a tenth of the tokens apart.
 static int part_tokens(int64_t B, int64_t V) {
   const int64_t parts = std::min<int64_t>({256 / std::max<int64_t>(B, 1), (V + 4095) / 4096, SM_PARTS});
-  if (parts <= 1 || V - V / parts < 14000 + 100 * B) return 0;
+  const int64_t least = std::max(std::min<int64_t>(14000 + 350 * B, 25000), 14000 + 100 * B);
+  if (parts <= 1 || V - V / parts < least) return 0;
   return (int)(((V + parts - 1) / parts + 1023) / 1024 * 1024);
 }
 

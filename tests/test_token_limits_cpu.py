@@ -1,4 +1,5 @@
-"""Outputs of the sampler that overlap what it reads: refused before any HIP call, so no GPU is needed."""
+"""Outputs of the sampler that overlap what it reads, refused before any HIP call, and the sizes from which it cuts rows:
+no GPU is needed."""
 import ctypes
 
 import pytest
@@ -76,3 +77,12 @@ def test_outputs_over_u_and_settings(lib, name):
 
 def test_empty_outputs_overlap_nothing(lib):
     assert sample(lib, b=0, token=FAKE, prob=FAKE, u=FAKE)[0] == q2.Q2_OK
+
+
+@pytest.mark.parametrize("b,v,cut", [(1, 16384, False), (1, 20000, True), (8, 18000, False), (8, 24000, True), (16, 20000, False),
+                                     (16, 24000, True), (32, 24000, False), (32, 40000, True), (48, 28000, False), (64, 32768, False),
+                                     (64, 50021, True), (80, 36000, False), (96, 40000, False), (96, 64000, True),
+                                     (128, 50021, False), (128, 128009, True), (129, 1 << 24, False)])
+def test_rows_are_cut_where_that_measured_less(b, v, cut):
+    """A workspace is needed where several workgroups share a row."""
+    assert (q2.sample_workspace_bytes(b, v) > 0) == cut
