@@ -277,6 +277,8 @@ int q2_linear_a8(const uint16_t* x_bf16, const uint8_t* packed, const uint16_t* 
  * that hid in one flipped bit" (nibble order), and We're Teaching Your
  * Browser to Paint, section "What's left" ((q - zero) * scale).  The group
  * length 128 and the f16 zero point in code units are this library's reading.
+ * The zero point enters as 1 + z / 16 in fp32: exactly where |z| >= 2^-9 or z = 0, else
+ * off by at most 2^-20 (q4_linear_fused and q4_linear_grouped alike).
  *   packed4    u8  [N, K/2]  (in);  scale_f16, zero_f16  u16 [N, K/128]  (in)
  *   y          f32 [M, N]    (out).   Asynchronous.
  */
@@ -510,7 +512,7 @@ typedef struct q2_sampling {
  *   settings  host pointer, read before the call returns (its arrays are device
  *             memory); NULL draws from the whole distribution at temperature 1
  *   u         f32 [B], uniform in [0, 1); below 0 or NaN counts as 0, 1 and
- *             above draws the last token that is left                      (in)
+ *             above draws the last token that is left with a p above 0     (in)
  *   token     i32 [B]; -1 for a row whose tokens are all masked            (out)
  *   prob      f32 [B]: the token's p over the sum of what is left; 0 with -1  (out)
  *   workspace device scratch of >= q2_sample_workspace_bytes(B, V) bytes, 256-byte
