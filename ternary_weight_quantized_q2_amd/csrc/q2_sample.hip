@@ -339,7 +339,10 @@ __device__ __forceinline__ uint64_t draw_target(float u, uint64_t total) {
   return std::min(t, total - 1) + 1;
 }
 
-// The row's borders by passes over it, whatever the histogram's parts hold.
+// The row's borders by passes over it, whatever the histogram's parts hold: by one
+// workgroup, also of a row that several share.  16-bit logits far from zero, whose steps are
+// wide, come here: 128009 of them around 16, top-p 0.99 339 us for one row (45 around 10, where
+// the list holds the tokens), 444 for 64 rows; 128009 equal ones 680 us.
 __device__ __noinline__ void sample_slow(SampleShared& s, const Measure& me, const void* row, int bf16, int V, int top_k,
                                          float top_p, float u, uint64_t total, uint32_t count, int32_t* token, float* prob) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
@@ -604,7 +607,8 @@ __device__ __forceinline__ void each_chosen(const Measure& me, const Borders& o,
 
 // The draw from the n tokens of the parts, in s.list in any order (n <= SM_LIST);
 // start_s, start_n: what lies before the parts.  By the first SM_DRAW threads alone (one row of
-// 4099: 15.3 us in place of 16.5 by all).
+// 4099: 15.3 us in place of 16.5 by all).  One row of 8192 with 100 equal logits at the border 19 us,
+// 300 26, 1000 37, 2000 62.
 __device__ __forceinline__ void draw(SampleShared& s, const Settings& c, const Measure& me, bool by_k, bool by_p, uint64_t total,
                                      const uint64_t* start_s, const uint32_t* start_n, uint32_t n, int32_t* token, float* prob) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
@@ -714,8 +718,9 @@ __device__ __forceinline__ const void* row_of(const SampleArgs& a, int64_t r) {
 // ---- a workgroup per row ------------------------------------------------------------
 // One row of 4099, top-k: 15.3 us, dependent steps of one workgroup (best 2.4, histogram 3.4,
 // borders 3.0, gathering 2.5, draw 2.6).  256 rows of 128009, min-p: 91 us for 131 MB;
-// the best logit 24 (5.4 TB/s), exponentials and LDS additions 24, gathering 16, the slowest
-// row 20 behind the median; vector instructions issue in 38 % of the cycles.
+// the best logit 24 (5.4 TB/s), a pass of exponentials and LDS additions 24, the one that gathers 16, the slowest
+// row 20 behind the median; vector instructions issue in 38 % of the cycles.  Greedy, 256
+// rows of 128009 48 us: the row is read once for its largest logit and once for its place.
 __global__ __launch_bounds__(SM_THREADS) void sample_kernel(SampleArgs a, SampleUnits of) {
   extern __shared__ __align__(16) uint8_t smem[];
   SampleShared& s = *reinterpret_cast<SampleShared*>(smem);
@@ -762,7 +767,7 @@ __global__ __launch_bounds__(SM_THREADS) void sample_kernel(SampleArgs a, Sample
 // Few rows leave most CUs idle: one row of 128009 takes one workgroup 87 us.  Here a row's
 // tokens are cut into parts, and what the workgroups of a row tell each other goes through
 // the workspace from one launch to the next: each part's best logit, the histogram, the
-// list of the tokens to sort.  One row of 128009 25 us, 32 rows 42, 64 rows bf16 64: the four
+// list of the tokens to sort.  One row of 128009 25 us, 32 rows 42, 64 rows bf16 61 to 64: the four
 // launches' dependent steps, then the 64-bit exponentials (8 and 13 us of the last two).
 struct RowSpace {
   uint64_t sum[SM_BUCKETS];

@@ -383,7 +383,9 @@ static hipError_t run_matvec(const MatvecArgs& m, hipStream_t stream) {
   const int64_t row_blocks = (a.M + ROWS - 1) / ROWS;
   // Waves.  One to four rows: about ten for each CU, where the strips are fewer by
   // sharing them; where they are more, two strips by two waves each per workgroup.  More
-  // waves pay more for their start, fewer leave memory idle.  Workgroups of up to
+  // waves pay more for their start, fewer leave memory idle.  A CU holds that many while
+  // the rows take up to 64 KB of LDS; beyond that x goes in two parts of up to 79 KB, one
+  // workgroup per CU (K = 11008, N = 16384: one row 28 us, two 47, three 81).  Workgroups of up to
   // sixteen for more rows, one per CU, whose x goes to its LDS once: as many tiles for each
   // as fill the fewest turns of the CUs.
   // One row, K = 2560: 1216 strips 11.1 us with two waves, 12.9 with one, 16.8 with five;
@@ -445,10 +447,12 @@ static hipError_t run_matvec(const MatvecArgs& m, hipStream_t stream) {
 template <int GM, int ZM>
 static hipError_t pick_matvec(const MatvecArgs& m, hipStream_t stream) {
   if (m.f.M <= 4) return run_matvec<GM, ZM, 1, 1>(m, stream);
-  // More rows share a decoded weight as there is work for all CUs.  In tiles of 16 x 16
-  // outputs, with 16, 32 and 64 rows: 320 tiles (K = 2560) 7.1 / 11.2 us, 640 8.5 / 11.2 / 22.5,
-  // 1216 14.1 / 14.9; 1536 (K = 4096) 18.8 / 17.7, 2432 (K = 2560) 20.0 / 18.5 / 23.2;
-  // 16384 85 / 66 / 70, 32004 167 / 141 / 132.
+  // More rows share a decoded weight as there is work for all CUs.  By tiles of 16 x 16
+  // outputs, groups of 64 with 4-bit zero points, 16 and 32 rows per decoded weight: K = 2560,
+  // 32 rows, 768 tiles 8.5 / 11.1 us, 1216 12.2 / 13.2, 2048 14.7 / 15.3, but 20 rows, 1216 tiles 11.8 /
+  // 11.2, and K = 4096, 32 rows, 1216 tiles 16.7 / 16.2, 1792 20.1 / 18.8; 61 rows, K = 2560, groups of
+  // 128, 2432 tiles 19.4 / 17.9.  The border lies where the first of these cross.  32 and 64 rows,
+  // 64 rows of K = 2560: 12288 tiles 51 / 61, 20480 87 / 89, 24576 91 / 90, 32004 120 / 117.
   const int64_t work = ((fused_n_out(m.f) + 15) / 16 << m.f.gated) * ((m.f.M + 15) / 16);
   if (m.f.M <= 16 || work <= 1200) return run_matvec<GM, ZM, 4, 1>(m, stream);
   if (m.f.M > 32 && work >= 24000) return run_matvec<GM, ZM, 4, 4>(m, stream);
