@@ -6,7 +6,7 @@
 // sum x (1 + q / 16) - (1 + z / 16) sum x = sum x (q - z) / 16 on the matrix cores,
 // exact products and fp32 sums, and one FMA per output applies the group's scale.  Of an
 // f16 zero point below 2^-9 the sum 1 + z / 16 would lose bits: sum x goes off first,
-// then (z / 16) sum x (over 17 to 64 rows up to 6 % slower than the one FMA with 1 + z / 16;
+// then (z / 16) sum x (over 17 to 64 rows up to 7 % slower than the one FMA with 1 + z / 16;
 // both forms with a branch by what the unit's zero points need spill, up to 35 % slower).
 // A group whose codes all equal a whole zero point takes a scale of 0, so it adds exactly
 // nothing; where the sums with 1.5, which stands for 8 without zero points, run through
@@ -450,9 +450,10 @@ static hipError_t pick_matvec(const MatvecArgs& m, hipStream_t stream) {
   // More rows share a decoded weight as there is work for all CUs.  By tiles of 16 x 16
   // outputs, groups of 64 with 4-bit zero points, 16 and 32 rows per decoded weight: K = 2560,
   // 32 rows, 768 tiles 8.5 / 11.1 us, 1216 12.2 / 13.2, 2048 14.7 / 15.3, but 20 rows, 1216 tiles 11.8 /
-  // 11.2, and K = 4096, 32 rows, 1216 tiles 16.7 / 16.2, 1792 20.1 / 18.8; 61 rows, K = 2560, groups of
-  // 128, 2432 tiles 19.4 / 17.9.  The border lies where the first of these cross.  32 and 64 rows,
-  // 64 rows of K = 2560: 12288 tiles 51 / 61, 20480 87 / 89, 24576 91 / 90, 32004 120 / 117.
+  // 11.2, and K = 4096, 32 rows, 1216 tiles 16.7 / 16.2, 1792 20.1 / 18.8; groups of 32 with f16 zero
+  // points, K = 2560, 32 rows, 1216 tiles 15.2 / 17.3; 61 rows, K = 2560, groups of 128, 2432 tiles 19.4 /
+  // 17.9.  The border lies where the first of these cross.  32 and 64 rows, 64 rows of K = 2560:
+  // 12288 tiles 51 / 61, 20480 87 / 89, 24576 91 / 90, 32004 120 / 117.
   const int64_t work = ((fused_n_out(m.f) + 15) / 16 << m.f.gated) * ((m.f.M + 15) / 16);
   if (m.f.M <= 16 || work <= 1200) return run_matvec<GM, ZM, 4, 1>(m, stream);
   if (m.f.M > 32 && work >= 24000) return run_matvec<GM, ZM, 4, 4>(m, stream);
